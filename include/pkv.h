@@ -687,6 +687,108 @@ PKV_API int pkv_decode_attention_noalloc(void *out, const void *q, const void *k
  * fails.  This is the only library call that synchronises. */
 PKV_API int pkv_get_device_error(pkv_stream_t stream, int *code);
 
+/* ================================================================ rotary positions
+ * Rotation of q and k by their positions, before the append: pair i of the first
+ * rotary_dim dims of a head turns by the angle position x f_i,
+ *     y_a = m (x_a cos - x_b sin),  y_b = m (x_b cos + x_a sin),
+ * the pair being dims (i, i + rotary_dim / 2), or (2i, 2i + 1) with interleaved != 0;
+ * dims past rotary_dim are copied unchanged.  float32 arithmetic, one rounding to fp16.
+ * The frequencies are fixed-point: f_i / 2 pi in units of 2^-64 turns, so the phase
+ * is exact at any int32 position (negative ones turn backwards). */
+
+/* How the frequencies are derived from the base. */
+#define PKV_ROPE_PLAIN 0  /* f_i = base^(-2i / d) */
+#define PKV_ROPE_LINEAR 1 /* f_i / factor: positions interpolated */
+#define PKV_ROPE_BASE 2   /* base x factor^(d / (d - 2)): the base stretched */
+#define PKV_ROPE_BANDS 3  /* pairs making over fast_turns turns in original_context tokens keep f_i, under
+                             slow_turns f_i / factor, between them blended linearly in the turns */
+#define PKV_ROPE_RAMP 4   /* the same ends, blended linearly in the pair's index; magnitude 0.1 ln(factor) + 1 */
+#define PKV_MAX_ROPE_HEAD_DIM 256
+
+typedef struct pkv_rope_spec {
+    double base;             /* > 1 */
+    double factor;           /* context extension, >= 1 (not read by PLAIN) */
+    double original_context; /* BANDS, RAMP: tokens the model was trained on */
+    double slow_turns;       /* BANDS, RAMP: > 0 */
+    double fast_turns;       /* BANDS, RAMP: > slow_turns */
+    int32_t method;          /* PKV_ROPE_* */
+    int32_t rotary_dim;      /* even, > 0 */
+} pkv_rope_spec;
+
+/* Host call: the rotary_dim / 2 fixed-point frequencies of a spec, and the magnitude m
+ * (1 except for RAMP).  Either output may be NULL.  Errors: INVALID_ARG. */
+PKV_API int pkv_rope_frequencies(int64_t *frequencies, double *magnitude, const pkv_rope_spec *spec);
+
+/* Rotate q [num_tokens][num_q_heads][head_dim] into q_out and k into k_out (num_kv_heads
+ * 0: q alone; num_q_heads 0: k alone).  fp16, heads contiguous; the strides are the elements between tokens
+ * (multiples of 8), so the slices of a fused projection are read where they lie.  An output may be
+ * its input (in place), else it must not overlap any input.
+ *   positions   : DEVICE int32 [num_tokens]
+ *   frequencies : DEVICE int64 [rotary_dim / 2] (pkv_rope_frequencies, copied there once)
+ * head_dim and rotary_dim are multiples of 16, rotary_dim <= head_dim <= PKV_MAX_ROPE_HEAD_DIM.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+PKV_API int pkv_rope(void *q_out, int64_t q_out_stride, void *k_out, int64_t k_out_stride, const void *q,
+                     int64_t q_stride, const void *k, int64_t k_stride, const int32_t *positions,
+                     const int64_t *frequencies, int num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+                     int rotary_dim, int interleaved, float magnitude, pkv_stream_t stream);
+
+/* pkv_rope with the append in the same launch: the rotated k_new and v_new as it is go to their
+ * slots of the cache, q is rotated into q_out.  slot_mapping as pkv_append's: a negative slot skips
+ * the token's k and v (its q is rotated all the same), one past the pool is skipped and recorded as
+ * PKV_DEV_BAD_SLOT.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+PKV_API int pkv_rope_append(void *q_out, int64_t q_out_stride, const void *q, int64_t q_stride, const void *k_new,
+                            int64_t k_stride, const void *v_new, int64_t v_stride, void *k_cache, void *v_cache,
+                            const int64_t *slot_mapping, const int32_t *positions, const int64_t *frequencies,
+                            int num_tokens, int num_q_heads, int num_kv_heads, int head_dim, int rotary_dim,
+                            int block_size, int64_t num_blocks, int interleaved, float magnitude,
+                            pkv_stream_t stream);
+
+/* ================================================================ accumulated attention weights
+ * scores is float32 [num_seqs][num_kv_heads][score_capacity], row (b, h) holding for each cached
+ * position of request b the sum of the attention weights it received from the q heads of kv head h:
+ * what pkv_evict ranks positions by.  Zero a request's rows when it starts.  Every entry has one
+ * writer per call (no atomics), so results do not depend on any order.  score_capacity must be at
+ * least max_blocks_per_seq * block_size.  Entries at or past context_lens[b] are left as they are. */
+
+/* Bytes of workspace pkv_decode_attention_weights needs for contexts up to max_context (the table's
+ * capacity max_blocks_per_seq * block_size).  Zero-filled once by the caller; every call leaves
+ * its counters zero.  Calls that may run at the same time need one each.  0: a bad argument. */
+PKV_API size_t pkv_weights_workspace_size(int num_seqs, int num_q_heads, int head_dim, int max_context);
+
+/* pkv_decode_attention, and scores[b][h][t] += the step's weights on position t.  A request with
+ * context 0 gets a zero output row.  Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */
+PKV_API int pkv_decode_attention_weights(void *out, float *scores, int64_t score_capacity, const void *q,
+                                         const void *k_cache, const void *v_cache, const int32_t *block_tables,
+                                         const int32_t *context_lens, int num_seqs, int max_blocks_per_seq,
+                                         int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                                         int64_t num_blocks, float scale, void *workspace, size_t workspace_bytes,
+                                         pkv_stream_t stream);
+
+/* ================================================================ eviction
+ * Cut every request longer than `budget` positions back to `budget`, per kv head: the first `sinks`
+ * positions, the last `recent`, and of those between them the ones with the largest scores (ties:
+ * the lower position; NaN counts as the smallest).  Kept rows of K, V and scores move in position
+ * order to positions 0, 1, ... of new_tables.  Keys are moved as they are: rotated keys keep the
+ * positions they were rotated by.
+ *   kept       : DEVICE int32 [num_seqs][num_kv_heads][budget], the kept positions, ascending, then -1
+ *   new_scores : float32 [num_seqs][num_kv_heads][score_capacity], the kept scores, then zeros;
+ *                may be scores itself
+ *   new_lens   : DEVICE int32 [num_seqs], min(context_lens[b], budget); may be context_lens itself
+ *   new_tables : DEVICE int32 [num_seqs][max_new_blocks]; each entry is either the request's own
+ *                block_tables entry of the same index (compaction in place; the blocks must not be shared
+ *                with another request) or a block that no block_tables row of the call names (a shared
+ *                block's rows are copied out).  May be block_tables itself.
+ * A context past its table is cut and recorded as PKV_DEV_BAD_CONTEXT, as is a new table too short;
+ * a bad block id skips its rows and is recorded as PKV_DEV_BAD_BLOCK_ID.  recent + sinks <= budget;
+ * a table covers at most PKV_MAX_EVICT_CONTEXT positions.  head_dim is PKV_HEAD_DIM.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+#define PKV_MAX_EVICT_CONTEXT 524288
+PKV_API int pkv_evict(void *k_cache, void *v_cache, int32_t *kept, float *new_scores, int32_t *new_lens,
+                      const float *scores, const int32_t *block_tables, const int32_t *new_tables,
+                      const int32_t *context_lens, int num_seqs, int max_blocks_per_seq, int max_new_blocks,
+                      int64_t score_capacity, int num_kv_heads, int head_dim, int block_size, int64_t num_blocks,
+                      int budget, int recent, int sinks, pkv_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

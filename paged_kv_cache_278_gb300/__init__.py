@@ -32,6 +32,8 @@ __all__ = [
     "decode_step_int8k", "empty_int8k_cache", "decode_attention_multi", "decode_step_multi", "make_multi_workspace",
     "copy_blocks_between", "empty_int8kv_cache", "append_int8kv", "decode_attention_int8kv", "decode_step_int8kv",
     "empty_fp8kv_cache", "append_fp8kv", "decode_attention_fp8kv", "decode_step_fp8kv",
+    "rope_frequencies", "rope_magnitude", "rope", "rope_append", "make_weights_workspace", "decode_attention_weights",
+    "evict",
     "device_error", "slot_mapping", "BlockPool", "PkvError", "library_path",
     "PKV_DEFAULT_PARTITION", "PKV_MAX_PARTITION", "PKV_HEAD_DIM",
     "PKV_DEV_OK", "PKV_DEV_BAD_BLOCK_ID", "PKV_DEV_BAD_CONTEXT", "PKV_DEV_BAD_SLOT", "PKV_DEV_WAIT_TIMEOUT",
@@ -644,6 +646,181 @@ def slot_mapping(block_tables: torch.Tensor, positions: torch.Tensor, block_size
                                ctypes.cast(pos.data_ptr(), _lib.c_i32p), pos.shape[0], bt.shape[1], block_size)
     _lib.check(st, "pkv_slot_mapping")
     return out
+
+
+# ---------------------------------------------------------------- rotary positions
+
+def _rope_spec(rotary_dim, base, method, factor, original_context, slow_turns, fast_turns):
+    if method not in _lib.ROPE_METHODS:
+        raise ValueError(f"method must be one of {sorted(_lib.ROPE_METHODS)}")
+    if fast_turns is None:
+        fast_turns = 32.0 if method == "ramp" else 4.0
+    return _lib.RopeSpec(float(base), float(factor), float(original_context), float(slow_turns), float(fast_turns),
+                         _lib.ROPE_METHODS[method], int(rotary_dim))
+
+
+def rope_frequencies(rotary_dim: int, base: float = 10000.0, method: str = "none", factor: float = 1.0,
+                     original_context: int = 0, slow_turns: float = 1.0, fast_turns: float | None = None,
+                     device="cuda") -> torch.Tensor:
+    """The fixed-point frequencies rope and rope_append take: int64 [rotary_dim / 2], f_i / 2 pi in units
+    of 2^-64 turns.  method "none", or for contexts stretched by `factor`: "linear" (positions interpolated),
+    "base" (the base stretched), "bands" (slow pairs stretched, fast ones kept, blended between slow_turns
+    and fast_turns turns over original_context tokens), "ramp" (the same, blended over the pair's index;
+    its rotations take magnitude=rope_magnitude(factor)).  Made once per model."""
+    spec = _rope_spec(rotary_dim, base, method, factor, original_context, slow_turns, fast_turns)
+    out = torch.empty(max(int(rotary_dim) // 2, 0), dtype=torch.int64)
+    st = _L().pkv_rope_frequencies(ctypes.cast(out.data_ptr(), _lib.c_i64p), None, ctypes.byref(spec))
+    _lib.check(st, "pkv_rope_frequencies")
+    return out.to(device)
+
+
+def rope_magnitude(factor: float) -> float:
+    """The factor on cos and sin that goes with method "ramp": 0.1 ln(factor) + 1."""
+    spec = _rope_spec(2, 10000.0, "ramp", factor, 1, 1.0, None)
+    m = ctypes.c_double(0.0)
+    _lib.check(_L().pkv_rope_frequencies(None, ctypes.byref(m), ctypes.byref(spec)), "pkv_rope_frequencies")
+    return m.value
+
+
+def _need_rows(t: torch.Tensor, name: str, device, shape=None):
+    """fp16 [tokens, heads, dim] whose heads lie together; returns the elements between tokens."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.float16 or t.dim() != 3:
+        raise ValueError(f"{name}: expected float16 [tokens, heads, dim], got {t.dtype} {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    n, h, d = t.shape
+    if d > 1 and t.stride(2) != 1 or h > 1 and t.stride(1) != d:
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    return t.stride(0) if n > 1 else h * d
+
+
+def _rope_inputs(q, positions, frequencies, device):
+    _need(positions, "positions", torch.int32, 1, device)
+    _need(frequencies, "frequencies", torch.int64, 1, device)
+    if positions.shape[0] != q.shape[0]:
+        raise ValueError("positions must have one entry per token")
+    return 2 * frequencies.shape[0]
+
+
+def rope(q_out: torch.Tensor, k_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor,
+         frequencies: torch.Tensor, interleaved: bool = False, magnitude: float = 1.0, stream=None) -> None:
+    """Rotate q [T, Hq, D] into q_out and k [T, Hkv, D] into k_out by their positions [T] (int32).  The first
+    2 * len(frequencies) dims of each head turn, in pairs (i, i + half) or, interleaved, (2i, 2i + 1); the
+    rest is copied.  Rows may be slices of a fused projection (any token stride); an output may be its input."""
+    dev = q.device
+    qs = _need_rows(q, "q", dev)
+    ks = _need_rows(k, "k", dev, (q.shape[0], k.shape[1], q.shape[2]) if k.dim() == 3 else None)
+    qos = _need_rows(q_out, "q_out", dev, q.shape)
+    kos = _need_rows(k_out, "k_out", dev, k.shape)
+    r = _rope_inputs(q, positions, frequencies, dev)
+    with torch.cuda.device(dev):
+        st = _L().pkv_rope(q_out.data_ptr(), qos, k_out.data_ptr(), kos, q.data_ptr(), qs, k.data_ptr(), ks,
+                           positions.data_ptr(), frequencies.data_ptr(), q.shape[0], q.shape[1], k.shape[1], q.shape[2], r,
+                           int(bool(interleaved)), float(magnitude), _stream(dev, stream))
+    _lib.check(st, "pkv_rope")
+
+
+def rope_append(q_out: torch.Tensor, q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, k_cache: torch.Tensor,
+                v_cache: torch.Tensor, slot_mapping: torch.Tensor, positions: torch.Tensor, frequencies: torch.Tensor,
+                interleaved: bool = False, magnitude: float = 1.0, stream=None) -> None:
+    """rope and append in one launch: q [T, Hq, D] rotated into q_out (which may be q), k_new [T, Hkv, D] rotated
+    into the cache slots slot_mapping [T] (int64; -1 = skip), v_new copied there.  Rows as rope's."""
+    nb, hkv, bs, d = _cache_shape(k_cache, v_cache)
+    dev = k_cache.device
+    qs = _need_rows(q, "q", dev)
+    t = q.shape[0]
+    if q.shape[2] != d:
+        raise ValueError("q head_dim differs from the cache's")
+    qos = _need_rows(q_out, "q_out", dev, q.shape)
+    ks = _need_rows(k_new, "k_new", dev, (t, hkv, d))
+    vs = _need_rows(v_new, "v_new", dev, (t, hkv, d))
+    _need(slot_mapping, "slot_mapping", torch.int64, 1, dev)
+    if slot_mapping.shape[0] != t:
+        raise ValueError("slot_mapping must have one entry per token")
+    r = _rope_inputs(q, positions, frequencies, dev)
+    with torch.cuda.device(dev):
+        st = _L().pkv_rope_append(q_out.data_ptr(), qos, q.data_ptr(), qs, k_new.data_ptr(), ks, v_new.data_ptr(), vs,
+                                  k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(),
+                                  frequencies.data_ptr(), t, q.shape[1], hkv, d, r, bs, nb, int(bool(interleaved)),
+                                  float(magnitude), _stream(dev, stream))
+    _lib.check(st, "pkv_rope_append")
+
+
+# ---------------------------------------------------------------- accumulated attention weights, eviction
+
+def make_weights_workspace(num_seqs: int, num_q_heads: int, max_context: int, device) -> torch.Tensor:
+    """Zero-filled workspace for decode_attention_weights; max_context is the table's capacity
+    (entries * block_size).  One per call in flight."""
+    n = int(_L().pkv_weights_workspace_size(num_seqs, num_q_heads, PKV_HEAD_DIM, max_context))
+    if n == 0:
+        raise ValueError("invalid weights workspace request")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def _need_scores(scores, name, b, hkv, capacity, device):
+    _need(scores, name, torch.float32, 3, device)
+    if scores.shape[0] != b or scores.shape[1] != hkv or scores.shape[2] < capacity:
+        raise ValueError(f"{name} must be [{b}, {hkv}, {capacity} or more], got {list(scores.shape)}")
+
+
+def decode_attention_weights(out: torch.Tensor, scores: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
+                             v_cache: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor, scale: float,
+                             workspace: torch.Tensor, stream=None) -> torch.Tensor:
+    """decode_attention, and scores [B, Hkv, capacity] (float32) += the weight each cached position received,
+    summed over the q heads of its kv head.  capacity is at least the table's entries * block_size."""
+    nb, hkv, bs, d, b, hq, dev = _decode_inputs(q, k_cache, v_cache, block_tables, context_lens)
+    _need(out, "out", torch.float16, 3, dev)
+    _need(workspace, "workspace", torch.uint8, 1, dev)
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    _need_scores(scores, "scores", b, hkv, block_tables.shape[1] * bs, dev)
+    with torch.cuda.device(dev):
+        st = _L().pkv_decode_attention_weights(out.data_ptr(), scores.data_ptr(), scores.shape[2], q.data_ptr(),
+                                               k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
+                                               context_lens.data_ptr(), b, block_tables.shape[1], hq, hkv, d, bs, nb,
+                                               float(scale), workspace.data_ptr(), workspace.numel(),
+                                               _stream(dev, stream))
+    _lib.check(st, "pkv_decode_attention_weights")
+    return out
+
+
+def evict(k_cache: torch.Tensor, v_cache: torch.Tensor, kept: torch.Tensor, new_scores: torch.Tensor,
+          new_lens: torch.Tensor, scores: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
+          budget: int, recent: int = 0, sinks: int = 0, new_tables: torch.Tensor | None = None, stream=None) -> None:
+    """Cut every request longer than `budget` cached positions to `budget`, per kv head: the first `sinks`, the
+    last `recent` and the largest of scores [B, Hkv, capacity] between them (ties: the lower position).  The kept
+    rows move, in order, to positions 0, 1, ... of new_tables (None: the request's own blocks, which must not be
+    shared).  kept [B, Hkv, budget] int32 receives their old positions (-1 past the end), new_scores (may be
+    scores) their scores and zeros behind them, new_lens [B] (may be context_lens) the new lengths."""
+    nb, hkv, bs, d = _cache_shape(k_cache, v_cache)
+    dev = k_cache.device
+    _need(block_tables, "block_tables", torch.int32, 2, dev)
+    _need(context_lens, "context_lens", torch.int32, 1, dev)
+    b = context_lens.shape[0]
+    new_tables = block_tables if new_tables is None else new_tables
+    _need(new_tables, "new_tables", torch.int32, 2, dev)
+    _need(new_lens, "new_lens", torch.int32, 1, dev)
+    if block_tables.shape[0] != b or new_tables.shape[0] != b or new_lens.shape[0] != b:
+        raise ValueError("block_tables, new_tables, context_lens and new_lens must have one row per request")
+    _need_scores(scores, "scores", b, hkv, block_tables.shape[1] * bs, dev)
+    _need(new_scores, "new_scores", torch.float32, 3, dev)
+    if new_scores.shape != scores.shape:
+        raise ValueError("new_scores must have the shape of scores")
+    _need(kept, "kept", torch.int32, 3, dev)
+    if kept.shape != (b, hkv, budget):
+        raise ValueError(f"kept must be [{b}, {hkv}, {budget}]")
+    with torch.cuda.device(dev):
+        st = _L().pkv_evict(k_cache.data_ptr(), v_cache.data_ptr(), kept.data_ptr(), new_scores.data_ptr(),
+                            new_lens.data_ptr(), scores.data_ptr(), block_tables.data_ptr(), new_tables.data_ptr(),
+                            context_lens.data_ptr(), b, block_tables.shape[1], new_tables.shape[1], scores.shape[2], hkv,
+                            d, bs, nb, int(budget), int(recent), int(sinks), _stream(dev, stream))
+    _lib.check(st, "pkv_evict")
 
 
 class BlockPool:

@@ -41,6 +41,19 @@ PKV_MAX_QUERY_LEN = 1024
 PKV_MAX_STEP_QUERY_LEN = 16
 PKV_NOALLOC_SCRATCH_BYTES = 16 << 20
 
+# how rotary frequencies are derived (PKV_ROPE_*)
+ROPE_METHODS = {"none": 0, "linear": 1, "base": 2, "bands": 3, "ramp": 4}
+PKV_MAX_ROPE_HEAD_DIM = 256
+PKV_MAX_EVICT_CONTEXT = 524288
+
+
+class RopeSpec(ctypes.Structure):
+    """pkv_rope_spec."""
+    _fields_ = [("base", ctypes.c_double), ("factor", ctypes.c_double), ("original_context", ctypes.c_double),
+                ("slow_turns", ctypes.c_double), ("fast_turns", ctypes.c_double), ("method", ctypes.c_int32),
+                ("rotary_dim", ctypes.c_int32)]
+
+
 # every symbol include/pkv.h declares: name -> (restype, argtypes)
 SIGNATURES = {
     "pkv_status_string": (ctypes.c_char_p, [c_int]),
@@ -107,6 +120,15 @@ SIGNATURES = {
     "pkv_merge": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_int,
                           c_void_p]),
     "pkv_get_device_error": (c_int, [c_void_p, ctypes.POINTER(c_int)]),
+    "pkv_rope_frequencies": (c_int, [c_i64p, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(RopeSpec)]),
+    "pkv_rope": (c_int, [c_void_p, c_int64] * 4 + [c_void_p] * 2 + [c_int] * 6 + [c_float, c_void_p]),
+    "pkv_rope_append": (c_int, [c_void_p, c_int64] * 4 + [c_void_p] * 5 + [c_int] * 6 + [c_int64, c_int, c_float,
+                                                                                          c_void_p]),
+    "pkv_weights_workspace_size": (c_size_t, [c_int] * 4),
+    "pkv_decode_attention_weights": (c_int, [c_void_p, c_void_p, c_int64] + [c_void_p] * 5 + [c_int] * 6 +
+                                     [c_int64, c_float, c_void_p, c_size_t, c_void_p]),
+    "pkv_evict": (c_int, [c_void_p] * 9 + [c_int] * 3 + [c_int64] + [c_int] * 3 + [c_int64] + [c_int] * 3 +
+                  [c_void_p]),
 }
 
 

@@ -14,6 +14,9 @@ inline bool aligned16(const void *p) { return aligned(p, 16); }
 int append_take_error(int *code);
 int decode_take_error(int *code);
 int prefix_take_error(int *code);
+int rope_take_error(int *code);
+int weights_take_error(int *code);
+int evict_take_error(int *code);
 
 inline size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
