@@ -743,6 +743,46 @@ PKV_API int pkv_rope_append(void *q_out, int64_t q_out_stride, const void *q, in
                             int block_size, int64_t num_blocks, int interleaved, float magnitude,
                             pkv_stream_t stream);
 
+/* ================================================================ prompts and chunks
+ * Causal attention of many new tokens per request:
+ *     out[t][hq] = softmax over the positions at or before t's (scale q[t][hq] . K) . V
+ * head_dim PKV_HEAD_DIM, 1, 2, 4 or 8 q heads per kv head, scale > 0.  q rows may be strided
+ * (q_stride elements between tokens, a multiple of 8); out is [total_q][num_q_heads][head_dim],
+ * contiguous and 32-byte aligned; lse, if not NULL, receives float32 [total_q][num_q_heads], the natural logarithm of
+ * each row's sum of exponentials.  Request b owns rows query_start[b] .. query_start[b + 1] - 1
+ * (DEVICE int32 [num_seqs + 1]; empty ranges allowed); rows outside every range are left as they were.
+ * A range that is negative, longer than max_query_len or past total_q is skipped and recorded as
+ * PKV_DEV_BAD_CONTEXT.  Weights are rounded to fp16 for the product with V; sums and the
+ * accumulator are float32.  Positions past a context never enter a product; a V row that a row must not
+ * see but another row of its 128-key tile does enters with weight 0, so it must be finite. */
+
+/* Bytes of workspace the two calls need (0: none).  max_context: the longest context the call may meet
+ * (max_seq_len, or max_blocks_per_seq * block_size).  No initial contents.  Calls that
+ * may run at the same time need one each. */
+PKV_API size_t pkv_prefill_workspace_size(int num_seqs, int total_q, int num_q_heads, int num_kv_heads, int head_dim,
+                                          int max_context);
+
+/* Whole prompts, packed: k and v are [total_tokens][num_kv_heads][head_dim] like q (token strides
+ * k_stride, v_stride), sequence b is rows seq_start[b] .. seq_start[b + 1] - 1 of all three.
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */
+PKV_API int pkv_prefill_attention(void *out, float *lse, const void *q, int64_t q_stride, const void *k,
+                                  int64_t k_stride, const void *v, int64_t v_stride, const int32_t *seq_start,
+                                  int num_seqs, int total_tokens, int max_seq_len, int num_q_heads, int num_kv_heads,
+                                  int head_dim, float scale, void *workspace, size_t workspace_bytes,
+                                  pkv_stream_t stream);
+
+/* A chunk of new tokens per request over the paged cache, which holds them already: request b's n_b
+ * rows are its positions context_lens[b] - n_b .. context_lens[b] - 1.  pkv_decode_attention_multi
+ * without its limit on n_b, on the 5th-generation tensor cores: for chunks of some tens of tokens and more.
+ * A context shorter than its chunk or past its table skips the request and is recorded as
+ * PKV_DEV_BAD_CONTEXT.  Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */
+PKV_API int pkv_prefill_attention_paged(void *out, float *lse, const void *q, int64_t q_stride, const void *k_cache,
+                                        const void *v_cache, const int32_t *block_tables,
+                                        const int32_t *context_lens, const int32_t *query_start, int num_seqs,
+                                        int total_q, int max_query_len, int max_blocks_per_seq, int num_q_heads,
+                                        int num_kv_heads, int head_dim, int block_size, int64_t num_blocks,
+                                        float scale, void *workspace, size_t workspace_bytes, pkv_stream_t stream);
+
 /* ================================================================ accumulated attention weights
  * scores is float32 [num_seqs][num_kv_heads][score_capacity], row (b, h) holding for each cached
  * position of request b the sum of the attention weights it received from the q heads of kv head h:
@@ -763,6 +803,19 @@ PKV_API int pkv_decode_attention_weights(void *out, float *scores, int64_t score
                                          int num_q_heads, int num_kv_heads, int head_dim, int block_size,
                                          int64_t num_blocks, float scale, void *workspace, size_t workspace_bytes,
                                          pkv_stream_t stream);
+
+/* The weights of a chunk's rows, as pkv_prefill_attention_paged computed them: for each request's rows
+ * query_start[b] .. query_start[b + 1] - 1 (its last n_b cached positions),
+ *     scores[b][h][s] += sum over rows t at or after s, q heads of kv head h, of exp(scale q . K[s] - lse[t][hq]).
+ * lse is the float32 [total_q][num_q_heads] that call wrote.  Passing only the last rows of a chunk (with their
+ * part of lse) accumulates over those alone.  A request without rows keeps its scores; bad requests as
+ * pkv_prefill_attention_paged's.  No workspace.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+PKV_API int pkv_prefill_attention_weights(float *scores, int64_t score_capacity, const void *q, int64_t q_stride,
+                                          const float *lse, const void *k_cache, const int32_t *block_tables,
+                                          const int32_t *context_lens, const int32_t *query_start, int num_seqs,
+                                          int total_q, int max_query_len, int max_blocks_per_seq, int num_q_heads,
+                                          int num_kv_heads, int head_dim, int block_size, int64_t num_blocks,
+                                          float scale, pkv_stream_t stream);
 
 /* ================================================================ eviction
  * Cut every request longer than `budget` positions back to `budget`, per kv head: the first `sinks`

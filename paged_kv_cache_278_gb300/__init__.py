@@ -32,8 +32,9 @@ __all__ = [
     "decode_step_int8k", "empty_int8k_cache", "decode_attention_multi", "decode_step_multi", "make_multi_workspace",
     "copy_blocks_between", "empty_int8kv_cache", "append_int8kv", "decode_attention_int8kv", "decode_step_int8kv",
     "empty_fp8kv_cache", "append_fp8kv", "decode_attention_fp8kv", "decode_step_fp8kv",
-    "rope_frequencies", "rope_magnitude", "rope", "rope_append", "make_weights_workspace", "decode_attention_weights",
-    "evict",
+    "rope_frequencies", "rope_magnitude", "rope", "rope_append", "make_prefill_workspace", "prefill_attention",
+    "prefill_attention_paged", "make_weights_workspace", "decode_attention_weights",
+    "prefill_attention_weights", "evict",
     "device_error", "slot_mapping", "BlockPool", "PkvError", "library_path",
     "PKV_DEFAULT_PARTITION", "PKV_MAX_PARTITION", "PKV_HEAD_DIM",
     "PKV_DEV_OK", "PKV_DEV_BAD_BLOCK_ID", "PKV_DEV_BAD_CONTEXT", "PKV_DEV_BAD_SLOT", "PKV_DEV_WAIT_TIMEOUT",
@@ -752,6 +753,84 @@ def rope_append(q_out: torch.Tensor, q: torch.Tensor, k_new: torch.Tensor, v_new
     _lib.check(st, "pkv_rope_append")
 
 
+# ---------------------------------------------------------------- prompts and chunks
+
+def make_prefill_workspace(num_seqs: int, total_q: int, num_q_heads: int, num_kv_heads: int, max_context: int,
+                           device) -> torch.Tensor | None:
+    """Workspace for prefill_attention (max_context: its max_seq_len) and prefill_attention_paged (the table's
+    entries * block_size); None when the call needs none.  One per call in flight."""
+    n = int(_L().pkv_prefill_workspace_size(num_seqs, total_q, num_q_heads, num_kv_heads, PKV_HEAD_DIM, max_context))
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def _prompt_outputs(out, lse, q, workspace, dev):
+    _need(out, "out", torch.float16, 3, dev)
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if lse is not None:
+        _need(lse, "lse", torch.float32, 2, dev)
+        if lse.shape != q.shape[:2]:
+            raise ValueError("lse must be [tokens, q heads]")
+    if workspace is None:
+        return None, 0
+    _need(workspace, "workspace", torch.uint8, 1, dev)
+    return workspace.data_ptr(), workspace.numel()
+
+
+def prefill_attention(out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seq_start: torch.Tensor,
+                      max_seq_len: int, scale: float, lse: torch.Tensor | None = None,
+                      workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Causal attention of whole prompts packed one behind another: q [T, Hq, D], k and v [T, Hkv, D] (any token
+    stride), sequence b being rows seq_start[b] .. seq_start[b + 1] - 1 (int32 [B + 1]).  out like q; lse
+    [T, Hq] float32 the rows' log-sum-exps; rows of no sequence stay as they are."""
+    dev = q.device
+    qs = _need_rows(q, "q", dev)
+    ks = _need_rows(k, "k", dev)
+    vs = _need_rows(v, "v", dev, k.shape)
+    if k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2]:
+        raise ValueError("q [T, Hq, D] and k, v [T, Hkv, D] disagree")
+    _need(seq_start, "seq_start", torch.int32, 1, dev)
+    if seq_start.shape[0] < 1:
+        raise ValueError("seq_start must be [B + 1]")
+    ws_ptr, ws_bytes = _prompt_outputs(out, lse, q, workspace, dev)
+    with torch.cuda.device(dev):
+        st = _L().pkv_prefill_attention(out.data_ptr(), None if lse is None else lse.data_ptr(), q.data_ptr(), qs,
+                                        k.data_ptr(), ks, v.data_ptr(), vs, seq_start.data_ptr(), seq_start.shape[0] - 1,
+                                        q.shape[0], int(max_seq_len), q.shape[1], k.shape[1], q.shape[2], float(scale), ws_ptr,
+                                        ws_bytes, _stream(dev, stream))
+    _lib.check(st, "pkv_prefill_attention")
+    return out
+
+
+def prefill_attention_paged(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                            block_tables: torch.Tensor, context_lens: torch.Tensor, query_start: torch.Tensor,
+                            max_query_len: int, scale: float, lse: torch.Tensor | None = None,
+                            workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Causal attention of a chunk of new tokens per request (q rows query_start[b] .. query_start[b + 1] - 1,
+    already appended, so context_lens counts them) over its paged cache: decode_attention_multi for chunks of any
+    length.  q may have any token stride; lse as prefill_attention's."""
+    nb, hkv, bs, d = _cache_shape(k_cache, v_cache)
+    dev = k_cache.device
+    qs = _need_rows(q, "q", dev)
+    if q.shape[2] != d:
+        raise ValueError("q head_dim differs from the cache's")
+    _need(block_tables, "block_tables", torch.int32, 2, dev)
+    _need(context_lens, "context_lens", torch.int32, 1, dev)
+    _need(query_start, "query_start", torch.int32, 1, dev)
+    b = context_lens.shape[0]
+    if block_tables.shape[0] != b or query_start.shape[0] != b + 1:
+        raise ValueError("block_tables [B, ...], context_lens [B] and query_start [B + 1] disagree")
+    ws_ptr, ws_bytes = _prompt_outputs(out, lse, q, workspace, dev)
+    with torch.cuda.device(dev):
+        st = _L().pkv_prefill_attention_paged(out.data_ptr(), None if lse is None else lse.data_ptr(), q.data_ptr(), qs,
+                                              k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
+                                              context_lens.data_ptr(), query_start.data_ptr(), b, q.shape[0],
+                                              int(max_query_len), block_tables.shape[1], q.shape[1], hkv, d, bs, nb,
+                                              float(scale), ws_ptr, ws_bytes, _stream(dev, stream))
+    _lib.check(st, "pkv_prefill_attention_paged")
+    return out
+
+
 # ---------------------------------------------------------------- accumulated attention weights, eviction
 
 def make_weights_workspace(num_seqs: int, num_q_heads: int, max_context: int, device) -> torch.Tensor:
@@ -788,6 +867,37 @@ def decode_attention_weights(out: torch.Tensor, scores: torch.Tensor, q: torch.T
                                                _stream(dev, stream))
     _lib.check(st, "pkv_decode_attention_weights")
     return out
+
+
+def prefill_attention_weights(scores: torch.Tensor, q: torch.Tensor, lse: torch.Tensor, k_cache: torch.Tensor,
+                              block_tables: torch.Tensor, context_lens: torch.Tensor, query_start: torch.Tensor,
+                              max_query_len: int, scale: float, stream=None) -> None:
+    """scores [B, Hkv, capacity] (float32) += the weights that a chunk's rows (q and query_start as
+    prefill_attention_paged's, lse [T, Hq] as it wrote it) give to each cached position, summed over the rows and
+    the q heads of the kv head.  With only the last rows of a chunk, over those alone."""
+    _need(k_cache, "k_cache", torch.float16, 4)
+    nb, hkv, bs, d = k_cache.shape
+    dev = k_cache.device
+    qs = _need_rows(q, "q", dev)
+    if q.shape[2] != d:
+        raise ValueError("q head_dim differs from the cache's")
+    _need(lse, "lse", torch.float32, 2, dev)
+    if lse.shape != q.shape[:2]:
+        raise ValueError("lse must be [tokens, q heads]")
+    _need(block_tables, "block_tables", torch.int32, 2, dev)
+    _need(context_lens, "context_lens", torch.int32, 1, dev)
+    _need(query_start, "query_start", torch.int32, 1, dev)
+    b = context_lens.shape[0]
+    if block_tables.shape[0] != b or query_start.shape[0] != b + 1:
+        raise ValueError("block_tables [B, ...], context_lens [B] and query_start [B + 1] disagree")
+    _need_scores(scores, "scores", b, hkv, block_tables.shape[1] * bs, dev)
+    with torch.cuda.device(dev):
+        st = _L().pkv_prefill_attention_weights(scores.data_ptr(), scores.shape[2], q.data_ptr(), qs, lse.data_ptr(),
+                                                k_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(),
+                                                query_start.data_ptr(), b, q.shape[0], int(max_query_len),
+                                                block_tables.shape[1], q.shape[1], hkv, d, bs, nb, float(scale),
+                                                _stream(dev, stream))
+    _lib.check(st, "pkv_prefill_attention_weights")
 
 
 def evict(k_cache: torch.Tensor, v_cache: torch.Tensor, kept: torch.Tensor, new_scores: torch.Tensor,

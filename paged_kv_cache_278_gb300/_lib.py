@@ -124,9 +124,16 @@ SIGNATURES = {
     "pkv_rope": (c_int, [c_void_p, c_int64] * 4 + [c_void_p] * 2 + [c_int] * 6 + [c_float, c_void_p]),
     "pkv_rope_append": (c_int, [c_void_p, c_int64] * 4 + [c_void_p] * 5 + [c_int] * 6 + [c_int64, c_int, c_float,
                                                                                           c_void_p]),
+    "pkv_prefill_workspace_size": (c_size_t, [c_int] * 6),
+    "pkv_prefill_attention": (c_int, [c_void_p] * 2 + [c_void_p, c_int64] * 3 + [c_void_p] + [c_int] * 6 +
+                              [c_float, c_void_p, c_size_t, c_void_p]),
+    "pkv_prefill_attention_paged": (c_int, [c_void_p] * 3 + [c_int64] + [c_void_p] * 5 + [c_int] * 8 +
+                                    [c_int64, c_float, c_void_p, c_size_t, c_void_p]),
     "pkv_weights_workspace_size": (c_size_t, [c_int] * 4),
     "pkv_decode_attention_weights": (c_int, [c_void_p, c_void_p, c_int64] + [c_void_p] * 5 + [c_int] * 6 +
                                      [c_int64, c_float, c_void_p, c_size_t, c_void_p]),
+    "pkv_prefill_attention_weights": (c_int, [c_void_p, c_int64] * 2 + [c_void_p] * 5 + [c_int] * 8 +
+                                      [c_int64, c_float, c_void_p]),
     "pkv_evict": (c_int, [c_void_p] * 9 + [c_int] * 3 + [c_int64] + [c_int] * 3 + [c_int64] + [c_int] * 3 +
                   [c_void_p]),
 }

@@ -1,0 +1,1241 @@
+// pkv_prompt.cu -- causal attention of whole prompts (packed) and of chunks of new tokens over the
+// paged cache, on the 5th-generation tensor cores.
+//
+//     out[t][hq] = softmax_s(scale q[t][hq] . K[s] : s at or before t's position) V,   lse[t][hq]
+//
+// Rows.  The (token, q head) rows that read one kv head are packed token by token, the group's heads
+// together: with G heads a 128-row tile is 128 / G tokens, so K and V are read once per group and the
+// causal border of a tile is only 128 / G tokens wide.  One CTA takes two neighbouring tiles, A and B.
+//
+// What bounds it: the tensor cores, 4 x 128 flops a (row, key) pair, with one exponential per pair close
+// behind (128 x 128 pairs: 1024 tensor cycles, 512 or more of the special-function units).  The two tiles
+// take turns: while the tensor cores run tile A's P V and next Q K^T, tile B's warps do their softmax.
+//
+//   TMEM (512 columns): S_A | S_B | O_A | O_B, 128 fp32 columns each.  P (fp16, two per column) replaces
+//       S in place and is the A operand of P V straight from TMEM.
+//   warps 0-3, 4-7  softmax of tile A, B: one thread per row, its 128 scores in registers; online max
+//       with lazy rescaling (O is rescaled only when a score exceeds the reference max by more than
+//       2^8, then by the row's own thread), row sums in fp32 of the unrounded weights.  P is rounded to
+//       fp16 once (2^-11 relative, as the output's own rounding), which keeps P V at the fp16 rate.
+//   warp 8  issues every tcgen05.mma (one lane); warp 9 issues every tensor copy: Q (64 KB) once per
+//       item, K and V tiles of 128 keys through a ring of four 32 KB stages.
+//
+// Work items are (pair of tiles, kv head, split of the keys), dealt to one persistent CTA per SM,
+// the longest first and in alternating direction, so that CTAs end together: warp 9 finds the next item
+// while the others work.  Calls with too few items to fill the SMs split each item's keys; partial
+// results are joined by a second launch.
+//
+// Keys past the context are never multiplied: the last key tile's MMAs stop at its 16-key group and
+// that group's unused V rows are zeroed in shared memory, whatever the cache holds there.
+#include <cuda.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <atomic>
+
+#include "pkv.h"
+#include "pkv_device.cuh"
+#include "pkv_internal.h"
+
+namespace {
+
+__device__ int g_prompt_error;
+
+constexpr int kDim = PKV_HEAD_DIM;
+constexpr int kTileRows = 128;             // query rows per tile (M) and keys per K/V tile (N)
+constexpr int kSlab = kTileRows * 128;     // 128 rows x 64 fp16 dims, 128-byte swizzle
+constexpr int kOperand = 2 * kSlab;        // a whole 128 x 128 fp16 operand tile
+constexpr int kRing = 4;                   // K/V stages
+constexpr int kSoftmaxWarps = 8;
+constexpr int kPromptThreads = 32 * (kSoftmaxWarps + 2);
+constexpr int kMmaWarp = kSoftmaxWarps, kLoadWarp = kSoftmaxWarps + 1;
+constexpr float kLazy = 8.0f;              // log2 units
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr int kMaxSplits = 64;
+
+struct PromptParams {
+    __half *out;
+    float *lse;                   // natural log, or null
+    const int32_t *query_start;   // [num_seqs + 1]
+    const int32_t *block_tables;  // null: K and V are packed like q
+    const int32_t *context_lens;
+    float *o_part, *m_part, *l_part;  // splits > 1: [total_q][Hq][splits](x 128), m in log2 units
+    int num_seqs, total_q, max_query_len, max_blocks, num_q_heads, num_kv_heads, block_size;
+    int64_t num_blocks;
+    int group_log2, box_rows, splits;
+    float q_scale;                // scale * log2(e)
+    CUtensorMap tmap_q, tmap_k, tmap_v;
+};
+
+// One unit of work; `kv_count` per tile is 0 for a tile without rows or without keys in this split.
+struct Item {
+    int seq;        // -1: no more items
+    int kvh, split;
+    int row0;       // q row (token) of the pair's first token
+    int live[2];    // live tokens of tiles A and B
+    int pos0;       // logical position of the first token
+    int keys;       // the request's context
+    int kv_first, kv_count[2];
+};
+
+struct PromptSmem {
+    static constexpr int q = 0;                              // two operand tiles
+    static constexpr int ring = 2 * kOperand;
+    static constexpr int bars = ring + kRing * kOperand;
+    static constexpr int n_bars = 2 * kRing + 2 + 4 + 6 + 1;
+    static constexpr int tmem_slot = bars + n_bars * 8;
+    static constexpr int items = (tmem_slot + 4 + 15) / 16 * 16;
+    static constexpr int total = items + 2 * static_cast<int>(sizeof(Item));
+};
+
+// Barriers by index.
+constexpr int kBarKvFull = 0, kBarKvEmpty = kRing, kBarQFull = 2 * kRing, kBarQEmpty = kBarQFull + 1,
+              kBarItemFull = kBarQEmpty + 1, kBarItemEmpty = kBarItemFull + 2, kBarS = kBarItemEmpty + 2, kBarP = kBarS + 2,
+              kBarO = kBarP + 2, kBarDrain = kBarO + 2;
+
+// ---- TMEM moves (one row per lane, consecutive 32-bit columns)
+__device__ __forceinline__ void tmem_ld128(uint32_t taddr, uint32_t (&r)[128]) {
+#define PKV_R8(i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x128.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+        "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+        "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63, "
+        "%64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, "
+        "%80, %81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95, "
+        "%96, %97, %98, %99, %100, %101, %102, %103, %104, %105, %106, %107, %108, %109, %110, %111, "
+        "%112, %113, %114, %115, %116, %117, %118, %119, %120, %121, %122, %123, %124, %125, %126, %127}, [%128];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : PKV_R8(0), PKV_R8(8), PKV_R8(16), PKV_R8(24), PKV_R8(32), PKV_R8(40), PKV_R8(48), PKV_R8(56), PKV_R8(64),
+          PKV_R8(72), PKV_R8(80), PKV_R8(88), PKV_R8(96), PKV_R8(104), PKV_R8(112), PKV_R8(120)
+        : "r"(taddr)
+        : "memory");
+#undef PKV_R8
+}
+
+// 32 columns out of registers; completed by tmem_wait_st.
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+#define PKV_R8(i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]), "r"(r[i + 6]), "r"(r[i + 7])
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        PKV_R8(0), PKV_R8(8), PKV_R8(16), PKV_R8(24)
+        : "memory");
+#undef PKV_R8
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// D[tmem] (+)= A[tmem] * B[smem]: A is 128 rows x 16 fp16, two per 32-bit column.
+__device__ __forceinline__ void umma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1 : 0)
+        : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// A 32-byte store: one whole sector from one thread.
+__device__ __forceinline__ void store_sector(void *p, const uint32_t (&r)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
+                 "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
+// The request's new tokens and context, checked; a bad one counts as no tokens.
+struct Request {
+    int start, tokens, keys;
+};
+__device__ __forceinline__ Request request_of(const PromptParams &P, int b, bool report) {
+    Request r;
+    r.start = __ldg(P.query_start + b);
+    r.tokens = __ldg(P.query_start + b + 1) - r.start;
+    const bool paged = P.block_tables != nullptr;
+    r.keys = paged ? __ldg(P.context_lens + b) : r.tokens;
+    bool bad = r.tokens < 0 || r.tokens > P.max_query_len || r.start < 0 || r.start > P.total_q - r.tokens;
+    if (paged) bad = bad || r.keys < r.tokens || r.keys > P.max_blocks * P.block_size;
+    if (bad) {
+        if (report) pkv::record_error(&g_prompt_error, PKV_DEV_BAD_CONTEXT);
+        r.tokens = 0;
+    }
+    return r;
+}
+
+// Pairs of tiles at or past level `level` of every request (all lanes get the sum).
+__device__ __forceinline__ int pairs_from(const PromptParams &P, int level, int pair_tokens, int lane, bool report) {
+    int c = 0;
+    for (int b = lane; b < P.num_seqs; b += 32) {
+        const int pairs = (request_of(P, b, report).tokens + pair_tokens - 1) / pair_tokens;
+        c += max(0, pairs - level);
+    }
+    return __reduce_add_sync(pkv::kFullMask, c);
+}
+
+// Item `index` of the call: pairs from the last level to the first (long rows first), for each the kv
+// heads and the splits.
+__device__ Item find_item(const PromptParams &P, int64_t index, int lane) {
+    const int tile_tokens = kTileRows >> P.group_log2, pair_tokens = 2 * tile_tokens;
+    Item it{};
+    it.split = static_cast<int>(index % P.splits);
+    it.kvh = static_cast<int>(index / P.splits % P.num_kv_heads);
+    const int rank = static_cast<int>(index / P.splits / P.num_kv_heads);
+    int lo = 0, hi = (P.max_query_len + pair_tokens - 1) / pair_tokens;  // pairs_from(lo) > rank >= pairs_from(hi)
+    int past = 0;                                                        // pairs_from(hi)
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        const int c = pairs_from(P, mid, pair_tokens, lane, false);
+        if (c > rank) {
+            lo = mid;
+        } else {
+            hi = mid;
+            past = c;
+        }
+    }
+    int nth = rank - past;  // which of the requests that have a pair at level lo
+    int seq = -1;
+    for (int b0 = 0; b0 < P.num_seqs; b0 += 32) {
+        const int b = b0 + lane;
+        const bool has = b < P.num_seqs && request_of(P, b, false).tokens > lo * pair_tokens;
+        const uint32_t mask = __ballot_sync(pkv::kFullMask, has);
+        const int c = __popc(mask);
+        if (nth < c) {
+            uint32_t m = mask;
+            for (int i = 0; i < nth; ++i) m &= m - 1;
+            seq = b0 + __ffs(m) - 1;
+            break;
+        }
+        nth -= c;
+    }
+    it.seq = seq;
+    const Request r = request_of(P, seq, false);
+    const int t0 = lo * pair_tokens;
+    it.row0 = r.start + t0;
+    it.pos0 = r.keys - r.tokens + t0;
+    it.keys = r.keys;
+    int count[2] = {0, 0};
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        it.live[t] = min(max(r.tokens - t0 - t * tile_tokens, 0), tile_tokens);
+        if (it.live[t] > 0) count[t] = (it.pos0 + t * tile_tokens + it.live[t] - 1) / kTileRows + 1;
+    }
+    const int all = max(count[0], count[1]);
+    const int per = (all + P.splits - 1) / P.splits;
+    it.kv_first = it.split * per;
+    const int end = min(all, it.kv_first + per);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) it.kv_count[t] = max(min(count[t], end) - it.kv_first, 0);
+    return it;
+}
+
+template <bool PAGED>
+__global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_constant__ PromptParams P) {
+    extern __shared__ __align__(1024) unsigned char smem[];
+    const uint32_t base = pkv::smem_addr(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t bars = base + PromptSmem::bars;
+    auto bar = [bars](int i) { return bars + 8 * i; };
+    volatile Item *slots = reinterpret_cast<volatile Item *>(smem + PromptSmem::items);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + PromptSmem::tmem_slot);
+
+    const bool aligned = (base & 1023) == 0;  // the swizzled operand tiles need it (the same in every CTA)
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < PromptSmem::n_bars; ++i) {
+            uint32_t count = 1;
+            if (i == kBarItemEmpty || i == kBarItemEmpty + 1) count = kSoftmaxWarps + 1;
+            if (i == kBarP || i == kBarP + 1) count = 4;  // one arrival per softmax warp of the tile
+            pkv::mbar_init(bar(i), count);
+        }
+        pkv::fence_mbar_init();
+    }
+    if (warp == kMmaWarp && aligned) pkv::tmem_alloc(pkv::smem_addr(tmem_slot), 512);
+    pkv::tmem_fence_before_sync();
+    __syncthreads();
+    pkv::tmem_fence_after_sync();
+    pkv::pdl_wait_primary();
+    pkv::pdl_launch_dependents();
+    if (!aligned) {
+        if (threadIdx.x == 0) pkv::record_error(&g_prompt_error, PKV_DEV_SMEM_MISALIGNED);
+        return;
+    }
+    const uint32_t tmem = *tmem_slot;
+    const int glog = P.group_log2, tile_tokens = kTileRows >> glog;
+    // A wait that runs out is recorded; its warp leaves its loop, and so do the others in their turn.
+    auto wait = [&](int b, uint32_t phase) {
+        if (__all_sync(pkv::kFullMask, pkv::mbar_wait_bounded(bar(b), phase & 1))) return true;
+        if (lane == 0) pkv::record_error(&g_prompt_error, PKV_DEV_WAIT_TIMEOUT);
+        return false;
+    };
+
+    if (warp == kLoadWarp) {
+        // ---------------------------------------------------------------- items and tensor copies
+        const int pairs = pairs_from(P, 0, 2 * tile_tokens, lane, blockIdx.x == 0);
+        const int64_t n_items = static_cast<int64_t>(pairs) * P.num_kv_heads * P.splits;
+        const int boxes_per_tile = PAGED ? kTileRows / P.box_rows : 1;
+        uint32_t stage = 0, loaded = 0;  // K/V stages filled, items with keys (one Q each)
+        bool ok = true;
+        for (uint32_t k = 0; ok; ++k) {
+            // alternating direction: a CTA's items are not always the longest of their round
+            const int64_t index = static_cast<int64_t>(k) * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+            Item it{};
+            it.seq = -1;
+            if (index < n_items) it = find_item(P, index, lane);
+            const int slot = k & 1;
+            if (!(ok = wait(kBarItemEmpty + slot, (k >> 1) + 1))) break;
+            if (lane == 0) {
+                volatile int *d = reinterpret_cast<volatile int *>(slots + slot);
+                const int *s = reinterpret_cast<const int *>(&it);
+#pragma unroll
+                for (int i = 0; i < static_cast<int>(sizeof(Item) / 4); ++i) d[i] = s[i];
+                mbar_arrive(bar(kBarItemFull + slot));
+            }
+            __syncwarp();
+            if (it.seq < 0) break;
+            const int n_kv = max(it.kv_count[0], it.kv_count[1]);
+            if (n_kv == 0) continue;
+            if (!(ok = wait(kBarQEmpty, loaded + 1))) break;
+            ++loaded;
+            if (lane == 0) {
+                const int tiles = it.live[1] > 0 ? 2 : 1;
+                pkv::mbar_arrive_expect_tx(bar(kBarQFull), tiles * kOperand);
+                for (int t = 0; t < tiles; ++t)
+                    for (int half = 0; half < 2; ++half)
+                        pkv::tma_load_3d(base + PromptSmem::q + t * kOperand + half * kSlab, &P.tmap_q, 64 * half, it.kvh << glog,
+                                         it.row0 + t * tile_tokens, bar(kBarQFull));
+            }
+            __syncwarp();
+            // The cache row at which this lane's box of a key tile starts (lane = 2 x box + half).
+            auto box_row = [&](int tile) -> int {
+                const int key = tile * kTileRows + (lane >> 1) * P.box_rows;
+                if (lane >= 2 * boxes_per_tile || key >= it.keys) return 0;
+                int32_t id = __ldg(P.block_tables + static_cast<int64_t>(it.seq) * P.max_blocks + key / P.block_size);
+                if (id < 0 || id >= P.num_blocks) {
+                    pkv::record_error(&g_prompt_error, PKV_DEV_BAD_BLOCK_ID);
+                    id = 0;
+                }
+                return static_cast<int>((static_cast<int64_t>(id) * P.num_kv_heads + it.kvh) * P.block_size + key % P.block_size);
+            };
+            int row = PAGED ? box_row(it.kv_first) : 0;
+            for (int j = 0; j < n_kv && ok; ++j) {
+                const int tile = it.kv_first + j;
+                const int next = PAGED && j + 1 < n_kv ? box_row(tile + 1) : 0;
+                const int valid = min(kTileRows, it.keys - tile * kTileRows);
+                for (int kv = 0; kv < 2; ++kv) {
+                    const int st = stage % kRing;
+                    if (!(ok = wait(kBarKvEmpty + st, stage / kRing + 1))) break;
+                    ++stage;
+                    const uint32_t dst = base + PromptSmem::ring + st * kOperand, full = bar(kBarKvFull + st);
+                    const void *map = kv ? static_cast<const void *>(&P.tmap_v) : static_cast<const void *>(&P.tmap_k);
+                    if (PAGED) {
+                        const int boxes = (valid + P.box_rows - 1) / P.box_rows;
+                        if (lane == 0) pkv::mbar_arrive_expect_tx(full, boxes * P.box_rows * 256);
+                        __syncwarp();
+                        if (lane < 2 * boxes)
+                            pkv::tma_load_2d(dst + (lane & 1) * kSlab + (lane >> 1) * P.box_rows * 128, map, 64 * (lane & 1), row, full);
+                    } else if (lane == 0) {  // rows past the sequence are the next one's, past the tensor zeros
+                        pkv::mbar_arrive_expect_tx(full, kOperand);
+                        for (int half = 0; half < 2; ++half)
+                            pkv::tma_load_2d(dst + half * kSlab, map, it.kvh * kDim + 64 * half, it.row0 - it.pos0 + tile * kTileRows,
+                                             full);
+                    }
+                    __syncwarp();
+                }
+                row = next;
+            }
+        }
+        if (!ok) {  // copies still in flight land before the CTA's memory goes (bounded)
+            if (loaded) pkv::mbar_wait_bounded(bar(kBarQFull), (loaded - 1) & 1);
+            for (uint32_t s = stage > kRing ? stage - kRing : 0; s < stage; ++s)
+                pkv::mbar_wait_bounded(bar(kBarKvFull + s % kRing), (s / kRing) & 1);
+        }
+    } else if (warp == kMmaWarp) {
+        // ---------------------------------------------------------------- tensor-core issue
+        constexpr uint32_t kIdescPV = pkv::umma_idesc_f16_f32(kTileRows, kDim) | (1u << 16);  // V: MN-major
+        uint32_t stage = 0, loaded = 0, p_count[2] = {0, 0};
+        bool ok = true;
+        for (uint32_t k = 0; ok; ++k) {
+            const int slot = k & 1;
+            if (!(ok = wait(kBarItemFull + slot, k >> 1))) break;
+            const int seq = slots[slot].seq, keys = slots[slot].keys, first = slots[slot].kv_first;
+            const int n[2] = {slots[slot].kv_count[0], slots[slot].kv_count[1]};
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kBarItemEmpty + slot));
+            if (seq < 0) break;
+            const int n_kv = max(n[0], n[1]);
+            if (n_kv == 0) continue;  // an empty split
+            // 16-key groups of key tile j that hold cached keys
+            auto groups_of = [&](int j) { return (min(kTileRows, keys - (first + j) * kTileRows) + 15) / 16; };
+            auto qk = [&](int t, uint32_t st, int groups) {
+                if (lane == 0) {
+                    const uint32_t q = base + PromptSmem::q + t * kOperand, kk = base + PromptSmem::ring + (st % kRing) * kOperand;
+                    const uint32_t idesc = pkv::umma_idesc_f16_f32(kTileRows, groups * 16);
+#pragma unroll
+                    for (int ks = 0; ks < kDim / 16; ++ks) {
+                        const uint32_t off = (ks >> 2) * kSlab + (ks & 3) * 32;
+                        pkv::umma_f16(tmem + t * kTileRows, pkv::umma_desc_k_sw128(q + off), pkv::umma_desc_k_sw128(kk + off), idesc,
+                                      ks > 0);
+                    }
+                    pkv::umma_commit(bar(kBarS + t));
+                }
+                __syncwarp();
+            };
+            auto commit = [&](int b) {
+                if (lane == 0) pkv::umma_commit(bar(b));
+                __syncwarp();
+            };
+            if (!(ok = wait(kBarQFull, loaded))) break;
+            ++loaded;
+            if (!(ok = wait(kBarKvFull + stage % kRing, stage / kRing))) break;
+            pkv::tmem_fence_after_sync();
+            for (int t = 0; t < 2; ++t)
+                if (n[t] > 0) qk(t, stage, groups_of(0));
+            commit(kBarKvEmpty + stage % kRing);
+            if (n_kv == 1) commit(kBarQEmpty);
+            ++stage;
+            for (int j = 0; j < n_kv && ok; ++j) {
+                const uint32_t v_stage = stage, k_stage = stage + 1;
+                const bool more = j + 1 < n_kv;
+                if (!(ok = wait(kBarKvFull + v_stage % kRing, v_stage / kRing))) break;
+                const uint32_t v = base + PromptSmem::ring + (v_stage % kRing) * kOperand;
+                const int groups = groups_of(j);
+                const int valid = min(kTileRows, keys - (first + j) * kTileRows);
+                if (valid < groups * 16) {  // V rows past the context: their weights are 0, their values may be anything
+                    for (int x = lane; x < (groups * 16 - valid) * 16; x += 32)
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v + ((x >> 3) & 1) * kSlab +
+                                                                                 (valid + (x >> 4)) * 128 + (x & 7) * 16),
+                                     "r"(0)
+                                     : "memory");
+                    pkv::fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                if (more && !(ok = wait(kBarKvFull + k_stage % kRing, k_stage / kRing))) break;
+                for (int t = 0; t < 2 && ok; ++t) {
+                    if (j >= n[t]) continue;
+                    if (!(ok = wait(kBarP + t, p_count[t]))) break;
+                    ++p_count[t];
+                    pkv::tmem_fence_after_sync();
+                    if (lane == 0) {
+                        for (int g = 0; g < groups; ++g)
+                            umma_f16_ta(tmem + 2 * kTileRows + t * kDim, tmem + t * kTileRows + g * 8,
+                                        pkv::umma_desc_mn_sw128(v + g * 2048, kSlab, 1024), kIdescPV, j > 0 || g > 0);
+                        if (j + 1 == n[t]) pkv::umma_commit(bar(kBarO + t));
+                    }
+                    __syncwarp();
+                    if (j + 1 < n[t]) qk(t, k_stage, groups_of(j + 1));
+                }
+                if (!ok) break;
+                commit(kBarKvEmpty + v_stage % kRing);
+                if (more) commit(kBarKvEmpty + k_stage % kRing);
+                if (j + 2 == n_kv) commit(kBarQEmpty);  // the item's last Q K^T has been issued
+                stage += more ? 2 : 1;
+            }
+        }
+        if (!ok) {  // MMAs in flight end before tensor memory is freed (bounded)
+            if (lane == 0) pkv::umma_commit(bar(kBarDrain));
+            __syncwarp();
+            pkv::mbar_wait_bounded(bar(kBarDrain), 0);
+        }
+    } else {
+        // ---------------------------------------------------------------- softmax and output of one tile
+        const int t = warp >> 2;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;  // this warp's TMEM lanes
+        const uint32_t t_s = tmem + lanes + t * kTileRows, t_o = tmem + lanes + 2 * kTileRows + t * kDim;
+        const int r = (warp & 3) * 32 + lane, tok = r >> glog;
+        const float sc = P.q_scale;
+        uint32_t s_count = 0, o_count = 0;
+        bool ok = true;
+        for (uint32_t k = 0; ok; ++k) {
+            const int slot = k & 1;
+            if (!(ok = wait(kBarItemFull + slot, k >> 1))) break;
+            const int seq = slots[slot].seq, kvh = slots[slot].kvh, split = slots[slot].split, first = slots[slot].kv_first;
+            const int n = slots[slot].kv_count[t], live = slots[slot].live[t];
+            const int tile_pos = slots[slot].pos0 + t * tile_tokens;  // position of the tile's first token
+            const int64_t q_row = slots[slot].row0 + t * tile_tokens + tok;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kBarItemEmpty + slot));
+            if (seq < 0) break;
+            const int pos = tile_pos + min(tok, live - 1);  // rows past the last token: computed like it, never stored
+            float m_ref = -INFINITY, l = 0.f;
+            for (int j = 0; j < n; ++j) {
+                if (!(ok = wait(kBarS + t, s_count))) break;
+                ++s_count;
+                pkv::tmem_fence_after_sync();
+                uint32_t s[128];
+                tmem_ld128(t_s, s);
+                const int key0 = (first + j) * kTileRows;
+                if (key0 + kTileRows - 1 > tile_pos) {  // the tile crosses the causal border (or the context's end)
+                    const int lim = pos - key0;
+#pragma unroll
+                    for (int c = 0; c < 128; ++c) s[c] = c <= lim ? s[c] : 0xff800000u;
+                }
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int c = 0; c < 128; c += 2)
+                    mx[(c >> 1) & 3] = fmaxf(fmaxf(mx[(c >> 1) & 3], __uint_as_float(s[c])), __uint_as_float(s[c + 1]));
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+                if (__any_sync(pkv::kFullMask, top > m_ref + kLazy)) {
+                    const float m_new = top > m_ref + kLazy ? top : m_ref;
+                    const float a = m_ref == -INFINITY ? 0.f : exp2f(m_ref - m_new);
+                    const float f = m_new == m_ref ? 1.f : a;
+                    l *= f;
+                    m_ref = m_new;
+                    if (j > 0) {  // P V of the earlier tiles has completed: S of this one was issued behind it
+#pragma unroll
+                        for (int c = 0; c < kDim; c += 32) {
+                            uint32_t o[32];
+                            pkv::tmem_ld32(t_o + c, o);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                            tmem_st32(t_o + c, o);
+                        }
+                    }
+                }
+                const float ms = m_ref == -INFINITY ? 0.f : m_ref;  // no visible key yet: weights exp2(-inf) = 0
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t p[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const float p0 = pkv::exp2_approx(fmaf(__uint_as_float(s[64 * h + 2 * i]), sc, -ms));
+                        const float p1 = pkv::exp2_approx(fmaf(__uint_as_float(s[64 * h + 2 * i + 1]), sc, -ms));
+                        sum[i & 1] += p0;
+                        sum[2 + (i & 1)] += p1;
+                        const __half2 pk = __floats2half2_rn(p0, p1);
+                        p[i] = *reinterpret_cast<const uint32_t *>(&pk);
+                    }
+                    tmem_st32(t_s + 32 * h, p);
+                }
+                tmem_wait_st();
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                pkv::tmem_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(kBarP + t));
+            }
+            if (!ok) break;
+            if (n > 0) {
+                if (!(ok = wait(kBarO + t, o_count))) break;
+                ++o_count;
+                pkv::tmem_fence_after_sync();
+            }
+            const bool store = tok < live;
+            const int64_t row = q_row * P.num_q_heads + (kvh << glog) + (r & ((1 << glog) - 1));
+            const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+            if (n > 0) {
+#pragma unroll
+                for (int c = 0; c < kDim; c += 32) {
+                    uint32_t o[32];
+                    __syncwarp();
+                    pkv::tmem_ld32(t_o + c, o);
+                    if (!store) continue;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
+                    if (P.splits == 1) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t w[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const __half2 v = __floats2half2_rn(__uint_as_float(o[16 * h + 2 * i]), __uint_as_float(o[16 * h + 2 * i + 1]));
+                                w[i] = *reinterpret_cast<const uint32_t *>(&v);
+                            }
+                            store_sector(P.out + row * kDim + c + 16 * h, w);
+                        }
+                    } else {
+#pragma unroll
+                        for (int h = 0; h < 4; ++h) {
+                            uint32_t w[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) w[i] = o[8 * h + i];
+                            store_sector(P.o_part + (row * P.splits + split) * kDim + c + 8 * h, w);
+                        }
+                    }
+                }
+                pkv::tmem_fence_before_sync();  // O read before the next item's first P V (ordered by its weights' arrival)
+            }
+            if (store) {
+                if (P.splits > 1) {
+                    P.m_part[row * P.splits + split] = l == 0.f ? -INFINITY : m_ref;
+                    P.l_part[row * P.splits + split] = l;
+                } else if (P.lse != nullptr) {
+                    P.lse[row] = (m_ref + log2f(l)) * kLn2;
+                }
+            }
+        }
+    }
+    pkv::tmem_fence_before_sync();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        pkv::tmem_fence_after_sync();
+        pkv::tmem_dealloc(tmem, 512);
+    }
+}
+
+// Joins the splits of each (token, head) row: one warp per row, four dims a lane.
+constexpr int kJoinThreads = 256;
+__global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const __grid_constant__ PromptParams P) {
+    pkv::pdl_wait_primary();
+    pkv::pdl_launch_dependents();
+    const Request r = request_of(P, blockIdx.y, false);
+    const int lane = threadIdx.x & 31;
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * (kJoinThreads / 32) + (threadIdx.x >> 5);
+    if (i >= static_cast<int64_t>(r.tokens) * P.num_q_heads) return;
+    const int64_t row = static_cast<int64_t>(r.start) * P.num_q_heads + i;
+    const float *m = P.m_part + row * P.splits, *l = P.l_part + row * P.splits;
+    float top = -INFINITY;
+    for (int s = lane; s < P.splits; s += 32) top = fmaxf(top, __ldcg(m + s));
+#pragma unroll
+    for (int sh = 16; sh >= 1; sh >>= 1) top = fmaxf(top, __shfl_xor_sync(pkv::kFullMask, top, sh));
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float total = 0.f;
+    for (int s0 = 0; s0 < P.splits; s0 += 4) {
+        float4 o[4];
+        float w[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int s = s0 + u;
+            const float ls = s < P.splits ? __ldcg(l + s) : 0.f;
+            w[u] = ls == 0.f ? 0.f : ls * exp2f(__ldcg(m + s) - top);  // a split without visible keys wrote no output
+            o[u] = ls == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                             : __ldcg(reinterpret_cast<const float4 *>(P.o_part + (row * P.splits + s) * kDim) + lane);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            acc.x = fmaf(w[u], o[u].x, acc.x);
+            acc.y = fmaf(w[u], o[u].y, acc.y);
+            acc.z = fmaf(w[u], o[u].z, acc.z);
+            acc.w = fmaf(w[u], o[u].w, acc.w);
+            total += w[u];
+        }
+    }
+    const float inv = 1.f / total;
+    const __half2 lo = __floats2half2_rn(acc.x * inv, acc.y * inv), hi = __floats2half2_rn(acc.z * inv, acc.w * inv);
+    *reinterpret_cast<uint2 *>(P.out + row * kDim + 4 * lane) =
+        make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+    if (lane == 0 && P.lse != nullptr) P.lse[row] = (top + log2f(total)) * kLn2;
+}
+
+// ---------------------------------------------------------------- weights of a chunk's rows
+// scores[b][h][s] += sum over the chunk's rows (token t at or after s, q head of kv head h) of
+// exp(scale q . K[s] - lse).  The sums run over rows, so the product is taken transposed: S^T = K Q^T with the
+// 128 keys of a tile as M (one TMEM lane, one thread each) and 128 packed rows as N; a thread adds up its
+// key's weights over all columns in its own registers and one thread adds them to scores: no exchange,
+// no atomics, a fixed order.  Bound by the exponentials, one per (row, key) pair (2 x 128 tensor flops),
+// until a chunk is so small that reading K bounds it.
+//   warps 0-3, 4-7  the even and odd row tiles of an item, each with two S^T buffers of 128 TMEM columns
+//   warp 8          issues the MMAs; warp 9 finds items (a 128-key tile of one request and kv head) and
+//                   issues the tensor copies: K tiles (two stages), Q tiles (ring of four)
+struct ChunkWeightParams {
+    PromptParams p;
+    const float *lse;
+    float *scores;
+    int64_t capacity;
+};
+
+constexpr int kKeyStages = 2, kRowRing = 4;
+
+struct ChunkWeightSmem {
+    static constexpr int keys = 0;
+    static constexpr int rows = kKeyStages * kOperand;
+    static constexpr int lse = rows + kRowRing * kOperand;        // [8 warps][128] floats, log2 units
+    static constexpr int sums = lse + kSoftmaxWarps * kTileRows * 4;  // [2 items][128] floats
+    static constexpr int bars = sums + 2 * kTileRows * 4;
+    static constexpr int n_bars = 2 * kKeyStages + 2 * kRowRing + 8 + 4 + 2 + 1;
+    static constexpr int tmem_slot = bars + n_bars * 8;
+    static constexpr int items = (tmem_slot + 4 + 15) / 16 * 16;
+    static constexpr int total = items + 2 * 32;
+};
+constexpr int kWKeyFull = 0, kWKeyEmpty = kKeyStages, kWRowFull = 2 * kKeyStages, kWRowEmpty = kWRowFull + kRowRing,
+              kWS = kWRowEmpty + kRowRing, kWSFree = kWS + 4, kWItemFull = kWSFree + 4, kWItemEmpty = kWItemFull + 2,
+              kWSum = kWItemEmpty + 2, kWDrain = kWSum + 2;
+
+// A 128-key tile of one request and kv head, and the row tiles [first, count) that see some of it.
+struct KeyItem {
+    int seq, kvh, tile, start, tokens, keys, first, count;
+};
+
+__device__ KeyItem find_key_item(const PromptParams &P, int64_t index, int lane) {
+    KeyItem it{};
+    it.seq = -1;
+    it.kvh = static_cast<int>(index % P.num_kv_heads);
+    int64_t rank = index / P.num_kv_heads;
+    for (int b0 = 0; b0 < P.num_seqs; b0 += 32) {
+        const int b = b0 + lane;
+        int tiles = 0;
+        if (b < P.num_seqs) {
+            const Request r = request_of(P, b, false);
+            tiles = r.tokens > 0 ? (r.keys + kTileRows - 1) / kTileRows : 0;
+        }
+        int upto = tiles;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int y = __shfl_up_sync(pkv::kFullMask, upto, d);
+            if (lane >= d) upto += y;
+        }
+        const int all = __shfl_sync(pkv::kFullMask, upto, 31);
+        if (rank >= all) {
+            rank -= all;
+            continue;
+        }
+        const int who = __ffs(__ballot_sync(pkv::kFullMask, rank < upto)) - 1;
+        it.seq = b0 + who;
+        it.tile = static_cast<int>(rank) - __shfl_sync(pkv::kFullMask, upto - tiles, who);
+        break;
+    }
+    if (it.seq < 0) return it;
+    const Request r = request_of(P, it.seq, false);
+    it.start = r.start;
+    it.tokens = r.tokens;
+    it.keys = r.keys;
+    const int skip = max(it.tile * kTileRows - (r.keys - r.tokens), 0);  // tokens before the tile's first key
+    it.first = (skip << P.group_log2) / kTileRows;
+    it.count = ((r.tokens << P.group_log2) + kTileRows - 1) / kTileRows;
+    return it;
+}
+
+__global__ void __launch_bounds__(kPromptThreads, 1) chunk_weights_kernel(const __grid_constant__ ChunkWeightParams W) {
+    using L = ChunkWeightSmem;
+    const PromptParams &P = W.p;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    const uint32_t base = pkv::smem_addr(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t bars = base + L::bars;
+    auto bar = [bars](int i) { return bars + 8 * i; };
+    volatile KeyItem *slots = reinterpret_cast<volatile KeyItem *>(smem + L::items);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::tmem_slot);
+    const bool aligned = (base & 1023) == 0;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < L::n_bars; ++i) {
+            uint32_t count = 1;
+            if ((i >= kWSFree && i < kWSFree + 4) || i == kWSum || i == kWSum + 1) count = 4;
+            if (i == kWItemEmpty || i == kWItemEmpty + 1) count = kSoftmaxWarps + 1;
+            pkv::mbar_init(bar(i), count);
+        }
+        pkv::fence_mbar_init();
+    }
+    if (warp == kMmaWarp && aligned) pkv::tmem_alloc(pkv::smem_addr(tmem_slot), 512);
+    pkv::tmem_fence_before_sync();
+    __syncthreads();
+    pkv::tmem_fence_after_sync();
+    pkv::pdl_wait_primary();
+    pkv::pdl_launch_dependents();
+    if (!aligned) {
+        if (threadIdx.x == 0) pkv::record_error(&g_prompt_error, PKV_DEV_SMEM_MISALIGNED);
+        return;
+    }
+    const uint32_t tmem = *tmem_slot;
+    const int glog = P.group_log2, tile_tokens = kTileRows >> glog;
+    auto wait = [&](int b, uint32_t phase) {
+        if (__all_sync(pkv::kFullMask, pkv::mbar_wait_bounded(bar(b), phase & 1))) return true;
+        if (lane == 0) pkv::record_error(&g_prompt_error, PKV_DEV_WAIT_TIMEOUT);
+        return false;
+    };
+
+    if (warp == kLoadWarp) {
+        int tiles = 0;
+        for (int b = lane; b < P.num_seqs; b += 32) {
+            const Request r = request_of(P, b, blockIdx.x == 0);
+            tiles += r.tokens > 0 ? (r.keys + kTileRows - 1) / kTileRows : 0;
+        }
+        const int64_t n_items = static_cast<int64_t>(__reduce_add_sync(pkv::kFullMask, tiles)) * P.num_kv_heads;
+        const int boxes_per_tile = kTileRows / P.box_rows;
+        uint32_t rows = 0, k = 0;
+        bool ok = true;
+        for (; ok; ++k) {
+            const int64_t index = static_cast<int64_t>(k) * gridDim.x + blockIdx.x;
+            KeyItem it{};
+            it.seq = -1;
+            if (index < n_items) it = find_key_item(P, index, lane);
+            const int slot = k & 1;
+            if (!(ok = wait(kWItemEmpty + slot, (k >> 1) + 1))) break;
+            if (lane == 0) {
+                volatile int *d = reinterpret_cast<volatile int *>(slots + slot);
+                const int *s = reinterpret_cast<const int *>(&it);
+#pragma unroll
+                for (int i = 0; i < static_cast<int>(sizeof(KeyItem) / 4); ++i) d[i] = s[i];
+                mbar_arrive(bar(kWItemFull + slot));
+            }
+            __syncwarp();
+            if (it.seq < 0) break;
+            const int ks = k % kKeyStages;
+            if (!(ok = wait(kWKeyEmpty + ks, k / kKeyStages + 1))) break;
+            const int valid = min(kTileRows, it.keys - it.tile * kTileRows);
+            const int boxes = (valid + P.box_rows - 1) / P.box_rows;
+            if (lane == 0) pkv::mbar_arrive_expect_tx(bar(kWKeyFull + ks), boxes * P.box_rows * 256);
+            __syncwarp();
+            if (lane < 2 * boxes && lane < 2 * boxes_per_tile) {
+                const int key = it.tile * kTileRows + (lane >> 1) * P.box_rows;
+                int32_t id = __ldg(P.block_tables + static_cast<int64_t>(it.seq) * P.max_blocks + key / P.block_size);
+                if (id < 0 || id >= P.num_blocks) {
+                    pkv::record_error(&g_prompt_error, PKV_DEV_BAD_BLOCK_ID);
+                    id = 0;
+                }
+                const int64_t row = (static_cast<int64_t>(id) * P.num_kv_heads + it.kvh) * P.block_size + key % P.block_size;
+                pkv::tma_load_2d(base + L::keys + ks * kOperand + (lane & 1) * kSlab + (lane >> 1) * P.box_rows * 128, &P.tmap_k,
+                                 64 * (lane & 1), static_cast<int>(row), bar(kWKeyFull + ks));
+            }
+            __syncwarp();
+            for (int i = it.first; i < it.count; ++i) {
+                const int st = rows % kRowRing;
+                if (!(ok = wait(kWRowEmpty + st, rows / kRowRing + 1))) break;
+                ++rows;
+                if (lane == 0) {
+                    pkv::mbar_arrive_expect_tx(bar(kWRowFull + st), kOperand);
+                    for (int half = 0; half < 2; ++half)
+                        pkv::tma_load_3d(base + L::rows + st * kOperand + half * kSlab, &P.tmap_q, 64 * half, it.kvh << glog,
+                                         it.start + i * tile_tokens, bar(kWRowFull + st));
+                }
+                __syncwarp();
+            }
+        }
+        if (!ok) {  // copies still in flight land before the CTA's memory goes (bounded)
+            for (uint32_t s = k > kKeyStages ? k - kKeyStages : 0; s <= k; ++s)
+                pkv::mbar_wait_bounded(bar(kWKeyFull + s % kKeyStages), (s / kKeyStages) & 1);
+            for (uint32_t s = rows > kRowRing ? rows - kRowRing : 0; s < rows; ++s)
+                pkv::mbar_wait_bounded(bar(kWRowFull + s % kRowRing), (s / kRowRing) & 1);
+        }
+    } else if (warp == kMmaWarp) {
+        uint32_t rows = 0;
+        uint32_t used[4] = {0, 0, 0, 0};  // times each S^T buffer has been filled
+        bool ok = true;
+        for (uint32_t k = 0; ok; ++k) {
+            const int slot = k & 1;
+            if (!(ok = wait(kWItemFull + slot, k >> 1))) break;
+            const int seq = slots[slot].seq, first = slots[slot].first, count = slots[slot].count;
+            const int all_rows = slots[slot].tokens << glog;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kWItemEmpty + slot));
+            if (seq < 0) break;
+            const int ks = k % kKeyStages;
+            if (!(ok = wait(kWKeyFull + ks, k / kKeyStages))) break;
+            for (int i = first; i < count; ++i, ++rows) {
+                const int st = rows % kRowRing, buf = i & 3;
+                if (!(ok = wait(kWRowFull + st, rows / kRowRing))) break;
+                uint32_t fills = 0;
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    if (u == buf) fills = used[u]++;
+                if (!(ok = wait(kWSFree + buf, fills + 1))) break;
+                pkv::tmem_fence_after_sync();
+                if (lane == 0) {
+                    const uint32_t a = base + L::keys + ks * kOperand, b = base + L::rows + st * kOperand;
+                    const uint32_t idesc = pkv::umma_idesc_f16_f32(kTileRows, (min(kTileRows, all_rows - i * kTileRows) + 15) / 16 * 16);
+#pragma unroll
+                    for (int x = 0; x < kDim / 16; ++x) {
+                        const uint32_t off = (x >> 2) * kSlab + (x & 3) * 32;
+                        pkv::umma_f16(tmem + buf * kTileRows, pkv::umma_desc_k_sw128(a + off), pkv::umma_desc_k_sw128(b + off), idesc, x > 0);
+                    }
+                    pkv::umma_commit(bar(kWS + buf));
+                    pkv::umma_commit(bar(kWRowEmpty + st));
+                    if (i + 1 == count) pkv::umma_commit(bar(kWKeyEmpty + ks));
+                }
+                __syncwarp();
+            }
+        }
+        if (!ok) {  // MMAs in flight end before tensor memory is freed (bounded)
+            if (lane == 0) pkv::umma_commit(bar(kWDrain));
+            __syncwarp();
+            pkv::mbar_wait_bounded(bar(kWDrain), 0);
+        }
+    } else {
+        const int grp = warp >> 2;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const int key_lane = (warp & 3) * 32 + lane;  // this thread's key in the tile
+        float4 *s_lse = reinterpret_cast<float4 *>(smem + L::lse) + warp * 32;  // this warp's own copy: no other warp waits for it
+        float *s_sum = reinterpret_cast<float *>(smem + L::sums);
+        const float sc = P.q_scale;
+        uint32_t seen[2] = {0, 0};  // times this group's two buffers have been read
+        bool ok = true;
+        for (uint32_t k = 0; ok; ++k) {
+            const int slot = k & 1;
+            if (!(ok = wait(kWItemFull + slot, k >> 1))) break;
+            const int seq = slots[slot].seq, kvh = slots[slot].kvh, tile = slots[slot].tile, start = slots[slot].start;
+            const int tokens = slots[slot].tokens, keys = slots[slot].keys, first = slots[slot].first, count = slots[slot].count;
+            if (seq < 0) break;
+            const int key = tile * kTileRows + key_lane;
+            const int rows = tokens << glog;
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            // lse of four neighbouring columns of row tile i, log2 units
+            auto column_lse = [&](int i) {
+                float z[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int c = i * kTileRows + 4 * lane + u;
+                    if (i < count && c < rows)
+                        z[u] = __ldg(W.lse + (static_cast<int64_t>(start) + (c >> glog)) * P.num_q_heads + (kvh << glog) +
+                                     (c & ((1 << glog) - 1))) *
+                               kLog2e;
+                }
+                return make_float4(z[0], z[1], z[2], z[3]);
+            };
+            int i = first + ((first & 1) != grp);
+            float4 z = column_lse(i);
+            for (; i < count; i += 2) {
+                const int buf = i & 3, which = buf >> 1;
+                __syncwarp();
+                s_lse[lane] = z;
+                z = column_lse(i + 2);
+                uint32_t fills = 0;
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+                    if (u == which) fills = seen[u]++;
+                if (!(ok = wait(kWS + buf, fills))) break;
+                pkv::tmem_fence_after_sync();
+                uint32_t s[128];
+                tmem_ld128(tmem + lanes + buf * kTileRows, s);
+                pkv::tmem_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(kWSFree + buf));
+                const int pos0 = keys - tokens + i * tile_tokens;  // position of the tile's first row
+                if (pos0 >= (tile + 1) * kTileRows - 1 && rows - i * kTileRows >= kTileRows) {
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        const float4 e = s_lse[c];
+                        sum[0] += pkv::exp2_approx(fmaf(__uint_as_float(s[4 * c]), sc, -e.x));
+                        sum[1] += pkv::exp2_approx(fmaf(__uint_as_float(s[4 * c + 1]), sc, -e.y));
+                        sum[2] += pkv::exp2_approx(fmaf(__uint_as_float(s[4 * c + 2]), sc, -e.z));
+                        sum[3] += pkv::exp2_approx(fmaf(__uint_as_float(s[4 * c + 3]), sc, -e.w));
+                    }
+                } else {  // columns from the first token at or after the key, to the last live row
+                    const int from = max(key - pos0, 0) << glog, to = rows - i * kTileRows;
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        const float4 e = s_lse[c];
+                        const float ez[4] = {e.x, e.y, e.z, e.w};
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            const float w = pkv::exp2_approx(fmaf(__uint_as_float(s[4 * c + u]), sc, -ez[u]));
+                            sum[u] += 4 * c + u >= from && 4 * c + u < to ? w : 0.f;
+                        }
+                    }
+                }
+            }
+            if (!ok) break;
+            const float total = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            if (grp == 1) {  // the slot's sums are read before the slot's next item is published
+                s_sum[slot * kTileRows + key_lane] = total;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(kWSum + slot));
+            } else {
+                if (!(ok = wait(kWSum + slot, k >> 1))) break;
+                if (key < keys) {
+                    float *at = W.scores + (static_cast<int64_t>(seq) * P.num_kv_heads + kvh) * W.capacity + key;
+                    *at += total + s_sum[slot * kTileRows + key_lane];
+                }
+                __syncwarp();
+            }
+            if (lane == 0) mbar_arrive(bar(kWItemEmpty + slot));
+        }
+    }
+    pkv::tmem_fence_before_sync();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        pkv::tmem_fence_after_sync();
+        pkv::tmem_dealloc(tmem, 512);
+    }
+}
+
+// ------------------------------------------------------------------ host side
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+int encode_map(CUtensorMap *map, int rank, const void *base, const cuuint64_t *dims, const cuuint64_t *strides, const cuuint32_t *box) {
+    static const EncodeTiledFn fn = [] {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return static_cast<EncodeTiledFn>(nullptr);
+        return reinterpret_cast<EncodeTiledFn>(ptr);
+    }();
+    if (!fn) return PKV_ERR_CUDA;
+    const cuuint32_t elem[3] = {1, 1, 1};
+    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank, const_cast<void *>(base), dims, strides, box, elem,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? PKV_OK : PKV_ERR_CUDA;
+}
+
+// q rows [total][Hq][128] with `stride` elements between tokens, read in (64 dims, group, 128 / group) boxes.
+int encode_query(CUtensorMap *map, const void *q, int64_t stride, int total, int num_q_heads, int group) {
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kDim), static_cast<cuuint64_t>(num_q_heads), static_cast<cuuint64_t>(total)};
+    const cuuint64_t strides[2] = {kDim * 2, static_cast<cuuint64_t>(stride) * 2};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(group), static_cast<cuuint32_t>(kTileRows / group)};
+    return encode_map(map, 3, q, dims, strides, box);
+}
+
+// [rows][cols] fp16 with `stride` elements between rows, read in `box_rows` x 64 boxes.
+int encode_rows(CUtensorMap *map, const void *base, int64_t rows, int64_t cols, int64_t stride, int box_rows) {
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride) * 2};
+    const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)};
+    return encode_map(map, 2, base, dims, strides, box);
+}
+
+constexpr int kPlannedSms = 152;  // the plan, and with it the workspace, is the same on every device
+
+// Splits of each item's keys: 1 when the items fill half of the SMs or the contexts are short (under
+// 512 keys a split, the second launch and the partial results cost more than they save).
+int plan_splits(int num_seqs, int total_q, int num_q_heads, int num_kv_heads, int max_context) {
+    const int pair_tokens = 2 * kTileRows / (num_q_heads / num_kv_heads);
+    const int64_t items = (static_cast<int64_t>(total_q) / pair_tokens + num_seqs) * num_kv_heads;
+    if (2 * items > kPlannedSms) return 1;
+    const int64_t by_keys = max_context / 512;
+    int64_t s = kPlannedSms / (items > 0 ? items : 1);
+    s = s < by_keys ? s : by_keys;
+    s = s < kMaxSplits ? s : kMaxSplits;
+    return s > 1 ? static_cast<int>(s) : 1;
+}
+
+using pkv_internal::align256;
+
+size_t prompt_workspace(int total_q, int num_q_heads, int splits) {
+    if (splits <= 1) return 0;
+    const size_t rows = static_cast<size_t>(total_q) * num_q_heads * splits;
+    return align256(rows * kDim * sizeof(float)) + 2 * align256(rows * sizeof(float));
+}
+
+bool group_ok(int num_q_heads, int num_kv_heads) {
+    const int g = num_q_heads / num_kv_heads;
+    return g == 1 || g == 2 || g == 4 || g == 8;
+}
+
+template <bool PAGED>
+int launch_prompt(PromptParams p, int max_context, void *workspace, size_t workspace_bytes, pkv_stream_t stream) {
+    p.splits = plan_splits(p.num_seqs, p.total_q, p.num_q_heads, p.num_kv_heads, max_context);
+    const size_t need = prompt_workspace(p.total_q, p.num_q_heads, p.splits);
+    if (need) {
+        if (!workspace || workspace_bytes < need || !pkv_internal::aligned(workspace, 256)) return PKV_ERR_WORKSPACE;
+        const size_t rows = static_cast<size_t>(p.total_q) * p.num_q_heads * p.splits;
+        unsigned char *ws = static_cast<unsigned char *>(workspace);
+        p.o_part = reinterpret_cast<float *>(ws);
+        p.m_part = reinterpret_cast<float *>(ws + align256(rows * kDim * sizeof(float)));
+        p.l_part = reinterpret_cast<float *>(ws + align256(rows * kDim * sizeof(float)) + align256(rows * sizeof(float)));
+    }
+    auto kernel = prompt_kernel<PAGED>;
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return PKV_ERR_CUDA;
+    static std::atomic<uint64_t> configured{0};  // one bit per device
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(configured.load(std::memory_order_acquire) & bit)) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PromptSmem::total) != cudaSuccess)
+            return PKV_ERR_CUDA;
+        configured.fetch_or(bit, std::memory_order_acq_rel);
+    }
+    const int pair_tokens = 2 * kTileRows >> p.group_log2;
+    const int64_t most = (static_cast<int64_t>(p.total_q) / pair_tokens + p.num_seqs) * p.num_kv_heads * p.splits;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(most < sms ? most : sms));
+    cfg.blockDim = dim3(kPromptThreads);
+    cfg.dynamicSmemBytes = PromptSmem::total;
+    cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, p) != cudaSuccess) return PKV_ERR_CUDA;
+    if (p.splits == 1) return PKV_OK;
+    const int64_t rows = static_cast<int64_t>(p.max_query_len) * p.num_q_heads;
+    cfg.gridDim = dim3(static_cast<unsigned>((rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32)), p.num_seqs);
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, prompt_join_kernel, p) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+int log2_of(int g) { return g == 1 ? 0 : (g == 2 ? 1 : (g == 4 ? 2 : 3)); }
+
+// What both forms check; PKV_OK with *done set when there is nothing to do.
+int check_prompt(const float *lse, const void *q, int64_t q_stride, const int32_t *start, int num_seqs,
+                 int total_q, int max_query_len, int num_q_heads, int num_kv_heads, int head_dim, float scale, bool *done) {
+    *done = false;
+    if (num_seqs < 0 || total_q < 0 || max_query_len < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0)
+        return PKV_ERR_INVALID_ARG;
+    if (num_q_heads % num_kv_heads != 0 || !(scale > 0.f) || !isfinite(scale)) return PKV_ERR_INVALID_ARG;
+    if (head_dim != kDim || !group_ok(num_q_heads, num_kv_heads) || num_seqs > 65535 || num_q_heads > 65535) return PKV_ERR_UNSUPPORTED;
+    if (num_seqs == 0 || total_q == 0 || max_query_len == 0) {
+        *done = true;
+        return PKV_OK;
+    }
+    if (!q || !start) return PKV_ERR_INVALID_ARG;
+    if (!pkv_internal::aligned16(q) || !pkv_internal::aligned(start, 4) ||
+        (lse && !pkv_internal::aligned(lse, 4)))
+        return PKV_ERR_INVALID_ARG;
+    if (q_stride % 8 != 0 || q_stride < static_cast<int64_t>(num_q_heads) * head_dim) return PKV_ERR_INVALID_ARG;
+    return PKV_OK;
+}
+
+}  // namespace
+
+extern "C" PKV_API size_t pkv_prefill_workspace_size(int num_seqs, int total_q, int num_q_heads, int num_kv_heads, int head_dim,
+                                                     int max_context) {
+    if (num_seqs <= 0 || total_q <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0 ||
+        head_dim != kDim || max_context <= 0 || !group_ok(num_q_heads, num_kv_heads))
+        return 0;
+    return prompt_workspace(total_q, num_q_heads, plan_splits(num_seqs, total_q, num_q_heads, num_kv_heads, max_context));
+}
+
+extern "C" PKV_API int pkv_prefill_attention(void *out, float *lse, const void *q, int64_t q_stride, const void *k,
+                                             int64_t k_stride, const void *v, int64_t v_stride, const int32_t *seq_start,
+                                             int num_seqs, int total_tokens, int max_seq_len, int num_q_heads,
+                                             int num_kv_heads, int head_dim, float scale, void *workspace,
+                                             size_t workspace_bytes, pkv_stream_t stream) {
+    bool done = false;
+    int st = check_prompt(lse, q, q_stride, seq_start, num_seqs, total_tokens, max_seq_len, num_q_heads, num_kv_heads,
+                          head_dim, scale, &done);
+    if (st != PKV_OK || done) return st;
+    if (!out || !pkv_internal::aligned(out, 32)) return PKV_ERR_INVALID_ARG;
+    const int64_t least = static_cast<int64_t>(num_kv_heads) * head_dim;
+    if (!k || !v || !pkv_internal::aligned16(k) || !pkv_internal::aligned16(v) || k_stride % 8 != 0 || v_stride % 8 != 0 ||
+        k_stride < least || v_stride < least)
+        return PKV_ERR_INVALID_ARG;
+    PromptParams p{};
+    p.out = static_cast<__half *>(out);
+    p.lse = lse;
+    p.query_start = seq_start;
+    p.num_seqs = num_seqs;
+    p.total_q = total_tokens;
+    p.max_query_len = max_seq_len;
+    p.num_q_heads = num_q_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.group_log2 = log2_of(num_q_heads / num_kv_heads);
+    p.q_scale = scale * kLog2e;
+    st = encode_query(&p.tmap_q, q, q_stride, total_tokens, num_q_heads, num_q_heads / num_kv_heads);
+    if (st == PKV_OK) st = encode_rows(&p.tmap_k, k, total_tokens, least, k_stride, kTileRows);
+    if (st == PKV_OK) st = encode_rows(&p.tmap_v, v, total_tokens, least, v_stride, kTileRows);
+    if (st != PKV_OK) return st;
+    return launch_prompt<false>(p, max_seq_len, workspace, workspace_bytes, stream);
+}
+
+extern "C" PKV_API int pkv_prefill_attention_paged(void *out, float *lse, const void *q, int64_t q_stride,
+                                                   const void *k_cache, const void *v_cache, const int32_t *block_tables,
+                                                   const int32_t *context_lens, const int32_t *query_start, int num_seqs,
+                                                   int total_q, int max_query_len, int max_blocks_per_seq, int num_q_heads,
+                                                   int num_kv_heads, int head_dim, int block_size, int64_t num_blocks,
+                                                   float scale, void *workspace, size_t workspace_bytes,
+                                                   pkv_stream_t stream) {
+    int st = pkv_internal::check_decode_args(q, k_cache, v_cache, block_tables, context_lens, num_seqs, max_blocks_per_seq,
+                                             num_q_heads, num_kv_heads, head_dim, block_size, num_blocks);
+    if (st != PKV_OK) return st;
+    bool done = false;
+    st = check_prompt(lse, q, q_stride, query_start, num_seqs, total_q, max_query_len, num_q_heads, num_kv_heads, head_dim,
+                      scale, &done);
+    if (st != PKV_OK || done) return st;
+    if (!out || !pkv_internal::aligned(out, 32)) return PKV_ERR_INVALID_ARG;
+    const int64_t rows = num_blocks * num_kv_heads * block_size;
+    if (rows >= 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;  // box row coordinates are signed 32-bit
+    PromptParams p{};
+    p.out = static_cast<__half *>(out);
+    p.lse = lse;
+    p.query_start = query_start;
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.num_seqs = num_seqs;
+    p.total_q = total_q;
+    p.max_query_len = max_query_len;
+    p.max_blocks = max_blocks_per_seq;
+    p.num_q_heads = num_q_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.block_size = block_size;
+    p.num_blocks = num_blocks;
+    p.group_log2 = log2_of(num_q_heads / num_kv_heads);
+    p.q_scale = scale * kLog2e;
+    p.box_rows = kTileRows;
+    while (block_size % p.box_rows != 0) p.box_rows /= 2;  // a box never leaves its block: 16 at least
+    st = encode_query(&p.tmap_q, q, q_stride, total_q, num_q_heads, num_q_heads / num_kv_heads);
+    if (st == PKV_OK) st = encode_rows(&p.tmap_k, k_cache, rows, kDim, kDim, p.box_rows);
+    if (st == PKV_OK) st = encode_rows(&p.tmap_v, v_cache, rows, kDim, kDim, p.box_rows);
+    if (st != PKV_OK) return st;
+    return launch_prompt<true>(p, static_cast<int>(static_cast<int64_t>(max_blocks_per_seq) * block_size), workspace, workspace_bytes,
+                               stream);
+}
+
+extern "C" PKV_API int pkv_prefill_attention_weights(float *scores, int64_t score_capacity, const void *q, int64_t q_stride,
+                                                     const float *lse, const void *k_cache, const int32_t *block_tables,
+                                                     const int32_t *context_lens, const int32_t *query_start, int num_seqs,
+                                                     int total_q, int max_query_len, int max_blocks_per_seq, int num_q_heads,
+                                                     int num_kv_heads, int head_dim, int block_size, int64_t num_blocks,
+                                                     float scale, pkv_stream_t stream) {
+    int st = pkv_internal::check_decode_args(q, k_cache, k_cache, block_tables, context_lens, num_seqs, max_blocks_per_seq,
+                                             num_q_heads, num_kv_heads, head_dim, block_size, num_blocks);
+    if (st != PKV_OK) return st;
+    bool done = false;
+    st = check_prompt(lse, q, q_stride, query_start, num_seqs, total_q,
+                      max_query_len, num_q_heads, num_kv_heads, head_dim, scale, &done);
+    if (st != PKV_OK) return st;
+    const int64_t cap = static_cast<int64_t>(max_blocks_per_seq) * block_size;
+    if (!scores || !pkv_internal::aligned(scores, 4) || score_capacity < cap || (!done && !lse)) return PKV_ERR_INVALID_ARG;
+    if (done) return PKV_OK;
+    const int64_t rows = num_blocks * num_kv_heads * block_size;
+    if (rows >= 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;  // box row coordinates are signed 32-bit
+    ChunkWeightParams w{};
+    PromptParams &p = w.p;
+    p.query_start = query_start;
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.num_seqs = num_seqs;
+    p.total_q = total_q;
+    p.max_query_len = max_query_len;
+    p.max_blocks = max_blocks_per_seq;
+    p.num_q_heads = num_q_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.block_size = block_size;
+    p.num_blocks = num_blocks;
+    p.group_log2 = log2_of(num_q_heads / num_kv_heads);
+    p.q_scale = scale * kLog2e;
+    p.box_rows = kTileRows;
+    while (block_size % p.box_rows != 0) p.box_rows /= 2;
+    w.lse = lse;
+    w.scores = scores;
+    w.capacity = score_capacity;
+    st = encode_query(&p.tmap_q, q, q_stride, total_q, num_q_heads, num_q_heads / num_kv_heads);
+    if (st == PKV_OK) st = encode_rows(&p.tmap_k, k_cache, rows, kDim, kDim, p.box_rows);
+    if (st != PKV_OK) return st;
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return PKV_ERR_CUDA;
+    static std::atomic<uint64_t> configured{0};  // one bit per device
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(configured.load(std::memory_order_acquire) & bit)) {
+        if (cudaFuncSetAttribute(chunk_weights_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ChunkWeightSmem::total) !=
+            cudaSuccess)
+            return PKV_ERR_CUDA;
+        configured.fetch_or(bit, std::memory_order_acq_rel);
+    }
+    const int64_t most = (cap + kTileRows - 1) / kTileRows * num_seqs * num_kv_heads;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(most < sms ? most : sms));
+    cfg.blockDim = dim3(kPromptThreads);
+    cfg.dynamicSmemBytes = ChunkWeightSmem::total;
+    cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, chunk_weights_kernel, w) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+namespace pkv_internal {
+
+int prompt_take_error(int *code) {
+    int value = 0;
+    if (cudaMemcpyFromSymbol(&value, g_prompt_error, sizeof(int)) != cudaSuccess) return PKV_ERR_CUDA;
+    if (value != 0) {
+        const int zero = 0;
+        if (cudaMemcpyToSymbol(g_prompt_error, &zero, sizeof(int)) != cudaSuccess) return PKV_ERR_CUDA;
+    }
+    *code = value;
+    return PKV_OK;
+}
+
+}  // namespace pkv_internal

@@ -118,3 +118,52 @@ def test_evict_refusals(lib):
     for key in ("kc", "vc", "kept", "new_scores", "new_lens", "scores", "bt", "nt", "cl"):
         assert call(lib, "pkv_evict", one, **{key: NULL}) == INVALID, key
         assert call(lib, "pkv_evict", one, **{key: BAD}) == INVALID, key
+
+
+PACKED = dict(out=P, lse=NULL, q=P, qs=1024, k=P, ks=256, v=P, vs=256, start=P, seqs=0, total=64, longest=64, hq=8, hkv=2, d=128,
+              scale=1.0, ws=NULL, ws_bytes=0, stream=NULL)
+PAGED = dict(out=P, lse=NULL, q=P, qs=1024, kc=P, vc=P, bt=P, cl=P, start=P, seqs=0, total=64, longest=64, width=4, hq=8, hkv=2, d=128,
+             bs=16, nb=9, scale=1.0, ws=NULL, ws_bytes=0, stream=NULL)
+CHUNK = dict(scores=P, capacity=64, q=P, qs=1024, lse=P, kc=P, bt=P, cl=P, start=P, seqs=0, total=64, longest=64, width=4, hq=8, hkv=2,
+             d=128, bs=16, nb=9, scale=1.0, stream=NULL)
+
+
+@pytest.mark.parametrize("name,good", [("pkv_prefill_attention", PACKED), ("pkv_prefill_attention_paged", PAGED),
+                                       ("pkv_prefill_attention_weights", CHUNK)])
+def test_prompt_refusals(lib, name, good):
+    for empty in (dict(), dict(seqs=1, total=0), dict(seqs=1, longest=0)):
+        assert call(lib, name, good, **empty) == OK, empty
+    for change in (dict(seqs=-1), dict(total=-1), dict(longest=-1), dict(hq=7), dict(hkv=0), dict(scale=0.0), dict(scale=-1.0),
+                   dict(scale=float("inf")), dict(scale=float("nan"))):
+        assert call(lib, name, good, **change) == INVALID, change
+    for change in (dict(hq=6), dict(hq=32), dict(d=64), dict(seqs=70000)):
+        assert call(lib, name, good, **change) == UNSUPPORTED, change
+    one = dict(good, seqs=1)
+    keys = [k for k in ("out", "q", "k", "v", "kc", "vc", "bt", "cl", "start", "scores") if k in good]
+    for key in keys:
+        assert call(lib, name, one, **{key: NULL}) == INVALID, key
+        assert call(lib, name, one, **{key: BAD}) == INVALID, key
+    if "out" in good:
+        assert call(lib, name, one, out=ctypes.c_void_p(4096 + 16)) == INVALID  # 32-byte stores
+    for key in ("qs", "ks", "vs"):
+        if key in good:
+            for stride in (good[key] - 8, good[key] + 4):
+                assert call(lib, name, one, **{key: stride}) == INVALID, key
+    assert call(lib, name, one, lse=BAD) == INVALID
+    if name == "pkv_prefill_attention_weights":
+        assert call(lib, name, one, lse=NULL) == INVALID
+        assert call(lib, name, one, capacity=63) == INVALID
+    if "nb" in good:
+        assert call(lib, name, one, nb=2 ** 26) == UNSUPPORTED
+
+
+def test_prefill_workspace(lib):
+    f = lib.pkv_prefill_workspace_size
+    assert f(1, 16384, 32, 8, 128, 16384) == 0       # enough rows: no split
+    assert f(64, 64, 32, 8, 128, 32768) == 0         # enough requests
+    few = f(1, 16, 32, 8, 128, 32768)
+    assert few > 0 and few % 256 == 0 and few >= 16 * 32 * 2 * (128 * 4 + 8)
+    assert f(1, 16, 32, 8, 128, 600) == 0            # a short axis
+    for bad in ((0, 16, 32, 8, 128, 4096), (1, 0, 32, 8, 128, 4096), (1, 16, 24, 8, 128, 4096), (1, 16, 32, 8, 64, 4096),
+                (1, 16, 32, 8, 128, 0)):
+        assert f(*bad) == 0

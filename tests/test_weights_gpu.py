@@ -147,3 +147,80 @@ def test_graph_and_other_stream():
     pkv.decode_attention_weights(out2, scores2, *args, stream=s)
     torch.cuda.synchronize()
     assert torch.equal(scores, scores2) and torch.equal(out, out2)
+
+
+# ---------------------------------------------------------------- a chunk's rows
+
+def run_chunk(ctxs, chunks, group, hkv, bs, seed, poison=False, last=None):
+    case = workloads.random_case(seed, ctxs, group * hkv, hkv, block_size=bs)
+    if poison:
+        for b, n in enumerate(ctxs):
+            if n % bs:
+                case.k_cache[int(case.block_tables[b, n // bs]), :, n % bs:] = float("nan")
+    rng = np.random.default_rng(seed)
+    start = np.concatenate([[0], np.cumsum(chunks)]).astype(np.int32)
+    q = rng.standard_normal((start[-1], group * hkv, 128)).astype(np.float16)
+    cap = case.max_blocks_per_seq * bs
+    prior = rng.exponential(1.0, (len(ctxs), hkv, cap + 3)).astype(np.float32)
+    lse = np.zeros(q.shape[:2])
+    add, tol = np.zeros(prior.shape), np.zeros(prior.shape)
+    for b, n in enumerate(ctxs):
+        if chunks[b] == 0:
+            continue
+        rows = slice(start[b], start[b + 1])
+        k = ref.rows_of(case.k_cache.numpy(), case.block_tables.numpy()[b], n)
+        p, z = ref.weights(q[rows], k, case.scale)
+        lse[rows] = z
+        w = p.reshape(chunks[b], hkv, group, n).sum((0, 2))
+        add[b, :, :n] = w
+        # lse arrives rounded to float32: 2^-24 of it, twice 2^-23 with its conversion to log2 units; the sum over the
+        # rows adds 2^-23 for each of the levels a value passes (128 columns / 4 in turn, then the row tiles)
+        size = 4 * float(np.abs(z).max()) * 2.0 ** -23 + (32 + chunks[b] * group / 128) * 2.0 ** -23
+        tol[b, :, :n] = score_tolerance(w, q[rows], k, case.scale, prior[b, :, :n].astype(np.float64)) + w * size
+    dev = case.to("cuda")
+    scores = torch.from_numpy(prior.copy()).cuda()
+    qd, zd = torch.from_numpy(q).cuda(), torch.from_numpy(lse.astype(np.float32)).cuda()
+    args = (qd, zd, dev.k_cache, dev.block_tables, dev.context_lens, torch.from_numpy(start).cuda(), max(1, max(chunks)), case.scale)
+    pkv.prefill_attention_weights(scores, *args)
+    got = scores.cpu().numpy().astype(np.float64)
+    err = np.abs(got - (prior + add))
+    assert (err <= tol).all(), (err.max(), np.argwhere(err > tol)[:3])
+    assert_no_device_error()
+    return scores, prior, args, dev
+
+
+@pytest.mark.parametrize("group", [1, 2, 4, 8])
+@pytest.mark.parametrize("bs", [16, 48, 256])
+def test_chunk_ragged(group, bs):
+    run_chunk([1, 17, 128, 129, 500, 1000, 300, 4, 260], [1, 5, 128, 1, 33, 200, 300, 0, 64], group, 2, bs, 50 + bs + group, poison=True)
+
+
+@pytest.mark.parametrize("ctxs,chunks,group,hkv,bs", [([5000], [600], 4, 1, 16), ([1300, 64], [1300, 64], 2, 3, 64), ([700] * 40, [1] * 40, 8, 1, 16)])
+def test_chunk_sizes(ctxs, chunks, group, hkv, bs):
+    run_chunk(ctxs, chunks, group, hkv, bs, 60)
+
+
+def test_chunk_follows_the_attention():
+    """With the log-sum-exps of prefill_attention_paged every row's weights sum to one; one row per request
+    adds what decode_attention_weights adds."""
+    scores, prior, args, dev = run_chunk([900, 333], [100, 333], 4, 2, 16, 61)
+    q, _, kc, bt, cl, qs, n, scale = args
+    lse, out = torch.empty(q.shape[:2], device="cuda"), torch.empty_like(q)
+    ws = pkv.make_prefill_workspace(2, q.shape[0], 8, 2, bt.shape[1] * 16, "cuda")
+    pkv.prefill_attention_paged(out, q, kc, dev.v_cache, bt, cl, qs, n, scale, lse=lse, workspace=ws)
+    s = torch.zeros_like(scores)
+    pkv.prefill_attention_weights(s, q, lse, kc, bt, cl, qs, n, scale)
+    sums = s.double().sum(-1).cpu().numpy()
+    assert np.abs(sums - 4 * np.array([[100], [333]])).max() <= 4 * 333 * 2e-4  # each weight within 2 x 1e-4 (see run_chunk)
+    one = torch.zeros_like(scores)
+    last = torch.tensor([99, 432], device="cuda")
+    pkv.prefill_attention_weights(one, q[last], lse[last], kc, bt, cl, torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda"), 1, scale)
+    step = torch.zeros_like(scores)
+    w = pkv.make_weights_workspace(2, 8, bt.shape[1] * 16, "cuda")
+    pkv.decode_attention_weights(torch.empty_like(q[last]), step, q[last], kc, dev.v_cache, bt, cl, scale, w)
+    assert torch.allclose(one, step, rtol=1e-3, atol=1e-9)
+    # a request cut by a bad range keeps its scores, the other's are the same
+    bad = torch.zeros_like(scores)
+    pkv.prefill_attention_weights(bad, q, lse, kc, bt, torch.tensor([99, 333], dtype=torch.int32, device="cuda"), qs, n, scale)
+    assert pkv.device_error() == pkv.PKV_DEV_BAD_CONTEXT
+    assert not bad[0].any() and torch.equal(bad[1], s[1])
