@@ -56,11 +56,29 @@ def _stream(device: torch.device, stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _call(name: str, device: torch.device, stream, *args) -> None:
+    """One library call on `device` (made current if it is not) and the given or its current stream, its status
+    checked.  The stream's handle is read without making a Stream object and the device context is entered only
+    where it changes something: together they were a third of a decode-size call's host time."""
+    fn = getattr(_L(), name)
+    raw = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == device.index:
+        st = fn(*args, raw)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, raw)
+    if st != _lib.PKV_OK:
+        raise PkvError(st, name)
+
+
 def _flags(overlap: bool) -> int:
     return _lib.PKV_STEP_OVERLAP if overlap else 0
 
 
 def _need(t: torch.Tensor, name: str, dtype, ndim: int, device=None):
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == ndim and t.is_cuda and t.is_contiguous()
+            and (device is None or t.get_device() == device.index)):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
@@ -683,8 +701,20 @@ def rope_magnitude(factor: float) -> float:
     return m.value
 
 
+def _device_of(t: torch.Tensor, name: str) -> torch.device:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    return t.device
+
+
 def _need_rows(t: torch.Tensor, name: str, device, shape=None):
     """fp16 [tokens, heads, dim] whose heads lie together; returns the elements between tokens."""
+    if (isinstance(t, torch.Tensor) and t.dtype is torch.float16 and t.dim() == 3 and t.get_device() == device.index
+            and (shape is None or t.shape == shape)):
+        n, h, d = t.shape
+        s0, s1, s2 = t.stride()
+        if s2 == 1 and s1 == d:
+            return s0 if n > 1 else h * d
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != torch.float16 or t.dim() != 3:
@@ -714,17 +744,15 @@ def rope(q_out: torch.Tensor, k_out: torch.Tensor, q: torch.Tensor, k: torch.Ten
     """Rotate q [T, Hq, D] into q_out and k [T, Hkv, D] into k_out by their positions [T] (int32).  The first
     2 * len(frequencies) dims of each head turn, in pairs (i, i + half) or, interleaved, (2i, 2i + 1); the
     rest is copied.  Rows may be slices of a fused projection (any token stride); an output may be its input."""
-    dev = q.device
+    dev = _device_of(q, "q")
     qs = _need_rows(q, "q", dev)
     ks = _need_rows(k, "k", dev, (q.shape[0], k.shape[1], q.shape[2]) if k.dim() == 3 else None)
     qos = _need_rows(q_out, "q_out", dev, q.shape)
     kos = _need_rows(k_out, "k_out", dev, k.shape)
     r = _rope_inputs(q, positions, frequencies, dev)
-    with torch.cuda.device(dev):
-        st = _L().pkv_rope(q_out.data_ptr(), qos, k_out.data_ptr(), kos, q.data_ptr(), qs, k.data_ptr(), ks,
-                           positions.data_ptr(), frequencies.data_ptr(), q.shape[0], q.shape[1], k.shape[1], q.shape[2], r,
-                           int(bool(interleaved)), float(magnitude), _stream(dev, stream))
-    _lib.check(st, "pkv_rope")
+    _call("pkv_rope", dev, stream, q_out.data_ptr(), qos, k_out.data_ptr(), kos, q.data_ptr(), qs, k.data_ptr(), ks,
+          positions.data_ptr(), frequencies.data_ptr(), q.shape[0], q.shape[1], k.shape[1], q.shape[2], r,
+          int(bool(interleaved)), float(magnitude))
 
 
 def rope_append(q_out: torch.Tensor, q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, k_cache: torch.Tensor,
@@ -745,12 +773,9 @@ def rope_append(q_out: torch.Tensor, q: torch.Tensor, k_new: torch.Tensor, v_new
     if slot_mapping.shape[0] != t:
         raise ValueError("slot_mapping must have one entry per token")
     r = _rope_inputs(q, positions, frequencies, dev)
-    with torch.cuda.device(dev):
-        st = _L().pkv_rope_append(q_out.data_ptr(), qos, q.data_ptr(), qs, k_new.data_ptr(), ks, v_new.data_ptr(), vs,
-                                  k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(),
-                                  frequencies.data_ptr(), t, q.shape[1], hkv, d, r, bs, nb, int(bool(interleaved)),
-                                  float(magnitude), _stream(dev, stream))
-    _lib.check(st, "pkv_rope_append")
+    _call("pkv_rope_append", dev, stream, q_out.data_ptr(), qos, q.data_ptr(), qs, k_new.data_ptr(), ks,
+          v_new.data_ptr(), vs, k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(),
+          frequencies.data_ptr(), t, q.shape[1], hkv, d, r, bs, nb, int(bool(interleaved)), float(magnitude))
 
 
 # ---------------------------------------------------------------- prompts and chunks
@@ -783,7 +808,7 @@ def prefill_attention(out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: to
     """Causal attention of whole prompts packed one behind another: q [T, Hq, D], k and v [T, Hkv, D] (any token
     stride), sequence b being rows seq_start[b] .. seq_start[b + 1] - 1 (int32 [B + 1]).  out like q; lse
     [T, Hq] float32 the rows' log-sum-exps; rows of no sequence stay as they are."""
-    dev = q.device
+    dev = _device_of(q, "q")
     qs = _need_rows(q, "q", dev)
     ks = _need_rows(k, "k", dev)
     vs = _need_rows(v, "v", dev, k.shape)
@@ -793,12 +818,9 @@ def prefill_attention(out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: to
     if seq_start.shape[0] < 1:
         raise ValueError("seq_start must be [B + 1]")
     ws_ptr, ws_bytes = _prompt_outputs(out, lse, q, workspace, dev)
-    with torch.cuda.device(dev):
-        st = _L().pkv_prefill_attention(out.data_ptr(), None if lse is None else lse.data_ptr(), q.data_ptr(), qs,
-                                        k.data_ptr(), ks, v.data_ptr(), vs, seq_start.data_ptr(), seq_start.shape[0] - 1,
-                                        q.shape[0], int(max_seq_len), q.shape[1], k.shape[1], q.shape[2], float(scale), ws_ptr,
-                                        ws_bytes, _stream(dev, stream))
-    _lib.check(st, "pkv_prefill_attention")
+    _call("pkv_prefill_attention", dev, stream, out.data_ptr(), None if lse is None else lse.data_ptr(), q.data_ptr(),
+          qs, k.data_ptr(), ks, v.data_ptr(), vs, seq_start.data_ptr(), seq_start.shape[0] - 1, q.shape[0],
+          int(max_seq_len), q.shape[1], k.shape[1], q.shape[2], float(scale), ws_ptr, ws_bytes)
     return out
 
 
@@ -821,13 +843,10 @@ def prefill_attention_paged(out: torch.Tensor, q: torch.Tensor, k_cache: torch.T
     if block_tables.shape[0] != b or query_start.shape[0] != b + 1:
         raise ValueError("block_tables [B, ...], context_lens [B] and query_start [B + 1] disagree")
     ws_ptr, ws_bytes = _prompt_outputs(out, lse, q, workspace, dev)
-    with torch.cuda.device(dev):
-        st = _L().pkv_prefill_attention_paged(out.data_ptr(), None if lse is None else lse.data_ptr(), q.data_ptr(), qs,
-                                              k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
-                                              context_lens.data_ptr(), query_start.data_ptr(), b, q.shape[0],
-                                              int(max_query_len), block_tables.shape[1], q.shape[1], hkv, d, bs, nb,
-                                              float(scale), ws_ptr, ws_bytes, _stream(dev, stream))
-    _lib.check(st, "pkv_prefill_attention_paged")
+    _call("pkv_prefill_attention_paged", dev, stream, out.data_ptr(), None if lse is None else lse.data_ptr(),
+          q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(),
+          query_start.data_ptr(), b, q.shape[0], int(max_query_len), block_tables.shape[1], q.shape[1], hkv, d, bs,
+          nb, float(scale), ws_ptr, ws_bytes)
     return out
 
 
@@ -859,13 +878,9 @@ def decode_attention_weights(out: torch.Tensor, scores: torch.Tensor, q: torch.T
     if out.shape != q.shape:
         raise ValueError("out must have q's shape")
     _need_scores(scores, "scores", b, hkv, block_tables.shape[1] * bs, dev)
-    with torch.cuda.device(dev):
-        st = _L().pkv_decode_attention_weights(out.data_ptr(), scores.data_ptr(), scores.shape[2], q.data_ptr(),
-                                               k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
-                                               context_lens.data_ptr(), b, block_tables.shape[1], hq, hkv, d, bs, nb,
-                                               float(scale), workspace.data_ptr(), workspace.numel(),
-                                               _stream(dev, stream))
-    _lib.check(st, "pkv_decode_attention_weights")
+    _call("pkv_decode_attention_weights", dev, stream, out.data_ptr(), scores.data_ptr(), scores.shape[2],
+          q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), b,
+          block_tables.shape[1], hq, hkv, d, bs, nb, float(scale), workspace.data_ptr(), workspace.numel())
     return out
 
 
@@ -891,13 +906,10 @@ def prefill_attention_weights(scores: torch.Tensor, q: torch.Tensor, lse: torch.
     if block_tables.shape[0] != b or query_start.shape[0] != b + 1:
         raise ValueError("block_tables [B, ...], context_lens [B] and query_start [B + 1] disagree")
     _need_scores(scores, "scores", b, hkv, block_tables.shape[1] * bs, dev)
-    with torch.cuda.device(dev):
-        st = _L().pkv_prefill_attention_weights(scores.data_ptr(), scores.shape[2], q.data_ptr(), qs, lse.data_ptr(),
-                                                k_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(),
-                                                query_start.data_ptr(), b, q.shape[0], int(max_query_len),
-                                                block_tables.shape[1], q.shape[1], hkv, d, bs, nb, float(scale),
-                                                _stream(dev, stream))
-    _lib.check(st, "pkv_prefill_attention_weights")
+    _call("pkv_prefill_attention_weights", dev, stream, scores.data_ptr(), scores.shape[2], q.data_ptr(), qs,
+          lse.data_ptr(), k_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(),
+          query_start.data_ptr(), b, q.shape[0], int(max_query_len), block_tables.shape[1], q.shape[1], hkv, d, bs,
+          nb, float(scale))
 
 
 def evict(k_cache: torch.Tensor, v_cache: torch.Tensor, kept: torch.Tensor, new_scores: torch.Tensor,
@@ -925,12 +937,10 @@ def evict(k_cache: torch.Tensor, v_cache: torch.Tensor, kept: torch.Tensor, new_
     _need(kept, "kept", torch.int32, 3, dev)
     if kept.shape != (b, hkv, budget):
         raise ValueError(f"kept must be [{b}, {hkv}, {budget}]")
-    with torch.cuda.device(dev):
-        st = _L().pkv_evict(k_cache.data_ptr(), v_cache.data_ptr(), kept.data_ptr(), new_scores.data_ptr(),
-                            new_lens.data_ptr(), scores.data_ptr(), block_tables.data_ptr(), new_tables.data_ptr(),
-                            context_lens.data_ptr(), b, block_tables.shape[1], new_tables.shape[1], scores.shape[2], hkv,
-                            d, bs, nb, int(budget), int(recent), int(sinks), _stream(dev, stream))
-    _lib.check(st, "pkv_evict")
+    _call("pkv_evict", dev, stream, k_cache.data_ptr(), v_cache.data_ptr(), kept.data_ptr(), new_scores.data_ptr(),
+          new_lens.data_ptr(), scores.data_ptr(), block_tables.data_ptr(), new_tables.data_ptr(),
+          context_lens.data_ptr(), b, block_tables.shape[1], new_tables.shape[1], scores.shape[2], hkv, d, bs, nb,
+          int(budget), int(recent), int(sinks))
 
 
 class BlockPool:

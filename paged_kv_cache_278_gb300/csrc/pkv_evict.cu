@@ -13,12 +13,11 @@
 //     registers; no atomics, so the result does not depend on any order.  The kept set is then a
 //     bitmap over the positions (above the border, the lowest ties, sinks, recent); prefix popcounts
 //     of its words give every kept position its place.
-//   * move: bound by HBM (each kept row is read once and written once).  A row's place may be the
-//     source of an earlier-placed row, so one CTA moves the rows of its (b, h) in order, a batch at a
-//     time: load a batch, barrier, store it.  The next batch's loads are issued before the stores
-//     (their sources lie behind every place being stored).  The bytes of a row are independent of one
-//     another: CTAs split each row into slices of 32 to 256 bytes (and K from V) until the grid
-//     covers the SMs, with no order between CTAs.
+//   * move: bound by HBM (each kept row is read once and written once).  In a block that both tables
+//     name, a row's place may be the source of a row placed earlier, so rows move in order: a cluster
+//     of CTAs takes a (request, kv head)'s K, or V, step by step, all its CTAs load their rows of the
+//     step, meet, and store them (later sources lie behind every place of the step).  Tables with no
+//     block in common need no meeting.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -33,8 +32,11 @@ __device__ int g_evict_error;
 
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kListKeys = 2;        // undecided keys per thread once they are listed
 constexpr int kMoveThreads = 256;
-constexpr int kMoveBatch = 4;  // rows in flight per thread and batch
+constexpr int kRowLanes = PKV_HEAD_DIM * 2 / 16;  // threads that move one row, 16 bytes each
+constexpr int kMoveBatch = 4;                     // rows in flight per thread
+constexpr int kMoveRows = kMoveThreads / kRowLanes * kMoveBatch;  // rows of a CTA's step
 
 struct EvictParams {
     unsigned char *k_cache, *v_cache;
@@ -46,8 +48,7 @@ struct EvictParams {
     int64_t capacity, num_blocks;
     int max_blocks, max_new_blocks, num_kv_heads, block_size, row_bytes;
     int budget, recent, sinks;
-    int slice_pieces;  // 16-byte pieces of a row per CTA of the move
-    int slices;
+    int cluster;  // CTAs that move one (request, kv head)'s K, or V, together
 };
 
 // Larger float <-> larger integer; NaN smallest, so that it is evicted first.
@@ -107,6 +108,8 @@ template <int KPT>
 __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_constant__ EvictParams P) {
     extern __shared__ uint32_t s_words[];  // [words] above the border, then kept | [words] at the border, then prefixes
     __shared__ int s_sum[2][kSelWarps];
+    __shared__ uint32_t s_list[kListKeys * kSelThreads];
+    __shared__ int s_listed;
     pkv::pdl_wait_primary();
     pkv::pdl_launch_dependents();
     const int h = blockIdx.x, b = blockIdx.y;
@@ -132,15 +135,65 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
         uint32_t border = 0;
         int flip = 0;
         if (need > 0) {
+            int upper = 0, inside = last - first;  // keys above the undecided range, and in it
+            int above_list = 0;                    // keys above the listed ones
+            uint32_t mine[kListKeys] = {};
+            bool listed = false;
             for (int bit = 31; bit >= 0; --bit) {
                 const uint32_t trial = border | (1u << bit);
                 int c = 0;
+                if (!listed) {
 #pragma unroll
-                for (int j = 0; j < KPT; ++j) c += key[j] >= trial;
-                for (int p = KPT * kSelThreads + tid; p < last; p += kSelThreads)
-                    c += p >= first && order_key(__ldcg(scores + p)) >= trial;
-                if (block_sum(c, s_sum[flip]) >= need) border = trial;
+                    for (int j = 0; j < KPT; ++j) c += key[j] >= trial;
+                    for (int p = KPT * kSelThreads + tid; p < last; p += kSelThreads)
+                        c += p >= first && order_key(__ldcg(scores + p)) >= trial;
+                    c = block_sum(c, s_sum[flip]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < kListKeys; ++j) c += mine[j] >= trial;
+                    c = above_list + block_sum(c, s_sum[flip]);
+                }
                 flip ^= 1;
+                if (c == need) {  // exactly the keys from `trial` on: none at the border itself
+                    border = trial - 1;
+                    break;
+                }
+                if (c > need) {
+                    border = trial;
+                    inside = c - upper;
+                } else {
+                    inside -= c - upper;
+                    upper = c;
+                }
+                if (!listed && bit > 0 && inside <= kListKeys * kSelThreads) {
+                    // The few undecided keys, in any order, spread over the threads: from here on a
+                    // count costs a barrier, not a pass over the row.
+                    if (tid == 0) s_listed = 0;
+                    __syncthreads();
+                    auto push = [&](uint32_t x, bool cand) {
+                        const bool in = cand && x >= border && (x - border) < (1u << bit);
+                        const uint32_t mask = __ballot_sync(pkv::kFullMask, in);
+                        int at = 0;
+                        if (lane == 0 && mask) at = atomicAdd(&s_listed, __popc(mask));
+                        at = __shfl_sync(pkv::kFullMask, at, 0) + __popc(mask & ((1u << lane) - 1u));
+                        if (in) s_list[at] = x;
+                    };
+#pragma unroll
+                    for (int j = 0; j < KPT; ++j) {
+                        const int p = j * kSelThreads + tid;
+                        push(key[j], p >= first && p < last);
+                    }
+                    for (int p0 = KPT * kSelThreads; p0 < last; p0 += kSelThreads) {
+                        const int p = p0 + tid;
+                        const bool cand = p >= first && p < last;
+                        push(cand ? order_key(__ldcg(scores + p)) : 0u, cand);
+                    }
+                    __syncthreads();
+#pragma unroll
+                    for (int j = 0; j < kListKeys; ++j) mine[j] = j * kSelThreads + tid < s_listed ? s_list[j * kSelThreads + tid] : 0u;
+                    listed = true;
+                    above_list = upper;
+                }
             }
         } else {
             border = 0xffffffffu;  // above every key: nothing between the sinks and the recent ones
@@ -204,21 +257,27 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
             place += __popc(s_above[w]);
         }
         __syncthreads();
-        // Places and scores, kSelThreads positions at a time: a round's scores are read before the
-        // barrier and written after it, to places at or before their positions, so that new_scores
-        // may be scores itself.
-        for (int64_t j = 0; j < rounds; ++j) {
-            const int p = static_cast<int>(j * kSelThreads + tid);
-            const int w = static_cast<int>(j * kSelWarps + warp);
-            const uint32_t bits = w < words ? s_above[w] : 0u;
-            const bool keep = (bits >> lane) & 1u;
-            float x = 0.f;
-            if (keep) x = __ldcg(scores + p);
-            __syncthreads();
-            if (keep) {
-                const int i = static_cast<int>(s_at[w]) + __popc(bits & ((1u << lane) - 1u));
-                kept[i] = p;
-                out[i] = x;
+        // Places and scores, kRounds x kSelThreads positions at a time.  new_scores may be scores itself:
+        // places lie at or before their positions, so all of a step's scores are read before any of its
+        // places is written, and the next step reads behind every place written so far.
+        constexpr int kRounds = 8;
+        for (int64_t j0 = 0; j0 < rounds; j0 += kRounds) {
+            float x[kRounds];
+#pragma unroll
+            for (int u = 0; u < kRounds; ++u) {
+                const int w = static_cast<int>((j0 + u) * kSelWarps + warp);
+                if (w < words && (s_above[w] >> lane) & 1u) x[u] = __ldcg(scores + w * 32 + lane);
+            }
+            if (out == scores) __syncthreads();
+#pragma unroll
+            for (int u = 0; u < kRounds; ++u) {
+                const int w = static_cast<int>((j0 + u) * kSelWarps + warp);
+                const uint32_t bits = w < words ? s_above[w] : 0u;
+                if ((bits >> lane) & 1u) {
+                    const int i = static_cast<int>(s_at[w]) + __popc(bits & ((1u << lane) - 1u));
+                    kept[i] = w * 32 + lane;
+                    out[i] = x[u];
+                }
             }
         }
     } else {
@@ -232,26 +291,33 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
     for (int64_t p = m + tid; p < P.capacity; p += kSelThreads) out[p] = 0.f;
 }
 
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 __global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constant__ EvictParams P) {
+    __shared__ unsigned char *s_src[2][kMoveRows], *s_dst[2][kMoveRows];
     pkv::pdl_wait_primary();
     pkv::pdl_launch_dependents();
-    const int part = blockIdx.x % P.slices, h = blockIdx.y, b = blockIdx.z;
-    unsigned char *cache = static_cast<int>(blockIdx.x) < P.slices ? P.k_cache : P.v_cache;
+    const int tid = threadIdx.x;
+    const int rank = blockIdx.x % P.cluster, h = blockIdx.y, b = blockIdx.z;
+    unsigned char *cache = static_cast<int>(blockIdx.x) < P.cluster ? P.k_cache : P.v_cache;
     const int n = cached(P, b, false);
     int m = min(n, P.budget);
     if (m > P.max_new_blocks * P.block_size) {
-        if (threadIdx.x == 0 && blockIdx.x == 0 && h == 0) pkv::record_error(&g_evict_error, PKV_DEV_BAD_CONTEXT);
+        if (tid == 0 && blockIdx.x == 0 && h == 0) pkv::record_error(&g_evict_error, PKV_DEV_BAD_CONTEXT);
         m = P.max_new_blocks * P.block_size;
     }
     const int32_t *kept = P.kept + (static_cast<int64_t>(b) * P.num_kv_heads + h) * P.budget;
     const int32_t *from = P.block_tables + static_cast<int64_t>(b) * P.max_blocks;
     const int32_t *to = P.new_tables + static_cast<int64_t>(b) * P.max_new_blocks;
-    const int pieces = P.slice_pieces;
-    const int rows_at_once = kMoveThreads / pieces;  // pieces is a power of two
-    const int sub = threadIdx.x / pieces;
-    const int64_t byte = static_cast<int64_t>(part) * pieces * 16 + (threadIdx.x % pieces) * 16;
-    const int batch = kMoveBatch * rows_at_once;
-
+    // Rows can only be in one another's way in blocks that both tables name (at the same index).
+    bool shared = from == to;
+    if (!shared) {
+        const int blocks = min((m + P.block_size - 1) / P.block_size, P.max_blocks);
+        bool same = false;
+        for (int i = tid; i < blocks; i += kMoveThreads) same = same || __ldg(from + i) == __ldg(to + i);
+        shared = __syncthreads_or(same);
+    }
     auto address = [&](const int32_t *table, int p) -> unsigned char * {
         const int blk = p / P.block_size;
         const int32_t id = __ldg(table + blk);
@@ -260,40 +326,46 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constan
             return nullptr;
         }
         const int64_t r = (static_cast<int64_t>(id) * P.num_kv_heads + h) * P.block_size + (p - blk * P.block_size);
-        return cache + r * P.row_bytes + byte;
+        return cache + r * P.row_bytes;
     };
-    uint4 x[kMoveBatch];
-    unsigned char *dst[kMoveBatch];
-    auto load = [&](int i0, uint4(&v)[kMoveBatch], unsigned char *(&d)[kMoveBatch]) {
+    const int stride = P.cluster * kMoveRows;  // rows of the cluster's step
+    const int steps = (m + stride - 1) / stride;
+    auto locate = [&](int step) {  // one thread per row: where it is and where it goes (null: nowhere)
+        if (tid >= kMoveRows) return;
+        const int i = step * stride + rank * kMoveRows + tid;
+        unsigned char *s = nullptr, *d = nullptr;
+        if (i < m) {
+            s = address(from, __ldg(kept + i));
+            d = address(to, i);
+            if (s == nullptr || s == d) d = nullptr;  // a bad block, or the row is where it belongs
+        }
+        s_src[step & 1][tid] = s;
+        s_dst[step & 1][tid] = d;
+    };
+    const int row = tid / kRowLanes, byte = tid % kRowLanes * 16;
+    locate(0);
+    __syncthreads();
+    for (int step = 0; step < steps; ++step) {
+        uint4 x[kMoveBatch];
+        unsigned char *dst[kMoveBatch];
 #pragma unroll
         for (int u = 0; u < kMoveBatch; ++u) {
-            const int i = i0 + u * rows_at_once + sub;
-            d[u] = nullptr;
-            if (i >= m) continue;
-            const int p = __ldg(kept + i);
-            unsigned char *s = address(from, p);
-            d[u] = address(to, i);
-            if (s == nullptr || s == d[u]) d[u] = nullptr;  // a bad block, or the row is where it belongs
-            if (d[u] != nullptr) v[u] = __ldcg(reinterpret_cast<const uint4 *>(s));
+            const int i = u * (kMoveThreads / kRowLanes) + row;
+            dst[u] = s_dst[step & 1][i];
+            if (dst[u] != nullptr) x[u] = __ldcg(reinterpret_cast<const uint4 *>(s_src[step & 1][i] + byte));
         }
-    };
-    load(0, x, dst);
-    for (int i0 = 0; i0 < m; i0 += batch) {
-        uint4 y[kMoveBatch];
-        unsigned char *next[kMoveBatch];
-        load(i0 + batch, y, next);
-        __syncthreads();  // every row of this batch has been read
+        if (step + 1 < steps) locate(step + 1);
+        if (shared) {  // every row of the cluster's step has been read before any is written
+            cluster_arrive();
+            cluster_wait();
+        }
 #pragma unroll
         for (int u = 0; u < kMoveBatch; ++u)
-            if (dst[u] != nullptr) *reinterpret_cast<uint4 *>(dst[u]) = x[u];
-#pragma unroll
-        for (int u = 0; u < kMoveBatch; ++u) {
-            x[u] = y[u];
-            dst[u] = next[u];
-        }
+            if (dst[u] != nullptr) *reinterpret_cast<uint4 *>(dst[u] + byte) = x[u];
+        __syncthreads();  // the next step's rows are located
     }
     // new_lens may be context_lens: the other CTAs' min(n, budget) is the same from either value
-    if (threadIdx.x == 0 && blockIdx.x == 0 && h == 0) P.new_lens[b] = min(n, P.budget);
+    if (tid == 0 && blockIdx.x == 0 && h == 0) P.new_lens[b] = min(n, P.budget);
 }
 
 template <int KPT>
@@ -362,11 +434,12 @@ extern "C" PKV_API int pkv_evict(void *k_cache, void *v_cache, int32_t *kept, fl
     p.budget = budget;
     p.recent = recent;
     p.sinks = sinks;
-    // Slices of a row: halved from 256 bytes to no less than one 32-byte sector while the grid is
-    // under two CTAs per SM.
-    p.slices = 1;
-    while (p.slices < 8 && static_cast<int64_t>(num_seqs) * num_kv_heads * 2 * p.slices < 2 * sms) p.slices *= 2;
-    p.slice_pieces = p.row_bytes / 16 / p.slices;
+    // CTAs per cluster: doubled, to at most eight, while the grid has fewer than three CTAs per SM and
+    // the kept rows fill a step of the larger cluster.
+    p.cluster = 1;
+    while (p.cluster < 8 && static_cast<int64_t>(num_seqs) * num_kv_heads * 2 * p.cluster < 3 * sms &&
+           budget >= 2 * p.cluster * kMoveRows)
+        p.cluster *= 2;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
@@ -378,11 +451,16 @@ extern "C" PKV_API int pkv_evict(void *k_cache, void *v_cache, int32_t *kept, fl
                                : launch_select<32>(p, num_seqs, smem, s, &attr);
     if (st != PKV_OK) return st;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(2 * p.slices, num_kv_heads, num_seqs);
+    cfg.gridDim = dim3(2 * p.cluster, num_kv_heads, num_seqs);
     cfg.blockDim = dim3(kMoveThreads);
     cfg.stream = s;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cudaLaunchAttribute attrs[2] = {attr, {}};
+    attrs[1].id = cudaLaunchAttributeClusterDimension;
+    attrs[1].val.clusterDim.x = p.cluster;
+    attrs[1].val.clusterDim.y = 1;
+    attrs[1].val.clusterDim.z = 1;
+    cfg.attrs = attrs;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, move_kernel, p) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 

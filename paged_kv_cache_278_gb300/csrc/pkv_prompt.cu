@@ -49,7 +49,8 @@ constexpr int kSlab = kTileRows * 128;     // 128 rows x 64 fp16 dims, 128-byte 
 constexpr int kOperand = 2 * kSlab;        // a whole 128 x 128 fp16 operand tile
 constexpr int kRing = 4;                   // K/V stages
 constexpr int kSoftmaxWarps = 8;
-constexpr int kPromptThreads = 32 * (kSoftmaxWarps + 2);
+constexpr int kPromptThreads = 32 * (kSoftmaxWarps + 4);  // three warpgroups; the last has two idle warps
+constexpr int kSoftmaxRegs = 200, kOtherRegs = 88;  // launch: 384 x 168 = 64,512 registers; 256 x 200 + 128 x 88 = 62,464
 constexpr int kMmaWarp = kSoftmaxWarps, kLoadWarp = kSoftmaxWarps + 1;
 constexpr float kLazy = 8.0f;              // log2 units
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -84,7 +85,7 @@ struct PromptSmem {
     static constexpr int q = 0;                              // two operand tiles
     static constexpr int ring = 2 * kOperand;
     static constexpr int bars = ring + kRing * kOperand;
-    static constexpr int n_bars = 2 * kRing + 2 + 4 + 6 + 1;
+    static constexpr int n_bars = 2 * kRing + 2 + 4 + 8 + 1;
     static constexpr int tmem_slot = bars + n_bars * 8;
     static constexpr int items = (tmem_slot + 4 + 15) / 16 * 16;
     static constexpr int total = items + 2 * static_cast<int>(sizeof(Item));
@@ -93,35 +94,78 @@ struct PromptSmem {
 // Barriers by index.
 constexpr int kBarKvFull = 0, kBarKvEmpty = kRing, kBarQFull = 2 * kRing, kBarQEmpty = kBarQFull + 1,
               kBarItemFull = kBarQEmpty + 1, kBarItemEmpty = kBarItemFull + 2, kBarS = kBarItemEmpty + 2, kBarP = kBarS + 2,
-              kBarO = kBarP + 2, kBarDrain = kBarO + 2;
+              kBarO = kBarP + 4, kBarDrain = kBarO + 2;
 
 // ---- TMEM moves (one row per lane, consecutive 32-bit columns)
-__device__ __forceinline__ void tmem_ld128(uint32_t taddr, uint32_t (&r)[128]) {
+// The load is asynchronous: its registers may be used after tmem_landed on them.
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64]) {
 #define PKV_R8(i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x128.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
         "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
         "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
-        "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63, "
-        "%64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, "
-        "%80, %81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95, "
-        "%96, %97, %98, %99, %100, %101, %102, %103, %104, %105, %106, %107, %108, %109, %110, %111, "
-        "%112, %113, %114, %115, %116, %117, %118, %119, %120, %121, %122, %123, %124, %125, %126, %127}, [%128];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : PKV_R8(0), PKV_R8(8), PKV_R8(16), PKV_R8(24), PKV_R8(32), PKV_R8(40), PKV_R8(48), PKV_R8(56), PKV_R8(64),
-          PKV_R8(72), PKV_R8(80), PKV_R8(88), PKV_R8(96), PKV_R8(104), PKV_R8(112), PKV_R8(120)
+        "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];"
+        : PKV_R8(0), PKV_R8(8), PKV_R8(16), PKV_R8(24), PKV_R8(32), PKV_R8(40), PKV_R8(48), PKV_R8(56)
         : "r"(taddr)
         : "memory");
 #undef PKV_R8
 }
+// Waits for every load issued so far and ties it to these registers, so that no use moves ahead of it.
+__device__ __forceinline__ void tmem_landed(uint32_t (&r)[64]) {
+#define PKV_R8(i) "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7])
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : PKV_R8(0), PKV_R8(8), PKV_R8(16), PKV_R8(24), PKV_R8(32), PKV_R8(40), PKV_R8(48), PKV_R8(56)
+                 :
+                 : "memory");
+#undef PKV_R8
+}
 
-// 32 columns out of registers; completed by tmem_wait_st.
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+// (a0, a1) * (b, b) + (c, c) and (a0, a1) + (b0, b1): packed two-lane float32, each lane rounded as the scalar form.
+__device__ __forceinline__ float2 fma2s(uint32_t a0, uint32_t a1, float b, float c) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rc;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %4};\n\tmov.b64 rc, {%5, %5};\n\t"
+        "fma.rn.f32x2 rc, ra, rb, rc;\n\tmov.b64 {%0, %1}, rc;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "r"(a0), "r"(a1), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float2 fma2v(uint32_t a0, uint32_t a1, float b, float c0, float c1) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rc;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %4};\n\tmov.b64 rc, {%5, %6};\n\t"
+        "fma.rn.f32x2 rc, ra, rb, rc;\n\tmov.b64 {%0, %1}, rc;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "r"(a0), "r"(a1), "f"(b), "f"(c0), "f"(c1));
+    return d;
+}
+__device__ __forceinline__ void add2(float2 &d, float b0, float b1) {
+    asm("{\n\t.reg .b64 ra, rb;\n\tmov.b64 ra, {%0, %1};\n\tmov.b64 rb, {%2, %3};\n\tadd.rn.f32x2 ra, ra, rb;\n\t"
+        "mov.b64 {%0, %1}, ra;\n\t}"
+        : "+f"(d.x), "+f"(d.y)
+        : "f"(b0), "f"(b1));
+}
+
+template <int N>
+__device__ __forceinline__ void grow_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void shrink_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// 16 columns into registers (waited for), and out of registers (completed by tmem_wait_st).
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+#define PKV_R8(i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : PKV_R8(0), PKV_R8(8)
+        : "r"(taddr)
+        : "memory");
+#undef PKV_R8
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
 #define PKV_R8(i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]), "r"(r[i + 6]), "r"(r[i + 7])
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-        PKV_R8(0), PKV_R8(8), PKV_R8(16), PKV_R8(24)
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(
+            taddr),
+        PKV_R8(0), PKV_R8(8)
         : "memory");
 #undef PKV_R8
 }
@@ -247,7 +291,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
         for (int i = 0; i < PromptSmem::n_bars; ++i) {
             uint32_t count = 1;
             if (i == kBarItemEmpty || i == kBarItemEmpty + 1) count = kSoftmaxWarps + 1;
-            if (i == kBarP || i == kBarP + 1) count = 4;  // one arrival per softmax warp of the tile
+            if (i >= kBarP && i < kBarP + 4) count = 4;  // one arrival per softmax warp of the tile
             pkv::mbar_init(bar(i), count);
         }
         pkv::fence_mbar_init();
@@ -271,176 +315,185 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
         return false;
     };
 
-    if (warp == kLoadWarp) {
-        // ---------------------------------------------------------------- items and tensor copies
-        const int pairs = pairs_from(P, 0, 2 * tile_tokens, lane, blockIdx.x == 0);
-        const int64_t n_items = static_cast<int64_t>(pairs) * P.num_kv_heads * P.splits;
-        const int boxes_per_tile = PAGED ? kTileRows / P.box_rows : 1;
-        uint32_t stage = 0, loaded = 0;  // K/V stages filled, items with keys (one Q each)
-        bool ok = true;
-        for (uint32_t k = 0; ok; ++k) {
-            // alternating direction: a CTA's items are not always the longest of their round
-            const int64_t index = static_cast<int64_t>(k) * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-            Item it{};
-            it.seq = -1;
-            if (index < n_items) it = find_item(P, index, lane);
-            const int slot = k & 1;
-            if (!(ok = wait(kBarItemEmpty + slot, (k >> 1) + 1))) break;
-            if (lane == 0) {
-                volatile int *d = reinterpret_cast<volatile int *>(slots + slot);
-                const int *s = reinterpret_cast<const int *>(&it);
-#pragma unroll
-                for (int i = 0; i < static_cast<int>(sizeof(Item) / 4); ++i) d[i] = s[i];
-                mbar_arrive(bar(kBarItemFull + slot));
-            }
-            __syncwarp();
-            if (it.seq < 0) break;
-            const int n_kv = max(it.kv_count[0], it.kv_count[1]);
-            if (n_kv == 0) continue;
-            if (!(ok = wait(kBarQEmpty, loaded + 1))) break;
-            ++loaded;
-            if (lane == 0) {
-                const int tiles = it.live[1] > 0 ? 2 : 1;
-                pkv::mbar_arrive_expect_tx(bar(kBarQFull), tiles * kOperand);
-                for (int t = 0; t < tiles; ++t)
-                    for (int half = 0; half < 2; ++half)
-                        pkv::tma_load_3d(base + PromptSmem::q + t * kOperand + half * kSlab, &P.tmap_q, 64 * half, it.kvh << glog,
-                                         it.row0 + t * tile_tokens, bar(kBarQFull));
-            }
-            __syncwarp();
-            // The cache row at which this lane's box of a key tile starts (lane = 2 x box + half).
-            auto box_row = [&](int tile) -> int {
-                const int key = tile * kTileRows + (lane >> 1) * P.box_rows;
-                if (lane >= 2 * boxes_per_tile || key >= it.keys) return 0;
-                int32_t id = __ldg(P.block_tables + static_cast<int64_t>(it.seq) * P.max_blocks + key / P.block_size);
-                if (id < 0 || id >= P.num_blocks) {
-                    pkv::record_error(&g_prompt_error, PKV_DEV_BAD_BLOCK_ID);
-                    id = 0;
-                }
-                return static_cast<int>((static_cast<int64_t>(id) * P.num_kv_heads + it.kvh) * P.block_size + key % P.block_size);
-            };
-            int row = PAGED ? box_row(it.kv_first) : 0;
-            for (int j = 0; j < n_kv && ok; ++j) {
-                const int tile = it.kv_first + j;
-                const int next = PAGED && j + 1 < n_kv ? box_row(tile + 1) : 0;
-                const int valid = min(kTileRows, it.keys - tile * kTileRows);
-                for (int kv = 0; kv < 2; ++kv) {
-                    const int st = stage % kRing;
-                    if (!(ok = wait(kBarKvEmpty + st, stage / kRing + 1))) break;
-                    ++stage;
-                    const uint32_t dst = base + PromptSmem::ring + st * kOperand, full = bar(kBarKvFull + st);
-                    const void *map = kv ? static_cast<const void *>(&P.tmap_v) : static_cast<const void *>(&P.tmap_k);
-                    if (PAGED) {
-                        const int boxes = (valid + P.box_rows - 1) / P.box_rows;
-                        if (lane == 0) pkv::mbar_arrive_expect_tx(full, boxes * P.box_rows * 256);
-                        __syncwarp();
-                        if (lane < 2 * boxes)
-                            pkv::tma_load_2d(dst + (lane & 1) * kSlab + (lane >> 1) * P.box_rows * 128, map, 64 * (lane & 1), row, full);
-                    } else if (lane == 0) {  // rows past the sequence are the next one's, past the tensor zeros
-                        pkv::mbar_arrive_expect_tx(full, kOperand);
-                        for (int half = 0; half < 2; ++half)
-                            pkv::tma_load_2d(dst + half * kSlab, map, it.kvh * kDim + 64 * half, it.row0 - it.pos0 + tile * kTileRows,
-                                             full);
-                    }
-                    __syncwarp();
-                }
-                row = next;
-            }
-        }
-        if (!ok) {  // copies still in flight land before the CTA's memory goes (bounded)
-            if (loaded) pkv::mbar_wait_bounded(bar(kBarQFull), (loaded - 1) & 1);
-            for (uint32_t s = stage > kRing ? stage - kRing : 0; s < stage; ++s)
-                pkv::mbar_wait_bounded(bar(kBarKvFull + s % kRing), (s / kRing) & 1);
-        }
-    } else if (warp == kMmaWarp) {
-        // ---------------------------------------------------------------- tensor-core issue
-        constexpr uint32_t kIdescPV = pkv::umma_idesc_f16_f32(kTileRows, kDim) | (1u << 16);  // V: MN-major
-        uint32_t stage = 0, loaded = 0, p_count[2] = {0, 0};
-        bool ok = true;
-        for (uint32_t k = 0; ok; ++k) {
-            const int slot = k & 1;
-            if (!(ok = wait(kBarItemFull + slot, k >> 1))) break;
-            const int seq = slots[slot].seq, keys = slots[slot].keys, first = slots[slot].kv_first;
-            const int n[2] = {slots[slot].kv_count[0], slots[slot].kv_count[1]};
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kBarItemEmpty + slot));
-            if (seq < 0) break;
-            const int n_kv = max(n[0], n[1]);
-            if (n_kv == 0) continue;  // an empty split
-            // 16-key groups of key tile j that hold cached keys
-            auto groups_of = [&](int j) { return (min(kTileRows, keys - (first + j) * kTileRows) + 15) / 16; };
-            auto qk = [&](int t, uint32_t st, int groups) {
+    if (warp >= kSoftmaxWarps) {
+        shrink_registers<kOtherRegs>();
+        if (warp == kLoadWarp) {
+            // ---------------------------------------------------------------- items and tensor copies
+            const int pairs = pairs_from(P, 0, 2 * tile_tokens, lane, blockIdx.x == 0);
+            const int64_t n_items = static_cast<int64_t>(pairs) * P.num_kv_heads * P.splits;
+            const int boxes_per_tile = PAGED ? kTileRows / P.box_rows : 1;
+            uint32_t stage = 0, loaded = 0;  // K/V stages filled, items with keys (one Q each)
+            bool ok = true;
+            for (uint32_t k = 0; ok; ++k) {
+                // alternating direction: a CTA's items are not always the longest of their round
+                const int64_t index = static_cast<int64_t>(k) * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+                Item it{};
+                it.seq = -1;
+                if (index < n_items) it = find_item(P, index, lane);
+                const int slot = k & 1;
+                if (!(ok = wait(kBarItemEmpty + slot, (k >> 1) + 1))) break;
                 if (lane == 0) {
-                    const uint32_t q = base + PromptSmem::q + t * kOperand, kk = base + PromptSmem::ring + (st % kRing) * kOperand;
-                    const uint32_t idesc = pkv::umma_idesc_f16_f32(kTileRows, groups * 16);
-#pragma unroll
-                    for (int ks = 0; ks < kDim / 16; ++ks) {
-                        const uint32_t off = (ks >> 2) * kSlab + (ks & 3) * 32;
-                        pkv::umma_f16(tmem + t * kTileRows, pkv::umma_desc_k_sw128(q + off), pkv::umma_desc_k_sw128(kk + off), idesc,
-                                      ks > 0);
-                    }
-                    pkv::umma_commit(bar(kBarS + t));
+                    volatile int *d = reinterpret_cast<volatile int *>(slots + slot);
+                    const int *s = reinterpret_cast<const int *>(&it);
+    #pragma unroll
+                    for (int i = 0; i < static_cast<int>(sizeof(Item) / 4); ++i) d[i] = s[i];
+                    mbar_arrive(bar(kBarItemFull + slot));
                 }
                 __syncwarp();
-            };
-            auto commit = [&](int b) {
-                if (lane == 0) pkv::umma_commit(bar(b));
+                if (it.seq < 0) break;
+                const int n_kv = max(it.kv_count[0], it.kv_count[1]);
+                if (n_kv == 0) continue;
+                if (!(ok = wait(kBarQEmpty, loaded + 1))) break;
+                ++loaded;
+                if (lane == 0) {
+                    const int tiles = it.live[1] > 0 ? 2 : 1;
+                    pkv::mbar_arrive_expect_tx(bar(kBarQFull), tiles * kOperand);
+                    for (int t = 0; t < tiles; ++t)
+                        for (int half = 0; half < 2; ++half)
+                            pkv::tma_load_3d(base + PromptSmem::q + t * kOperand + half * kSlab, &P.tmap_q, 64 * half, it.kvh << glog,
+                                             it.row0 + t * tile_tokens, bar(kBarQFull));
+                }
                 __syncwarp();
-            };
-            if (!(ok = wait(kBarQFull, loaded))) break;
-            ++loaded;
-            if (!(ok = wait(kBarKvFull + stage % kRing, stage / kRing))) break;
-            pkv::tmem_fence_after_sync();
-            for (int t = 0; t < 2; ++t)
-                if (n[t] > 0) qk(t, stage, groups_of(0));
-            commit(kBarKvEmpty + stage % kRing);
-            if (n_kv == 1) commit(kBarQEmpty);
-            ++stage;
-            for (int j = 0; j < n_kv && ok; ++j) {
-                const uint32_t v_stage = stage, k_stage = stage + 1;
-                const bool more = j + 1 < n_kv;
-                if (!(ok = wait(kBarKvFull + v_stage % kRing, v_stage / kRing))) break;
-                const uint32_t v = base + PromptSmem::ring + (v_stage % kRing) * kOperand;
-                const int groups = groups_of(j);
-                const int valid = min(kTileRows, keys - (first + j) * kTileRows);
-                if (valid < groups * 16) {  // V rows past the context: their weights are 0, their values may be anything
-                    for (int x = lane; x < (groups * 16 - valid) * 16; x += 32)
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v + ((x >> 3) & 1) * kSlab +
-                                                                                 (valid + (x >> 4)) * 128 + (x & 7) * 16),
-                                     "r"(0)
-                                     : "memory");
-                    pkv::fence_proxy_async_smem();
-                    __syncwarp();
-                }
-                if (more && !(ok = wait(kBarKvFull + k_stage % kRing, k_stage / kRing))) break;
-                for (int t = 0; t < 2 && ok; ++t) {
-                    if (j >= n[t]) continue;
-                    if (!(ok = wait(kBarP + t, p_count[t]))) break;
-                    ++p_count[t];
-                    pkv::tmem_fence_after_sync();
-                    if (lane == 0) {
-                        for (int g = 0; g < groups; ++g)
-                            umma_f16_ta(tmem + 2 * kTileRows + t * kDim, tmem + t * kTileRows + g * 8,
-                                        pkv::umma_desc_mn_sw128(v + g * 2048, kSlab, 1024), kIdescPV, j > 0 || g > 0);
-                        if (j + 1 == n[t]) pkv::umma_commit(bar(kBarO + t));
+                // The cache row at which this lane's box of a key tile starts (lane = 2 x box + half).
+                auto box_row = [&](int tile) -> int {
+                    const int key = tile * kTileRows + (lane >> 1) * P.box_rows;
+                    if (lane >= 2 * boxes_per_tile || key >= it.keys) return 0;
+                    int32_t id = __ldg(P.block_tables + static_cast<int64_t>(it.seq) * P.max_blocks + key / P.block_size);
+                    if (id < 0 || id >= P.num_blocks) {
+                        pkv::record_error(&g_prompt_error, PKV_DEV_BAD_BLOCK_ID);
+                        id = 0;
                     }
-                    __syncwarp();
-                    if (j + 1 < n[t]) qk(t, k_stage, groups_of(j + 1));
+                    return static_cast<int>((static_cast<int64_t>(id) * P.num_kv_heads + it.kvh) * P.block_size + key % P.block_size);
+                };
+                int row = PAGED ? box_row(it.kv_first) : 0;
+                for (int j = 0; j < n_kv && ok; ++j) {
+                    const int tile = it.kv_first + j;
+                    const int next = PAGED && j + 1 < n_kv ? box_row(tile + 1) : 0;
+                    const int valid = min(kTileRows, it.keys - tile * kTileRows);
+                    for (int kv = 0; kv < 2; ++kv) {
+                        const int st = stage % kRing;
+                        if (!(ok = wait(kBarKvEmpty + st, stage / kRing + 1))) break;
+                        ++stage;
+                        const uint32_t dst = base + PromptSmem::ring + st * kOperand, full = bar(kBarKvFull + st);
+                        const void *map = kv ? static_cast<const void *>(&P.tmap_v) : static_cast<const void *>(&P.tmap_k);
+                        if (PAGED) {
+                            const int boxes = (valid + P.box_rows - 1) / P.box_rows;
+                            if (lane == 0) pkv::mbar_arrive_expect_tx(full, boxes * P.box_rows * 256);
+                            __syncwarp();
+                            if (lane < 2 * boxes)
+                                pkv::tma_load_2d(dst + (lane & 1) * kSlab + (lane >> 1) * P.box_rows * 128, map, 64 * (lane & 1), row, full);
+                        } else if (lane == 0) {  // rows past the sequence are the next one's, past the tensor zeros
+                            pkv::mbar_arrive_expect_tx(full, kOperand);
+                            for (int half = 0; half < 2; ++half)
+                                pkv::tma_load_2d(dst + half * kSlab, map, it.kvh * kDim + 64 * half, it.row0 - it.pos0 + tile * kTileRows,
+                                                 full);
+                        }
+                        __syncwarp();
+                    }
+                    row = next;
                 }
-                if (!ok) break;
-                commit(kBarKvEmpty + v_stage % kRing);
-                if (more) commit(kBarKvEmpty + k_stage % kRing);
-                if (j + 2 == n_kv) commit(kBarQEmpty);  // the item's last Q K^T has been issued
-                stage += more ? 2 : 1;
             }
-        }
-        if (!ok) {  // MMAs in flight end before tensor memory is freed (bounded)
-            if (lane == 0) pkv::umma_commit(bar(kBarDrain));
-            __syncwarp();
-            pkv::mbar_wait_bounded(bar(kBarDrain), 0);
+            if (!ok) {  // copies still in flight land before the CTA's memory goes (bounded)
+                if (loaded) pkv::mbar_wait_bounded(bar(kBarQFull), (loaded - 1) & 1);
+                for (uint32_t s = stage > kRing ? stage - kRing : 0; s < stage; ++s)
+                    pkv::mbar_wait_bounded(bar(kBarKvFull + s % kRing), (s / kRing) & 1);
+            }
+        } else if (warp == kMmaWarp) {
+            // ---------------------------------------------------------------- tensor-core issue
+            constexpr uint32_t kIdescPV = pkv::umma_idesc_f16_f32(kTileRows, kDim) | (1u << 16);  // V: MN-major
+            uint32_t stage = 0, loaded = 0, p_count[2] = {0, 0};
+            bool ok = true;
+            for (uint32_t k = 0; ok; ++k) {
+                const int slot = k & 1;
+                if (!(ok = wait(kBarItemFull + slot, k >> 1))) break;
+                const int seq = slots[slot].seq, keys = slots[slot].keys, first = slots[slot].kv_first;
+                const int n[2] = {slots[slot].kv_count[0], slots[slot].kv_count[1]};
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(kBarItemEmpty + slot));
+                if (seq < 0) break;
+                const int n_kv = max(n[0], n[1]);
+                if (n_kv == 0) continue;  // an empty split
+                // 16-key groups of key tile j that hold cached keys
+                auto groups_of = [&](int j) { return (min(kTileRows, keys - (first + j) * kTileRows) + 15) / 16; };
+                auto qk = [&](int t, uint32_t st, int groups) {
+                    if (lane == 0) {
+                        const uint32_t q = base + PromptSmem::q + t * kOperand, kk = base + PromptSmem::ring + (st % kRing) * kOperand;
+                        const uint32_t idesc = pkv::umma_idesc_f16_f32(kTileRows, groups * 16);
+    #pragma unroll
+                        for (int ks = 0; ks < kDim / 16; ++ks) {
+                            const uint32_t off = (ks >> 2) * kSlab + (ks & 3) * 32;
+                            pkv::umma_f16(tmem + t * kTileRows, pkv::umma_desc_k_sw128(q + off), pkv::umma_desc_k_sw128(kk + off), idesc,
+                                          ks > 0);
+                        }
+                        pkv::umma_commit(bar(kBarS + t));
+                    }
+                    __syncwarp();
+                };
+                auto commit = [&](int b) {
+                    if (lane == 0) pkv::umma_commit(bar(b));
+                    __syncwarp();
+                };
+                if (!(ok = wait(kBarQFull, loaded))) break;
+                ++loaded;
+                if (!(ok = wait(kBarKvFull + stage % kRing, stage / kRing))) break;
+                pkv::tmem_fence_after_sync();
+                for (int t = 0; t < 2; ++t)
+                    if (n[t] > 0) qk(t, stage, groups_of(0));
+                commit(kBarKvEmpty + stage % kRing);
+                if (n_kv == 1) commit(kBarQEmpty);
+                ++stage;
+                for (int j = 0; j < n_kv && ok; ++j) {
+                    const uint32_t v_stage = stage, k_stage = stage + 1;
+                    const bool more = j + 1 < n_kv;
+                    if (!(ok = wait(kBarKvFull + v_stage % kRing, v_stage / kRing))) break;
+                    const uint32_t v = base + PromptSmem::ring + (v_stage % kRing) * kOperand;
+                    const int groups = groups_of(j);
+                    const int valid = min(kTileRows, keys - (first + j) * kTileRows);
+                    if (valid < groups * 16) {  // V rows past the context: their weights are 0, their values may be anything
+                        for (int x = lane; x < (groups * 16 - valid) * 16; x += 32)
+                            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v + ((x >> 3) & 1) * kSlab +
+                                                                                     (valid + (x >> 4)) * 128 + (x & 7) * 16),
+                                         "r"(0)
+                                         : "memory");
+                        pkv::fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                    if (more && !(ok = wait(kBarKvFull + k_stage % kRing, k_stage / kRing))) break;
+                    for (int t = 0; t < 2 && ok; ++t) {
+                        if (j >= n[t]) continue;
+                        for (int half = 0; half < 2 && ok; ++half) {  // keys 0-63 while the softmax finishes 64-127
+                            if (!(ok = wait(kBarP + 2 * t + half, p_count[t]))) break;
+                            pkv::tmem_fence_after_sync();
+                            if (lane == 0) {
+    #pragma unroll
+                                for (int g = 4 * half; g < 4 * half + 4; ++g)
+                                    if (g < groups)
+                                        umma_f16_ta(tmem + 2 * kTileRows + t * kDim, tmem + t * kTileRows + g * 8,
+                                                    pkv::umma_desc_mn_sw128(v + g * 2048, kSlab, 1024), kIdescPV, j > 0 || g > 0);
+                                if (half == 1 && j + 1 == n[t]) pkv::umma_commit(bar(kBarO + t));
+                            }
+                            __syncwarp();
+                        }
+                        if (!ok) break;
+                        ++p_count[t];
+                        if (j + 1 < n[t]) qk(t, k_stage, groups_of(j + 1));
+                    }
+                    if (!ok) break;
+                    commit(kBarKvEmpty + v_stage % kRing);
+                    if (more) commit(kBarKvEmpty + k_stage % kRing);
+                    if (j + 2 == n_kv) commit(kBarQEmpty);  // the item's last Q K^T has been issued
+                    stage += more ? 2 : 1;
+                }
+            }
+            if (!ok) {  // MMAs in flight end before tensor memory is freed (bounded)
+                if (lane == 0) pkv::umma_commit(bar(kBarDrain));
+                __syncwarp();
+                pkv::mbar_wait_bounded(bar(kBarDrain), 0);
+            }
         }
     } else {
         // ---------------------------------------------------------------- softmax and output of one tile
+        grow_registers<kSoftmaxRegs>();
         const int t = warp >> 2;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;  // this warp's TMEM lanes
         const uint32_t t_s = tmem + lanes + t * kTileRows, t_o = tmem + lanes + 2 * kTileRows + t * kDim;
@@ -464,18 +517,29 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                 if (!(ok = wait(kBarS + t, s_count))) break;
                 ++s_count;
                 pkv::tmem_fence_after_sync();
-                uint32_t s[128];
-                tmem_ld128(t_s, s);
+                uint32_t s0[64], s1[64];
+                tmem_ld64(t_s, s0);
+                tmem_landed(s0);
+                tmem_ld64(t_s + 64, s1);
                 const int key0 = (first + j) * kTileRows;
-                if (key0 + kTileRows - 1 > tile_pos) {  // the tile crosses the causal border (or the context's end)
-                    const int lim = pos - key0;
+                const bool border = key0 + kTileRows - 1 > tile_pos;  // the causal border, or the context's end
+                const int lim = pos - key0;
+                if (border) {
 #pragma unroll
-                    for (int c = 0; c < 128; ++c) s[c] = c <= lim ? s[c] : 0xff800000u;
+                    for (int c = 0; c < 64; ++c) s0[c] = c <= lim ? s0[c] : 0xff800000u;
                 }
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int c = 0; c < 128; c += 2)
-                    mx[(c >> 1) & 3] = fmaxf(fmaxf(mx[(c >> 1) & 3], __uint_as_float(s[c])), __uint_as_float(s[c + 1]));
+                for (int c = 0; c < 64; c += 2)
+                    mx[(c >> 1) & 3] = fmaxf(fmaxf(mx[(c >> 1) & 3], __uint_as_float(s0[c])), __uint_as_float(s0[c + 1]));
+                tmem_landed(s1);
+                if (border) {
+#pragma unroll
+                    for (int c = 0; c < 64; ++c) s1[c] = 64 + c <= lim ? s1[c] : 0xff800000u;
+                }
+#pragma unroll
+                for (int c = 0; c < 64; c += 2)
+                    mx[(c >> 1) & 3] = fmaxf(fmaxf(mx[(c >> 1) & 3], __uint_as_float(s1[c])), __uint_as_float(s1[c + 1]));
                 const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
                 if (__any_sync(pkv::kFullMask, top > m_ref + kLazy)) {
                     const float m_new = top > m_ref + kLazy ? top : m_ref;
@@ -485,36 +549,39 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                     m_ref = m_new;
                     if (j > 0) {  // P V of the earlier tiles has completed: S of this one was issued behind it
 #pragma unroll
-                        for (int c = 0; c < kDim; c += 32) {
-                            uint32_t o[32];
-                            pkv::tmem_ld32(t_o + c, o);
+                        for (int c = 0; c < kDim; c += 16) {
+                            uint32_t o[16];
+                            tmem_ld16(t_o + c, o);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                            tmem_st32(t_o + c, o);
+                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                            tmem_st16(t_o + c, o);
                         }
                     }
                 }
                 const float ms = m_ref == -INFINITY ? 0.f : m_ref;  // no visible key yet: weights exp2(-inf) = 0
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
+                auto weights = [&](const uint32_t(&x)[64], int half) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t p[32];
+                    for (int q = 0; q < 64; q += 32) {
+                        uint32_t p[16];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const float p0 = pkv::exp2_approx(fmaf(__uint_as_float(s[64 * h + 2 * i]), sc, -ms));
-                        const float p1 = pkv::exp2_approx(fmaf(__uint_as_float(s[64 * h + 2 * i + 1]), sc, -ms));
-                        sum[i & 1] += p0;
-                        sum[2 + (i & 1)] += p1;
-                        const __half2 pk = __floats2half2_rn(p0, p1);
-                        p[i] = *reinterpret_cast<const uint32_t *>(&pk);
+                        for (int i = 0; i < 16; ++i) {
+                            const float2 e = fma2s(x[q + 2 * i], x[q + 2 * i + 1], sc, -ms);
+                            const float p0 = pkv::exp2_approx(e.x), p1 = pkv::exp2_approx(e.y);
+                            add2(sum[i & 1], p0, p1);
+                            const __half2 pk = __floats2half2_rn(p0, p1);
+                            p[i] = *reinterpret_cast<const uint32_t *>(&pk);
+                        }
+                        tmem_st16(t_s + 32 * half + q / 2, p);
                     }
-                    tmem_st32(t_s + 32 * h, p);
-                }
-                tmem_wait_st();
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                pkv::tmem_fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(kBarP + t));
+                    tmem_wait_st();
+                    pkv::tmem_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(kBarP + 2 * t + half));
+                };
+                weights(s0, 0);
+                weights(s1, 1);
+                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             }
             if (!ok) break;
             if (n > 0) {
@@ -735,113 +802,117 @@ __global__ void __launch_bounds__(kPromptThreads, 1) chunk_weights_kernel(const 
         return false;
     };
 
-    if (warp == kLoadWarp) {
-        int tiles = 0;
-        for (int b = lane; b < P.num_seqs; b += 32) {
-            const Request r = request_of(P, b, blockIdx.x == 0);
-            tiles += r.tokens > 0 ? (r.keys + kTileRows - 1) / kTileRows : 0;
-        }
-        const int64_t n_items = static_cast<int64_t>(__reduce_add_sync(pkv::kFullMask, tiles)) * P.num_kv_heads;
-        const int boxes_per_tile = kTileRows / P.box_rows;
-        uint32_t rows = 0, k = 0;
-        bool ok = true;
-        for (; ok; ++k) {
-            const int64_t index = static_cast<int64_t>(k) * gridDim.x + blockIdx.x;
-            KeyItem it{};
-            it.seq = -1;
-            if (index < n_items) it = find_key_item(P, index, lane);
-            const int slot = k & 1;
-            if (!(ok = wait(kWItemEmpty + slot, (k >> 1) + 1))) break;
-            if (lane == 0) {
-                volatile int *d = reinterpret_cast<volatile int *>(slots + slot);
-                const int *s = reinterpret_cast<const int *>(&it);
-#pragma unroll
-                for (int i = 0; i < static_cast<int>(sizeof(KeyItem) / 4); ++i) d[i] = s[i];
-                mbar_arrive(bar(kWItemFull + slot));
+    if (warp >= kSoftmaxWarps) {
+        shrink_registers<kOtherRegs>();
+        if (warp == kLoadWarp) {
+            int tiles = 0;
+            for (int b = lane; b < P.num_seqs; b += 32) {
+                const Request r = request_of(P, b, blockIdx.x == 0);
+                tiles += r.tokens > 0 ? (r.keys + kTileRows - 1) / kTileRows : 0;
             }
-            __syncwarp();
-            if (it.seq < 0) break;
-            const int ks = k % kKeyStages;
-            if (!(ok = wait(kWKeyEmpty + ks, k / kKeyStages + 1))) break;
-            const int valid = min(kTileRows, it.keys - it.tile * kTileRows);
-            const int boxes = (valid + P.box_rows - 1) / P.box_rows;
-            if (lane == 0) pkv::mbar_arrive_expect_tx(bar(kWKeyFull + ks), boxes * P.box_rows * 256);
-            __syncwarp();
-            if (lane < 2 * boxes && lane < 2 * boxes_per_tile) {
-                const int key = it.tile * kTileRows + (lane >> 1) * P.box_rows;
-                int32_t id = __ldg(P.block_tables + static_cast<int64_t>(it.seq) * P.max_blocks + key / P.block_size);
-                if (id < 0 || id >= P.num_blocks) {
-                    pkv::record_error(&g_prompt_error, PKV_DEV_BAD_BLOCK_ID);
-                    id = 0;
-                }
-                const int64_t row = (static_cast<int64_t>(id) * P.num_kv_heads + it.kvh) * P.block_size + key % P.block_size;
-                pkv::tma_load_2d(base + L::keys + ks * kOperand + (lane & 1) * kSlab + (lane >> 1) * P.box_rows * 128, &P.tmap_k,
-                                 64 * (lane & 1), static_cast<int>(row), bar(kWKeyFull + ks));
-            }
-            __syncwarp();
-            for (int i = it.first; i < it.count; ++i) {
-                const int st = rows % kRowRing;
-                if (!(ok = wait(kWRowEmpty + st, rows / kRowRing + 1))) break;
-                ++rows;
+            const int64_t n_items = static_cast<int64_t>(__reduce_add_sync(pkv::kFullMask, tiles)) * P.num_kv_heads;
+            const int boxes_per_tile = kTileRows / P.box_rows;
+            uint32_t rows = 0, k = 0;
+            bool ok = true;
+            for (; ok; ++k) {
+                const int64_t index = static_cast<int64_t>(k) * gridDim.x + blockIdx.x;
+                KeyItem it{};
+                it.seq = -1;
+                if (index < n_items) it = find_key_item(P, index, lane);
+                const int slot = k & 1;
+                if (!(ok = wait(kWItemEmpty + slot, (k >> 1) + 1))) break;
                 if (lane == 0) {
-                    pkv::mbar_arrive_expect_tx(bar(kWRowFull + st), kOperand);
-                    for (int half = 0; half < 2; ++half)
-                        pkv::tma_load_3d(base + L::rows + st * kOperand + half * kSlab, &P.tmap_q, 64 * half, it.kvh << glog,
-                                         it.start + i * tile_tokens, bar(kWRowFull + st));
+                    volatile int *d = reinterpret_cast<volatile int *>(slots + slot);
+                    const int *s = reinterpret_cast<const int *>(&it);
+    #pragma unroll
+                    for (int i = 0; i < static_cast<int>(sizeof(KeyItem) / 4); ++i) d[i] = s[i];
+                    mbar_arrive(bar(kWItemFull + slot));
                 }
                 __syncwarp();
-            }
-        }
-        if (!ok) {  // copies still in flight land before the CTA's memory goes (bounded)
-            for (uint32_t s = k > kKeyStages ? k - kKeyStages : 0; s <= k; ++s)
-                pkv::mbar_wait_bounded(bar(kWKeyFull + s % kKeyStages), (s / kKeyStages) & 1);
-            for (uint32_t s = rows > kRowRing ? rows - kRowRing : 0; s < rows; ++s)
-                pkv::mbar_wait_bounded(bar(kWRowFull + s % kRowRing), (s / kRowRing) & 1);
-        }
-    } else if (warp == kMmaWarp) {
-        uint32_t rows = 0;
-        uint32_t used[4] = {0, 0, 0, 0};  // times each S^T buffer has been filled
-        bool ok = true;
-        for (uint32_t k = 0; ok; ++k) {
-            const int slot = k & 1;
-            if (!(ok = wait(kWItemFull + slot, k >> 1))) break;
-            const int seq = slots[slot].seq, first = slots[slot].first, count = slots[slot].count;
-            const int all_rows = slots[slot].tokens << glog;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kWItemEmpty + slot));
-            if (seq < 0) break;
-            const int ks = k % kKeyStages;
-            if (!(ok = wait(kWKeyFull + ks, k / kKeyStages))) break;
-            for (int i = first; i < count; ++i, ++rows) {
-                const int st = rows % kRowRing, buf = i & 3;
-                if (!(ok = wait(kWRowFull + st, rows / kRowRing))) break;
-                uint32_t fills = 0;
-#pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    if (u == buf) fills = used[u]++;
-                if (!(ok = wait(kWSFree + buf, fills + 1))) break;
-                pkv::tmem_fence_after_sync();
-                if (lane == 0) {
-                    const uint32_t a = base + L::keys + ks * kOperand, b = base + L::rows + st * kOperand;
-                    const uint32_t idesc = pkv::umma_idesc_f16_f32(kTileRows, (min(kTileRows, all_rows - i * kTileRows) + 15) / 16 * 16);
-#pragma unroll
-                    for (int x = 0; x < kDim / 16; ++x) {
-                        const uint32_t off = (x >> 2) * kSlab + (x & 3) * 32;
-                        pkv::umma_f16(tmem + buf * kTileRows, pkv::umma_desc_k_sw128(a + off), pkv::umma_desc_k_sw128(b + off), idesc, x > 0);
+                if (it.seq < 0) break;
+                const int ks = k % kKeyStages;
+                if (!(ok = wait(kWKeyEmpty + ks, k / kKeyStages + 1))) break;
+                const int valid = min(kTileRows, it.keys - it.tile * kTileRows);
+                const int boxes = (valid + P.box_rows - 1) / P.box_rows;
+                if (lane == 0) pkv::mbar_arrive_expect_tx(bar(kWKeyFull + ks), boxes * P.box_rows * 256);
+                __syncwarp();
+                if (lane < 2 * boxes && lane < 2 * boxes_per_tile) {
+                    const int key = it.tile * kTileRows + (lane >> 1) * P.box_rows;
+                    int32_t id = __ldg(P.block_tables + static_cast<int64_t>(it.seq) * P.max_blocks + key / P.block_size);
+                    if (id < 0 || id >= P.num_blocks) {
+                        pkv::record_error(&g_prompt_error, PKV_DEV_BAD_BLOCK_ID);
+                        id = 0;
                     }
-                    pkv::umma_commit(bar(kWS + buf));
-                    pkv::umma_commit(bar(kWRowEmpty + st));
-                    if (i + 1 == count) pkv::umma_commit(bar(kWKeyEmpty + ks));
+                    const int64_t row = (static_cast<int64_t>(id) * P.num_kv_heads + it.kvh) * P.block_size + key % P.block_size;
+                    pkv::tma_load_2d(base + L::keys + ks * kOperand + (lane & 1) * kSlab + (lane >> 1) * P.box_rows * 128, &P.tmap_k,
+                                     64 * (lane & 1), static_cast<int>(row), bar(kWKeyFull + ks));
                 }
                 __syncwarp();
+                for (int i = it.first; i < it.count; ++i) {
+                    const int st = rows % kRowRing;
+                    if (!(ok = wait(kWRowEmpty + st, rows / kRowRing + 1))) break;
+                    ++rows;
+                    if (lane == 0) {
+                        pkv::mbar_arrive_expect_tx(bar(kWRowFull + st), kOperand);
+                        for (int half = 0; half < 2; ++half)
+                            pkv::tma_load_3d(base + L::rows + st * kOperand + half * kSlab, &P.tmap_q, 64 * half, it.kvh << glog,
+                                             it.start + i * tile_tokens, bar(kWRowFull + st));
+                    }
+                    __syncwarp();
+                }
             }
-        }
-        if (!ok) {  // MMAs in flight end before tensor memory is freed (bounded)
-            if (lane == 0) pkv::umma_commit(bar(kWDrain));
-            __syncwarp();
-            pkv::mbar_wait_bounded(bar(kWDrain), 0);
+            if (!ok) {  // copies still in flight land before the CTA's memory goes (bounded)
+                for (uint32_t s = k > kKeyStages ? k - kKeyStages : 0; s <= k; ++s)
+                    pkv::mbar_wait_bounded(bar(kWKeyFull + s % kKeyStages), (s / kKeyStages) & 1);
+                for (uint32_t s = rows > kRowRing ? rows - kRowRing : 0; s < rows; ++s)
+                    pkv::mbar_wait_bounded(bar(kWRowFull + s % kRowRing), (s / kRowRing) & 1);
+            }
+        } else if (warp == kMmaWarp) {
+            uint32_t rows = 0;
+            uint32_t used[4] = {0, 0, 0, 0};  // times each S^T buffer has been filled
+            bool ok = true;
+            for (uint32_t k = 0; ok; ++k) {
+                const int slot = k & 1;
+                if (!(ok = wait(kWItemFull + slot, k >> 1))) break;
+                const int seq = slots[slot].seq, first = slots[slot].first, count = slots[slot].count;
+                const int all_rows = slots[slot].tokens << glog;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(kWItemEmpty + slot));
+                if (seq < 0) break;
+                const int ks = k % kKeyStages;
+                if (!(ok = wait(kWKeyFull + ks, k / kKeyStages))) break;
+                for (int i = first; i < count; ++i, ++rows) {
+                    const int st = rows % kRowRing, buf = i & 3;
+                    if (!(ok = wait(kWRowFull + st, rows / kRowRing))) break;
+                    uint32_t fills = 0;
+    #pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        if (u == buf) fills = used[u]++;
+                    if (!(ok = wait(kWSFree + buf, fills + 1))) break;
+                    pkv::tmem_fence_after_sync();
+                    if (lane == 0) {
+                        const uint32_t a = base + L::keys + ks * kOperand, b = base + L::rows + st * kOperand;
+                        const uint32_t idesc = pkv::umma_idesc_f16_f32(kTileRows, (min(kTileRows, all_rows - i * kTileRows) + 15) / 16 * 16);
+    #pragma unroll
+                        for (int x = 0; x < kDim / 16; ++x) {
+                            const uint32_t off = (x >> 2) * kSlab + (x & 3) * 32;
+                            pkv::umma_f16(tmem + buf * kTileRows, pkv::umma_desc_k_sw128(a + off), pkv::umma_desc_k_sw128(b + off), idesc, x > 0);
+                        }
+                        pkv::umma_commit(bar(kWS + buf));
+                        pkv::umma_commit(bar(kWRowEmpty + st));
+                        if (i + 1 == count) pkv::umma_commit(bar(kWKeyEmpty + ks));
+                    }
+                    __syncwarp();
+                }
+            }
+            if (!ok) {  // MMAs in flight end before tensor memory is freed (bounded)
+                if (lane == 0) pkv::umma_commit(bar(kWDrain));
+                __syncwarp();
+                pkv::mbar_wait_bounded(bar(kWDrain), 0);
+            }
         }
     } else {
+        grow_registers<kSoftmaxRegs>();
         const int grp = warp >> 2;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const int key_lane = (warp & 3) * 32 + lane;  // this thread's key in the tile
@@ -858,8 +929,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) chunk_weights_kernel(const 
             if (seq < 0) break;
             const int key = tile * kTileRows + key_lane;
             const int rows = tokens << glog;
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
-            // lse of four neighbouring columns of row tile i, log2 units
+            float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
+            // minus the lse of four neighbouring columns of row tile i, log2 units
             auto column_lse = [&](int i) {
                 float z[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -868,7 +939,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) chunk_weights_kernel(const 
                     if (i < count && c < rows)
                         z[u] = __ldg(W.lse + (static_cast<int64_t>(start) + (c >> glog)) * P.num_q_heads + (kvh << glog) +
                                      (c & ((1 << glog) - 1))) *
-                               kLog2e;
+                               -kLog2e;
                 }
                 return make_float4(z[0], z[1], z[2], z[3]);
             };
@@ -885,37 +956,45 @@ __global__ void __launch_bounds__(kPromptThreads, 1) chunk_weights_kernel(const 
                     if (u == which) fills = seen[u]++;
                 if (!(ok = wait(kWS + buf, fills))) break;
                 pkv::tmem_fence_after_sync();
-                uint32_t s[128];
-                tmem_ld128(tmem + lanes + buf * kTileRows, s);
+                uint32_t s0[64], s1[64];
+                tmem_ld64(tmem + lanes + buf * kTileRows, s0);
+                tmem_ld64(tmem + lanes + buf * kTileRows + 64, s1);
+                tmem_landed(s0);
+                tmem_landed(s1);
                 pkv::tmem_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(kWSFree + buf));
                 const int pos0 = keys - tokens + i * tile_tokens;  // position of the tile's first row
                 if (pos0 >= (tile + 1) * kTileRows - 1 && rows - i * kTileRows >= kTileRows) {
+                    auto all = [&](const uint32_t(&x)[64], const float4 *lse4) {
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) {
-                        const float4 e = s_lse[c];
-                        sum[0] += pkv::exp2_approx(fmaf(__uint_as_float(s[4 * c]), sc, -e.x));
-                        sum[1] += pkv::exp2_approx(fmaf(__uint_as_float(s[4 * c + 1]), sc, -e.y));
-                        sum[2] += pkv::exp2_approx(fmaf(__uint_as_float(s[4 * c + 2]), sc, -e.z));
-                        sum[3] += pkv::exp2_approx(fmaf(__uint_as_float(s[4 * c + 3]), sc, -e.w));
-                    }
+                        for (int c = 0; c < 16; ++c) {
+                            const float4 e = lse4[c];  // negated
+                            const float2 a = fma2v(x[4 * c], x[4 * c + 1], sc, e.x, e.y), b = fma2v(x[4 * c + 2], x[4 * c + 3], sc, e.z, e.w);
+                            add2(sum[0], pkv::exp2_approx(a.x), pkv::exp2_approx(a.y));
+                            add2(sum[1], pkv::exp2_approx(b.x), pkv::exp2_approx(b.y));
+                        }
+                    };
+                    all(s0, s_lse);
+                    all(s1, s_lse + 16);
                 } else {  // columns from the first token at or after the key, to the last live row
                     const int from = max(key - pos0, 0) << glog, to = rows - i * kTileRows;
+                    auto some = [&](const uint32_t(&x)[64], int c0) {
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) {
-                        const float4 e = s_lse[c];
-                        const float ez[4] = {e.x, e.y, e.z, e.w};
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            const float w = pkv::exp2_approx(fmaf(__uint_as_float(s[4 * c + u]), sc, -ez[u]));
-                            sum[u] += 4 * c + u >= from && 4 * c + u < to ? w : 0.f;
+                        for (int c = 0; c < 64; c += 2) {
+                            const float2 e = reinterpret_cast<const float2 *>(s_lse)[(c0 + c) / 2];
+                            const float2 a = fma2v(x[c], x[c + 1], sc, e.x, e.y);
+                            const float w0 = pkv::exp2_approx(a.x), w1 = pkv::exp2_approx(a.y);
+                            add2(sum[(c >> 1) & 1], c0 + c >= from && c0 + c < to ? w0 : 0.f,
+                                 c0 + c + 1 >= from && c0 + c + 1 < to ? w1 : 0.f);
                         }
-                    }
+                    };
+                    some(s0, 0);
+                    some(s1, 64);
                 }
             }
             if (!ok) break;
-            const float total = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            const float total = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             if (grp == 1) {  // the slot's sums are read before the slot's next item is published
                 s_sum[slot * kTileRows + key_lane] = total;
                 __syncwarp();
