@@ -54,9 +54,9 @@ struct EvictParams {
 // Larger float <-> larger integer; NaN smallest, so that it is evicted first.
 __device__ __forceinline__ uint32_t order_key(float x) {
     const uint32_t u = __float_as_uint(x);
-    if ((u & 0x7fffffffu) > 0x7f800000u) return 0u;
     const uint32_t k = u == 0x80000000u ? 0u : u;  // -0 ties with +0
-    return (k & 0x80000000u) ? ~k : k | 0x80000000u;
+    const uint32_t o = k ^ (static_cast<uint32_t>(static_cast<int32_t>(k) >> 31) | 0x80000000u);
+    return (u & 0x7fffffffu) > 0x7f800000u ? 0u : o;
 }
 
 // The request's cached positions, within its table.
@@ -126,9 +126,12 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
         const int need = P.budget - P.sinks - P.recent;
         uint32_t key[KPT];
 #pragma unroll
+        for (int j = 0; j < KPT; ++j) key[j] = __float_as_uint(__ldcg(scores + min(j * kSelThreads + tid, n - 1)));  // all in flight
+#pragma unroll
         for (int j = 0; j < KPT; ++j) {
             const int p = j * kSelThreads + tid;
-            key[j] = p >= first && p < last ? order_key(__ldcg(scores + p)) : 0u;
+            const uint32_t k = order_key(__uint_as_float(key[j]));
+            key[j] = p >= first && p < last ? k : 0u;
         }
         // The largest border with at least `need` candidate keys >= it (keys of 0 outside the
         // candidates are never counted: every tested border is above 0).
@@ -266,7 +269,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
 #pragma unroll
             for (int u = 0; u < kRounds; ++u) {
                 const int w = static_cast<int>((j0 + u) * kSelWarps + warp);
-                if (w < words && (s_above[w] >> lane) & 1u) x[u] = __ldcg(scores + w * 32 + lane);
+                x[u] = __ldcg(scores + min(w * 32 + lane, n - 1));
             }
             if (out == scores) __syncthreads();
 #pragma unroll

@@ -13,6 +13,8 @@
 //
 //   TMEM (512 columns): S_A | S_B | O_A | O_B, 128 fp32 columns each.  P (fp16, two per column) replaces
 //       S in place and is the A operand of P V straight from TMEM.
+//       A pair whose rows fit tile A alone is run by both softmax groups: A takes the even key tiles, B the
+//       odd ones, with a row state each, joined at the end (B's accumulator lies in the same TMEM lanes).
 //   warps 0-3, 4-7  softmax of tile A, B: one thread per row, its 128 scores in registers; online max
 //       with lazy rescaling (O is rescaled only when a score exceeds the reference max by more than
 //       2^8, then by the row's own thread), row sums in fp32 of the unrounded weights.  P is rounded to
@@ -70,31 +72,33 @@ struct PromptParams {
     CUtensorMap tmap_q, tmap_k, tmap_v;
 };
 
-// One unit of work; `kv_count` per tile is 0 for a tile without rows or without keys in this split.
+// One unit of work; `kv_count` per softmax group is 0 for a group without rows or without keys here.
 struct Item {
     int seq;        // -1: no more items
     int kvh, split;
     int row0;       // q row (token) of the pair's first token
-    int live[2];    // live tokens of tiles A and B
+    int live[2];    // live tokens of the groups' tiles (both tile A's where the groups share it)
     int pos0;       // logical position of the first token
     int keys;       // the request's context
     int kv_first, kv_count[2];
+    int shared;     // 1: the groups share tile A, taking its key tiles in turn
 };
 
 struct PromptSmem {
     static constexpr int q = 0;                              // two operand tiles
     static constexpr int ring = 2 * kOperand;
     static constexpr int bars = ring + kRing * kOperand;
-    static constexpr int n_bars = 2 * kRing + 2 + 4 + 8 + 1;
+    static constexpr int n_bars = 2 * kRing + 2 + 4 + 8 + 2 + 1;
     static constexpr int tmem_slot = bars + n_bars * 8;
     static constexpr int items = (tmem_slot + 4 + 15) / 16 * 16;
-    static constexpr int total = items + 2 * static_cast<int>(sizeof(Item));
+    static constexpr int state = items + 2 * static_cast<int>(sizeof(Item));  // [2 groups][128 rows] (m, l)
+    static constexpr int total = state + 2 * kTileRows * 8;
 };
 
 // Barriers by index.
 constexpr int kBarKvFull = 0, kBarKvEmpty = kRing, kBarQFull = 2 * kRing, kBarQEmpty = kBarQFull + 1,
               kBarItemFull = kBarQEmpty + 1, kBarItemEmpty = kBarItemFull + 2, kBarS = kBarItemEmpty + 2, kBarP = kBarS + 2,
-              kBarO = kBarP + 4, kBarDrain = kBarO + 2;
+              kBarO = kBarP + 4, kBarState = kBarO + 2, kBarJoined = kBarState + 1, kBarDrain = kBarJoined + 1;
 
 // ---- TMEM moves (one row per lane, consecutive 32-bit columns)
 // The load is asynchronous: its registers may be used after tmem_landed on them.
@@ -273,8 +277,17 @@ __device__ Item find_item(const PromptParams &P, int64_t index, int lane) {
     const int end = min(all, it.kv_first + per);
 #pragma unroll
     for (int t = 0; t < 2; ++t) it.kv_count[t] = max(min(count[t], end) - it.kv_first, 0);
+    it.shared = it.live[1] == 0;
+    if (it.shared) {
+        it.live[1] = it.live[0];
+        it.kv_count[1] = it.kv_count[0] / 2;
+        it.kv_count[0] -= it.kv_count[1];
+    }
     return it;
 }
+
+// Key tiles that an item's groups go through: the same ones, or each its own.
+__device__ __forceinline__ int key_tiles(bool shared, int a, int b) { return shared ? a + b : max(a, b); }
 
 template <bool PAGED>
 __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_constant__ PromptParams P) {
@@ -292,6 +305,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
             uint32_t count = 1;
             if (i == kBarItemEmpty || i == kBarItemEmpty + 1) count = kSoftmaxWarps + 1;
             if (i >= kBarP && i < kBarP + 4) count = 4;  // one arrival per softmax warp of the tile
+            if (i == kBarState || i == kBarJoined) count = kSoftmaxWarps;
             pkv::mbar_init(bar(i), count);
         }
         pkv::fence_mbar_init();
@@ -324,12 +338,17 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
             const int boxes_per_tile = PAGED ? kTileRows / P.box_rows : 1;
             uint32_t stage = 0, loaded = 0;  // K/V stages filled, items with keys (one Q each)
             bool ok = true;
-            for (uint32_t k = 0; ok; ++k) {
-                // alternating direction: a CTA's items are not always the longest of their round
+            // Item k of this CTA, the rounds in alternating direction: not always the longest of its round.
+            auto nth_item = [&](uint32_t k) {
                 const int64_t index = static_cast<int64_t>(k) * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
                 Item it{};
                 it.seq = -1;
                 if (index < n_items) it = find_item(P, index, lane);
+                return it;
+            };
+            Item next = nth_item(0);
+            for (uint32_t k = 0; ok; ++k) {
+                const Item it = next;
                 const int slot = k & 1;
                 if (!(ok = wait(kBarItemEmpty + slot, (k >> 1) + 1))) break;
                 if (lane == 0) {
@@ -341,12 +360,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                 }
                 __syncwarp();
                 if (it.seq < 0) break;
-                const int n_kv = max(it.kv_count[0], it.kv_count[1]);
-                if (n_kv == 0) continue;
+                const int n_kv = key_tiles(it.shared, it.kv_count[0], it.kv_count[1]);
+                if (n_kv == 0) {
+                    next = nth_item(k + 1);
+                    continue;
+                }
                 if (!(ok = wait(kBarQEmpty, loaded + 1))) break;
                 ++loaded;
                 if (lane == 0) {
-                    const int tiles = it.live[1] > 0 ? 2 : 1;
+                    const int tiles = it.shared ? 1 : 2;
                     pkv::mbar_arrive_expect_tx(bar(kBarQFull), tiles * kOperand);
                     for (int t = 0; t < tiles; ++t)
                         for (int half = 0; half < 2; ++half)
@@ -354,6 +376,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                                              it.row0 + t * tile_tokens, bar(kBarQFull));
                 }
                 __syncwarp();
+                next = nth_item(k + 1);  // while the copies run
                 // The cache row at which this lane's box of a key tile starts (lane = 2 x box + half).
                 auto box_row = [&](int tile) -> int {
                     const int key = tile * kTileRows + (lane >> 1) * P.box_rows;
@@ -365,23 +388,36 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                     }
                     return static_cast<int>((static_cast<int64_t>(id) * P.num_kv_heads + it.kvh) * P.block_size + key % P.block_size);
                 };
-                int row = PAGED ? box_row(it.kv_first) : 0;
-                for (int j = 0; j < n_kv && ok; ++j) {
-                    const int tile = it.kv_first + j;
-                    const int next = PAGED && j + 1 < n_kv ? box_row(tile + 1) : 0;
-                    const int valid = min(kTileRows, it.keys - tile * kTileRows);
+                // Order of use: K of the first tile (both first tiles where the groups share Q), then V of tile j
+                // and K of the next tile of j's group.
+                const int ahead = it.shared ? 2 : 1;
+                int k_row = PAGED ? box_row(it.kv_first) : 0;
+                int rows[2] = {0, 0};  // V's boxes lag K's by `ahead` tiles
+                for (int x = -ahead; x < n_kv && ok; ++x) {
                     for (int kv = 0; kv < 2; ++kv) {
+                        const int j = kv ? x + ahead : x;  // V of tile x, then K of tile x + ahead
+                        if (j < 0 || j >= n_kv) continue;
+                        const int tile = it.kv_first + j;
+                        const int valid = min(kTileRows, it.keys - tile * kTileRows);
                         const int st = stage % kRing;
                         if (!(ok = wait(kBarKvEmpty + st, stage / kRing + 1))) break;
                         ++stage;
                         const uint32_t dst = base + PromptSmem::ring + st * kOperand, full = bar(kBarKvFull + st);
-                        const void *map = kv ? static_cast<const void *>(&P.tmap_v) : static_cast<const void *>(&P.tmap_k);
+                        const void *map = kv ? static_cast<const void *>(&P.tmap_k) : static_cast<const void *>(&P.tmap_v);
                         if (PAGED) {
                             const int boxes = (valid + P.box_rows - 1) / P.box_rows;
+                            const int row = kv ? k_row : (ahead == 2 && (x & 1) ? rows[1] : rows[0]);
                             if (lane == 0) pkv::mbar_arrive_expect_tx(full, boxes * P.box_rows * 256);
                             __syncwarp();
                             if (lane < 2 * boxes)
                                 pkv::tma_load_2d(dst + (lane & 1) * kSlab + (lane >> 1) * P.box_rows * 128, map, 64 * (lane & 1), row, full);
+                            if (kv) {  // V of this tile follows; the next tile's boxes meanwhile
+                                if (ahead == 2 && (j & 1))
+                                    rows[1] = row;
+                                else
+                                    rows[0] = row;
+                                k_row = j + 1 < n_kv ? box_row(tile + 1) : 0;
+                            }
                         } else if (lane == 0) {  // rows past the sequence are the next one's, past the tensor zeros
                             pkv::mbar_arrive_expect_tx(full, kOperand);
                             for (int half = 0; half < 2; ++half)
@@ -390,7 +426,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                         }
                         __syncwarp();
                     }
-                    row = next;
                 }
             }
             if (!ok) {  // copies still in flight land before the CTA's memory goes (bounded)
@@ -408,16 +443,17 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                 if (!(ok = wait(kBarItemFull + slot, k >> 1))) break;
                 const int seq = slots[slot].seq, keys = slots[slot].keys, first = slots[slot].kv_first;
                 const int n[2] = {slots[slot].kv_count[0], slots[slot].kv_count[1]};
+                const bool shared = slots[slot].shared != 0;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(kBarItemEmpty + slot));
                 if (seq < 0) break;
-                const int n_kv = max(n[0], n[1]);
+                const int n_kv = key_tiles(shared, n[0], n[1]);
                 if (n_kv == 0) continue;  // an empty split
                 // 16-key groups of key tile j that hold cached keys
                 auto groups_of = [&](int j) { return (min(kTileRows, keys - (first + j) * kTileRows) + 15) / 16; };
                 auto qk = [&](int t, uint32_t st, int groups) {
                     if (lane == 0) {
-                        const uint32_t q = base + PromptSmem::q + t * kOperand, kk = base + PromptSmem::ring + (st % kRing) * kOperand;
+                        const uint32_t q = base + PromptSmem::q + (shared ? 0 : t) * kOperand, kk = base + PromptSmem::ring + (st % kRing) * kOperand;
                         const uint32_t idesc = pkv::umma_idesc_f16_f32(kTileRows, groups * 16);
     #pragma unroll
                         for (int ks = 0; ks < kDim / 16; ++ks) {
@@ -435,53 +471,69 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                 };
                 if (!(ok = wait(kBarQFull, loaded))) break;
                 ++loaded;
-                if (!(ok = wait(kBarKvFull + stage % kRing, stage / kRing))) break;
-                pkv::tmem_fence_after_sync();
-                for (int t = 0; t < 2; ++t)
-                    if (n[t] > 0) qk(t, stage, groups_of(0));
-                commit(kBarKvEmpty + stage % kRing);
-                if (n_kv == 1) commit(kBarQEmpty);
-                ++stage;
-                for (int j = 0; j < n_kv && ok; ++j) {
-                    const uint32_t v_stage = stage, k_stage = stage + 1;
-                    const bool more = j + 1 < n_kv;
-                    if (!(ok = wait(kBarKvFull + v_stage % kRing, v_stage / kRing))) break;
-                    const uint32_t v = base + PromptSmem::ring + (v_stage % kRing) * kOperand;
-                    const int groups = groups_of(j);
+                // Zeroes the V rows past the context in a tile's last 16-key group: their weights are 0, their values
+                // may be anything.
+                auto clean_tail = [&](uint32_t v, int j, int groups) {
                     const int valid = min(kTileRows, keys - (first + j) * kTileRows);
-                    if (valid < groups * 16) {  // V rows past the context: their weights are 0, their values may be anything
-                        for (int x = lane; x < (groups * 16 - valid) * 16; x += 32)
-                            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v + ((x >> 3) & 1) * kSlab +
-                                                                                     (valid + (x >> 4)) * 128 + (x & 7) * 16),
-                                         "r"(0)
-                                         : "memory");
-                        pkv::fence_proxy_async_smem();
+                    if (valid >= groups * 16) return;
+                    for (int x = lane; x < (groups * 16 - valid) * 16; x += 32)
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v + ((x >> 3) & 1) * kSlab +
+                                                                                 (valid + (x >> 4)) * 128 + (x & 7) * 16),
+                                     "r"(0)
+                                     : "memory");
+                    pkv::fence_proxy_async_smem();
+                    __syncwarp();
+                };
+                // O of group t += P V of key tile j (the group's `local`-th)
+                auto pv = [&](int t, uint32_t v, int groups, int local) {
+                    for (int half = 0; half < 2; ++half) {  // keys 0-63 while the softmax finishes 64-127
+                        if (!wait(kBarP + 2 * t + half, p_count[t])) return false;
+                        pkv::tmem_fence_after_sync();
+                        if (lane == 0) {
+#pragma unroll
+                            for (int g = 4 * half; g < 4 * half + 4; ++g)
+                                if (g < groups)
+                                    umma_f16_ta(tmem + 2 * kTileRows + t * kDim, tmem + t * kTileRows + g * 8,
+                                                pkv::umma_desc_mn_sw128(v + g * 2048, kSlab, 1024), kIdescPV, local > 0 || g > 0);
+                            if (half == 1 && local + 1 == n[t]) pkv::umma_commit(bar(kBarO + t));
+                        }
                         __syncwarp();
                     }
-                    if (more && !(ok = wait(kBarKvFull + k_stage % kRing, k_stage / kRing))) break;
+                    ++p_count[t];
+                    return true;
+                };
+                auto landed = [&](uint32_t s) { return wait(kBarKvFull + s % kRing, s / kRing); };
+                // Q K^T of the first key tile for both groups, or of the first two for one each
+                const int firsts = shared ? min(2, n_kv) : 1;
+                for (int x = 0; x < firsts && ok; ++x) {
+                    if (!(ok = landed(stage))) break;
+                    pkv::tmem_fence_after_sync();
+                    for (int t = 0; t < 2; ++t)
+                        if (shared ? t == x : n[t] > 0) qk(t, stage, groups_of(x));
+                    commit(kBarKvEmpty + stage % kRing);
+                    ++stage;
+                }
+                if (!ok) break;
+                if (n_kv == firsts) commit(kBarQEmpty);
+                for (int j = 0; j < n_kv && ok; ++j) {
+                    const uint32_t v_stage = stage, k_stage = stage + 1;
+                    const int k_tile = j + (shared ? 2 : 1);
+                    const bool more = k_tile < n_kv;
+                    if (!(ok = landed(v_stage))) break;
+                    const uint32_t v = base + PromptSmem::ring + (v_stage % kRing) * kOperand;
+                    const int groups = groups_of(j);
+                    clean_tail(v, j, groups);
+                    if (more && !(ok = landed(k_stage))) break;
                     for (int t = 0; t < 2 && ok; ++t) {
-                        if (j >= n[t]) continue;
-                        for (int half = 0; half < 2 && ok; ++half) {  // keys 0-63 while the softmax finishes 64-127
-                            if (!(ok = wait(kBarP + 2 * t + half, p_count[t]))) break;
-                            pkv::tmem_fence_after_sync();
-                            if (lane == 0) {
-    #pragma unroll
-                                for (int g = 4 * half; g < 4 * half + 4; ++g)
-                                    if (g < groups)
-                                        umma_f16_ta(tmem + 2 * kTileRows + t * kDim, tmem + t * kTileRows + g * 8,
-                                                    pkv::umma_desc_mn_sw128(v + g * 2048, kSlab, 1024), kIdescPV, j > 0 || g > 0);
-                                if (half == 1 && j + 1 == n[t]) pkv::umma_commit(bar(kBarO + t));
-                            }
-                            __syncwarp();
-                        }
-                        if (!ok) break;
-                        ++p_count[t];
-                        if (j + 1 < n[t]) qk(t, k_stage, groups_of(j + 1));
+                        const int local = shared ? j >> 1 : j;
+                        if (shared ? t != (j & 1) : j >= n[t]) continue;
+                        if (!(ok = pv(t, v, groups, local))) break;
+                        if (local + 1 < n[t]) qk(t, k_stage, groups_of(k_tile));
                     }
                     if (!ok) break;
                     commit(kBarKvEmpty + v_stage % kRing);
                     if (more) commit(kBarKvEmpty + k_stage % kRing);
-                    if (j + 2 == n_kv) commit(kBarQEmpty);  // the item's last Q K^T has been issued
+                    if (more && k_tile + 1 == n_kv) commit(kBarQEmpty);  // the item's last Q K^T has been issued
                     stage += more ? 2 : 1;
                 }
             }
@@ -499,15 +551,18 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
         const uint32_t t_s = tmem + lanes + t * kTileRows, t_o = tmem + lanes + 2 * kTileRows + t * kDim;
         const int r = (warp & 3) * 32 + lane, tok = r >> glog;
         const float sc = P.q_scale;
-        uint32_t s_count = 0, o_count = 0;
+        uint32_t s_count = 0, o_count = 0, joins = 0;
+        float2 *s_state = reinterpret_cast<float2 *>(smem + PromptSmem::state);
         bool ok = true;
         for (uint32_t k = 0; ok; ++k) {
             const int slot = k & 1;
             if (!(ok = wait(kBarItemFull + slot, k >> 1))) break;
             const int seq = slots[slot].seq, kvh = slots[slot].kvh, split = slots[slot].split, first = slots[slot].kv_first;
-            const int n = slots[slot].kv_count[t], live = slots[slot].live[t];
-            const int tile_pos = slots[slot].pos0 + t * tile_tokens;  // position of the tile's first token
-            const int64_t q_row = slots[slot].row0 + t * tile_tokens + tok;
+            const int n = slots[slot].kv_count[t], n_of_other = slots[slot].kv_count[t ^ 1], live = slots[slot].live[t];
+            const bool shared = slots[slot].shared != 0;
+            const int tile = shared ? 0 : t;
+            const int tile_pos = slots[slot].pos0 + tile * tile_tokens;  // position of the tile's first token
+            const int64_t q_row = slots[slot].row0 + tile * tile_tokens + tok;
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kBarItemEmpty + slot));
             if (seq < 0) break;
@@ -521,7 +576,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                 tmem_ld64(t_s, s0);
                 tmem_landed(s0);
                 tmem_ld64(t_s + 64, s1);
-                const int key0 = (first + j) * kTileRows;
+                const int key0 = (first + (shared ? 2 * j + t : j)) * kTileRows;
                 const bool border = key0 + kTileRows - 1 > tile_pos;  // the causal border, or the context's end
                 const int lim = pos - key0;
                 if (border) {
@@ -591,16 +646,48 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
             }
             const bool store = tok < live;
             const int64_t row = q_row * P.num_q_heads + (kvh << glog) + (r & ((1 << glog) - 1));
-            const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-            if (n > 0) {
-#pragma unroll
-                for (int c = 0; c < kDim; c += 32) {
+            // The row's state and the two accumulators that make it up: its own alone, or where the groups
+            // share the rows both, each group finishing half of the dims.
+            float m = m_ref, total = l, w_own = 1.f, w_other = 0.f;
+            if (shared) {
+                s_state[t * kTileRows + r] = make_float2(m_ref, l);
+                pkv::tmem_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(kBarState));
+                if (!(ok = wait(kBarState, joins))) break;
+                pkv::tmem_fence_after_sync();
+                const float2 o = s_state[(t ^ 1) * kTileRows + r];
+                m = fmaxf(m_ref, o.x);
+                w_own = m_ref == -INFINITY ? 0.f : exp2f(m_ref - m);
+                w_other = o.x == -INFINITY ? 0.f : exp2f(o.x - m);
+                total = l * w_own + o.y * w_other;
+            }
+            const int n_other = shared ? n_of_other : 0;
+            const float inv = total == 0.f ? 0.f : 1.f / total;
+            w_own *= inv;
+            w_other *= inv;
+            const int c_begin = shared ? t * (kDim / 2) : 0, c_end = shared ? c_begin + kDim / 2 : kDim;
+            const uint32_t t_other = tmem + lanes + 2 * kTileRows + (t ^ 1) * kDim;
+            if (n > 0 || n_other > 0) {
+#pragma unroll 1
+                for (int c = c_begin; c < c_end; c += 32) {
                     uint32_t o[32];
                     __syncwarp();
-                    pkv::tmem_ld32(t_o + c, o);
-                    if (!store) continue;
+                    if (n > 0) {
+                        pkv::tmem_ld32(t_o + c, o);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * w_own);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = 0u;
+                    }
+                    if (n_other > 0) {
+                        uint32_t q[32];
+                        pkv::tmem_ld32(t_other + c, q);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(fmaf(__uint_as_float(q[i]), w_other, __uint_as_float(o[i])));
+                    }
+                    if (!store) continue;
                     if (P.splits == 1) {
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
@@ -622,15 +709,22 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                         }
                     }
                 }
+                __syncwarp();
                 pkv::tmem_fence_before_sync();  // O read before the next item's first P V (ordered by its weights' arrival)
             }
-            if (store) {
+            if (store && (t == 0 || !shared)) {
                 if (P.splits > 1) {
-                    P.m_part[row * P.splits + split] = l == 0.f ? -INFINITY : m_ref;
-                    P.l_part[row * P.splits + split] = l;
+                    P.m_part[row * P.splits + split] = total == 0.f ? -INFINITY : m;
+                    P.l_part[row * P.splits + split] = total;
                 } else if (P.lse != nullptr) {
-                    P.lse[row] = (m_ref + log2f(l)) * kLn2;
+                    P.lse[row] = (m + log2f(total)) * kLn2;
                 }
+            }
+            if (shared) {  // neither accumulator is written again before both groups have read both
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(kBarJoined));
+                if (!(ok = wait(kBarJoined, joins))) break;
+                ++joins;
             }
         }
     }
@@ -1066,7 +1160,7 @@ int plan_splits(int num_seqs, int total_q, int num_q_heads, int num_kv_heads, in
     const int64_t items = (static_cast<int64_t>(total_q) / pair_tokens + num_seqs) * num_kv_heads;
     if (2 * items > kPlannedSms) return 1;
     const int64_t by_keys = max_context / 512;
-    int64_t s = kPlannedSms / (items > 0 ? items : 1);
+    int64_t s = 2 * kPlannedSms / (items > 0 ? items : 1);  // two items per SM, the longer ones first
     s = s < by_keys ? s : by_keys;
     s = s < kMaxSplits ? s : kMaxSplits;
     return s > 1 ? static_cast<int>(s) : 1;
