@@ -188,6 +188,34 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+// Waits for phase `parity` of the barrier; false after kWaitLimitNs.  The waits here are links of the chain
+// softmax -> MMA -> softmax, mostly shorter than a read of the global timer, so that is read only once
+// every 256 polls.
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity) {
+    uint64_t since = 0;
+    for (uint32_t polls = 0;; ++polls) {
+        if (pkv::mbar_try_wait(bar, parity)) return true;
+        if ((polls & 255u) == 255u) {
+            const uint64_t now = pkv::global_timer_ns();
+            if (since == 0) since = now;
+            if (now - since > pkv::kWaitLimitNs) return false;
+        }
+    }
+}
+
+// A value that is the same in all lanes, as the compiler can see: what the MMA warp computes from it
+// stays in uniform registers, which the MMA instructions take their descriptors from.  (With the
+// items' fields as loaded, a tcgen05.mma cost about 130 cycles of issue, twice its execution.)
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(pkv::kFullMask, x, 0); }
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(pkv::kFullMask, x, 0); }
+
+// True in one lane of the (converged) warp, always the same one.
+__device__ __forceinline__ bool elected() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 // A 32-byte store: one whole sector from one thread.
 __device__ __forceinline__ void store_sector(void *p, const uint32_t (&r)[8]) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
@@ -293,7 +321,7 @@ template <bool PAGED>
 __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_constant__ PromptParams P) {
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t base = pkv::smem_addr(smem);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
     const uint32_t bars = base + PromptSmem::bars;
     auto bar = [bars](int i) { return bars + 8 * i; };
     volatile Item *slots = reinterpret_cast<volatile Item *>(smem + PromptSmem::items);
@@ -320,11 +348,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
         if (threadIdx.x == 0) pkv::record_error(&g_prompt_error, PKV_DEV_SMEM_MISALIGNED);
         return;
     }
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = uniform(*tmem_slot);
     const int glog = P.group_log2, tile_tokens = kTileRows >> glog;
     // A wait that runs out is recorded; its warp leaves its loop, and so do the others in their turn.
     auto wait = [&](int b, uint32_t phase) {
-        if (__all_sync(pkv::kFullMask, pkv::mbar_wait_bounded(bar(b), phase & 1))) return true;
+        if (__all_sync(pkv::kFullMask, wait_phase(bar(b), phase & 1))) return true;
         if (lane == 0) pkv::record_error(&g_prompt_error, PKV_DEV_WAIT_TIMEOUT);
         return false;
     };
@@ -429,9 +457,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                 }
             }
             if (!ok) {  // copies still in flight land before the CTA's memory goes (bounded)
-                if (loaded) pkv::mbar_wait_bounded(bar(kBarQFull), (loaded - 1) & 1);
+                if (loaded) wait_phase(bar(kBarQFull), (loaded - 1) & 1);
                 for (uint32_t s = stage > kRing ? stage - kRing : 0; s < stage; ++s)
-                    pkv::mbar_wait_bounded(bar(kBarKvFull + s % kRing), (s / kRing) & 1);
+                    wait_phase(bar(kBarKvFull + s % kRing), (s / kRing) & 1);
             }
         } else if (warp == kMmaWarp) {
             // ---------------------------------------------------------------- tensor-core issue
@@ -441,9 +469,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
             for (uint32_t k = 0; ok; ++k) {
                 const int slot = k & 1;
                 if (!(ok = wait(kBarItemFull + slot, k >> 1))) break;
-                const int seq = slots[slot].seq, keys = slots[slot].keys, first = slots[slot].kv_first;
-                const int n[2] = {slots[slot].kv_count[0], slots[slot].kv_count[1]};
-                const bool shared = slots[slot].shared != 0;
+                const int seq = uniform(slots[slot].seq), keys = uniform(slots[slot].keys), first = uniform(slots[slot].kv_first);
+                const int n[2] = {uniform(slots[slot].kv_count[0]), uniform(slots[slot].kv_count[1])};
+                const bool shared = uniform(slots[slot].shared) != 0;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(kBarItemEmpty + slot));
                 if (seq < 0) break;
@@ -452,7 +480,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                 // 16-key groups of key tile j that hold cached keys
                 auto groups_of = [&](int j) { return (min(kTileRows, keys - (first + j) * kTileRows) + 15) / 16; };
                 auto qk = [&](int t, uint32_t st, int groups) {
-                    if (lane == 0) {
+                    if (elected()) {
                         const uint32_t q = base + PromptSmem::q + (shared ? 0 : t) * kOperand, kk = base + PromptSmem::ring + (st % kRing) * kOperand;
                         const uint32_t idesc = pkv::umma_idesc_f16_f32(kTileRows, groups * 16);
     #pragma unroll
@@ -466,7 +494,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                     __syncwarp();
                 };
                 auto commit = [&](int b) {
-                    if (lane == 0) pkv::umma_commit(bar(b));
+                    if (elected()) pkv::umma_commit(bar(b));
                     __syncwarp();
                 };
                 if (!(ok = wait(kBarQFull, loaded))) break;
@@ -489,7 +517,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                     for (int half = 0; half < 2; ++half) {  // keys 0-63 while the softmax finishes 64-127
                         if (!wait(kBarP + 2 * t + half, p_count[t])) return false;
                         pkv::tmem_fence_after_sync();
-                        if (lane == 0) {
+                        if (elected()) {
 #pragma unroll
                             for (int g = 4 * half; g < 4 * half + 4; ++g)
                                 if (g < groups)
@@ -538,9 +566,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                 }
             }
             if (!ok) {  // MMAs in flight end before tensor memory is freed (bounded)
-                if (lane == 0) pkv::umma_commit(bar(kBarDrain));
+                if (elected()) pkv::umma_commit(bar(kBarDrain));
                 __syncwarp();
-                pkv::mbar_wait_bounded(bar(kBarDrain), 0);
+                wait_phase(bar(kBarDrain), 0);
             }
         }
     } else {
@@ -863,7 +891,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) chunk_weights_kernel(const 
     const PromptParams &P = W.p;
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t base = pkv::smem_addr(smem);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
     const uint32_t bars = base + L::bars;
     auto bar = [bars](int i) { return bars + 8 * i; };
     volatile KeyItem *slots = reinterpret_cast<volatile KeyItem *>(smem + L::items);
@@ -888,10 +916,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) chunk_weights_kernel(const 
         if (threadIdx.x == 0) pkv::record_error(&g_prompt_error, PKV_DEV_SMEM_MISALIGNED);
         return;
     }
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = uniform(*tmem_slot);
     const int glog = P.group_log2, tile_tokens = kTileRows >> glog;
     auto wait = [&](int b, uint32_t phase) {
-        if (__all_sync(pkv::kFullMask, pkv::mbar_wait_bounded(bar(b), phase & 1))) return true;
+        if (__all_sync(pkv::kFullMask, wait_phase(bar(b), phase & 1))) return true;
         if (lane == 0) pkv::record_error(&g_prompt_error, PKV_DEV_WAIT_TIMEOUT);
         return false;
     };
@@ -957,9 +985,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) chunk_weights_kernel(const 
             }
             if (!ok) {  // copies still in flight land before the CTA's memory goes (bounded)
                 for (uint32_t s = k > kKeyStages ? k - kKeyStages : 0; s <= k; ++s)
-                    pkv::mbar_wait_bounded(bar(kWKeyFull + s % kKeyStages), (s / kKeyStages) & 1);
+                    wait_phase(bar(kWKeyFull + s % kKeyStages), (s / kKeyStages) & 1);
                 for (uint32_t s = rows > kRowRing ? rows - kRowRing : 0; s < rows; ++s)
-                    pkv::mbar_wait_bounded(bar(kWRowFull + s % kRowRing), (s / kRowRing) & 1);
+                    wait_phase(bar(kWRowFull + s % kRowRing), (s / kRowRing) & 1);
             }
         } else if (warp == kMmaWarp) {
             uint32_t rows = 0;
@@ -968,8 +996,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) chunk_weights_kernel(const 
             for (uint32_t k = 0; ok; ++k) {
                 const int slot = k & 1;
                 if (!(ok = wait(kWItemFull + slot, k >> 1))) break;
-                const int seq = slots[slot].seq, first = slots[slot].first, count = slots[slot].count;
-                const int all_rows = slots[slot].tokens << glog;
+                const int seq = uniform(slots[slot].seq), first = uniform(slots[slot].first), count = uniform(slots[slot].count);
+                const int all_rows = uniform(slots[slot].tokens) << glog;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(kWItemEmpty + slot));
                 if (seq < 0) break;
@@ -984,7 +1012,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) chunk_weights_kernel(const 
                         if (u == buf) fills = used[u]++;
                     if (!(ok = wait(kWSFree + buf, fills + 1))) break;
                     pkv::tmem_fence_after_sync();
-                    if (lane == 0) {
+                    if (elected()) {
                         const uint32_t a = base + L::keys + ks * kOperand, b = base + L::rows + st * kOperand;
                         const uint32_t idesc = pkv::umma_idesc_f16_f32(kTileRows, (min(kTileRows, all_rows - i * kTileRows) + 15) / 16 * 16);
     #pragma unroll
@@ -1000,9 +1028,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) chunk_weights_kernel(const 
                 }
             }
             if (!ok) {  // MMAs in flight end before tensor memory is freed (bounded)
-                if (lane == 0) pkv::umma_commit(bar(kWDrain));
+                if (elected()) pkv::umma_commit(bar(kWDrain));
                 __syncwarp();
-                pkv::mbar_wait_bounded(bar(kWDrain), 0);
+                wait_phase(bar(kWDrain), 0);
             }
         }
     } else {
