@@ -19,8 +19,10 @@
 //       with lazy rescaling (O is rescaled only when a score exceeds the reference max by more than
 //       2^8, then by the row's own thread), row sums in fp32 of the unrounded weights.  P is rounded to
 //       fp16 once (2^-11 relative, as the output's own rounding), which keeps P V at the fp16 rate.
-//   warp 8  issues every tcgen05.mma (one lane); warp 9 issues every tensor copy: Q (64 KB) once per
-//       item, K and V tiles of 128 keys through a ring of four 32 KB stages.
+//   warp 8  issues every tcgen05.mma (one lane).
+//   warps 9, 10  issue the tensor copies: Q (64 KB) once per item and the K tiles of 128 keys, and the V tiles,
+//       each through a ring of two 32 KB stages.  Two warps: with 16-token blocks a tile is 16 copies of 2 KB, and
+//       one warp issuing both K's and V's held the MMAs up.
 //
 // Work items are (pair of tiles, kv head, split of the keys), dealt to one persistent CTA per SM,
 // the longest first and in alternating direction, so that CTAs end together: warp 9 finds the next item
@@ -49,11 +51,11 @@ constexpr int kDim = PKV_HEAD_DIM;
 constexpr int kTileRows = 128;             // query rows per tile (M) and keys per K/V tile (N)
 constexpr int kSlab = kTileRows * 128;     // 128 rows x 64 fp16 dims, 128-byte swizzle
 constexpr int kOperand = 2 * kSlab;        // a whole 128 x 128 fp16 operand tile
-constexpr int kRing = 4;                   // K/V stages
+constexpr int kRing = 2;                   // stages of K, and of V
 constexpr int kSoftmaxWarps = 8;
-constexpr int kPromptThreads = 32 * (kSoftmaxWarps + 4);  // three warpgroups; the last has two idle warps
+constexpr int kPromptThreads = 32 * (kSoftmaxWarps + 4);  // three warpgroups
 constexpr int kSoftmaxRegs = 200, kOtherRegs = 88;  // launch: 384 x 168 = 64,512 registers; 256 x 200 + 128 x 88 = 62,464
-constexpr int kMmaWarp = kSoftmaxWarps, kLoadWarp = kSoftmaxWarps + 1;
+constexpr int kMmaWarp = kSoftmaxWarps, kLoadWarp = kSoftmaxWarps + 1, kValueWarp = kSoftmaxWarps + 2;
 constexpr float kLazy = 8.0f;              // log2 units
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kMaxSplits = 64;
@@ -87,8 +89,9 @@ struct Item {
 struct PromptSmem {
     static constexpr int q = 0;                              // two operand tiles
     static constexpr int ring = 2 * kOperand;
-    static constexpr int bars = ring + kRing * kOperand;
-    static constexpr int n_bars = 2 * kRing + 2 + 4 + 8 + 2 + 1;
+    static constexpr int values = ring + kRing * kOperand;   // ring: K stages, values: V stages
+    static constexpr int bars = values + kRing * kOperand;
+    static constexpr int n_bars = 4 * kRing + 2 + 4 + 8 + 2 + 1;
     static constexpr int tmem_slot = bars + n_bars * 8;
     static constexpr int items = (tmem_slot + 4 + 15) / 16 * 16;
     static constexpr int state = items + 2 * static_cast<int>(sizeof(Item));  // [2 groups][128 rows] (m, l)
@@ -96,7 +99,7 @@ struct PromptSmem {
 };
 
 // Barriers by index.
-constexpr int kBarKvFull = 0, kBarKvEmpty = kRing, kBarQFull = 2 * kRing, kBarQEmpty = kBarQFull + 1,
+constexpr int kBarKFull = 0, kBarKEmpty = kRing, kBarVFull = 2 * kRing, kBarVEmpty = 3 * kRing, kBarQFull = 4 * kRing, kBarQEmpty = kBarQFull + 1,
               kBarItemFull = kBarQEmpty + 1, kBarItemEmpty = kBarItemFull + 2, kBarS = kBarItemEmpty + 2, kBarP = kBarS + 2,
               kBarO = kBarP + 4, kBarState = kBarO + 2, kBarJoined = kBarState + 1, kBarDrain = kBarJoined + 1;
 
@@ -331,7 +334,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
     if (threadIdx.x == 0) {
         for (int i = 0; i < PromptSmem::n_bars; ++i) {
             uint32_t count = 1;
-            if (i == kBarItemEmpty || i == kBarItemEmpty + 1) count = kSoftmaxWarps + 1;
+            if (i == kBarItemEmpty || i == kBarItemEmpty + 1) count = kSoftmaxWarps + 2;
             if (i >= kBarP && i < kBarP + 4) count = 4;  // one arrival per softmax warp of the tile
             if (i == kBarState || i == kBarJoined) count = kSoftmaxWarps;
             pkv::mbar_init(bar(i), count);
@@ -359,12 +362,39 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
 
     if (warp >= kSoftmaxWarps) {
         shrink_registers<kOtherRegs>();
+        // The cache row at which this lane's box of a key tile starts (lane = 2 x box + half).
+        const int boxes_per_tile = PAGED ? kTileRows / P.box_rows : 1;
+        auto box_row = [&](int seq, int kvh, int keys, int tile) -> int {
+            const int key = tile * kTileRows + (lane >> 1) * P.box_rows;
+            if (!PAGED || lane >= 2 * boxes_per_tile || key >= keys) return 0;
+            int32_t id = __ldg(P.block_tables + static_cast<int64_t>(seq) * P.max_blocks + key / P.block_size);
+            if (id < 0 || id >= P.num_blocks) {
+                pkv::record_error(&g_prompt_error, PKV_DEV_BAD_BLOCK_ID);
+                id = 0;
+            }
+            return static_cast<int>((static_cast<int64_t>(id) * P.num_kv_heads + kvh) * P.block_size + key % P.block_size);
+        };
+        // Copies of one K or V tile into a stage (box by box where paged; packed, rows past the sequence are
+        // the next one's, past the tensor zeros).
+        auto copy_tile = [&](const void *map, uint32_t dst, uint32_t full, int keys, int kvh, int tile, int first_row, int row) {
+            if (PAGED) {
+                const int boxes = (min(kTileRows, keys - tile * kTileRows) + P.box_rows - 1) / P.box_rows;
+                if (lane == 0) pkv::mbar_arrive_expect_tx(full, boxes * P.box_rows * 256);
+                __syncwarp();
+                if (lane < 2 * boxes)
+                    pkv::tma_load_2d(dst + (lane & 1) * kSlab + (lane >> 1) * P.box_rows * 128, map, 64 * (lane & 1), row, full);
+            } else if (lane == 0) {
+                pkv::mbar_arrive_expect_tx(full, kOperand);
+                for (int half = 0; half < 2; ++half)
+                    pkv::tma_load_2d(dst + half * kSlab, map, kvh * kDim + 64 * half, first_row + tile * kTileRows, full);
+            }
+            __syncwarp();
+        };
         if (warp == kLoadWarp) {
-            // ---------------------------------------------------------------- items and tensor copies
+            // ---------------------------------------------------------------- items, Q and K
             const int pairs = pairs_from(P, 0, 2 * tile_tokens, lane, blockIdx.x == 0);
             const int64_t n_items = static_cast<int64_t>(pairs) * P.num_kv_heads * P.splits;
-            const int boxes_per_tile = PAGED ? kTileRows / P.box_rows : 1;
-            uint32_t stage = 0, loaded = 0;  // K/V stages filled, items with keys (one Q each)
+            uint32_t stage = 0, loaded = 0;  // K stages filled, items with keys (one Q each)
             bool ok = true;
             // Item k of this CTA, the rounds in alternating direction: not always the longest of its round.
             auto nth_item = [&](uint32_t k) {
@@ -382,7 +412,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                 if (lane == 0) {
                     volatile int *d = reinterpret_cast<volatile int *>(slots + slot);
                     const int *s = reinterpret_cast<const int *>(&it);
-    #pragma unroll
+#pragma unroll
                     for (int i = 0; i < static_cast<int>(sizeof(Item) / 4); ++i) d[i] = s[i];
                     mbar_arrive(bar(kBarItemFull + slot));
                 }
@@ -393,6 +423,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                     next = nth_item(k + 1);
                     continue;
                 }
+                int row = box_row(it.seq, it.kvh, it.keys, it.kv_first);
                 if (!(ok = wait(kBarQEmpty, loaded + 1))) break;
                 ++loaded;
                 if (lane == 0) {
@@ -404,67 +435,50 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                                              it.row0 + t * tile_tokens, bar(kBarQFull));
                 }
                 __syncwarp();
-                next = nth_item(k + 1);  // while the copies run
-                // The cache row at which this lane's box of a key tile starts (lane = 2 x box + half).
-                auto box_row = [&](int tile) -> int {
-                    const int key = tile * kTileRows + (lane >> 1) * P.box_rows;
-                    if (lane >= 2 * boxes_per_tile || key >= it.keys) return 0;
-                    int32_t id = __ldg(P.block_tables + static_cast<int64_t>(it.seq) * P.max_blocks + key / P.block_size);
-                    if (id < 0 || id >= P.num_blocks) {
-                        pkv::record_error(&g_prompt_error, PKV_DEV_BAD_BLOCK_ID);
-                        id = 0;
-                    }
-                    return static_cast<int>((static_cast<int64_t>(id) * P.num_kv_heads + it.kvh) * P.block_size + key % P.block_size);
-                };
-                // Order of use: K of the first tile (both first tiles where the groups share Q), then V of tile j
-                // and K of the next tile of j's group.
-                const int ahead = it.shared ? 2 : 1;
-                int k_row = PAGED ? box_row(it.kv_first) : 0;
-                int rows[2] = {0, 0};  // V's boxes lag K's by `ahead` tiles
-                for (int x = -ahead; x < n_kv && ok; ++x) {
-                    for (int kv = 0; kv < 2; ++kv) {
-                        const int j = kv ? x + ahead : x;  // V of tile x, then K of tile x + ahead
-                        if (j < 0 || j >= n_kv) continue;
-                        const int tile = it.kv_first + j;
-                        const int valid = min(kTileRows, it.keys - tile * kTileRows);
-                        const int st = stage % kRing;
-                        if (!(ok = wait(kBarKvEmpty + st, stage / kRing + 1))) break;
-                        ++stage;
-                        const uint32_t dst = base + PromptSmem::ring + st * kOperand, full = bar(kBarKvFull + st);
-                        const void *map = kv ? static_cast<const void *>(&P.tmap_k) : static_cast<const void *>(&P.tmap_v);
-                        if (PAGED) {
-                            const int boxes = (valid + P.box_rows - 1) / P.box_rows;
-                            const int row = kv ? k_row : (ahead == 2 && (x & 1) ? rows[1] : rows[0]);
-                            if (lane == 0) pkv::mbar_arrive_expect_tx(full, boxes * P.box_rows * 256);
-                            __syncwarp();
-                            if (lane < 2 * boxes)
-                                pkv::tma_load_2d(dst + (lane & 1) * kSlab + (lane >> 1) * P.box_rows * 128, map, 64 * (lane & 1), row, full);
-                            if (kv) {  // V of this tile follows; the next tile's boxes meanwhile
-                                if (ahead == 2 && (j & 1))
-                                    rows[1] = row;
-                                else
-                                    rows[0] = row;
-                                k_row = j + 1 < n_kv ? box_row(tile + 1) : 0;
-                            }
-                        } else if (lane == 0) {  // rows past the sequence are the next one's, past the tensor zeros
-                            pkv::mbar_arrive_expect_tx(full, kOperand);
-                            for (int half = 0; half < 2; ++half)
-                                pkv::tma_load_2d(dst + half * kSlab, map, it.kvh * kDim + 64 * half, it.row0 - it.pos0 + tile * kTileRows,
-                                                 full);
-                        }
-                        __syncwarp();
-                    }
+                for (int j = 0; j < n_kv; ++j, ++stage) {
+                    const int tile = it.kv_first + j, st = stage % kRing;
+                    const int ahead = j + 1 < n_kv ? box_row(it.seq, it.kvh, it.keys, tile + 1) : 0;
+                    if (!(ok = wait(kBarKEmpty + st, stage / kRing + 1))) break;
+                    copy_tile(&P.tmap_k, base + PromptSmem::ring + st * kOperand, bar(kBarKFull + st), it.keys, it.kvh, tile,
+                              it.row0 - it.pos0, row);
+                    row = ahead;
+                    if (j == 0) next = nth_item(k + 1);  // while the copies run
                 }
             }
             if (!ok) {  // copies still in flight land before the CTA's memory goes (bounded)
                 if (loaded) wait_phase(bar(kBarQFull), (loaded - 1) & 1);
                 for (uint32_t s = stage > kRing ? stage - kRing : 0; s < stage; ++s)
-                    wait_phase(bar(kBarKvFull + s % kRing), (s / kRing) & 1);
+                    wait_phase(bar(kBarKFull + s % kRing), (s / kRing) & 1);
             }
+        } else if (warp == kValueWarp) {
+            // ---------------------------------------------------------------- V
+            uint32_t stage = 0;
+            bool ok = true;
+            for (uint32_t k = 0; ok; ++k) {
+                const int slot = k & 1;
+                if (!(ok = wait(kBarItemFull + slot, k >> 1))) break;
+                const int seq = slots[slot].seq, kvh = slots[slot].kvh, keys = slots[slot].keys, first = slots[slot].kv_first;
+                const int n_kv = key_tiles(slots[slot].shared != 0, slots[slot].kv_count[0], slots[slot].kv_count[1]);
+                const int first_row = slots[slot].row0 - slots[slot].pos0;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(kBarItemEmpty + slot));
+                if (seq < 0) break;
+                int row = n_kv > 0 ? box_row(seq, kvh, keys, first) : 0;
+                for (int j = 0; j < n_kv; ++j, ++stage) {
+                    const int tile = first + j, st = stage % kRing;
+                    const int ahead = j + 1 < n_kv ? box_row(seq, kvh, keys, tile + 1) : 0;
+                    if (!(ok = wait(kBarVEmpty + st, stage / kRing + 1))) break;
+                    copy_tile(&P.tmap_v, base + PromptSmem::values + st * kOperand, bar(kBarVFull + st), keys, kvh, tile, first_row, row);
+                    row = ahead;
+                }
+            }
+            if (!ok)
+                for (uint32_t s = stage > kRing ? stage - kRing : 0; s < stage; ++s)
+                    wait_phase(bar(kBarVFull + s % kRing), (s / kRing) & 1);
         } else if (warp == kMmaWarp) {
             // ---------------------------------------------------------------- tensor-core issue
             constexpr uint32_t kIdescPV = pkv::umma_idesc_f16_f32(kTileRows, kDim) | (1u << 16);  // V: MN-major
-            uint32_t stage = 0, loaded = 0, p_count[2] = {0, 0};
+            uint32_t k_stage = 0, v_stage = 0, loaded = 0, p_count[2] = {0, 0};
             bool ok = true;
             for (uint32_t k = 0; ok; ++k) {
                 const int slot = k & 1;
@@ -530,39 +544,44 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                     ++p_count[t];
                     return true;
                 };
-                auto landed = [&](uint32_t s) { return wait(kBarKvFull + s % kRing, s / kRing); };
+                auto k_landed = [&]() { return wait(kBarKFull + k_stage % kRing, k_stage / kRing); };
                 // Q K^T of the first key tile for both groups, or of the first two for one each
                 const int firsts = shared ? min(2, n_kv) : 1;
                 for (int x = 0; x < firsts && ok; ++x) {
-                    if (!(ok = landed(stage))) break;
+                    if (!(ok = k_landed())) break;
                     pkv::tmem_fence_after_sync();
                     for (int t = 0; t < 2; ++t)
-                        if (shared ? t == x : n[t] > 0) qk(t, stage, groups_of(x));
-                    commit(kBarKvEmpty + stage % kRing);
-                    ++stage;
+                        if (shared ? t == x : n[t] > 0) qk(t, k_stage, groups_of(x));
+                    commit(kBarKEmpty + k_stage % kRing);
+                    ++k_stage;
                 }
                 if (!ok) break;
                 if (n_kv == firsts) commit(kBarQEmpty);
                 for (int j = 0; j < n_kv && ok; ++j) {
-                    const uint32_t v_stage = stage, k_stage = stage + 1;
                     const int k_tile = j + (shared ? 2 : 1);
                     const bool more = k_tile < n_kv;
-                    if (!(ok = landed(v_stage))) break;
-                    const uint32_t v = base + PromptSmem::ring + (v_stage % kRing) * kOperand;
-                    const int groups = groups_of(j);
+                    if (!(ok = wait(kBarVFull + v_stage % kRing, v_stage / kRing))) break;
+                    const uint32_t v = base + PromptSmem::values + (v_stage % kRing) * kOperand;
+                    const int groups = groups_of(j), local = shared ? j >> 1 : j;
                     clean_tail(v, j, groups);
-                    if (more && !(ok = landed(k_stage))) break;
-                    for (int t = 0; t < 2 && ok; ++t) {
-                        const int local = shared ? j >> 1 : j;
+                    bool k_here = false;
+                    for (int t = 0; t < 2; ++t) {
                         if (shared ? t != (j & 1) : j >= n[t]) continue;
                         if (!(ok = pv(t, v, groups, local))) break;
-                        if (local + 1 < n[t]) qk(t, k_stage, groups_of(k_tile));
+                        if (local + 1 < n[t]) {
+                            if (!k_here && !(ok = k_landed())) break;
+                            k_here = true;
+                            qk(t, k_stage, groups_of(k_tile));
+                        }
                     }
                     if (!ok) break;
-                    commit(kBarKvEmpty + v_stage % kRing);
-                    if (more) commit(kBarKvEmpty + k_stage % kRing);
-                    if (more && k_tile + 1 == n_kv) commit(kBarQEmpty);  // the item's last Q K^T has been issued
-                    stage += more ? 2 : 1;
+                    commit(kBarVEmpty + v_stage % kRing);
+                    ++v_stage;
+                    if (more) {  // (some group always takes the next K tile)
+                        commit(kBarKEmpty + k_stage % kRing);
+                        ++k_stage;
+                        if (k_tile + 1 == n_kv) commit(kBarQEmpty);  // the item's last Q K^T has been issued
+                    }
                 }
             }
             if (!ok) {  // MMAs in flight end before tensor memory is freed (bounded)
