@@ -748,7 +748,7 @@ PKV_API int pkv_rope_append(void *q_out, int64_t q_out_stride, const void *q, in
  *     out[t][hq] = softmax over the positions at or before t's (scale q[t][hq] . K) . V
  * head_dim PKV_HEAD_DIM, 1, 2, 4 or 8 q heads per kv head, scale > 0.  q rows may be strided
  * (q_stride elements between tokens, a multiple of 8); out is [total_q][num_q_heads][head_dim],
- * contiguous and 32-byte aligned; lse, if not NULL, receives float32 [total_q][num_q_heads], the natural logarithm of
+ * contiguous; lse, if not NULL, receives float32 [total_q][num_q_heads], the natural logarithm of
  * each row's sum of exponentials.  Request b owns rows query_start[b] .. query_start[b + 1] - 1
  * (DEVICE int32 [num_seqs + 1]; empty ranges allowed); rows outside every range are left as they were.
  * A range that is negative, longer than max_query_len or past total_q is skipped and recorded as

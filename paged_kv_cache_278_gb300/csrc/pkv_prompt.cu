@@ -59,6 +59,7 @@ constexpr int kMmaWarp = kSoftmaxWarps, kLoadWarp = kSoftmaxWarps + 1, kValueWar
 constexpr float kLazy = 8.0f;              // log2 units
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kMaxSplits = 64;
+constexpr int kPlannedSms = 152;  // the split plan, and with it the workspace, is the same on every device
 
 struct PromptParams {
     __half *out;
@@ -69,7 +70,8 @@ struct PromptParams {
     float *o_part, *m_part, *l_part;  // splits > 1: [total_q][Hq][splits](x 128), m in log2 units
     int num_seqs, total_q, max_query_len, max_blocks, num_q_heads, num_kv_heads, block_size;
     int64_t num_blocks;
-    int group_log2, box_rows, splits;
+    int group_log2, box_rows;
+    int splits;  // at most; the kernels take split_count of it
     float q_scale;                // scale * log2(e)
     CUtensorMap tmap_q, tmap_k, tmap_v;
 };
@@ -85,6 +87,7 @@ struct Item {
     int kv_first, kv_count[2];
     int shared;     // 1: the groups share tile A, taking its key tiles in turn
 };
+static_assert(sizeof(Item) == 48, "read as three 16-byte pieces");
 
 struct PromptSmem {
     static constexpr int q = 0;                              // two operand tiles
@@ -95,7 +98,9 @@ struct PromptSmem {
     static constexpr int tmem_slot = bars + n_bars * 8;
     static constexpr int items = (tmem_slot + 4 + 15) / 16 * 16;
     static constexpr int state = items + 2 * static_cast<int>(sizeof(Item));  // [2 groups][128 rows] (m, l)
-    static constexpr int total = state + 2 * kTileRows * 8;
+    static constexpr int staging = (state + 2 * kTileRows * 8 + 127) / 128 * 128;  // [8 warps][32 rows][128 bytes]
+    static constexpr int total = staging + kSoftmaxWarps * 32 * 128;
+    static_assert(total <= 227 * 1024, "a CTA's shared memory");
 };
 
 // Barriers by index.
@@ -219,11 +224,18 @@ __device__ __forceinline__ bool elected() {
     return p != 0;
 }
 
-// A 32-byte store: one whole sector from one thread.
-__device__ __forceinline__ void store_sector(void *p, const uint32_t (&r)[8]) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
-                 "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+__device__ __forceinline__ void tma_prefetch_3d(const void *tensor_map, int x, int y, int z) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global [%0, {%1, %2, %3}];" ::"l"(tensor_map), "r"(x), "r"(y), "r"(z)
                  : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128v(uint32_t addr) {  // ordered behind the barrier that published it
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
 // The request's new tokens and context, checked; a bad one counts as no tokens.
@@ -245,26 +257,39 @@ __device__ __forceinline__ Request request_of(const PromptParams &P, int b, bool
     return r;
 }
 
-// Pairs of tiles at or past level `level` of every request (all lanes get the sum).
-__device__ __forceinline__ int pairs_from(const PromptParams &P, int level, int pair_tokens, int lane, bool report) {
+// Pairs of tiles of a request whose last key tile is `tile` or a later one.
+__device__ __forceinline__ int pairs_past(const Request &r, int tile, int pair_tokens) {
+    const int pairs = (r.tokens + pair_tokens - 1) / pair_tokens;
+    const int64_t need = static_cast<int64_t>(tile) * kTileRows + 1 - (r.keys - r.tokens);  // tokens up to the pair's end
+    if (need <= 0) return pairs;
+    if (r.tokens < need) return 0;
+    return pairs - (static_cast<int>(need) + pair_tokens - 1) / pair_tokens + 1;
+}
+
+// The same over every request (all lanes get the sum).
+__device__ __forceinline__ int pairs_from(const PromptParams &P, int tile, int pair_tokens, int lane, bool report) {
     int c = 0;
-    for (int b = lane; b < P.num_seqs; b += 32) {
-        const int pairs = (request_of(P, b, report).tokens + pair_tokens - 1) / pair_tokens;
-        c += max(0, pairs - level);
-    }
+    for (int b = lane; b < P.num_seqs; b += 32) c += pairs_past(request_of(P, b, report), tile, pair_tokens);
     return __reduce_add_sync(pkv::kFullMask, c);
 }
 
-// Item `index` of the call: pairs from the last level to the first (long rows first), for each the kv
-// heads and the splits.
-__device__ Item find_item(const PromptParams &P, int64_t index, int lane) {
+// Splits of each item's keys: two items per SM (the longer ones come first), from the call's actual
+// pairs, which the host does not know; the same in every CTA and in the joining launch.
+__device__ __forceinline__ int split_count(const PromptParams &P, int pairs) {
+    if (P.splits <= 1) return 1;
+    return max(min(P.splits, 2 * kPlannedSms / max(pairs * P.num_kv_heads, 1)), 2);
+}
+
+// Item `index` of the call: pairs by their last key tile, from the last to the first (the longest first), for
+// each the kv heads and the splits.
+__device__ Item find_item(const PromptParams &P, int64_t index, int splits, int tiles, int lane) {
     const int tile_tokens = kTileRows >> P.group_log2, pair_tokens = 2 * tile_tokens;
     Item it{};
-    it.split = static_cast<int>(index % P.splits);
-    it.kvh = static_cast<int>(index / P.splits % P.num_kv_heads);
-    const int rank = static_cast<int>(index / P.splits / P.num_kv_heads);
-    int lo = 0, hi = (P.max_query_len + pair_tokens - 1) / pair_tokens;  // pairs_from(lo) > rank >= pairs_from(hi)
-    int past = 0;                                                        // pairs_from(hi)
+    it.split = static_cast<int>(index % splits);
+    it.kvh = static_cast<int>(index / splits % P.num_kv_heads);
+    const int rank = static_cast<int>(index / splits / P.num_kv_heads);
+    int lo = 0, hi = tiles;  // pairs_from(lo) > rank >= pairs_from(hi) = past
+    int past = 0;
     while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
         const int c = pairs_from(P, mid, pair_tokens, lane, false);
@@ -275,24 +300,37 @@ __device__ Item find_item(const PromptParams &P, int64_t index, int lane) {
             past = c;
         }
     }
-    int nth = rank - past;  // which of the requests that have a pair at level lo
-    int seq = -1;
+    int nth = rank - past;  // which of the pairs that end in tile lo
+    int seq = -1, pair = 0;
     for (int b0 = 0; b0 < P.num_seqs; b0 += 32) {
         const int b = b0 + lane;
-        const bool has = b < P.num_seqs && request_of(P, b, false).tokens > lo * pair_tokens;
-        const uint32_t mask = __ballot_sync(pkv::kFullMask, has);
-        const int c = __popc(mask);
-        if (nth < c) {
-            uint32_t m = mask;
-            for (int i = 0; i < nth; ++i) m &= m - 1;
-            seq = b0 + __ffs(m) - 1;
-            break;
+        int here = 0, last = 0;  // pairs of request b that end in tile lo, and the last of them
+        if (b < P.num_seqs) {
+            const Request r = request_of(P, b, false);
+            const int later = pairs_past(r, lo + 1, pair_tokens);
+            here = pairs_past(r, lo, pair_tokens) - later;
+            last = (r.tokens + pair_tokens - 1) / pair_tokens - later - 1;
         }
-        nth -= c;
+        int upto = here;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int y = __shfl_up_sync(pkv::kFullMask, upto, d);
+            if (lane >= d) upto += y;
+        }
+        const int all = __shfl_sync(pkv::kFullMask, upto, 31);
+        if (nth >= all) {
+            nth -= all;
+            continue;
+        }
+        const int who = __ffs(__ballot_sync(pkv::kFullMask, nth < upto)) - 1;
+        seq = b0 + who;
+        pair = __shfl_sync(pkv::kFullMask, last + (upto - here), who) - nth;
+        break;
     }
     it.seq = seq;
+    if (seq < 0) return it;
     const Request r = request_of(P, seq, false);
-    const int t0 = lo * pair_tokens;
+    const int t0 = pair * pair_tokens;
     it.row0 = r.start + t0;
     it.pos0 = r.keys - r.tokens + t0;
     it.keys = r.keys;
@@ -303,7 +341,7 @@ __device__ Item find_item(const PromptParams &P, int64_t index, int lane) {
         if (it.live[t] > 0) count[t] = (it.pos0 + t * tile_tokens + it.live[t] - 1) / kTileRows + 1;
     }
     const int all = max(count[0], count[1]);
-    const int per = (all + P.splits - 1) / P.splits;
+    const int per = (all + splits - 1) / splits;
     it.kv_first = it.split * per;
     const int end = min(all, it.kv_first + per);
 #pragma unroll
@@ -393,7 +431,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
         if (warp == kLoadWarp) {
             // ---------------------------------------------------------------- items, Q and K
             const int pairs = pairs_from(P, 0, 2 * tile_tokens, lane, blockIdx.x == 0);
-            const int64_t n_items = static_cast<int64_t>(pairs) * P.num_kv_heads * P.splits;
+            const int splits = split_count(P, pairs);
+            int tiles = 0;  // key tiles of the longest context
+            for (int b = lane; b < P.num_seqs; b += 32) {
+                const Request r = request_of(P, b, false);
+                if (r.tokens > 0) tiles = max(tiles, (r.keys + kTileRows - 1) / kTileRows);
+            }
+            tiles = __reduce_max_sync(pkv::kFullMask, tiles);
+            const int64_t n_items = static_cast<int64_t>(pairs) * P.num_kv_heads * splits;
             uint32_t stage = 0, loaded = 0;  // K stages filled, items with keys (one Q each)
             bool ok = true;
             // Item k of this CTA, the rounds in alternating direction: not always the longest of its round.
@@ -401,7 +446,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                 const int64_t index = static_cast<int64_t>(k) * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
                 Item it{};
                 it.seq = -1;
-                if (index < n_items) it = find_item(P, index, lane);
+                if (index < n_items) it = find_item(P, index, splits, tiles, lane);
                 return it;
             };
             Item next = nth_item(0);
@@ -424,17 +469,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                     continue;
                 }
                 int row = box_row(it.seq, it.kvh, it.keys, it.kv_first);
-                if (!(ok = wait(kBarQEmpty, loaded + 1))) break;
-                ++loaded;
-                if (lane == 0) {
-                    const int tiles = it.shared ? 1 : 2;
-                    pkv::mbar_arrive_expect_tx(bar(kBarQFull), tiles * kOperand);
-                    for (int t = 0; t < tiles; ++t)
-                        for (int half = 0; half < 2; ++half)
-                            pkv::tma_load_3d(base + PromptSmem::q + t * kOperand + half * kSlab, &P.tmap_q, 64 * half, it.kvh << glog,
-                                             it.row0 + t * tile_tokens, bar(kBarQFull));
-                }
-                __syncwarp();
                 for (int j = 0; j < n_kv; ++j, ++stage) {
                     const int tile = it.kv_first + j, st = stage % kRing;
                     const int ahead = j + 1 < n_kv ? box_row(it.seq, it.kvh, it.keys, tile + 1) : 0;
@@ -442,7 +476,24 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                     copy_tile(&P.tmap_k, base + PromptSmem::ring + st * kOperand, bar(kBarKFull + st), it.keys, it.kvh, tile,
                               it.row0 - it.pos0, row);
                     row = ahead;
-                    if (j == 0) next = nth_item(k + 1);  // while the copies run
+                    if (j > 0) continue;
+                    // The first K tile is under way: Q, once the last item's Q K^T are done, and the next item, whose Q
+                    // is brought near meanwhile.
+                    if (!(ok = wait(kBarQEmpty, loaded + 1))) break;
+                    ++loaded;
+                    if (lane == 0) {
+                        const int tiles = it.shared ? 1 : 2;
+                        pkv::mbar_arrive_expect_tx(bar(kBarQFull), tiles * kOperand);
+                        for (int t = 0; t < tiles; ++t)
+                            for (int half = 0; half < 2; ++half)
+                                pkv::tma_load_3d(base + PromptSmem::q + t * kOperand + half * kSlab, &P.tmap_q, 64 * half, it.kvh << glog,
+                                                 it.row0 + t * tile_tokens, bar(kBarQFull));
+                    }
+                    __syncwarp();
+                    next = nth_item(k + 1);
+                    if (next.seq >= 0 && lane < (next.shared ? 2 : 4))
+                        tma_prefetch_3d(&P.tmap_q, 64 * (lane & 1), next.kvh << glog, next.row0 + (lane >> 1) * tile_tokens);
+                    __syncwarp();
                 }
             }
             if (!ok) {  // copies still in flight land before the CTA's memory goes (bounded)
@@ -604,12 +655,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
         for (uint32_t k = 0; ok; ++k) {
             const int slot = k & 1;
             if (!(ok = wait(kBarItemFull + slot, k >> 1))) break;
-            const int seq = slots[slot].seq, kvh = slots[slot].kvh, split = slots[slot].split, first = slots[slot].kv_first;
-            const int n = slots[slot].kv_count[t], n_of_other = slots[slot].kv_count[t ^ 1], live = slots[slot].live[t];
-            const bool shared = slots[slot].shared != 0;
+            const uint4 i0 = lds128v(base + PromptSmem::items + slot * sizeof(Item)), i1 = lds128v(base + PromptSmem::items + slot * sizeof(Item) + 16),
+                        i2 = lds128v(base + PromptSmem::items + slot * sizeof(Item) + 32);
+            const int seq = i0.x, kvh = i0.y, split = i0.z, slot_row0 = i0.w;
+            const int live = t ? i1.y : i1.x, pos0 = i1.z, first = i2.x;
+            const int n = t ? i2.z : i2.y, n_of_other = t ? i2.y : i2.z;
+            const bool shared = i2.w != 0;
             const int tile = shared ? 0 : t;
-            const int tile_pos = slots[slot].pos0 + tile * tile_tokens;  // position of the tile's first token
-            const int64_t q_row = slots[slot].row0 + tile * tile_tokens + tok;
+            const int tile_pos = pos0 + tile * tile_tokens;  // position of the tile's first token
+            const int64_t q_row = static_cast<int64_t>(slot_row0) + tile * tile_tokens + tok;
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kBarItemEmpty + slot));
             if (seq < 0) break;
@@ -716,6 +770,16 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
             const int c_begin = shared ? t * (kDim / 2) : 0, c_end = shared ? c_begin + kDim / 2 : kDim;
             const uint32_t t_other = tmem + lanes + 2 * kTileRows + (t ^ 1) * kDim;
             if (n > 0 || n_other > 0) {
+                // 128 bytes of each row at a time (64 fp16 dims, or 32 float32 ones of a partial result) through the
+                // warp's own 4 KB, so that eight lanes store a whole line: stores of 32 bytes from every row at
+                // once took 3000 cycles an item.  The 16-byte pieces of row r lie at piece ^ (r % 8).
+                const bool whole = P.splits == 1;
+                const int per_line = whole ? 64 : 32;
+                const uint32_t lines = base + PromptSmem::staging + warp * 4096;
+                const int64_t first_row = slot_row0 + tile * tile_tokens;
+                unsigned char *const dst = reinterpret_cast<unsigned char *>(whole ? static_cast<void *>(P.out) : static_cast<void *>(P.o_part));
+                const int64_t row_bytes = whole ? kDim * 2 : static_cast<int64_t>(P.splits) * kDim * 4;
+                const int64_t begin_bytes = whole ? 0 : static_cast<int64_t>(split) * kDim * 4;
 #pragma unroll 1
                 for (int c = c_begin; c < c_end; c += 32) {
                     uint32_t o[32];
@@ -734,25 +798,34 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
 #pragma unroll
                         for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(fmaf(__uint_as_float(q[i]), w_other, __uint_as_float(o[i])));
                     }
-                    if (!store) continue;
-                    if (P.splits == 1) {
+                    const uint32_t mine = lines + lane * 128;
+                    if (whole) {
+                        const int half = (c / 32) & 1;
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            uint32_t w[8];
+                        for (int u = 0; u < 4; ++u) {
+                            uint32_t w[4];
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const __half2 v = __floats2half2_rn(__uint_as_float(o[16 * h + 2 * i]), __uint_as_float(o[16 * h + 2 * i + 1]));
+                            for (int i = 0; i < 4; ++i) {
+                                const __half2 v = __floats2half2_rn(__uint_as_float(o[8 * u + 2 * i]), __uint_as_float(o[8 * u + 2 * i + 1]));
                                 w[i] = *reinterpret_cast<const uint32_t *>(&v);
                             }
-                            store_sector(P.out + row * kDim + c + 16 * h, w);
+                            sts128(mine + (((4 * half + u) ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
                         }
+                        if (!half) continue;
                     } else {
 #pragma unroll
-                        for (int h = 0; h < 4; ++h) {
-                            uint32_t w[8];
+                        for (int u = 0; u < 8; ++u) sts128(mine + ((u ^ (lane & 7)) << 4), o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+                    }
+                    __syncwarp();
+                    const int line = c / per_line;
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) w[i] = o[8 * h + i];
-                            store_sector(P.o_part + (row * P.splits + split) * kDim + c + 8 * h, w);
+                    for (int i = 0; i < 8; ++i) {
+                        const int rr = 4 * i + (lane >> 3), piece = lane & 7;
+                        const int tile_row = (warp & 3) * 32 + rr;
+                        const uint4 v = lds128v(lines + rr * 128 + ((piece ^ (rr & 7)) << 4));
+                        if ((tile_row >> glog) < live) {
+                            const int64_t to = (first_row + (tile_row >> glog)) * P.num_q_heads + (kvh << glog) + (tile_row & ((1 << glog) - 1));
+                            *reinterpret_cast<uint4 *>(dst + to * row_bytes + begin_bytes + line * 128 + piece * 16) = v;
                         }
                     }
                 }
@@ -788,36 +861,55 @@ constexpr int kJoinThreads = 256;
 __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const __grid_constant__ PromptParams P) {
     pkv::pdl_wait_primary();
     pkv::pdl_launch_dependents();
-    const Request r = request_of(P, blockIdx.y, false);
+    __shared__ int s_splits;
     const int lane = threadIdx.x & 31;
+    if (threadIdx.x < 32) {
+        const int n = split_count(P, pairs_from(P, 0, 2 * kTileRows >> P.group_log2, lane, false));
+        if (lane == 0) s_splits = n;
+    }
+    __syncthreads();
+    const Request r = request_of(P, blockIdx.y, false);
     const int64_t i = static_cast<int64_t>(blockIdx.x) * (kJoinThreads / 32) + (threadIdx.x >> 5);
     if (i >= static_cast<int64_t>(r.tokens) * P.num_q_heads) return;
     const int64_t row = static_cast<int64_t>(r.start) * P.num_q_heads + i;
+    const int splits = s_splits;
     const float *m = P.m_part + row * P.splits, *l = P.l_part + row * P.splits;
-    float top = -INFINITY;
-    for (int s = lane; s < P.splits; s += 32) top = fmaxf(top, __ldcg(m + s));
+    // lane s holds splits s and s + 32: all of the row's (m, l) in one round of loads
+    float ms[2], ls[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const int s = lane + 32 * u;
+        ms[u] = s < splits ? __ldcg(m + s) : -INFINITY;
+        ls[u] = s < splits ? __ldcg(l + s) : 0.f;
+    }
+    float top = fmaxf(ms[0], ms[1]);
 #pragma unroll
     for (int sh = 16; sh >= 1; sh >>= 1) top = fmaxf(top, __shfl_xor_sync(pkv::kFullMask, top, sh));
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float total = 0.f;
-    for (int s0 = 0; s0 < P.splits; s0 += 4) {
-        float4 o[4];
-        float w[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+    for (int u = 0; u < 2; ++u) {
+        ls[u] = ls[u] == 0.f ? 0.f : ls[u] * exp2f(ms[u] - top);  // a split without visible keys wrote no output
+        total += ls[u];
+    }
+#pragma unroll
+    for (int sh = 16; sh >= 1; sh >>= 1) total += __shfl_xor_sync(pkv::kFullMask, total, sh);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s0 = 0; s0 < splits; s0 += 8) {
+        float4 o[8];
+        float w[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
             const int s = s0 + u;
-            const float ls = s < P.splits ? __ldcg(l + s) : 0.f;
-            w[u] = ls == 0.f ? 0.f : ls * exp2f(__ldcg(m + s) - top);  // a split without visible keys wrote no output
-            o[u] = ls == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
-                             : __ldcg(reinterpret_cast<const float4 *>(P.o_part + (row * P.splits + s) * kDim) + lane);
+            w[u] = __shfl_sync(pkv::kFullMask, s < 32 ? ls[0] : ls[1], s & 31);
+            o[u] = w[u] == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                               : __ldcg(reinterpret_cast<const float4 *>(P.o_part + (row * P.splits + s) * kDim) + lane);
         }
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < 8; ++u) {
             acc.x = fmaf(w[u], o[u].x, acc.x);
             acc.y = fmaf(w[u], o[u].y, acc.y);
             acc.z = fmaf(w[u], o[u].z, acc.z);
             acc.w = fmaf(w[u], o[u].w, acc.w);
-            total += w[u];
         }
     }
     const float inv = 1.f / total;
@@ -1198,16 +1290,16 @@ int encode_rows(CUtensorMap *map, const void *base, int64_t rows, int64_t cols, 
     return encode_map(map, 2, base, dims, strides, box);
 }
 
-constexpr int kPlannedSms = 152;  // the plan, and with it the workspace, is the same on every device
 
-// Splits of each item's keys: 1 when the items fill half of the SMs or the contexts are short (under
-// 512 keys a split, the second launch and the partial results cost more than they save).
+// The most splits of each item's keys: 1 when the items fill half of the SMs or the contexts are short (under
+// 512 keys a split, the second launch and the partial results cost more than they save), else what
+// gives four items per SM by the most pairs that total_q rows can make.
 int plan_splits(int num_seqs, int total_q, int num_q_heads, int num_kv_heads, int max_context) {
     const int pair_tokens = 2 * kTileRows / (num_q_heads / num_kv_heads);
     const int64_t items = (static_cast<int64_t>(total_q) / pair_tokens + num_seqs) * num_kv_heads;
     if (2 * items > kPlannedSms) return 1;
     const int64_t by_keys = max_context / 512;
-    int64_t s = 2 * kPlannedSms / (items > 0 ? items : 1);  // two items per SM, the longer ones first
+    int64_t s = 4 * kPlannedSms / (items > 0 ? items : 1);
     s = s < by_keys ? s : by_keys;
     s = s < kMaxSplits ? s : kMaxSplits;
     return s > 1 ? static_cast<int>(s) : 1;
@@ -1312,7 +1404,7 @@ extern "C" PKV_API int pkv_prefill_attention(void *out, float *lse, const void *
     int st = check_prompt(lse, q, q_stride, seq_start, num_seqs, total_tokens, max_seq_len, num_q_heads, num_kv_heads,
                           head_dim, scale, &done);
     if (st != PKV_OK || done) return st;
-    if (!out || !pkv_internal::aligned(out, 32)) return PKV_ERR_INVALID_ARG;
+    if (!out || !pkv_internal::aligned16(out)) return PKV_ERR_INVALID_ARG;
     const int64_t least = static_cast<int64_t>(num_kv_heads) * head_dim;
     if (!k || !v || !pkv_internal::aligned16(k) || !pkv_internal::aligned16(v) || k_stride % 8 != 0 || v_stride % 8 != 0 ||
         k_stride < least || v_stride < least)
@@ -1349,7 +1441,7 @@ extern "C" PKV_API int pkv_prefill_attention_paged(void *out, float *lse, const 
     st = check_prompt(lse, q, q_stride, query_start, num_seqs, total_q, max_query_len, num_q_heads, num_kv_heads, head_dim,
                       scale, &done);
     if (st != PKV_OK || done) return st;
-    if (!out || !pkv_internal::aligned(out, 32)) return PKV_ERR_INVALID_ARG;
+    if (!out || !pkv_internal::aligned16(out)) return PKV_ERR_INVALID_ARG;
     const int64_t rows = num_blocks * num_kv_heads * block_size;
     if (rows >= 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;  // box row coordinates are signed 32-bit
     PromptParams p{};

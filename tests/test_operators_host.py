@@ -144,7 +144,7 @@ def test_prompt_refusals(lib, name, good):
         assert call(lib, name, one, **{key: NULL}) == INVALID, key
         assert call(lib, name, one, **{key: BAD}) == INVALID, key
     if "out" in good:
-        assert call(lib, name, one, out=ctypes.c_void_p(4096 + 16)) == INVALID  # 32-byte stores
+        assert call(lib, name, one, out=ctypes.c_void_p(4096 + 8)) == INVALID  # 16-byte stores
     for key in ("qs", "ks", "vs"):
         if key in good:
             for stride in (good[key] - 8, good[key] + 4):
