@@ -25,8 +25,8 @@
 //       one warp issuing both K's and V's held the MMAs up.
 //
 // Work items are (pair of tiles, kv head, split of the keys), dealt to one persistent CTA per SM,
-// the longest first and in alternating direction, so that CTAs end together: warp 9 finds the next item
-// while the others work.  Calls with too few items to fill the SMs split each item's keys; partial
+// the longest first and in alternating direction, so that CTAs end together: warp 11 finds them, a few
+// ahead of the others.  Calls with too few items to fill the SMs split each item's keys; partial
 // results are joined by a second launch.
 //
 // Keys past the context are never multiplied: the last key tile's MMAs stop at its 16-key group and
@@ -52,10 +52,12 @@ constexpr int kTileRows = 128;             // query rows per tile (M) and keys p
 constexpr int kSlab = kTileRows * 128;     // 128 rows x 64 fp16 dims, 128-byte swizzle
 constexpr int kOperand = 2 * kSlab;        // a whole 128 x 128 fp16 operand tile
 constexpr int kRing = 2;                   // stages of K, and of V
+constexpr int kItems = 4;                  // work items found ahead
 constexpr int kSoftmaxWarps = 8;
 constexpr int kPromptThreads = 32 * (kSoftmaxWarps + 4);  // three warpgroups
 constexpr int kSoftmaxRegs = 200, kOtherRegs = 88;  // launch: 384 x 168 = 64,512 registers; 256 x 200 + 128 x 88 = 62,464
-constexpr int kMmaWarp = kSoftmaxWarps, kLoadWarp = kSoftmaxWarps + 1, kValueWarp = kSoftmaxWarps + 2;
+constexpr int kMmaWarp = kSoftmaxWarps, kLoadWarp = kSoftmaxWarps + 1, kValueWarp = kSoftmaxWarps + 2,
+              kItemWarp = kSoftmaxWarps + 3;
 constexpr float kLazy = 8.0f;              // log2 units
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kMaxSplits = 64;
@@ -77,7 +79,7 @@ struct PromptParams {
 };
 
 // One unit of work; `kv_count` per softmax group is 0 for a group without rows or without keys here.
-struct Item {
+struct alignas(16) Item {
     int seq;        // -1: no more items
     int kvh, split;
     int row0;       // q row (token) of the pair's first token
@@ -94,10 +96,10 @@ struct PromptSmem {
     static constexpr int ring = 2 * kOperand;
     static constexpr int values = ring + kRing * kOperand;   // ring: K stages, values: V stages
     static constexpr int bars = values + kRing * kOperand;
-    static constexpr int n_bars = 4 * kRing + 2 + 4 + 8 + 2 + 1;
+    static constexpr int n_bars = 4 * kRing + 2 + 2 * kItems + 8 + 2 + 1;
     static constexpr int tmem_slot = bars + n_bars * 8;
     static constexpr int items = (tmem_slot + 4 + 15) / 16 * 16;
-    static constexpr int state = items + 2 * static_cast<int>(sizeof(Item));  // [2 groups][128 rows] (m, l)
+    static constexpr int state = items + kItems * static_cast<int>(sizeof(Item));  // [2 groups][128 rows] (m, l)
     static constexpr int staging = (state + 2 * kTileRows * 8 + 127) / 128 * 128;  // [8 warps][32 rows][128 bytes]
     static constexpr int total = staging + kSoftmaxWarps * 32 * 128;
     static_assert(total <= 227 * 1024, "a CTA's shared memory");
@@ -105,7 +107,7 @@ struct PromptSmem {
 
 // Barriers by index.
 constexpr int kBarKFull = 0, kBarKEmpty = kRing, kBarVFull = 2 * kRing, kBarVEmpty = 3 * kRing, kBarQFull = 4 * kRing, kBarQEmpty = kBarQFull + 1,
-              kBarItemFull = kBarQEmpty + 1, kBarItemEmpty = kBarItemFull + 2, kBarS = kBarItemEmpty + 2, kBarP = kBarS + 2,
+              kBarItemFull = kBarQEmpty + 1, kBarItemEmpty = kBarItemFull + kItems, kBarS = kBarItemEmpty + kItems, kBarP = kBarS + 2,
               kBarO = kBarP + 4, kBarState = kBarO + 2, kBarJoined = kBarState + 1, kBarDrain = kBarJoined + 1;
 
 // ---- TMEM moves (one row per lane, consecutive 32-bit columns)
@@ -372,7 +374,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
     if (threadIdx.x == 0) {
         for (int i = 0; i < PromptSmem::n_bars; ++i) {
             uint32_t count = 1;
-            if (i == kBarItemEmpty || i == kBarItemEmpty + 1) count = kSoftmaxWarps + 2;
+            if (i >= kBarItemEmpty && i < kBarItemEmpty + kItems) count = kSoftmaxWarps + 3;
             if (i >= kBarP && i < kBarP + 4) count = 4;  // one arrival per softmax warp of the tile
             if (i == kBarState || i == kBarJoined) count = kSoftmaxWarps;
             pkv::mbar_init(bar(i), count);
@@ -428,8 +430,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
             }
             __syncwarp();
         };
-        if (warp == kLoadWarp) {
-            // ---------------------------------------------------------------- items, Q and K
+        if (warp == kItemWarp) {
+            // ---------------------------------------------------------------- work items, up to kItems ahead
             const int pairs = pairs_from(P, 0, 2 * tile_tokens, lane, blockIdx.x == 0);
             const int splits = split_count(P, pairs);
             int tiles = 0;  // key tiles of the longest context
@@ -438,22 +440,16 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                 if (r.tokens > 0) tiles = max(tiles, (r.keys + kTileRows - 1) / kTileRows);
             }
             tiles = __reduce_max_sync(pkv::kFullMask, tiles);
-            const int64_t n_items = static_cast<int64_t>(pairs) * P.num_kv_heads * splits;
-            uint32_t stage = 0, loaded = 0;  // K stages filled, items with keys (one Q each)
+            const uint32_t n_items = static_cast<uint32_t>(pairs) * P.num_kv_heads * splits;  // (bounded by the host)
             bool ok = true;
-            // Item k of this CTA, the rounds in alternating direction: not always the longest of its round.
-            auto nth_item = [&](uint32_t k) {
-                const int64_t index = static_cast<int64_t>(k) * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+            for (uint32_t k = 0; ok; ++k) {
+                // the rounds go in alternating direction: a CTA's items are not always the longest of their round
+                const uint32_t index = k * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
                 Item it{};
                 it.seq = -1;
                 if (index < n_items) it = find_item(P, index, splits, tiles, lane);
-                return it;
-            };
-            Item next = nth_item(0);
-            for (uint32_t k = 0; ok; ++k) {
-                const Item it = next;
-                const int slot = k & 1;
-                if (!(ok = wait(kBarItemEmpty + slot, (k >> 1) + 1))) break;
+                const int slot = k % kItems;
+                if (!(ok = wait(kBarItemEmpty + slot, k / kItems + 1))) break;
                 if (lane == 0) {
                     volatile int *d = reinterpret_cast<volatile int *>(slots + slot);
                     const int *s = reinterpret_cast<const int *>(&it);
@@ -463,11 +459,26 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                 }
                 __syncwarp();
                 if (it.seq < 0) break;
-                const int n_kv = key_tiles(it.shared, it.kv_count[0], it.kv_count[1]);
-                if (n_kv == 0) {
-                    next = nth_item(k + 1);
-                    continue;
+            }
+        } else if (warp == kLoadWarp) {
+            // ---------------------------------------------------------------- Q and K
+            uint32_t stage = 0, loaded = 0;  // K stages filled, items with keys (one Q each)
+            bool ok = true;
+            for (uint32_t k = 0; ok; ++k) {
+                const int slot = k % kItems;
+                if (!(ok = wait(kBarItemFull + slot, k / kItems))) break;
+                Item it;
+                {
+                    const uint32_t at = base + PromptSmem::items + slot * sizeof(Item);
+                    uint4 *d = reinterpret_cast<uint4 *>(&it);
+                    d[0] = lds128v(at);
+                    d[1] = lds128v(at + 16);
+                    d[2] = lds128v(at + 32);
                 }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(kBarItemEmpty + slot));
+                if (it.seq < 0) break;
+                const int n_kv = key_tiles(it.shared, it.kv_count[0], it.kv_count[1]);
                 int row = box_row(it.seq, it.kvh, it.keys, it.kv_first);
                 for (int j = 0; j < n_kv; ++j, ++stage) {
                     const int tile = it.kv_first + j, st = stage % kRing;
@@ -477,8 +488,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                               it.row0 - it.pos0, row);
                     row = ahead;
                     if (j > 0) continue;
-                    // The first K tile is under way: Q, once the last item's Q K^T are done, and the next item, whose Q
-                    // is brought near meanwhile.
+                    // The first K tile is under way: now Q, once the last item's Q K^T are done (it is brought near meanwhile).
+                    if (lane < (it.shared ? 2 : 4))
+                        tma_prefetch_3d(&P.tmap_q, 64 * (lane & 1), it.kvh << glog, it.row0 + (lane >> 1) * tile_tokens);
+                    __syncwarp();
                     if (!(ok = wait(kBarQEmpty, loaded + 1))) break;
                     ++loaded;
                     if (lane == 0) {
@@ -489,10 +502,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                                 pkv::tma_load_3d(base + PromptSmem::q + t * kOperand + half * kSlab, &P.tmap_q, 64 * half, it.kvh << glog,
                                                  it.row0 + t * tile_tokens, bar(kBarQFull));
                     }
-                    __syncwarp();
-                    next = nth_item(k + 1);
-                    if (next.seq >= 0 && lane < (next.shared ? 2 : 4))
-                        tma_prefetch_3d(&P.tmap_q, 64 * (lane & 1), next.kvh << glog, next.row0 + (lane >> 1) * tile_tokens);
                     __syncwarp();
                 }
             }
@@ -506,8 +515,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
             uint32_t stage = 0;
             bool ok = true;
             for (uint32_t k = 0; ok; ++k) {
-                const int slot = k & 1;
-                if (!(ok = wait(kBarItemFull + slot, k >> 1))) break;
+                const int slot = k % kItems;
+                if (!(ok = wait(kBarItemFull + slot, k / kItems))) break;
                 const int seq = slots[slot].seq, kvh = slots[slot].kvh, keys = slots[slot].keys, first = slots[slot].kv_first;
                 const int n_kv = key_tiles(slots[slot].shared != 0, slots[slot].kv_count[0], slots[slot].kv_count[1]);
                 const int first_row = slots[slot].row0 - slots[slot].pos0;
@@ -532,8 +541,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
             uint32_t k_stage = 0, v_stage = 0, loaded = 0, p_count[2] = {0, 0};
             bool ok = true;
             for (uint32_t k = 0; ok; ++k) {
-                const int slot = k & 1;
-                if (!(ok = wait(kBarItemFull + slot, k >> 1))) break;
+                const int slot = k % kItems;
+                if (!(ok = wait(kBarItemFull + slot, k / kItems))) break;
                 const int seq = uniform(slots[slot].seq), keys = uniform(slots[slot].keys), first = uniform(slots[slot].kv_first);
                 const int n[2] = {uniform(slots[slot].kv_count[0]), uniform(slots[slot].kv_count[1])};
                 const bool shared = uniform(slots[slot].shared) != 0;
@@ -653,8 +662,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
         float2 *s_state = reinterpret_cast<float2 *>(smem + PromptSmem::state);
         bool ok = true;
         for (uint32_t k = 0; ok; ++k) {
-            const int slot = k & 1;
-            if (!(ok = wait(kBarItemFull + slot, k >> 1))) break;
+            const int slot = k % kItems;
+            if (!(ok = wait(kBarItemFull + slot, k / kItems))) break;
             const uint4 i0 = lds128v(base + PromptSmem::items + slot * sizeof(Item)), i1 = lds128v(base + PromptSmem::items + slot * sizeof(Item) + 16),
                         i2 = lds128v(base + PromptSmem::items + slot * sizeof(Item) + 32);
             const int seq = i0.x, kvh = i0.y, split = i0.z, slot_row0 = i0.w;
@@ -746,7 +755,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                 pkv::tmem_fence_after_sync();
             }
             const bool store = tok < live;
-            const int64_t row = q_row * P.num_q_heads + (kvh << glog) + (r & ((1 << glog) - 1));
             // The row's state and the two accumulators that make it up: its own alone, or where the groups
             // share the rows both, each group finishing half of the dims.
             float m = m_ref, total = l, w_own = 1.f, w_other = 0.f;
@@ -767,69 +775,86 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
             const float inv = total == 0.f ? 0.f : 1.f / total;
             w_own *= inv;
             w_other *= inv;
-            const int c_begin = shared ? t * (kDim / 2) : 0, c_end = shared ? c_begin + kDim / 2 : kDim;
-            const uint32_t t_other = tmem + lanes + 2 * kTileRows + (t ^ 1) * kDim;
+            const int64_t row = q_row * P.num_q_heads + (kvh << glog) + (r & ((1 << glog) - 1));
             if (n > 0 || n_other > 0) {
                 // 128 bytes of each row at a time (64 fp16 dims, or 32 float32 ones of a partial result) through the
-                // warp's own 4 KB, so that eight lanes store a whole line: stores of 32 bytes from every row at
-                // once took 3000 cycles an item.  The 16-byte pieces of row r lie at piece ^ (r % 8).
+                // warp's own 4 KB, so that eight lanes store a whole line.  The 16-byte pieces of row x lie at piece
+                // ^ (x % 8).  Lane's share of a line: piece lane % 8 of rows 4 i + lane / 8.
                 const bool whole = P.splits == 1;
-                const int per_line = whole ? 64 : 32;
-                const uint32_t lines = base + PromptSmem::staging + warp * 4096;
-                const int64_t first_row = slot_row0 + tile * tile_tokens;
-                unsigned char *const dst = reinterpret_cast<unsigned char *>(whole ? static_cast<void *>(P.out) : static_cast<void *>(P.o_part));
-                const int64_t row_bytes = whole ? kDim * 2 : static_cast<int64_t>(P.splits) * kDim * 4;
-                const int64_t begin_bytes = whole ? 0 : static_cast<int64_t>(split) * kDim * 4;
-#pragma unroll 1
-                for (int c = c_begin; c < c_end; c += 32) {
-                    uint32_t o[32];
-                    __syncwarp();
-                    if (n > 0) {
-                        pkv::tmem_ld32(t_o + c, o);
+                const uint32_t lines = base + PromptSmem::staging + warp * 4096, mine = lines + lane * 128;
+                const uint32_t row_bytes = whole ? kDim * 2 : P.splits * kDim * 4;
+                const int group_mask = (1 << glog) - 1;
+                unsigned char *const dst = reinterpret_cast<unsigned char *>(whole ? static_cast<void *>(P.out) : static_cast<void *>(P.o_part)) +
+                                           ((static_cast<int64_t>(slot_row0) + tile * tile_tokens) * P.num_q_heads + (kvh << glog)) * row_bytes +
+                                           (whole ? 0 : split * kDim * 4) + (lane & 7) * 16;
+                uint32_t offset[8];  // of the lane's rows, from the tile's first (under 2^32: 128 tokens' rows)
+                bool keep[8];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * w_own);
+                for (int i = 0; i < 8; ++i) {
+                    const int x = (warp & 3) * 32 + 4 * i + (lane >> 3);
+                    offset[i] = ((x >> glog) * P.num_q_heads + (x & group_mask)) * row_bytes;
+                    keep[i] = (x >> glog) < live;
+                }
+                auto store_line = [&](int line) {
+                    __syncwarp();
+                    uint4 v[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int x = 4 * i + (lane >> 3);
+                        v[i] = lds128v(lines + x * 128 + (((lane & 7) ^ (x & 7)) << 4));
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (keep[i]) *reinterpret_cast<uint4 *>(dst + offset[i] + line * 128) = v[i];
+                    __syncwarp();
+                };
+                const int c_begin = shared ? t * (kDim / 2) : 0, c_end = shared ? c_begin + kDim / 2 : kDim;
+                const uint32_t t_other = tmem + lanes + 2 * kTileRows + (t ^ 1) * kDim;
+#pragma unroll 1
+                for (int c = c_begin; c < c_end; c += 64) {
+                    uint32_t o[64];
+                    if (n > 0) {
+                        tmem_ld64(t_o + c, o);
+                        tmem_landed(o);
+#pragma unroll
+                        for (int i = 0; i < 64; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * w_own);
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = 0u;
+                        for (int i = 0; i < 64; ++i) o[i] = 0u;
                     }
                     if (n_other > 0) {
-                        uint32_t q[32];
-                        pkv::tmem_ld32(t_other + c, q);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(fmaf(__uint_as_float(q[i]), w_other, __uint_as_float(o[i])));
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t q[32];
+                            pkv::tmem_ld32(t_other + c + 32 * h, q);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                o[32 * h + i] = __float_as_uint(fmaf(__uint_as_float(q[i]), w_other, __uint_as_float(o[32 * h + i])));
+                        }
                     }
-                    const uint32_t mine = lines + lane * 128;
                     if (whole) {
-                        const int half = (c / 32) & 1;
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) {
+                        for (int u = 0; u < 8; ++u) {
                             uint32_t w[4];
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
                                 const __half2 v = __floats2half2_rn(__uint_as_float(o[8 * u + 2 * i]), __uint_as_float(o[8 * u + 2 * i + 1]));
                                 w[i] = *reinterpret_cast<const uint32_t *>(&v);
                             }
-                            sts128(mine + (((4 * half + u) ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
+                            sts128(mine + ((u ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
                         }
-                        if (!half) continue;
+                        store_line(c / 64);
                     } else {
 #pragma unroll
-                        for (int u = 0; u < 8; ++u) sts128(mine + ((u ^ (lane & 7)) << 4), o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
-                    }
-                    __syncwarp();
-                    const int line = c / per_line;
+                        for (int h = 0; h < 2; ++h) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int rr = 4 * i + (lane >> 3), piece = lane & 7;
-                        const int tile_row = (warp & 3) * 32 + rr;
-                        const uint4 v = lds128v(lines + rr * 128 + ((piece ^ (rr & 7)) << 4));
-                        if ((tile_row >> glog) < live) {
-                            const int64_t to = (first_row + (tile_row >> glog)) * P.num_q_heads + (kvh << glog) + (tile_row & ((1 << glog) - 1));
-                            *reinterpret_cast<uint4 *>(dst + to * row_bytes + begin_bytes + line * 128 + piece * 16) = v;
+                            for (int u = 0; u < 8; ++u)
+                                sts128(mine + ((u ^ (lane & 7)) << 4), o[32 * h + 4 * u], o[32 * h + 4 * u + 1], o[32 * h + 4 * u + 2],
+                                       o[32 * h + 4 * u + 3]);
+                            store_line(c / 32 + h);
                         }
                     }
                 }
-                __syncwarp();
                 pkv::tmem_fence_before_sync();  // O read before the next item's first P V (ordered by its weights' arrival)
             }
             if (store && (t == 0 || !shared)) {
