@@ -807,7 +807,7 @@ PKV_API int pkv_decode_attention_weights(void *out, float *scores, int64_t score
 /* The weights of a chunk's rows, as pkv_prefill_attention_paged computed them: for each request's rows
  * query_start[b] .. query_start[b + 1] - 1 (its last n_b cached positions),
  *     scores[b][h][s] += sum over rows t at or after s, q heads of kv head h, of exp(scale q . K[s] - lse[t][hq]).
- * lse is the float32 [total_q][num_q_heads] that call wrote.  Passing only the last rows of a chunk (with their
+ * lse is the float32 [total_q][num_q_heads] that call wrote (16-byte aligned with 4 or 8 q heads per kv head).  Passing only the last rows of a chunk (with their
  * part of lse) accumulates over those alone.  A request without rows keeps its scores; bad requests as
  * pkv_prefill_attention_paged's.  No workspace.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 PKV_API int pkv_prefill_attention_weights(float *scores, int64_t score_capacity, const void *q, int64_t q_stride,

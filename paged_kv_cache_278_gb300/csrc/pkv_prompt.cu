@@ -884,8 +884,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
 // Joins the splits of each (token, head) row: one warp per row, four dims a lane.
 constexpr int kJoinThreads = 256;
 __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const __grid_constant__ PromptParams P) {
-    pkv::pdl_wait_primary();
-    pkv::pdl_launch_dependents();
     __shared__ int s_splits;
     const int lane = threadIdx.x & 31;
     if (threadIdx.x < 32) {
@@ -894,6 +892,10 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const __grid_
     }
     __syncthreads();
     const Request r = request_of(P, blockIdx.y, false);
+    // So far only the call's inputs, which the attention launch (every CTA of which has started, behind its own wait
+    // for what came before) does not write; its partial results from here on.
+    pkv::pdl_wait_primary();
+    pkv::pdl_launch_dependents();
     const int64_t i = static_cast<int64_t>(blockIdx.x) * (kJoinThreads / 32) + (threadIdx.x >> 5);
     if (i >= static_cast<int64_t>(r.tokens) * P.num_q_heads) return;
     const int64_t row = static_cast<int64_t>(r.start) * P.num_q_heads + i;
@@ -919,22 +921,22 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const __grid_
 #pragma unroll
     for (int sh = 16; sh >= 1; sh >>= 1) total += __shfl_xor_sync(pkv::kFullMask, total, sh);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s0 = 0; s0 < splits; s0 += 8) {
-        float4 o[8];
-        float w[8];
+    for (int s0 = 0; s0 < splits; s0 += 16) {
+        float4 o[16];
+        float w[16];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
+        for (int u = 0; u < 16; ++u) {
             const int s = s0 + u;
-            w[u] = __shfl_sync(pkv::kFullMask, s < 32 ? ls[0] : ls[1], s & 31);
-            o[u] = w[u] == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
-                               : __ldcg(reinterpret_cast<const float4 *>(P.o_part + (row * P.splits + s) * kDim) + lane);
+            w[u] = __shfl_sync(pkv::kFullMask, s < 32 ? ls[0] : ls[1], s & 31);  // (0 past the last split)
+            o[u] = __ldcg(reinterpret_cast<const float4 *>(P.o_part + (row * P.splits + min(s, splits - 1)) * kDim) + lane);
         }
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            acc.x = fmaf(w[u], o[u].x, acc.x);
-            acc.y = fmaf(w[u], o[u].y, acc.y);
-            acc.z = fmaf(w[u], o[u].z, acc.z);
-            acc.w = fmaf(w[u], o[u].w, acc.w);
+        for (int u = 0; u < 16; ++u) {
+            const bool written = w[u] != 0.f;  // else the slot holds anything (selected away, so that all loads are in flight)
+            acc.x = fmaf(w[u], written ? o[u].x : 0.f, acc.x);
+            acc.y = fmaf(w[u], written ? o[u].y : 0.f, acc.y);
+            acc.z = fmaf(w[u], written ? o[u].z : 0.f, acc.z);
+            acc.w = fmaf(w[u], written ? o[u].w : 0.f, acc.w);
         }
     }
     const float inv = 1.f / total;
@@ -952,8 +954,9 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const __grid_
 // no atomics, a fixed order.  Bound by the exponentials, one per (row, key) pair (2 x 128 tensor flops),
 // until a chunk is so small that reading K bounds it.
 //   warps 0-3, 4-7  the even and odd row tiles of an item, each with two S^T buffers of 128 TMEM columns
-//   warp 8          issues the MMAs; warp 9 finds items (a 128-key tile of one request and kv head) and
-//                   issues the tensor copies: K tiles (two stages), Q tiles (ring of four)
+//   warp 8          issues the MMAs
+//   warps 9, 10     issue the tensor copies of K tiles (two stages) and of Q tiles (ring of four)
+//   warp 11         finds the items (a 128-key tile of one request and kv head), a few ahead
 struct ChunkWeightParams {
     PromptParams p;
     const float *lse;
@@ -967,21 +970,22 @@ struct ChunkWeightSmem {
     static constexpr int keys = 0;
     static constexpr int rows = kKeyStages * kOperand;
     static constexpr int lse = rows + kRowRing * kOperand;        // [8 warps][128] floats, log2 units
-    static constexpr int sums = lse + kSoftmaxWarps * kTileRows * 4;  // [2 items][128] floats
-    static constexpr int bars = sums + 2 * kTileRows * 4;
-    static constexpr int n_bars = 2 * kKeyStages + 2 * kRowRing + 8 + 4 + 2 + 1;
+    static constexpr int sums = lse + kSoftmaxWarps * kTileRows * 4;  // [kItems][128] floats
+    static constexpr int bars = sums + kItems * kTileRows * 4;
+    static constexpr int n_bars = 2 * kKeyStages + 2 * kRowRing + 8 + 3 * kItems + 1;
     static constexpr int tmem_slot = bars + n_bars * 8;
     static constexpr int items = (tmem_slot + 4 + 15) / 16 * 16;
-    static constexpr int total = items + 2 * 32;
+    static constexpr int total = items + kItems * 32;
 };
 constexpr int kWKeyFull = 0, kWKeyEmpty = kKeyStages, kWRowFull = 2 * kKeyStages, kWRowEmpty = kWRowFull + kRowRing,
-              kWS = kWRowEmpty + kRowRing, kWSFree = kWS + 4, kWItemFull = kWSFree + 4, kWItemEmpty = kWItemFull + 2,
-              kWSum = kWItemEmpty + 2, kWDrain = kWSum + 2;
+              kWS = kWRowEmpty + kRowRing, kWSFree = kWS + 4, kWItemFull = kWSFree + 4, kWItemEmpty = kWItemFull + kItems,
+              kWSum = kWItemEmpty + kItems, kWDrain = kWSum + kItems;
 
 // A 128-key tile of one request and kv head, and the row tiles [first, count) that see some of it.
-struct KeyItem {
+struct alignas(16) KeyItem {
     int seq, kvh, tile, start, tokens, keys, first, count;
 };
+static_assert(sizeof(KeyItem) == 32, "read as two 16-byte pieces");
 
 __device__ KeyItem find_key_item(const PromptParams &P, int64_t index, int lane) {
     KeyItem it{};
@@ -1036,8 +1040,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) chunk_weights_kernel(const 
     if (threadIdx.x == 0) {
         for (int i = 0; i < L::n_bars; ++i) {
             uint32_t count = 1;
-            if ((i >= kWSFree && i < kWSFree + 4) || i == kWSum || i == kWSum + 1) count = 4;
-            if (i == kWItemEmpty || i == kWItemEmpty + 1) count = kSoftmaxWarps + 1;
+            if ((i >= kWSFree && i < kWSFree + 4) || (i >= kWSum && i < kWSum + kItems)) count = 4;
+            if (i >= kWItemEmpty && i < kWItemEmpty + kItems) count = kSoftmaxWarps + 3;
             pkv::mbar_init(bar(i), count);
         }
         pkv::fence_mbar_init();
@@ -1062,50 +1066,80 @@ __global__ void __launch_bounds__(kPromptThreads, 1) chunk_weights_kernel(const 
 
     if (warp >= kSoftmaxWarps) {
         shrink_registers<kOtherRegs>();
-        if (warp == kLoadWarp) {
+        const int boxes_per_tile = kTileRows / P.box_rows;
+        // A published item, its slot released.
+        auto take = [&](uint32_t k, KeyItem &it) {
+            const int slot = k % kItems;
+            if (!wait(kWItemFull + slot, k / kItems)) return false;
+            uint4 *d = reinterpret_cast<uint4 *>(&it);
+            d[0] = lds128v(base + L::items + slot * sizeof(KeyItem));
+            d[1] = lds128v(base + L::items + slot * sizeof(KeyItem) + 16);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kWItemEmpty + slot));
+            return true;
+        };
+        if (warp == kItemWarp) {
+            // ---------------------------------------------------------------- work items, up to kItems ahead
             int tiles = 0;
             for (int b = lane; b < P.num_seqs; b += 32) {
                 const Request r = request_of(P, b, blockIdx.x == 0);
                 tiles += r.tokens > 0 ? (r.keys + kTileRows - 1) / kTileRows : 0;
             }
-            const int64_t n_items = static_cast<int64_t>(__reduce_add_sync(pkv::kFullMask, tiles)) * P.num_kv_heads;
-            const int boxes_per_tile = kTileRows / P.box_rows;
-            uint32_t rows = 0, k = 0;
+            const uint32_t n_items = static_cast<uint32_t>(__reduce_add_sync(pkv::kFullMask, tiles)) * P.num_kv_heads;
             bool ok = true;
-            for (; ok; ++k) {
-                const int64_t index = static_cast<int64_t>(k) * gridDim.x + blockIdx.x;
+            for (uint32_t k = 0; ok; ++k) {
+                const uint32_t index = k * gridDim.x + blockIdx.x;
                 KeyItem it{};
                 it.seq = -1;
                 if (index < n_items) it = find_key_item(P, index, lane);
-                const int slot = k & 1;
-                if (!(ok = wait(kWItemEmpty + slot, (k >> 1) + 1))) break;
+                const int slot = k % kItems;
+                if (!(ok = wait(kWItemEmpty + slot, k / kItems + 1))) break;
                 if (lane == 0) {
                     volatile int *d = reinterpret_cast<volatile int *>(slots + slot);
                     const int *s = reinterpret_cast<const int *>(&it);
-    #pragma unroll
+#pragma unroll
                     for (int i = 0; i < static_cast<int>(sizeof(KeyItem) / 4); ++i) d[i] = s[i];
                     mbar_arrive(bar(kWItemFull + slot));
                 }
                 __syncwarp();
                 if (it.seq < 0) break;
+            }
+        } else if (warp == kLoadWarp) {
+            // ---------------------------------------------------------------- K tiles
+            uint32_t k = 0;
+            bool ok = true;
+            for (; ok; ++k) {
+                KeyItem it;
+                if (!(ok = take(k, it)) || it.seq < 0) break;
+                const int key = it.tile * kTileRows + (lane >> 1) * P.box_rows;
+                int32_t id = 0;
+                if (lane < 2 * boxes_per_tile && key < it.keys)
+                    id = __ldg(P.block_tables + static_cast<int64_t>(it.seq) * P.max_blocks + key / P.block_size);
+                if (id < 0 || id >= P.num_blocks) {
+                    pkv::record_error(&g_prompt_error, PKV_DEV_BAD_BLOCK_ID);
+                    id = 0;
+                }
+                const int64_t row = (static_cast<int64_t>(id) * P.num_kv_heads + it.kvh) * P.block_size + key % P.block_size;
                 const int ks = k % kKeyStages;
                 if (!(ok = wait(kWKeyEmpty + ks, k / kKeyStages + 1))) break;
-                const int valid = min(kTileRows, it.keys - it.tile * kTileRows);
-                const int boxes = (valid + P.box_rows - 1) / P.box_rows;
+                const int boxes = (min(kTileRows, it.keys - it.tile * kTileRows) + P.box_rows - 1) / P.box_rows;
                 if (lane == 0) pkv::mbar_arrive_expect_tx(bar(kWKeyFull + ks), boxes * P.box_rows * 256);
                 __syncwarp();
-                if (lane < 2 * boxes && lane < 2 * boxes_per_tile) {
-                    const int key = it.tile * kTileRows + (lane >> 1) * P.box_rows;
-                    int32_t id = __ldg(P.block_tables + static_cast<int64_t>(it.seq) * P.max_blocks + key / P.block_size);
-                    if (id < 0 || id >= P.num_blocks) {
-                        pkv::record_error(&g_prompt_error, PKV_DEV_BAD_BLOCK_ID);
-                        id = 0;
-                    }
-                    const int64_t row = (static_cast<int64_t>(id) * P.num_kv_heads + it.kvh) * P.block_size + key % P.block_size;
+                if (lane < 2 * boxes)
                     pkv::tma_load_2d(base + L::keys + ks * kOperand + (lane & 1) * kSlab + (lane >> 1) * P.box_rows * 128, &P.tmap_k,
                                      64 * (lane & 1), static_cast<int>(row), bar(kWKeyFull + ks));
-                }
                 __syncwarp();
+            }
+            if (!ok)  // copies still in flight land before the CTA's memory goes (bounded)
+                for (uint32_t s = k > kKeyStages ? k - kKeyStages : 0; s < k; ++s)
+                    wait_phase(bar(kWKeyFull + s % kKeyStages), (s / kKeyStages) & 1);
+        } else if (warp == kValueWarp) {
+            // ---------------------------------------------------------------- Q tiles
+            uint32_t rows = 0;
+            bool ok = true;
+            for (uint32_t k = 0; ok; ++k) {
+                KeyItem it;
+                if (!(ok = take(k, it)) || it.seq < 0) break;
                 for (int i = it.first; i < it.count; ++i) {
                     const int st = rows % kRowRing;
                     if (!(ok = wait(kWRowEmpty + st, rows / kRowRing + 1))) break;
@@ -1119,19 +1153,16 @@ __global__ void __launch_bounds__(kPromptThreads, 1) chunk_weights_kernel(const 
                     __syncwarp();
                 }
             }
-            if (!ok) {  // copies still in flight land before the CTA's memory goes (bounded)
-                for (uint32_t s = k > kKeyStages ? k - kKeyStages : 0; s <= k; ++s)
-                    wait_phase(bar(kWKeyFull + s % kKeyStages), (s / kKeyStages) & 1);
+            if (!ok)
                 for (uint32_t s = rows > kRowRing ? rows - kRowRing : 0; s < rows; ++s)
                     wait_phase(bar(kWRowFull + s % kRowRing), (s / kRowRing) & 1);
-            }
         } else if (warp == kMmaWarp) {
             uint32_t rows = 0;
             uint32_t used[4] = {0, 0, 0, 0};  // times each S^T buffer has been filled
             bool ok = true;
             for (uint32_t k = 0; ok; ++k) {
-                const int slot = k & 1;
-                if (!(ok = wait(kWItemFull + slot, k >> 1))) break;
+                const int slot = k % kItems;
+                if (!(ok = wait(kWItemFull + slot, k / kItems))) break;
                 const int seq = uniform(slots[slot].seq), first = uniform(slots[slot].first), count = uniform(slots[slot].count);
                 const int all_rows = uniform(slots[slot].tokens) << glog;
                 __syncwarp();
@@ -1180,26 +1211,35 @@ __global__ void __launch_bounds__(kPromptThreads, 1) chunk_weights_kernel(const 
         uint32_t seen[2] = {0, 0};  // times this group's two buffers have been read
         bool ok = true;
         for (uint32_t k = 0; ok; ++k) {
-            const int slot = k & 1;
-            if (!(ok = wait(kWItemFull + slot, k >> 1))) break;
-            const int seq = slots[slot].seq, kvh = slots[slot].kvh, tile = slots[slot].tile, start = slots[slot].start;
-            const int tokens = slots[slot].tokens, keys = slots[slot].keys, first = slots[slot].first, count = slots[slot].count;
+            const int slot = k % kItems;
+            if (!(ok = wait(kWItemFull + slot, k / kItems))) break;
+            const uint4 i0 = lds128v(base + L::items + slot * sizeof(KeyItem)), i1 = lds128v(base + L::items + slot * sizeof(KeyItem) + 16);
+            const int seq = i0.x, kvh = i0.y, tile = i0.z, start = i0.w, tokens = i1.x, keys = i1.y, first = i1.z, count = i1.w;
             if (seq < 0) break;
             const int key = tile * kTileRows + key_lane;
             const int rows = tokens << glog;
             float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
-            // minus the lse of four neighbouring columns of row tile i, log2 units
+            // What scores holds, in flight through the whole item.
+            float *const at = W.scores + (static_cast<int64_t>(seq) * P.num_kv_heads + kvh) * W.capacity + key;
+            const float before = grp == 0 && key < keys ? __ldcg(at) : 0.f;
+            // minus the lse of four neighbouring columns of row tile i, log2 units (of one token with 4 heads or more)
+            const float *const lse = W.lse + static_cast<int64_t>(start) * P.num_q_heads + (kvh << glog);
             auto column_lse = [&](int i) {
-                float z[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int c = i * kTileRows + 4 * lane + u;
-                    if (i < count && c < rows)
-                        z[u] = __ldg(W.lse + (static_cast<int64_t>(start) + (c >> glog)) * P.num_q_heads + (kvh << glog) +
-                                     (c & ((1 << glog) - 1))) *
-                               -kLog2e;
+                const int c = i * kTileRows + 4 * lane;
+                float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i < count && c < rows) {  // (rows is a multiple of the group: with 4 heads all four columns are live)
+                    const float *p = lse + (c >> glog) * P.num_q_heads + (c & ((1 << glog) - 1));
+                    if (glog >= 2) {
+                        z = __ldg(reinterpret_cast<const float4 *>(p));
+                    } else {
+                        const int step = glog == 1 ? 1 : P.num_q_heads;  // columns c, c + 1: two heads, or two tokens
+                        z.x = __ldg(p);
+                        if (c + 1 < rows) z.y = __ldg(p + step);
+                        if (c + 2 < rows) z.z = __ldg(p + (glog == 1 ? P.num_q_heads : 2 * step));
+                        if (c + 3 < rows) z.w = __ldg(p + (glog == 1 ? P.num_q_heads + 1 : 3 * step));
+                    }
                 }
-                return make_float4(z[0], z[1], z[2], z[3]);
+                return make_float4(z.x * -kLog2e, z.y * -kLog2e, z.z * -kLog2e, z.w * -kLog2e);
             };
             int i = first + ((first & 1) != grp);
             float4 z = column_lse(i);
@@ -1258,11 +1298,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) chunk_weights_kernel(const 
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(kWSum + slot));
             } else {
-                if (!(ok = wait(kWSum + slot, k >> 1))) break;
-                if (key < keys) {
-                    float *at = W.scores + (static_cast<int64_t>(seq) * P.num_kv_heads + kvh) * W.capacity + key;
-                    *at += total + s_sum[slot * kTileRows + key_lane];
-                }
+                if (!(ok = wait(kWSum + slot, k / kItems))) break;
+                if (key < keys) *at = before + (total + s_sum[slot * kTileRows + key_lane]);
                 __syncwarp();
             }
             if (lane == 0) mbar_arrive(bar(kWItemEmpty + slot));
@@ -1510,6 +1547,8 @@ extern "C" PKV_API int pkv_prefill_attention_weights(float *scores, int64_t scor
     if (st != PKV_OK) return st;
     const int64_t cap = static_cast<int64_t>(max_blocks_per_seq) * block_size;
     if (!scores || !pkv_internal::aligned(scores, 4) || score_capacity < cap || (!done && !lse)) return PKV_ERR_INVALID_ARG;
+    // four heads' values are read at once (whole rows of a 16-byte aligned lse begin so too)
+    if (num_q_heads / num_kv_heads >= 4 && !pkv_internal::aligned16(lse)) return PKV_ERR_INVALID_ARG;
     if (done) return PKV_OK;
     const int64_t rows = num_blocks * num_kv_heads * block_size;
     if (rows >= 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;  // box row coordinates are signed 32-bit

@@ -15,7 +15,8 @@
 //     finish merges.  Bound by HBM, as the decode kernels are.
 //   * weights pass: one CTA per (request, kv head, 1024 tokens): the partitions' (m, l) give the
 //     group's log-sum-exps, then one exponential per (token, head) and one read-modify-write of
-//     scores per token, by exactly one thread: no atomics, a fixed order.
+//     scores per token, by exactly one thread: no atomics, a fixed order.  Bound by latency: its loads
+//     are issued together, those of scores while the attention pass still runs.
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -246,14 +247,47 @@ template <int G>
 __global__ void __launch_bounds__(kWeightThreads) accumulate_weights_kernel(const __grid_constant__ WeightParams W) {
     const DecodeParams &P = W.d;
     __shared__ float s_lse[G];
-    pkv::pdl_wait_primary();
-    pkv::pdl_launch_dependents();
     const int part = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
     const int ctx = context_of(P, b, false);
     const int start = part * kPart;
+    const int end = min(ctx, start + kPart);
+    const int64_t cap = static_cast<int64_t>(P.max_blocks_per_seq) * P.block_size;
+    const int64_t head = static_cast<int64_t>(b) * P.num_kv_heads + kvh;
+    const float *raw = W.raw + head * cap * G;
+    float *scores = W.scores + head * W.capacity;
+    // What scores holds: like context_lens it is not written by the attention pass, whose CTAs have all started,
+    // behind their own wait for what came before; so it is read while the last of them run.
+    constexpr int kPerThread = kPart / kWeightThreads;
+    float before[kPerThread];
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) {
+        const int t = start + i * kWeightThreads + static_cast<int>(threadIdx.x);
+        before[i] = t < end ? __ldcg(scores + t) : 0.f;
+    }
+    pkv::pdl_wait_primary();
+    pkv::pdl_launch_dependents();
     if (start >= ctx) return;
     const int n_parts = (ctx + kPart - 1) / kPart;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float s[kPerThread][G];
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) {
+        const int t = min(start + i * kWeightThreads + static_cast<int>(threadIdx.x), end - 1);
+        const float *at = raw + static_cast<int64_t>(t) * G;
+        if constexpr (G >= 4) {
+#pragma unroll
+            for (int k = 0; k < G / 4; ++k) {
+                const float4 v = __ldcg(reinterpret_cast<const float4 *>(at) + k);
+                s[i][4 * k] = v.x;
+                s[i][4 * k + 1] = v.y;
+                s[i][4 * k + 2] = v.z;
+                s[i][4 * k + 3] = v.w;
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < G; ++k) s[i][k] = __ldcg(at + k);
+        }
+    }
     if (warp < G) {  // one warp per head: its log-sum-exp in log2 units from the partitions' (m, l)
         const int64_t row = (static_cast<int64_t>(b) * P.num_q_heads + kvh * G + warp) * P.max_partitions;
         float M = -INFINITY, S = 0.f;
@@ -266,31 +300,13 @@ __global__ void __launch_bounds__(kWeightThreads) accumulate_weights_kernel(cons
         if (lane == 0) s_lse[warp] = fmaf(M, kLog2e, log2f(S));
     }
     __syncthreads();
-    const int64_t cap = static_cast<int64_t>(P.max_blocks_per_seq) * P.block_size;
-    const int64_t head = static_cast<int64_t>(b) * P.num_kv_heads + kvh;
-    const float *raw = W.raw + head * cap * G;
-    float *scores = W.scores + head * W.capacity;
-    const int end = min(ctx, start + kPart);
-#pragma unroll 4
-    for (int t = start + static_cast<int>(threadIdx.x); t < end; t += kWeightThreads) {
-        float s[G];
-        if constexpr (G >= 4) {
 #pragma unroll
-            for (int k = 0; k < G / 4; ++k) {
-                const float4 v = __ldcg(reinterpret_cast<const float4 *>(raw + static_cast<int64_t>(t) * G) + k);
-                s[4 * k] = v.x;
-                s[4 * k + 1] = v.y;
-                s[4 * k + 2] = v.z;
-                s[4 * k + 3] = v.w;
-            }
-        } else {
-#pragma unroll
-            for (int k = 0; k < G; ++k) s[k] = __ldcg(raw + static_cast<int64_t>(t) * G + k);
-        }
+    for (int i = 0; i < kPerThread; ++i) {
+        const int t = start + i * kWeightThreads + static_cast<int>(threadIdx.x);
         float w = 0.f;
 #pragma unroll
-        for (int k = 0; k < G; ++k) w += pkv::exp2_approx(s[k] - s_lse[k]);
-        scores[t] += w;
+        for (int k = 0; k < G; ++k) w += pkv::exp2_approx(s[i][k] - s_lse[k]);
+        if (t < end) scores[t] = before[i] + w;
     }
 }
 
