@@ -835,7 +835,7 @@ PKV_API int pkv_prefill_attention_weights(float *scores, int64_t score_capacity,
  * a bad block id skips its rows and is recorded as PKV_DEV_BAD_BLOCK_ID.  recent + sinks <= budget;
  * a table covers at most PKV_MAX_EVICT_CONTEXT positions.  head_dim is PKV_HEAD_DIM.
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
-#define PKV_MAX_EVICT_CONTEXT 524288
+#define PKV_MAX_EVICT_CONTEXT 262144
 PKV_API int pkv_evict(void *k_cache, void *v_cache, int32_t *kept, float *new_scores, int32_t *new_lens,
                       const float *scores, const int32_t *block_tables, const int32_t *new_tables,
                       const int32_t *context_lens, int num_seqs, int max_blocks_per_seq, int max_new_blocks,

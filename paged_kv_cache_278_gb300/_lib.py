@@ -44,7 +44,7 @@ PKV_NOALLOC_SCRATCH_BYTES = 16 << 20
 # how rotary frequencies are derived (PKV_ROPE_*)
 ROPE_METHODS = {"none": 0, "linear": 1, "base": 2, "bands": 3, "ramp": 4}
 PKV_MAX_ROPE_HEAD_DIM = 256
-PKV_MAX_EVICT_CONTEXT = 524288
+PKV_MAX_EVICT_CONTEXT = 262144
 
 
 class RopeSpec(ctypes.Structure):

@@ -8,11 +8,13 @@
 // moves towards the front.
 //
 // Two launches:
-//   * select: one CTA per (b, h).  The border value is found by bisection on the order-preserving
-//     integer image of the float bits, 32 counts of "how many keys are >= x" over keys held in
-//     registers; no atomics, so the result does not depend on any order.  The kept set is then a
-//     bitmap over the positions (above the border, the lowest ties, sinks, recent); prefix popcounts
-//     of its words give every kept position its place.
+//   * select: one cluster of CTAs per (b, h), its scores in registers.  The border value is the need-th largest
+//     of the order-preserving integer images of the candidates, found by three histograms (11, 11, 10
+//     bits) that the CTAs add up through distributed shared memory; counts do not depend on the
+//     order of the atomics that made them.  The kept set is then a bitmap over the positions (above the
+//     border, the lowest ties, sinks, recent); prefix popcounts of its words give every kept position
+//     its place.  Bound by latency and by issue: a score costs some hundred instructions in all, and one CTA
+//     took 20 us for 32768 of them.
 //   * move: bound by HBM (each kept row is read once and written once).  In a block that both tables
 //     name, a row's place may be the source of a row placed earlier, so rows move in order: a cluster
 //     of CTAs takes a (request, kv head)'s K, or V, step by step, all its CTAs load their rows of the
@@ -30,9 +32,8 @@ namespace {
 
 __device__ int g_evict_error;
 
-constexpr int kSelThreads = 1024;
-constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kListKeys = 2;        // undecided keys per thread once they are listed
+constexpr int kSelThreads = 512;
+constexpr int kBins = 2048, kPasses = 3;  // digits of 11, 11 and 10 bits
 constexpr int kMoveThreads = 256;
 constexpr int kRowLanes = PKV_HEAD_DIM * 2 / 16;  // threads that move one row, 16 bytes each
 constexpr int kMoveBatch = 4;                     // rows in flight per thread
@@ -48,7 +49,9 @@ struct EvictParams {
     int64_t capacity, num_blocks;
     int max_blocks, max_new_blocks, num_kv_heads, block_size, row_bytes;
     int budget, recent, sinks;
-    int cluster;  // CTAs that move one (request, kv head)'s K, or V, together
+    int quads;    // scores and new_scores rows are 16-byte aligned
+    int select_cluster;  // CTAs that select of one (request, kv head) together
+    int cluster;         // CTAs that move one's K, or V, together
 };
 
 // Larger float <-> larger integer; NaN smallest, so that it is evicted first.
@@ -70,16 +73,19 @@ __device__ __forceinline__ int cached(const EvictParams &P, int b, bool report) 
     return max(n, 0);
 }
 
-// Sum over the CTA; every thread gets it.  `s` holds kSelWarps + 1 ints, alternated by the caller
-// between two arrays so that one barrier per sum is enough.
+// Sum over the CTA's W warps; every thread gets it.  The caller alternates between two arrays `s`, so
+// that one barrier per sum is enough.
+template <int W>
 __device__ __forceinline__ int block_sum(int v, int *s) {
+    const int lane = threadIdx.x & 31;
     v = __reduce_add_sync(pkv::kFullMask, v);
-    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
+    if (lane == 0) s[threadIdx.x >> 5] = v;
     __syncthreads();
-    return __reduce_add_sync(pkv::kFullMask, s[threadIdx.x & 31]);
+    return __reduce_add_sync(pkv::kFullMask, lane < W ? s[lane] : 0);
 }
 
-// Exclusive prefix sum over the CTA's threads and the total.
+// Exclusive prefix sum over the CTA's threads, and the total.
+template <int W>
 __device__ __forceinline__ int block_scan(int v, int *s, int &total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int x = v;
@@ -91,7 +97,7 @@ __device__ __forceinline__ int block_scan(int v, int *s, int &total) {
     __syncthreads();
     if (lane == 31) s[warp] = x;
     __syncthreads();
-    int w = s[lane];
+    int w = lane < W ? s[lane] : 0;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
         const int y = __shfl_up_sync(pkv::kFullMask, w, d);
@@ -102,141 +108,167 @@ __device__ __forceinline__ int block_scan(int v, int *s, int &total) {
     return x - v + (warp ? before : 0);
 }
 
-// KPT keys per thread live in registers (positions j * kSelThreads + thread); positions past
-// KPT * kSelThreads are read again for each count.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// The same shared-memory address in the cluster's CTA `rank`.
+__device__ __forceinline__ uint32_t of_rank(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ int4 load_remote4(uint32_t addr) {
+    int4 v;
+    asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
+// One cluster per (b, h), each CTA with a run of kSelThreads KPT positions: thread's are (j kSelThreads + thread) 4 + e
+// of its CTA's run, e < 4, j < KPT / 4, in registers.
 template <int KPT>
 __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_constant__ EvictParams P) {
-    extern __shared__ uint32_t s_words[];  // [words] above the border, then kept | [words] at the border, then prefixes
-    __shared__ int s_sum[2][kSelWarps];
-    __shared__ uint32_t s_list[kListKeys * kSelThreads];
-    __shared__ int s_listed;
+    constexpr int T = kSelThreads, W = T / 32, J = KPT / 4, kRun = T * KPT, kWords = kRun / 32;
+    static_assert(kBins == 4 * T, "a thread's bins are one 16-byte piece");
+    __shared__ __align__(16) int s_hist[kPasses][kBins];
+    __shared__ uint32_t s_above[kWords], s_at[kWords];  // bitmaps: above the border, then kept; at the border, then places
+    __shared__ int s_sum[2][W];
+    __shared__ __align__(16) int4 s_count;  // this CTA's positions above and at the border
+    __shared__ int s_bin, s_upper, s_inside;
+    const int tid = threadIdx.x, lane = tid & 31;
+    for (int i = tid; i < kPasses * kBins; i += T) (&s_hist[0][0])[i] = 0;
+    __syncthreads();
     pkv::pdl_wait_primary();
     pkv::pdl_launch_dependents();
-    const int h = blockIdx.x, b = blockIdx.y;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int ranks = P.select_cluster, rank = blockIdx.x % ranks;
+    const int h = blockIdx.x / ranks, b = blockIdx.y;
     const int64_t row = static_cast<int64_t>(b) * P.num_kv_heads + h;
     const float *scores = P.scores + row * P.capacity;
     float *out = P.new_scores + row * P.capacity;
     int32_t *kept = P.kept + row * P.budget;
-    const int n = cached(P, b, tid == 0 && h == 0);
+    const int n = cached(P, b, tid == 0 && blockIdx.x == 0);
     const int m = min(n, P.budget);
+    const bool quads = P.quads != 0;  // rows of scores start on 16 bytes
+    const int run = rank * kRun;      // the CTA's first position
 
-    if (n > P.budget) {
+    if (n > P.budget) {  // (the whole cluster)
         const int first = min(P.sinks, n), last = n - P.recent;  // candidates [first, last)
         const int need = P.budget - P.sinks - P.recent;
-        uint32_t key[KPT];
+        float raw[KPT];
 #pragma unroll
-        for (int j = 0; j < KPT; ++j) key[j] = __float_as_uint(__ldcg(scores + min(j * kSelThreads + tid, n - 1)));  // all in flight
+        for (int j = 0; j < J; ++j) {  // all in flight (clamped: what lies past n is never looked at)
+            const int p = run + (j * T + tid) * 4;
+            if (quads) {
+                const float4 v = __ldcg(reinterpret_cast<const float4 *>(scores + min(p, (n - 1) & ~3)));
+                raw[4 * j] = v.x;
+                raw[4 * j + 1] = v.y;
+                raw[4 * j + 2] = v.z;
+                raw[4 * j + 3] = v.w;
+            } else {
 #pragma unroll
-        for (int j = 0; j < KPT; ++j) {
-            const int p = j * kSelThreads + tid;
-            const uint32_t k = order_key(__uint_as_float(key[j]));
-            key[j] = p >= first && p < last ? k : 0u;
+                for (int e = 0; e < 4; ++e) raw[4 * j + e] = __ldcg(scores + min(p + e, n - 1));
+            }
         }
-        // The largest border with at least `need` candidate keys >= it (keys of 0 outside the
-        // candidates are never counted: every tested border is above 0).
-        uint32_t border = 0;
-        int flip = 0;
+        auto position = [&](int i) { return run + ((i / 4) * T + tid) * 4 + i % 4; };
+        auto candidate = [&](int p) { return p >= first && p < last; };
+        uint32_t border = 0xffffffffu;  // above every key: nothing between the sinks and the recent ones
         if (need > 0) {
-            int upper = 0, inside = last - first;  // keys above the undecided range, and in it
-            int above_list = 0;                    // keys above the listed ones
-            uint32_t mine[kListKeys] = {};
-            bool listed = false;
-            for (int bit = 31; bit >= 0; --bit) {
-                const uint32_t trial = border | (1u << bit);
-                int c = 0;
-                if (!listed) {
+            // Digit by digit: the bin of the need-th largest key among those that share the digits so far, from the
+            // cluster's histograms.  Every CTA finds the same.
+            border = 0;
+            int left = need;  // of the keys that share the digits so far, this many are above or at the border
+#pragma unroll 1
+            for (int pass = 0; pass < kPasses; ++pass) {
+                const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
+                const uint32_t digit = pass == 2 ? 0x3ffu : 0x7ffu;
+                const uint32_t known = pass == 0 ? 0u : (pass == 1 ? 0xffe00000u : 0xfffffc00u);
 #pragma unroll
-                    for (int j = 0; j < KPT; ++j) c += key[j] >= trial;
-                    for (int p = KPT * kSelThreads + tid; p < last; p += kSelThreads)
-                        c += p >= first && order_key(__ldcg(scores + p)) >= trial;
-                    c = block_sum(c, s_sum[flip]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < kListKeys; ++j) c += mine[j] >= trial;
-                    c = above_list + block_sum(c, s_sum[flip]);
+                for (int i = 0; i < KPT; ++i) {
+                    const uint32_t k = order_key(raw[i]);
+                    if (candidate(position(i)) && ((k ^ border) & known) == 0) atomicAdd(&s_hist[pass][(k >> shift) & digit], 1);
                 }
-                flip ^= 1;
-                if (c == need) {  // exactly the keys from `trial` on: none at the border itself
-                    border = trial - 1;
+                cluster_arrive();
+                cluster_wait();
+                const uint32_t mine = pkv::smem_addr(&s_hist[pass][kBins - 4 - 4 * tid]);  // the thread's four bins, from the top
+                int4 sum = make_int4(0, 0, 0, 0);
+                for (int r = 0; r < ranks; ++r) {
+                    const int4 v = load_remote4(of_rank(mine, r));
+                    sum.x += v.x;
+                    sum.y += v.y;
+                    sum.z += v.z;
+                    sum.w += v.w;
+                }
+                const int own = sum.x + sum.y + sum.z + sum.w;
+                int all = 0;
+                int upper = block_scan<W>(own, s_sum[0], all);
+                if (upper < left && left <= upper + own) {  // one thread
+                    int bin = kBins - 1 - 4 * tid, c = sum.w;
+                    if (upper + c < left) upper += c, c = sum.z, --bin;
+                    if (upper + c < left) upper += c, c = sum.y, --bin;
+                    if (upper + c < left) upper += c, c = sum.x, --bin;
+                    s_bin = bin;
+                    s_upper = upper;
+                    s_inside = c;
+                }
+                __syncthreads();
+                border |= static_cast<uint32_t>(s_bin) << shift;
+                left -= s_upper;
+                if (left == s_inside && border > 0) {  // the whole bin is taken: every key from its lower end on
+                    border -= 1;
                     break;
                 }
-                if (c > need) {
-                    border = trial;
-                    inside = c - upper;
-                } else {
-                    inside -= c - upper;
-                    upper = c;
-                }
-                if (!listed && bit > 0 && inside <= kListKeys * kSelThreads) {
-                    // The few undecided keys, in any order, spread over the threads: from here on a
-                    // count costs a barrier, not a pass over the row.
-                    if (tid == 0) s_listed = 0;
-                    __syncthreads();
-                    auto push = [&](uint32_t x, bool cand) {
-                        const bool in = cand && x >= border && (x - border) < (1u << bit);
-                        const uint32_t mask = __ballot_sync(pkv::kFullMask, in);
-                        int at = 0;
-                        if (lane == 0 && mask) at = atomicAdd(&s_listed, __popc(mask));
-                        at = __shfl_sync(pkv::kFullMask, at, 0) + __popc(mask & ((1u << lane) - 1u));
-                        if (in) s_list[at] = x;
-                    };
-#pragma unroll
-                    for (int j = 0; j < KPT; ++j) {
-                        const int p = j * kSelThreads + tid;
-                        push(key[j], p >= first && p < last);
-                    }
-                    for (int p0 = KPT * kSelThreads; p0 < last; p0 += kSelThreads) {
-                        const int p = p0 + tid;
-                        const bool cand = p >= first && p < last;
-                        push(cand ? order_key(__ldcg(scores + p)) : 0u, cand);
-                    }
-                    __syncthreads();
-#pragma unroll
-                    for (int j = 0; j < kListKeys; ++j) mine[j] = j * kSelThreads + tid < s_listed ? s_list[j * kSelThreads + tid] : 0u;
-                    listed = true;
-                    above_list = upper;
-                }
             }
-        } else {
-            border = 0xffffffffu;  // above every key: nothing between the sinks and the recent ones
         }
         // Bitmaps of the positions above and at the border.
-        const int words = (n + 31) / 32;
-        uint32_t *s_above = s_words, *s_at = s_words + words;
-        const int64_t rounds = (n + kSelThreads - 1) / kSelThreads;
-        auto mark = [&](int j, uint32_t k) {
-            const int p = j * kSelThreads + tid;
-            const bool cand = p >= first && p < last, fixed = p < n && !cand;
-            const uint32_t above = __ballot_sync(pkv::kFullMask, fixed || (cand && k > border));
-            const uint32_t at = __ballot_sync(pkv::kFullMask, cand && need > 0 && k == border);
-            const int w = j * kSelWarps + warp;
-            if (lane == 0 && w < words) {
-                s_above[w] = above;
-                s_at[w] = at;
-            }
-        };
+        int above = 0, at = 0;
 #pragma unroll
-        for (int j = 0; j < KPT; ++j)
-            if (j < rounds) mark(j, key[j]);
-        for (int j = KPT; j < rounds; ++j) {
-            const int p = j * kSelThreads + tid;
-            mark(j, p < n ? order_key(__ldcg(scores + p)) : 0u);
+        for (int j = 0; j < J; ++j) {
+            uint32_t x = 0, y = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int p = position(4 * j + e);
+                const uint32_t k = order_key(raw[4 * j + e]);
+                const bool c = candidate(p);
+                x |= static_cast<uint32_t>(p < n && (!c || k > border)) << e;
+                y |= static_cast<uint32_t>(c && need > 0 && k == border) << e;
+            }
+            x <<= 4 * (lane & 7);
+            y <<= 4 * (lane & 7);
+#pragma unroll
+            for (int d = 1; d < 8; d <<= 1) {  // eight lanes make a word
+                x |= __shfl_xor_sync(pkv::kFullMask, x, d);
+                y |= __shfl_xor_sync(pkv::kFullMask, y, d);
+            }
+            if ((lane & 7) == 0) {
+                s_above[(j * T + tid) / 8] = x;
+                s_at[(j * T + tid) / 8] = y;
+            }
         }
         __syncthreads();
-        // Ties left to take, from the lowest position on: thread t owns `per` neighbouring words.
-        const int per = (words + kSelThreads - 1) / kSelThreads;
-        const int w0 = tid * per, w1 = min(words, w0 + per);
-        int above = 0, at = 0;
+        // Thread t owns `kPer` neighbouring words.
+        constexpr int kPer = (kWords + T - 1) / T;
+        const int w0 = min(kWords, tid * kPer), w1 = min(kWords, w0 + kPer);
         for (int w = w0; w < w1; ++w) {
             above += __popc(s_above[w]);
             at += __popc(s_at[w]);
         }
         int total_above = 0, total_at = 0;
-        block_scan(above, s_sum[0], total_above);
-        int before = block_scan(at, s_sum[1], total_at);
-        int room = m - total_above - before;  // ties that may still be taken at this thread's first word
-        int mine = 0;
+        const int above_before = block_scan<W>(above, s_sum[0], total_above), at_before = block_scan<W>(at, s_sum[1], total_at);
+        if (tid == 0) s_count = make_int4(total_above, total_at, 0, 0);
+        cluster_arrive();
+        cluster_wait();
+        // Ties are taken from the lowest position on: `room` of the cluster's, of which `lower` lie in earlier runs.
+        int room = m, place = 0, lower = 0;
+        for (int r = 0; r < ranks; ++r) {
+            const int4 c = load_remote4(of_rank(pkv::smem_addr(&s_count), r));
+            room -= c.x;
+            if (r < rank) {
+                place += c.x;
+                lower += c.y;
+            }
+        }
+        // (ties taken so far: in earlier runs, then before this thread's words)
+        place += min(lower, room) + above_before + max(min(lower + at_before, room) - min(lower, room), 0);
+        room -= lower + at_before;
         for (int w = w0; w < w1; ++w) {
             uint32_t ties = s_at[w];
             const int c = __popc(ties);
@@ -251,51 +283,42 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
             }
             room -= c;
             s_above[w] |= ties;
-            mine += __popc(s_above[w]);
-        }
-        int total = 0;
-        int place = block_scan(mine, s_sum[0], total);
-        for (int w = w0; w < w1; ++w) {
             s_at[w] = place;
             place += __popc(s_above[w]);
         }
         __syncthreads();
-        // Places and scores, kRounds x kSelThreads positions at a time.  new_scores may be scores itself:
-        // places lie at or before their positions, so all of a step's scores are read before any of its
-        // places is written, and the next step reads behind every place written so far.
-        constexpr int kRounds = 8;
-        for (int64_t j0 = 0; j0 < rounds; j0 += kRounds) {
-            float x[kRounds];
+        // Every kept position and score to its place.  (new_scores may be scores itself: every CTA has read all of its
+        // scores by the cluster's last meeting.)
 #pragma unroll
-            for (int u = 0; u < kRounds; ++u) {
-                const int w = static_cast<int>((j0 + u) * kSelWarps + warp);
-                x[u] = __ldcg(scores + min(w * 32 + lane, n - 1));
-            }
-            if (out == scores) __syncthreads();
-#pragma unroll
-            for (int u = 0; u < kRounds; ++u) {
-                const int w = static_cast<int>((j0 + u) * kSelWarps + warp);
-                const uint32_t bits = w < words ? s_above[w] : 0u;
-                if ((bits >> lane) & 1u) {
-                    const int i = static_cast<int>(s_at[w]) + __popc(bits & ((1u << lane) - 1u));
-                    kept[i] = w * 32 + lane;
-                    out[i] = x[u];
-                }
+        for (int i = 0; i < KPT; ++i) {
+            const int p = position(i), w = (p - run) / 32;
+            const uint32_t bits = s_above[w];
+            if ((bits >> (p & 31)) & 1u) {
+                const int to = static_cast<int>(s_at[w]) + __popc(bits & ((1u << (p & 31)) - 1u));
+                kept[to] = p;
+                out[to] = raw[i];
             }
         }
     } else {
-        for (int p = tid; p < n; p += kSelThreads) {
+        for (int p = rank * T + tid; p < n; p += ranks * T) {
             kept[p] = p;
             if (out != scores) out[p] = __ldcg(scores + p);
         }
-        for (int p = n + tid; p < P.budget; p += kSelThreads) kept[p] = -1;
+        for (int p = n + rank * T + tid; p < P.budget; p += ranks * T) kept[p] = -1;
     }
-    __syncthreads();
-    for (int64_t p = m + tid; p < P.capacity; p += kSelThreads) out[p] = 0.f;
+    // Zeros behind the kept scores (read by every CTA, see above), shared out between the CTAs.
+    int64_t tail = m;
+    if (quads) {
+        tail = min((static_cast<int64_t>(m) + 3) & ~static_cast<int64_t>(3), P.capacity);
+        if (rank == 0 && m + tid < tail) out[m + tid] = 0.f;
+        for (int64_t p = tail + 4 * (rank * T + tid); p < P.capacity; p += 4 * ranks * T)
+            *reinterpret_cast<float4 *>(out + p) = make_float4(0.f, 0.f, 0.f, 0.f);
+    } else {
+        for (int64_t p = tail + rank * T + tid; p < P.capacity; p += ranks * T) out[p] = 0.f;
+    }
+    cluster_arrive();  // no CTA's shared memory goes while another may read it
+    cluster_wait();
 }
-
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 __global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constant__ EvictParams P) {
     __shared__ unsigned char *s_src[2][kMoveRows], *s_dst[2][kMoveRows];
@@ -372,19 +395,21 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constan
 }
 
 template <int KPT>
-int launch_select(const EvictParams &p, int num_seqs, size_t smem, cudaStream_t stream, cudaLaunchAttribute *attr) {
-    auto kernel = select_kernel<KPT>;
-    if (smem > 48 * 1024 &&
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
-        return PKV_ERR_CUDA;
+int launch_select(const EvictParams &p, int num_seqs, cudaStream_t stream) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(p.num_kv_heads, num_seqs);
+    cfg.gridDim = dim3(p.num_kv_heads * p.select_cluster, num_seqs);
     cfg.blockDim = dim3(kSelThreads);
-    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+    cudaLaunchAttribute attrs[2] = {};
+    attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[0].val.programmaticStreamSerializationAllowed = 1;
+    attrs[1].id = cudaLaunchAttributeClusterDimension;
+    attrs[1].val.clusterDim.x = p.select_cluster;
+    attrs[1].val.clusterDim.y = 1;
+    attrs[1].val.clusterDim.z = 1;
+    cfg.attrs = attrs;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, select_kernel<KPT>, p) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
 }  // namespace
@@ -447,11 +472,16 @@ extern "C" PKV_API int pkv_evict(void *k_cache, void *v_cache, int32_t *kept, fl
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const size_t smem = (static_cast<size_t>(cap) + 31) / 32 * 8;
-    const int64_t kpt = (cap + kSelThreads - 1) / kSelThreads;
-    const int st = kpt <= 4    ? launch_select<4>(p, num_seqs, smem, s, &attr)
-                   : kpt <= 16 ? launch_select<16>(p, num_seqs, smem, s, &attr)
-                               : launch_select<32>(p, num_seqs, smem, s, &attr);
+    p.quads = score_capacity % 4 == 0 && pkv_internal::aligned16(scores) && pkv_internal::aligned16(new_scores);
+    // Eight CTAs to a row as long as a thread has four scores left; more than 32 a thread only past 131072.
+    const int64_t runs = (cap + kSelThreads - 1) / kSelThreads;  // scores per thread of a single CTA
+    p.select_cluster = runs <= 4 ? 1 : (runs <= 8 ? 2 : (runs <= 16 ? 4 : 8));
+    const int64_t each = (runs + p.select_cluster - 1) / p.select_cluster;
+    const int st = each <= 4    ? launch_select<4>(p, num_seqs, s)
+                   : each <= 8  ? launch_select<8>(p, num_seqs, s)
+                   : each <= 16 ? launch_select<16>(p, num_seqs, s)
+                   : each <= 32 ? launch_select<32>(p, num_seqs, s)
+                                : launch_select<64>(p, num_seqs, s);
     if (st != PKV_OK) return st;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(2 * p.cluster, num_kv_heads, num_seqs);

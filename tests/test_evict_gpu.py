@@ -105,10 +105,11 @@ def test_narrower_new_table():
     check(k, v, s, old, np.ascontiguousarray(fresh[:, :7]), lens, 100, 20, 4)
 
 
-@pytest.mark.parametrize("n,budget", [(16384, 5000), (32768, 32767), (40001, 20000)])
+@pytest.mark.parametrize("n,budget", [(4097, 4096), (8192, 500), (16384, 5000), (32768, 32767), (40001, 20000), (70000, 130),
+                                      (140001, 60000)])
 def test_long_rows(n, budget):
-    """16 and 32 register keys per thread, and positions past them."""
-    k, v, s, old, _, lens = state([n, 1025], 1, 256, n, "ties" if n == 40001 else "heavy")
+    """Two to eight CTAs to a row, 4 to 64 scores a thread."""
+    k, v, s, old, _, lens = state([n, 1025], 1, 256, n, "ties" if n == 40001 else "wild" if n == 70000 else "heavy")
     check(k, v, s, old, old, lens, budget, 100, 4, in_place=True, alias=True)
 
 

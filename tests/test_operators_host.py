@@ -112,7 +112,7 @@ def test_evict_refusals(lib):
     for change in (dict(seqs=-1), dict(width=0), dict(new_width=0), dict(capacity=63), dict(budget=0), dict(recent=-1),
                    dict(sinks=-1), dict(recent=17), dict(recent=10, sinks=7), dict(nb=0), dict(hkv=0), dict(bs=0)):
         assert call(lib, "pkv_evict", EVICT, **change) == INVALID, change
-    for change in (dict(d=64), dict(width=524288 // 16 + 1, capacity=1 << 20), dict(hkv=70000)):
+    for change in (dict(d=64), dict(width=262144 // 16 + 1, capacity=1 << 20), dict(hkv=70000)):
         assert call(lib, "pkv_evict", EVICT, **change) == UNSUPPORTED, change
     one = dict(EVICT, seqs=1)
     for key in ("kc", "vc", "kept", "new_scores", "new_lens", "scores", "bt", "nt", "cl"):
