@@ -9,7 +9,7 @@
 //
 // Two launches:
 //   * select: one cluster of CTAs per (b, h), its scores in registers.  The border value is the need-th largest
-//     of the order-preserving integer images of the candidates, found by three histograms (11, 11, 10
+//     of the order-preserving integer images of the candidates, found by four histograms (9, 8, 8, 7
 //     bits) that the CTAs add up through distributed shared memory; counts do not depend on the
 //     order of the atomics that made them.  The kept set is then a bitmap over the positions (above the
 //     border, the lowest ties, sinks, recent); prefix popcounts of its words give every kept position
@@ -33,10 +33,10 @@ namespace {
 __device__ int g_evict_error;
 
 constexpr int kSelThreads = 512;
-constexpr int kBins = 2048, kPasses = 3;  // digits of 11, 11 and 10 bits
+constexpr int kBins = 512, kPasses = 4;  // digits of 9, 8, 8 and 7 bits
 constexpr int kMoveThreads = 256;
 constexpr int kRowLanes = PKV_HEAD_DIM * 2 / 16;  // threads that move one row, 16 bytes each
-constexpr int kMoveBatch = 4;                     // rows in flight per thread
+constexpr int kMoveBatch = 4;                     // rows in flight per thread (2 and 8 measured 15 and 13 % slower on 4 x 32k -> 4k)
 constexpr int kMoveRows = kMoveThreads / kRowLanes * kMoveBatch;  // rows of a CTA's step
 
 struct EvictParams {
@@ -73,17 +73,6 @@ __device__ __forceinline__ int cached(const EvictParams &P, int b, bool report) 
     return max(n, 0);
 }
 
-// Sum over the CTA's W warps; every thread gets it.  The caller alternates between two arrays `s`, so
-// that one barrier per sum is enough.
-template <int W>
-__device__ __forceinline__ int block_sum(int v, int *s) {
-    const int lane = threadIdx.x & 31;
-    v = __reduce_add_sync(pkv::kFullMask, v);
-    if (lane == 0) s[threadIdx.x >> 5] = v;
-    __syncthreads();
-    return __reduce_add_sync(pkv::kFullMask, lane < W ? s[lane] : 0);
-}
-
 // Exclusive prefix sum over the CTA's threads, and the total.
 template <int W>
 __device__ __forceinline__ int block_scan(int v, int *s, int &total) {
@@ -117,6 +106,11 @@ __device__ __forceinline__ uint32_t of_rank(uint32_t addr, uint32_t rank) {
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
+__device__ __forceinline__ int load_remote(uint32_t addr) {
+    int v;
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
 __device__ __forceinline__ int4 load_remote4(uint32_t addr) {
     int4 v;
     asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
@@ -128,9 +122,10 @@ __device__ __forceinline__ int4 load_remote4(uint32_t addr) {
 template <int KPT>
 __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_constant__ EvictParams P) {
     constexpr int T = kSelThreads, W = T / 32, J = KPT / 4, kRun = T * KPT, kWords = kRun / 32;
-    static_assert(kBins == 4 * T, "a thread's bins are one 16-byte piece");
+    static_assert(kBins == T, "a thread adds up one bin");
     __shared__ __align__(16) int s_hist[kPasses][kBins];
     __shared__ uint32_t s_above[kWords], s_at[kWords];  // bitmaps: above the border, then kept; at the border, then places
+    __shared__ __align__(16) int s_total[kBins];  // the cluster's histogram of a pass, from the highest bin to the lowest
     __shared__ int s_sum[2][W];
     __shared__ __align__(16) int4 s_count;  // this CTA's positions above and at the border
     __shared__ int s_bin, s_upper, s_inside;
@@ -178,9 +173,10 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
             int left = need;  // of the keys that share the digits so far, this many are above or at the border
 #pragma unroll 1
             for (int pass = 0; pass < kPasses; ++pass) {
-                const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
-                const uint32_t digit = pass == 2 ? 0x3ffu : 0x7ffu;
-                const uint32_t known = pass == 0 ? 0u : (pass == 1 ? 0xffe00000u : 0xfffffc00u);
+                constexpr int kShift[kPasses] = {23, 15, 7, 0};
+                const int shift = pass == 0 ? kShift[0] : pass == 1 ? kShift[1] : pass == 2 ? kShift[2] : kShift[3];
+                const uint32_t digit = pass == 0 ? 0x1ffu : pass == 3 ? 0x7fu : 0xffu;
+                const uint32_t known = pass == 0 ? 0u : 0xffffffffu << (shift + (pass == 3 ? 7 : 8));
 #pragma unroll
                 for (int i = 0; i < KPT; ++i) {
                     const uint32_t k = order_key(raw[i]);
@@ -188,26 +184,42 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
                 }
                 cluster_arrive();
                 cluster_wait();
-                const uint32_t mine = pkv::smem_addr(&s_hist[pass][kBins - 4 - 4 * tid]);  // the thread's four bins, from the top
-                int4 sum = make_int4(0, 0, 0, 0);
-                for (int r = 0; r < ranks; ++r) {
-                    const int4 v = load_remote4(of_rank(mine, r));
-                    sum.x += v.x;
-                    sum.y += v.y;
-                    sum.z += v.z;
-                    sum.w += v.w;
-                }
-                const int own = sum.x + sum.y + sum.z + sum.w;
-                int all = 0;
-                int upper = block_scan<W>(own, s_sum[0], all);
-                if (upper < left && left <= upper + own) {  // one thread
-                    int bin = kBins - 1 - 4 * tid, c = sum.w;
-                    if (upper + c < left) upper += c, c = sum.z, --bin;
-                    if (upper + c < left) upper += c, c = sum.y, --bin;
-                    if (upper + c < left) upper += c, c = sum.x, --bin;
-                    s_bin = bin;
-                    s_upper = upper;
-                    s_inside = c;
+                const uint32_t mine = pkv::smem_addr(&s_hist[pass][kBins - 1 - tid]);
+                int c = 0;
+                for (int r = 0; r < ranks; ++r) c += load_remote(of_rank(mine, r));
+                s_total[tid] = c;
+                __syncthreads();
+                if (tid < 32) {  // one warp finds the bin: each lane sixteen neighbouring ones
+                    int own[kBins / 32], sum = 0;
+#pragma unroll
+                    for (int i = 0; i < kBins / 32; i += 4) {
+                        const int4 v = *reinterpret_cast<const int4 *>(s_total + lane * (kBins / 32) + i);
+                        own[i] = v.x;
+                        own[i + 1] = v.y;
+                        own[i + 2] = v.z;
+                        own[i + 3] = v.w;
+                        sum += v.x + v.y + v.z + v.w;
+                    }
+                    int upper = sum;
+#pragma unroll
+                    for (int d = 1; d < 32; d <<= 1) {
+                        const int y = __shfl_up_sync(pkv::kFullMask, upper, d);
+                        if (lane >= d) upper += y;
+                    }
+                    upper -= sum;
+                    if (upper < left && left <= upper + sum) {  // one lane
+                        bool found = false;
+#pragma unroll
+                        for (int i = 0; i < kBins / 32; ++i) {
+                            if (!found && left <= upper + own[i]) {
+                                found = true;
+                                s_bin = kBins - 1 - (lane * (kBins / 32) + i);
+                                s_upper = upper;
+                                s_inside = own[i];
+                            }
+                            upper += own[i];
+                        }
+                    }
                 }
                 __syncthreads();
                 border |= static_cast<uint32_t>(s_bin) << shift;
