@@ -753,8 +753,8 @@ PKV_API int pkv_rope_append(void *q_out, int64_t q_out_stride, const void *q, in
  * (DEVICE int32 [num_seqs + 1]; empty ranges allowed); rows outside every range are left as they were.
  * A range that is negative, longer than max_query_len or past total_q is skipped and recorded as
  * PKV_DEV_BAD_CONTEXT.  Weights are rounded to fp16 for the product with V; sums and the
- * accumulator are float32.  Positions past a context never enter a product; a V row that a row must not
- * see but another row of its 128-key tile does enters with weight 0, so it must be finite. */
+ * accumulator are float32.  What lies past a context never enters a result; infinities and NaN in a
+ * position's K or V reach the rows that see the position and no others. */
 
 /* Bytes of workspace the two calls need (0: none).  max_context: the longest context the call may meet
  * (max_seq_len, or max_blocks_per_seq * block_size).  No initial contents.  Calls that

@@ -30,7 +30,8 @@
 // results are joined by a second launch.
 //
 // Keys past the context are never multiplied: the last key tile's MMAs stop at its 16-key group and
-// that group's unused V rows are zeroed in shared memory, whatever the cache holds there.
+// that group's unused V rows are zeroed in shared memory, whatever the cache holds there.  Infinities and NaN in V
+// reach the rows that see their position and no others (clean_values).
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -75,6 +76,8 @@ struct PromptParams {
     int group_log2, box_rows;
     int splits;  // at most; the kernels take split_count of it
     float q_scale;                // scale * log2(e)
+    const __half *v;   // V as the maps read it: [rows][128], rows v_stride elements apart where packed
+    int64_t v_stride;
     CUtensorMap tmap_q, tmap_k, tmap_v;
 };
 
@@ -100,7 +103,8 @@ struct PromptSmem {
     static constexpr int tmem_slot = bars + n_bars * 8;
     static constexpr int items = (tmem_slot + 4 + 15) / 16 * 16;
     static constexpr int state = items + kItems * static_cast<int>(sizeof(Item));  // [2 groups][128 rows] (m, l)
-    static constexpr int staging = (state + 2 * kTileRows * 8 + 127) / 128 * 128;  // [8 warps][32 rows][128 bytes]
+    static constexpr int dirty = state + 2 * kTileRows * 8;                   // [kItems] item number + 1, see clean_values
+    static constexpr int staging = (dirty + kItems * 4 + 127) / 128 * 128;  // [8 warps][32 rows][128 bytes]
     static constexpr int total = staging + kSoftmaxWarps * 32 * 128;
     static_assert(total <= 227 * 1024, "a CTA's shared memory");
 };
@@ -357,6 +361,46 @@ __device__ Item find_item(const PromptParams &P, int64_t index, int splits, int 
     return it;
 }
 
+// V rows of a tile that not every row of the item may see: weights there can be 0, and 0 x inf is NaN.  A group's
+// four warps (`part` 0-3) go over the tile before its weights are delivered: rows past the context become
+// zeros (whatever lies there), and infinities and NaN of cached rows too, with the item marked: its epilogue gives
+// them to the rows that do see them.  Both groups may do this to one tile: the second finds zeros.
+__device__ __forceinline__ void clean_values(uint32_t v, int valid, int part, int lane, volatile uint32_t *dirty, uint32_t mark) {
+    // 512 bytes at a time: rows 4 (i % 8) + lane / 8 of this part, half i / 8 of the dims
+    const uint32_t at0 = v + (32 * part + (lane >> 3)) * 128 + (lane & 7) * 16;
+    auto bad_of = [](uint32_t w) { return ((w & 0x7c007c00u) + 0x04000400u) & 0x80008000u; };  // exponent 31, per half
+    uint32_t bad = 0;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        uint4 x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = pkv::lds128(at0 + half * kSlab + i * 512);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) bad |= bad_of(x[i].x) | bad_of(x[i].y) | bad_of(x[i].z) | bad_of(x[i].w);
+    }
+    if (__any_sync(pkv::kFullMask, bad != 0) || 32 * part + 32 > valid) {
+#pragma unroll 1
+        for (int i = 0; i < 16; ++i) {
+            const int row = 32 * part + 4 * (i & 7) + (lane >> 3);
+            const uint32_t at = at0 + (i >> 3) * kSlab + (i & 7) * 512;
+            const uint4 x = lds128v(at);
+            const uint32_t b[4] = {bad_of(x.x), bad_of(x.y), bad_of(x.z), bad_of(x.w)};
+            const bool past = row >= valid;
+            if (!past && (b[0] | b[1] | b[2] | b[3])) {
+                *dirty = mark;
+                __threadfence_block();  // whoever finds the zeros finds the mark
+            }
+            if (past)
+                sts128(at, 0u, 0u, 0u, 0u);
+            else if (b[0] | b[1] | b[2] | b[3])
+                sts128(at, x.x & ~((b[0] >> 15) * 0xffffu), x.y & ~((b[1] >> 15) * 0xffffu), x.z & ~((b[2] >> 15) * 0xffffu),
+                       x.w & ~((b[3] >> 15) * 0xffffu));
+        }
+        pkv::fence_proxy_async_smem();  // before the arrival that lets the MMA read the tile
+    }
+    __syncwarp();
+}
+
 // Key tiles that an item's groups go through: the same ones, or each its own.
 __device__ __forceinline__ int key_tiles(bool shared, int a, int b) { return shared ? a + b : max(a, b); }
 
@@ -381,6 +425,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
         }
         pkv::fence_mbar_init();
     }
+    volatile uint32_t *dirty = reinterpret_cast<volatile uint32_t *>(smem + PromptSmem::dirty);
+    if (threadIdx.x < kItems) dirty[threadIdx.x] = 0;
     if (warp == kMmaWarp && aligned) pkv::tmem_alloc(pkv::smem_addr(tmem_slot), 512);
     pkv::tmem_fence_before_sync();
     __syncthreads();
@@ -573,19 +619,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                 };
                 if (!(ok = wait(kBarQFull, loaded))) break;
                 ++loaded;
-                // Zeroes the V rows past the context in a tile's last 16-key group: their weights are 0, their values
-                // may be anything.
-                auto clean_tail = [&](uint32_t v, int j, int groups) {
-                    const int valid = min(kTileRows, keys - (first + j) * kTileRows);
-                    if (valid >= groups * 16) return;
-                    for (int x = lane; x < (groups * 16 - valid) * 16; x += 32)
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v + ((x >> 3) & 1) * kSlab +
-                                                                                 (valid + (x >> 4)) * 128 + (x & 7) * 16),
-                                     "r"(0)
-                                     : "memory");
-                    pkv::fence_proxy_async_smem();
-                    __syncwarp();
-                };
                 // O of group t += P V of key tile j (the group's `local`-th)
                 auto pv = [&](int t, uint32_t v, int groups, int local) {
                     for (int half = 0; half < 2; ++half) {  // keys 0-63 while the softmax finishes 64-127
@@ -623,7 +656,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                     if (!(ok = wait(kBarVFull + v_stage % kRing, v_stage / kRing))) break;
                     const uint32_t v = base + PromptSmem::values + (v_stage % kRing) * kOperand;
                     const int groups = groups_of(j), local = shared ? j >> 1 : j;
-                    clean_tail(v, j, groups);
                     bool k_here = false;
                     for (int t = 0; t < 2; ++t) {
                         if (shared ? t != (j & 1) : j >= n[t]) continue;
@@ -658,7 +690,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
         const uint32_t t_s = tmem + lanes + t * kTileRows, t_o = tmem + lanes + 2 * kTileRows + t * kDim;
         const int r = (warp & 3) * 32 + lane, tok = r >> glog;
         const float sc = P.q_scale;
-        uint32_t s_count = 0, o_count = 0, joins = 0;
+        uint32_t s_count = 0, o_count = 0, joins = 0, v_stage = 0;  // v_stage: V stages of the items so far
         float2 *s_state = reinterpret_cast<float2 *>(smem + PromptSmem::state);
         bool ok = true;
         for (uint32_t k = 0; ok; ++k) {
@@ -677,19 +709,39 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
             if (lane == 0) mbar_arrive(bar(kBarItemEmpty + slot));
             if (seq < 0) break;
             const int pos = tile_pos + min(tok, live - 1);  // rows past the last token: computed like it, never stored
+            const int n_kv = key_tiles(shared, n, n_of_other), keys = i1.w;
             float m_ref = -INFINITY, l = 0.f;
             for (int j = 0; j < n; ++j) {
-                if (!(ok = wait(kBarS + t, s_count))) break;
-                ++s_count;
+                const int key0 = (first + (shared ? 2 * j + t : j)) * kTileRows;
+                // A tile that some row of the item does not see to its end is cleaned first, while S is on its way.  Its V
+                // barrier may be asked for this phase only once the last one is over (its parity would pass for this
+                // one's): that is so where P V of the stage's last tile precedes what this group has waited for
+                // already, and for shared rows and split keys once S is there, which was issued behind it.
+                const bool border = key0 + kTileRows - 1 > pos0, early = P.splits == 1 && !shared;
+                const uint32_t vs = v_stage + (shared ? 2 * j + t : j);
+                const uint32_t v = base + PromptSmem::values + (vs % kRing) * kOperand;
+                bool cleaned = !border;
+#pragma unroll 1
+                for (int step = 0; step < 2; ++step) {
+                    if (step == 1) {
+                        if (!(ok = wait(kBarS + t, s_count))) break;
+                        ++s_count;
+                    }
+                    if (!cleaned && (early || step == 1)) {
+                        if (!(ok = wait(kBarVFull + vs % kRing, vs / kRing))) break;
+                        clean_values(v, min(kTileRows, keys - key0), warp & 3, lane, dirty + k % kItems, k + 1);
+                        cleaned = true;
+                    }
+                }
+                if (!ok) break;
                 pkv::tmem_fence_after_sync();
                 uint32_t s0[64], s1[64];
                 tmem_ld64(t_s, s0);
                 tmem_landed(s0);
                 tmem_ld64(t_s + 64, s1);
-                const int key0 = (first + (shared ? 2 * j + t : j)) * kTileRows;
-                const bool border = key0 + kTileRows - 1 > tile_pos;  // the causal border, or the context's end
+                const bool masked = key0 + kTileRows - 1 > tile_pos;  // the causal border, or the context's end
                 const int lim = pos - key0;
-                if (border) {
+                if (masked) {
 #pragma unroll
                     for (int c = 0; c < 64; ++c) s0[c] = c <= lim ? s0[c] : 0xff800000u;
                 }
@@ -698,7 +750,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                 for (int c = 0; c < 64; c += 2)
                     mx[(c >> 1) & 3] = fmaxf(fmaxf(mx[(c >> 1) & 3], __uint_as_float(s0[c])), __uint_as_float(s0[c + 1]));
                 tmem_landed(s1);
-                if (border) {
+                if (masked) {
 #pragma unroll
                     for (int c = 0; c < 64; ++c) s1[c] = 64 + c <= lim ? s1[c] : 0xff800000u;
                 }
@@ -749,6 +801,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                 l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             }
             if (!ok) break;
+            v_stage += n_kv;
             if (n > 0) {
                 if (!(ok = wait(kBarO + t, o_count))) break;
                 ++o_count;
@@ -830,6 +883,25 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
                                 o[32 * h + i] = __float_as_uint(fmaf(__uint_as_float(q[i]), w_other, __uint_as_float(o[32 * h + i])));
+                        }
+                    }
+                    if (dirty[k % kItems] == k + 1) {
+                        // Infinities and NaN that were taken out of V: every row that sees their key gets them whole
+                        // (an infinity times a weight above 0 is one; a weight that underflowed is taken for one above 0).
+                        for (int key = max(pos0 / kTileRows, first) * kTileRows; key <= pos && key < (first + n_kv) * kTileRows; ++key) {
+                            const __half *row_v;
+                            if (PAGED) {
+                                const int32_t id = __ldg(P.block_tables + static_cast<int64_t>(i0.x) * P.max_blocks + key / P.block_size);
+                                row_v = P.v + ((static_cast<int64_t>(id < 0 || id >= P.num_blocks ? 0 : id) * P.num_kv_heads + kvh) * P.block_size +
+                                               key % P.block_size) * kDim;
+                            } else {
+                                row_v = P.v + (slot_row0 - pos0 + static_cast<int64_t>(key)) * P.v_stride + kvh * kDim;
+                            }
+#pragma unroll
+                            for (int i = 0; i < 64; ++i) {
+                                const float x = __half2float(row_v[c + i]);
+                                if (!isfinite(x)) o[i] = __float_as_uint(__uint_as_float(o[i]) + x);
+                            }
                         }
                     }
                     if (whole) {
@@ -1475,6 +1547,8 @@ extern "C" PKV_API int pkv_prefill_attention(void *out, float *lse, const void *
     p.out = static_cast<__half *>(out);
     p.lse = lse;
     p.query_start = seq_start;
+    p.v = static_cast<const __half *>(v);
+    p.v_stride = v_stride;
     p.num_seqs = num_seqs;
     p.total_q = total_tokens;
     p.max_query_len = max_seq_len;
@@ -1509,6 +1583,7 @@ extern "C" PKV_API int pkv_prefill_attention_paged(void *out, float *lse, const 
     PromptParams p{};
     p.out = static_cast<__half *>(out);
     p.lse = lse;
+    p.v = static_cast<const __half *>(v_cache);
     p.query_start = query_start;
     p.block_tables = block_tables;
     p.context_lens = context_lens;

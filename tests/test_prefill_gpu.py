@@ -98,6 +98,42 @@ def test_other_sequences_do_not_leak():
     assert_no_device_error()
 
 
+@pytest.mark.parametrize("hq,hkv", [(2, 2), (8, 1)])
+@pytest.mark.parametrize("paged", [False, True])
+def test_infinities_in_later_values(hq, hkv, paged):
+    """An infinity or NaN in a token's V reaches the rows at and after that token, in its dim and kv head, and no others:
+    everything else is bit for bit what it is with zeros there."""
+    n = 420
+    g = torch.Generator(device="cuda").manual_seed(hq)
+    q, k, v = (torch.randn((n, h, 128), generator=g, device="cuda").half() for h in (hq, hkv, hkv))
+    start = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    spots = [(3, 0, 5, float("inf")), (130, hkv - 1, 127, float("nan")), (131, 0, 64, float("-inf")), (300, 0, 5, float("-inf")),
+             (419, 0, 9, float("inf"))]
+    zeros, values = v.clone(), v.clone()
+    for t, h, d, x in spots:
+        zeros[t, h, d] = 0
+        values[t, h, d] = x
+
+    def run(x):
+        out = torch.empty_like(q)
+        if not paged:
+            return pkv.prefill_attention(out, q, k, x, start, n, SCALE)
+        bs, nb = 32, -(-n // 32)
+        table = torch.randperm(nb, generator=torch.Generator().manual_seed(1)).to(torch.int32).view(1, -1)
+        kc, vc = (torch.full((nb, hkv, bs, 128), float("nan"), dtype=torch.float16, device="cuda") for _ in range(2))
+        slots = pkv.slot_mapping(table.expand(n, -1).contiguous(), torch.arange(n, dtype=torch.int32), bs).cuda()
+        pkv.append(kc, vc, slots, k, x)
+        return pkv.prefill_attention_paged(out, q, kc, vc, table.cuda(), torch.tensor([n], dtype=torch.int32, device="cuda"), start, n, SCALE)
+    clean, got = run(zeros).view(n, hkv, -1, 128), run(values).view(n, hkv, -1, 128)
+    expect = clean.float()
+    for t, h, d, x in spots:
+        expect[t:, h, :, d] += x  # inf - inf is NaN here too
+    assert torch.equal(torch.isnan(got), torch.isnan(expect))
+    same = ~torch.isnan(expect)
+    assert torch.equal(got.float()[same], expect[same])
+    assert_no_device_error()
+
+
 def run_paged(ctxs, chunks, group, hkv, bs, seed, peaky=0.0, poison=False):
     case = workloads.random_case(seed, ctxs, group * hkv, hkv, block_size=bs, peaky_fraction=peaky, peaky_factor=6.0)
     if poison:  # whatever lies behind a context in its last block, and in blocks of nobody
