@@ -2,7 +2,9 @@
  * pkv.h -- C ABI of the paged-KV-cache decode-attention library (libpkv.so).
  *
  * One decode step of a transformer layer over a paged KV cache, for one GPU
- * (NVIDIA GB300, sm_103a):
+ * (NVIDIA GB300, sm_103a), and what a server runs around it (rotary positions, attention of
+ * prompts and chunks, accumulated attention weights, eviction: the sections at the end).
+ * The step:
  *
  *   1. the new token's K and V are written in place into their cache slots
  *      (pkv_append) -- no reallocation, old entries are never recomputed
@@ -735,7 +737,8 @@ PKV_API int pkv_rope(void *q_out, int64_t q_out_stride, void *k_out, int64_t k_o
 /* pkv_rope with the append in the same launch: the rotated k_new and v_new as it is go to their
  * slots of the cache, q is rotated into q_out.  slot_mapping as pkv_append's: a negative slot skips
  * the token's k and v (its q is rotated all the same), one past the pool is skipped and recorded as
- * PKV_DEV_BAD_SLOT.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+ * PKV_DEV_BAD_SLOT.  It writes the cache, so a step call issued right behind it on the same cache must not
+ * set PKV_STEP_OVERLAP.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 PKV_API int pkv_rope_append(void *q_out, int64_t q_out_stride, const void *q, int64_t q_stride, const void *k_new,
                             int64_t k_stride, const void *v_new, int64_t v_stride, void *k_cache, void *v_cache,
                             const int64_t *slot_mapping, const int32_t *positions, const int64_t *frequencies,
@@ -750,7 +753,8 @@ PKV_API int pkv_rope_append(void *q_out, int64_t q_out_stride, const void *q, in
  * (q_stride elements between tokens, a multiple of 8); out is [total_q][num_q_heads][head_dim],
  * contiguous; lse, if not NULL, receives float32 [total_q][num_q_heads], the natural logarithm of
  * each row's sum of exponentials.  Request b owns rows query_start[b] .. query_start[b + 1] - 1
- * (DEVICE int32 [num_seqs + 1]; empty ranges allowed); rows outside every range are left as they were.
+ * (DEVICE int32 [num_seqs + 1]; empty ranges allowed, overlapping ones not); rows outside every range are
+ * left as they were.
  * A range that is negative, longer than max_query_len or past total_q is skipped and recorded as
  * PKV_DEV_BAD_CONTEXT.  Weights are rounded to fp16 for the product with V; sums and the
  * accumulator are float32.  What lies past a context never enters a result; infinities and NaN in a

@@ -62,6 +62,7 @@ constexpr int kMmaWarp = kSoftmaxWarps, kLoadWarp = kSoftmaxWarps + 1, kValueWar
 constexpr float kLazy = 8.0f;              // log2 units
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kMaxSplits = 64;
+constexpr int64_t kMaxContext = 1 << 30;  // positions and their sums with a tile's stay in 32 bits
 constexpr int kPlannedSms = 152;  // the split plan, and with it the workspace, is the same on every device
 
 struct PromptParams {
@@ -1490,7 +1491,7 @@ int launch_prompt(PromptParams p, int max_context, void *workspace, size_t works
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, kernel, p) != cudaSuccess) return PKV_ERR_CUDA;
     if (p.splits == 1) return PKV_OK;
-    const int64_t rows = static_cast<int64_t>(p.max_query_len) * p.num_q_heads;
+    const int64_t rows = static_cast<int64_t>(p.max_query_len < p.total_q ? p.max_query_len : p.total_q) * p.num_q_heads;
     cfg.gridDim = dim3(static_cast<unsigned>((rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32)), p.num_seqs);
     cfg.blockDim = dim3(kJoinThreads);
     cfg.dynamicSmemBytes = 0;
@@ -1580,6 +1581,7 @@ extern "C" PKV_API int pkv_prefill_attention_paged(void *out, float *lse, const 
     if (!out || !pkv_internal::aligned16(out)) return PKV_ERR_INVALID_ARG;
     const int64_t rows = num_blocks * num_kv_heads * block_size;
     if (rows >= 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;  // box row coordinates are signed 32-bit
+    if (static_cast<int64_t>(max_blocks_per_seq) * block_size > kMaxContext) return PKV_ERR_UNSUPPORTED;
     PromptParams p{};
     p.out = static_cast<__half *>(out);
     p.lse = lse;
@@ -1627,6 +1629,7 @@ extern "C" PKV_API int pkv_prefill_attention_weights(float *scores, int64_t scor
     if (done) return PKV_OK;
     const int64_t rows = num_blocks * num_kv_heads * block_size;
     if (rows >= 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;  // box row coordinates are signed 32-bit
+    if (static_cast<int64_t>(max_blocks_per_seq) * block_size > kMaxContext) return PKV_ERR_UNSUPPORTED;
     ChunkWeightParams w{};
     PromptParams &p = w.p;
     p.query_start = query_start;

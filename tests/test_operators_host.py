@@ -167,3 +167,9 @@ def test_prefill_workspace(lib):
     for bad in ((0, 16, 32, 8, 128, 4096), (1, 0, 32, 8, 128, 4096), (1, 16, 24, 8, 128, 4096), (1, 16, 32, 8, 64, 4096),
                 (1, 16, 32, 8, 128, 0)):
         assert f(*bad) == 0
+
+
+def test_long_tables_are_refused(lib):
+    wide = dict(width=(1 << 30) // 16 + 1, seqs=1, nb=1000)
+    assert call(lib, "pkv_prefill_attention_paged", dict(PAGED, **wide)) == UNSUPPORTED
+    assert call(lib, "pkv_prefill_attention_weights", dict(CHUNK, **wide), capacity=1 << 31) == UNSUPPORTED
