@@ -85,6 +85,8 @@ __device__ __forceinline__ void rotate_unit(uint4 &x, uint4 &y, const float4 *cs
     y = make_uint4(b[0], b[1], b[2], b[3]);
 }
 
+// UNITS: units per row where known at compile time (8: heads of 128 dims), else 0.
+template <int UNITS>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams P) {
     // (cos, sin) of pair i = 8 u + 2 j + e at float4 j * (rotary / 16) + u: neighbouring units' reads
     // of one j are neighbouring float4s.
@@ -92,7 +94,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     pkv::pdl_wait_primary();  // by every thread: the next kernel may rely on it
     pkv::pdl_launch_dependents();
     const int64_t t = blockIdx.x;
-    const int units_per_row = P.head_dim / 16;
+    const int units_per_row = UNITS ? UNITS : P.head_dim / 16;
     const int r16 = P.rotary_dim / 16;
     const int heads = P.num_q_heads + P.num_kv_heads + (P.v ? P.num_kv_heads : 0);
     const int begin = blockIdx.y * P.units_per_cta;
@@ -106,6 +108,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
             slot = -1;
         }
     }
+    const int64_t block = P.k_cache && slot >= 0 ? slot / P.block_size : 0;
+    const int64_t cache_row = P.k_cache ? block * P.num_kv_heads * P.block_size + (max(slot, static_cast<int64_t>(0)) - block * P.block_size) : 0;
     // A unit's two pieces: where they are read and written; `first` is the piece in its row.
     struct Unit {
         const uint4 *src;
@@ -133,9 +137,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
             x.src = (is_v ? P.v + t * P.v_stride : P.k + t * P.k_stride) + static_cast<int64_t>(kvh) * pieces;
             if (P.k_cache) {
                 x.live = slot >= 0;  // a padding token: its k and v go nowhere
-                const int64_t block = x.live ? slot / P.block_size : 0;
-                const int64_t at = (block * P.num_kv_heads + kvh) * P.block_size + (x.live ? slot - block * P.block_size : 0);
-                x.dst = (is_v ? P.v_cache : P.k_cache) + at * pieces;
+                x.dst = (is_v ? P.v_cache : P.k_cache) + (cache_row + static_cast<int64_t>(kvh) * P.block_size) * pieces;
             } else {
                 x.dst = P.k_out + t * P.k_out_stride + static_cast<int64_t>(kvh) * pieces;
             }
@@ -203,7 +205,7 @@ int launch_rope(RopeParams p, int num_tokens, pkv_stream_t stream) {
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, rope_kernel, p) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, p.head_dim == 128 ? rope_kernel<8> : rope_kernel<0>, p) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
 int check_rope(const void *q_out, const void *q, const void *k, const int32_t *positions, const int64_t *frequencies,
