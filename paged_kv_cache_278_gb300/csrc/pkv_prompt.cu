@@ -75,7 +75,8 @@ struct PromptParams {
     int num_seqs, total_q, max_query_len, max_blocks, num_q_heads, num_kv_heads, block_size;
     int64_t num_blocks;
     int group_log2, box_rows;
-    int splits;  // at most; the kernels take split_count of it
+    int splits;       // at most; the kernels take split_count of it
+    int split_tiles;  // key tiles that a split is worth
     float q_scale;                // scale * log2(e)
     const __half *v;   // V as the maps read it: [rows][128], rows v_stride elements apart where packed
     int64_t v_stride;
@@ -85,7 +86,8 @@ struct PromptParams {
 // One unit of work; `kv_count` per softmax group is 0 for a group without rows or without keys here.
 struct alignas(16) Item {
     int seq;        // -1: no more items
-    int kvh, split;
+    int kvh;
+    int split;      // -1: the only one, which writes the output itself
     int row0;       // q row (token) of the pair's first token
     int live[2];    // live tokens of the groups' tiles (both tile A's where the groups share it)
     int pos0;       // logical position of the first token
@@ -280,11 +282,29 @@ __device__ __forceinline__ int pairs_from(const PromptParams &P, int tile, int p
     return __reduce_add_sync(pkv::kFullMask, c);
 }
 
-// Splits of each item's keys: two items per SM (the longer ones come first), from the call's actual
-// pairs, which the host does not know; the same in every CTA and in the joining launch.
-__device__ __forceinline__ int split_count(const PromptParams &P, int pairs) {
+// Key tiles of the longest context.
+__device__ __forceinline__ int most_tiles(const PromptParams &P, int lane) {
+    int tiles = 0;
+    for (int b = lane; b < P.num_seqs; b += 32) {
+        const Request r = request_of(P, b, false);
+        if (r.tokens > 0) tiles = max(tiles, (r.keys + kTileRows - 1) / kTileRows);
+    }
+    return __reduce_max_sync(pkv::kFullMask, tiles);
+}
+
+// Splits of each item's keys, from the call's actual pairs and contexts, which the host does not know; the
+// same in every CTA and in the joining launch.  Two items per SM (the longer ones come first) where the
+// items are fewer than half of the SMs; up to two thirds of them, three splits make two rounds of a third of the
+// work; past that the rounds cost what the splits save.  (G = 4, 8 kv heads, whole against split: 2 x 37 tokens behind
+// 32k 419 and 84 us, 37 behind 4k 66 and 26, 4 x 100 behind 8k 117 and 88, 8 x 64 behind 4k 70 and 66; two
+// splits of 128 items 119 and 146.)
+__device__ __forceinline__ int split_count(const PromptParams &P, int pairs, int tiles) {
     if (P.splits <= 1) return 1;
-    return max(min(P.splits, 2 * kPlannedSms / max(pairs * P.num_kv_heads, 1)), 2);
+    const int items = max(pairs * P.num_kv_heads, 1);
+    int s = 2 * items <= kPlannedSms ? 2 * kPlannedSms / items : (3 * items <= 2 * kPlannedSms ? 3 : 1);
+    const int most = min(P.splits, tiles / P.split_tiles);
+    if (most < s) s = most * items > kPlannedSms ? kPlannedSms / items : most;  // two rounds are full, or it is one
+    return max(s, 1);
 }
 
 // Item `index` of the call: pairs by their last key tile, from the last to the first (the longest first), for
@@ -292,7 +312,8 @@ __device__ __forceinline__ int split_count(const PromptParams &P, int pairs) {
 __device__ Item find_item(const PromptParams &P, int64_t index, int splits, int tiles, int lane) {
     const int tile_tokens = kTileRows >> P.group_log2, pair_tokens = 2 * tile_tokens;
     Item it{};
-    it.split = static_cast<int>(index % splits);
+    const int split = static_cast<int>(index % splits);
+    it.split = splits > 1 ? split : -1;
     it.kvh = static_cast<int>(index / splits % P.num_kv_heads);
     const int rank = static_cast<int>(index / splits / P.num_kv_heads);
     int lo = 0, hi = tiles;  // pairs_from(lo) > rank >= pairs_from(hi) = past
@@ -349,7 +370,7 @@ __device__ Item find_item(const PromptParams &P, int64_t index, int splits, int 
     }
     const int all = max(count[0], count[1]);
     const int per = (all + splits - 1) / splits;
-    it.kv_first = it.split * per;
+    it.kv_first = split * per;
     const int end = min(all, it.kv_first + per);
 #pragma unroll
     for (int t = 0; t < 2; ++t) it.kv_count[t] = max(min(count[t], end) - it.kv_first, 0);
@@ -480,13 +501,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
         if (warp == kItemWarp) {
             // ---------------------------------------------------------------- work items, up to kItems ahead
             const int pairs = pairs_from(P, 0, 2 * tile_tokens, lane, blockIdx.x == 0);
-            const int splits = split_count(P, pairs);
-            int tiles = 0;  // key tiles of the longest context
-            for (int b = lane; b < P.num_seqs; b += 32) {
-                const Request r = request_of(P, b, false);
-                if (r.tokens > 0) tiles = max(tiles, (r.keys + kTileRows - 1) / kTileRows);
-            }
-            tiles = __reduce_max_sync(pkv::kFullMask, tiles);
+            const int tiles = most_tiles(P, lane);
+            const int splits = split_count(P, pairs, tiles);
             const uint32_t n_items = static_cast<uint32_t>(pairs) * P.num_kv_heads * splits;  // (bounded by the host)
             bool ok = true;
             for (uint32_t k = 0; ok; ++k) {
@@ -718,7 +734,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                 // barrier may be asked for this phase only once the last one is over (its parity would pass for this
                 // one's): that is so where P V of the stage's last tile precedes what this group has waited for
                 // already, and for shared rows and split keys once S is there, which was issued behind it.
-                const bool border = key0 + kTileRows - 1 > pos0, early = P.splits == 1 && !shared;
+                const bool border = key0 + kTileRows - 1 > pos0, early = split < 0 && !shared;
                 const uint32_t vs = v_stage + (shared ? 2 * j + t : j);
                 const uint32_t v = base + PromptSmem::values + (vs % kRing) * kOperand;
                 bool cleaned = !border;
@@ -834,7 +850,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                 // 128 bytes of each row at a time (64 fp16 dims, or 32 float32 ones of a partial result) through the
                 // warp's own 4 KB, so that eight lanes store a whole line.  The 16-byte pieces of row x lie at piece
                 // ^ (x % 8).  Lane's share of a line: piece lane % 8 of rows 4 i + lane / 8.
-                const bool whole = P.splits == 1;
+                const bool whole = split < 0;
                 const uint32_t lines = base + PromptSmem::staging + warp * 4096, mine = lines + lane * 128;
                 const uint32_t row_bytes = whole ? kDim * 2 : P.splits * kDim * 4;
                 const int group_mask = (1 << glog) - 1;
@@ -931,7 +947,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                 pkv::tmem_fence_before_sync();  // O read before the next item's first P V (ordered by its weights' arrival)
             }
             if (store && (t == 0 || !shared)) {
-                if (P.splits > 1) {
+                if (split >= 0) {
                     P.m_part[row * P.splits + split] = total == 0.f ? -INFINITY : m;
                     P.l_part[row * P.splits + split] = total;
                 } else if (P.lse != nullptr) {
@@ -954,13 +970,17 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
     }
 }
 
-// Joins the splits of each (token, head) row: one warp per row, four dims a lane.
+// Joins the splits of each (token, head) row: one warp per row, four dims a lane, BATCH splits' loads in flight.
+// Sixteen take 120 registers, two CTAs per SM; where those hold fewer rows than there are, eight loads a lane and
+// four CTAs do better (512 tokens behind 7680, three splits: 90 -> 87 us in all; 2 x 37 tokens behind 32k the other
+// way, 89 -> 84).
 constexpr int kJoinThreads = 256;
-__global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const __grid_constant__ PromptParams P) {
+template <int BATCH>
+__global__ void __launch_bounds__(kJoinThreads, BATCH == 8 ? 4 : 2) prompt_join_kernel(const __grid_constant__ PromptParams P) {
     __shared__ int s_splits;
     const int lane = threadIdx.x & 31;
     if (threadIdx.x < 32) {
-        const int n = split_count(P, pairs_from(P, 0, 2 * kTileRows >> P.group_log2, lane, false));
+        const int n = split_count(P, pairs_from(P, 0, 2 * kTileRows >> P.group_log2, lane, false), most_tiles(P, lane));
         if (lane == 0) s_splits = n;
     }
     __syncthreads();
@@ -969,54 +989,57 @@ __global__ void __launch_bounds__(kJoinThreads) prompt_join_kernel(const __grid_
     // for what came before) does not write; its partial results from here on.
     pkv::pdl_wait_primary();
     pkv::pdl_launch_dependents();
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * (kJoinThreads / 32) + (threadIdx.x >> 5);
-    if (i >= static_cast<int64_t>(r.tokens) * P.num_q_heads) return;
-    const int64_t row = static_cast<int64_t>(r.start) * P.num_q_heads + i;
     const int splits = s_splits;
-    const float *m = P.m_part + row * P.splits, *l = P.l_part + row * P.splits;
-    // lane s holds splits s and s + 32: all of the row's (m, l) in one round of loads
-    float ms[2], ls[2];
+    if (splits == 1) return;  // the outputs are there
+    const int64_t rows = static_cast<int64_t>(r.tokens) * P.num_q_heads;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * (kJoinThreads / 32) + (threadIdx.x >> 5); i < rows;
+         i += static_cast<int64_t>(gridDim.x) * (kJoinThreads / 32)) {
+        const int64_t row = static_cast<int64_t>(r.start) * P.num_q_heads + i;
+        const float *m = P.m_part + row * P.splits, *l = P.l_part + row * P.splits;
+        // lane s holds splits s and s + 32: all of the row's (m, l) in one round of loads
+        float ms[2], ls[2];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-        const int s = lane + 32 * u;
-        ms[u] = s < splits ? __ldcg(m + s) : -INFINITY;
-        ls[u] = s < splits ? __ldcg(l + s) : 0.f;
-    }
-    float top = fmaxf(ms[0], ms[1]);
+        for (int u = 0; u < 2; ++u) {
+            const int s = lane + 32 * u;
+            ms[u] = s < splits ? __ldcg(m + s) : -INFINITY;
+            ls[u] = s < splits ? __ldcg(l + s) : 0.f;
+        }
+        float top = fmaxf(ms[0], ms[1]);
 #pragma unroll
-    for (int sh = 16; sh >= 1; sh >>= 1) top = fmaxf(top, __shfl_xor_sync(pkv::kFullMask, top, sh));
-    float total = 0.f;
+        for (int sh = 16; sh >= 1; sh >>= 1) top = fmaxf(top, __shfl_xor_sync(pkv::kFullMask, top, sh));
+        float total = 0.f;
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-        ls[u] = ls[u] == 0.f ? 0.f : ls[u] * exp2f(ms[u] - top);  // a split without visible keys wrote no output
-        total += ls[u];
-    }
-#pragma unroll
-    for (int sh = 16; sh >= 1; sh >>= 1) total += __shfl_xor_sync(pkv::kFullMask, total, sh);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s0 = 0; s0 < splits; s0 += 16) {
-        float4 o[16];
-        float w[16];
-#pragma unroll
-        for (int u = 0; u < 16; ++u) {
-            const int s = s0 + u;
-            w[u] = __shfl_sync(pkv::kFullMask, s < 32 ? ls[0] : ls[1], s & 31);  // (0 past the last split)
-            o[u] = __ldcg(reinterpret_cast<const float4 *>(P.o_part + (row * P.splits + min(s, splits - 1)) * kDim) + lane);
+        for (int u = 0; u < 2; ++u) {
+            ls[u] = ls[u] == 0.f ? 0.f : ls[u] * exp2f(ms[u] - top);  // a split without visible keys wrote no output
+            total += ls[u];
         }
 #pragma unroll
-        for (int u = 0; u < 16; ++u) {
-            const bool written = w[u] != 0.f;  // else the slot holds anything (selected away, so that all loads are in flight)
-            acc.x = fmaf(w[u], written ? o[u].x : 0.f, acc.x);
-            acc.y = fmaf(w[u], written ? o[u].y : 0.f, acc.y);
-            acc.z = fmaf(w[u], written ? o[u].z : 0.f, acc.z);
-            acc.w = fmaf(w[u], written ? o[u].w : 0.f, acc.w);
+        for (int sh = 16; sh >= 1; sh >>= 1) total += __shfl_xor_sync(pkv::kFullMask, total, sh);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int s0 = 0; s0 < splits; s0 += BATCH) {
+            float4 o[BATCH];
+            float w[BATCH];
+#pragma unroll
+            for (int u = 0; u < BATCH; ++u) {
+                const int s = s0 + u;
+                w[u] = __shfl_sync(pkv::kFullMask, s < 32 ? ls[0] : ls[1], s & 31);  // (0 past the last split)
+                o[u] = __ldcg(reinterpret_cast<const float4 *>(P.o_part + (row * P.splits + min(s, splits - 1)) * kDim) + lane);
+            }
+#pragma unroll
+            for (int u = 0; u < BATCH; ++u) {
+                const bool written = w[u] != 0.f;  // else the slot holds anything (selected away, so that all loads are in flight)
+                acc.x = fmaf(w[u], written ? o[u].x : 0.f, acc.x);
+                acc.y = fmaf(w[u], written ? o[u].y : 0.f, acc.y);
+                acc.z = fmaf(w[u], written ? o[u].z : 0.f, acc.z);
+                acc.w = fmaf(w[u], written ? o[u].w : 0.f, acc.w);
+            }
         }
+        const float inv = 1.f / total;
+        const __half2 lo = __floats2half2_rn(acc.x * inv, acc.y * inv), hi = __floats2half2_rn(acc.z * inv, acc.w * inv);
+        *reinterpret_cast<uint2 *>(P.out + row * kDim + 4 * lane) =
+            make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+        if (lane == 0 && P.lse != nullptr) P.lse[row] = (top + log2f(total)) * kLn2;
     }
-    const float inv = 1.f / total;
-    const __half2 lo = __floats2half2_rn(acc.x * inv, acc.y * inv), hi = __floats2half2_rn(acc.z * inv, acc.w * inv);
-    *reinterpret_cast<uint2 *>(P.out + row * kDim + 4 * lane) =
-        make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
-    if (lane == 0 && P.lse != nullptr) P.lse[row] = (top + log2f(total)) * kLn2;
 }
 
 // ---------------------------------------------------------------- weights of a chunk's rows
@@ -1426,14 +1449,23 @@ int encode_rows(CUtensorMap *map, const void *base, int64_t rows, int64_t cols, 
 }
 
 
-// The most splits of each item's keys: 1 when the items fill half of the SMs or the contexts are short (under
-// 512 keys a split, the second launch and the partial results cost more than they save), else what
-// gives four items per SM by the most pairs that total_q rows can make.
+// Key tiles that a split is worth: the joining launch costs by the rows, so one per 1024 rows, two at least and
+// eight at most.  (37 tokens x 32 heads over 1000 keys: 22.5 us with two tiles, 27 with four, 27.5 whole; 160 over
+// 4096: 42 with two or four, 34 with five; 512 over 2048: 49 with four, 41 whole.)
+int split_tiles(int total_q, int num_q_heads) {
+    const int64_t t = static_cast<int64_t>(total_q) * num_q_heads / 1024;
+    return t < 2 ? 2 : (t > 8 ? 8 : static_cast<int>(t));
+}
+
+// The most splits of each item's keys: 1 when the items, by the fewest pairs that total_q rows make, fill two
+// thirds of the SMs or the contexts are short, else what gives four items per SM.
 int plan_splits(int num_seqs, int total_q, int num_q_heads, int num_kv_heads, int max_context) {
     const int pair_tokens = 2 * kTileRows / (num_q_heads / num_kv_heads);
-    const int64_t items = (static_cast<int64_t>(total_q) / pair_tokens + num_seqs) * num_kv_heads;
-    if (2 * items > kPlannedSms) return 1;
-    const int64_t by_keys = max_context / 512;
+    const int64_t pairs = (static_cast<int64_t>(total_q) + pair_tokens - 1) / pair_tokens;
+    const int64_t items = (pairs > num_seqs ? pairs : num_seqs) * num_kv_heads;
+    if (3 * items > 2 * kPlannedSms) return 1;
+    const int64_t by_keys = max_context / (split_tiles(total_q, num_q_heads) * kTileRows);
+    if (by_keys < 3) return 1;
     int64_t s = 4 * kPlannedSms / (items > 0 ? items : 1);
     s = s < by_keys ? s : by_keys;
     s = s < kMaxSplits ? s : kMaxSplits;
@@ -1456,6 +1488,7 @@ bool group_ok(int num_q_heads, int num_kv_heads) {
 template <bool PAGED>
 int launch_prompt(PromptParams p, int max_context, void *workspace, size_t workspace_bytes, pkv_stream_t stream) {
     p.splits = plan_splits(p.num_seqs, p.total_q, p.num_q_heads, p.num_kv_heads, max_context);
+    p.split_tiles = split_tiles(p.total_q, p.num_q_heads);
     const size_t need = prompt_workspace(p.total_q, p.num_q_heads, p.splits);
     if (need) {
         if (!workspace || workspace_bytes < need || !pkv_internal::aligned(workspace, 256)) return PKV_ERR_WORKSPACE;
@@ -1492,10 +1525,12 @@ int launch_prompt(PromptParams p, int max_context, void *workspace, size_t works
     if (cudaLaunchKernelEx(&cfg, kernel, p) != cudaSuccess) return PKV_ERR_CUDA;
     if (p.splits == 1) return PKV_OK;
     const int64_t rows = static_cast<int64_t>(p.max_query_len < p.total_q ? p.max_query_len : p.total_q) * p.num_q_heads;
-    cfg.gridDim = dim3(static_cast<unsigned>((rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32)), p.num_seqs);
+    const int64_t by_rows = (rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32), by_sms = (4 * sms + p.num_seqs - 1) / p.num_seqs;
+    const bool many = static_cast<int64_t>(p.total_q) * p.num_q_heads > 2 * sms * (kJoinThreads / 32);
+    cfg.gridDim = dim3(static_cast<unsigned>(by_rows < by_sms ? by_rows : by_sms), p.num_seqs);
     cfg.blockDim = dim3(kJoinThreads);
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, prompt_join_kernel, p) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, many ? prompt_join_kernel<8> : prompt_join_kernel<16>, p) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
 int log2_of(int g) { return g == 1 ? 0 : (g == 2 ? 1 : (g == 4 ? 2 : 3)); }

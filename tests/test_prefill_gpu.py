@@ -179,6 +179,18 @@ def test_paged_split_keys(ctxs, chunks, group, hkv, bs):
     assert ws is not None  # the plan splits these
 
 
+# The plan, which knows no lengths, allows splits; the launch takes one (short contexts behind a wide table, or more
+# tiles than the rows' number needs), or three.
+@pytest.mark.parametrize("ctxs,chunks,group,hkv,bs,planned", [
+    ([5000, 200, 129], [0, 37, 2], 4, 2, 16, True), ([1100] * 17, [130] * 17, 2, 4, 32, False),  # under three splits' keys: none
+    ([3200] * 17, [130] * 17, 2, 4, 32, True), ([3100, 3073, 3090, 3099, 3076], [257] * 5, 1, 8, 64, True)])
+def test_paged_splits_by_the_actual_lengths(ctxs, chunks, group, hkv, bs, planned):
+    out, z, args, ws = run_paged(ctxs, chunks, group, hkv, bs, 81)
+    again, z2 = torch.empty_like(out), torch.empty_like(z)
+    pkv.prefill_attention_paged(again, *args, lse=z2, workspace=ws)
+    assert (ws is not None) == planned and torch.equal(again, out) and torch.equal(z2, z)
+
+
 def test_paged_long_chunk_past_the_multi_call():
     run_paged([1400], [1300], 4, 2, 16, 78)
 
