@@ -49,7 +49,6 @@ struct EvictParams {
     int64_t capacity, num_blocks;
     int max_blocks, max_new_blocks, num_kv_heads, block_size, row_bytes;
     int budget, recent, sinks;
-    int quads;    // scores and new_scores rows are 16-byte aligned
     int select_cluster;  // CTAs that select of one (request, kv head) together
     int cluster;         // CTAs that move one's K, or V, together
 };
@@ -142,7 +141,6 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
     int32_t *kept = P.kept + row * P.budget;
     const int n = cached(P, b, tid == 0 && blockIdx.x == 0);
     const int m = min(n, P.budget);
-    const bool quads = P.quads != 0;  // rows of scores start on 16 bytes
     const int run = rank * kRun;      // the CTA's first position
 
     if (n > P.budget) {  // (the whole cluster)
@@ -150,18 +148,10 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
         const int need = P.budget - P.sinks - P.recent;
         float raw[KPT];
 #pragma unroll
-        for (int j = 0; j < J; ++j) {  // all in flight (clamped: what lies past n is never looked at)
+        for (int j = 0; j < J; ++j) {  // all in flight (clamped: what lies past n is never looked at); 16-byte loads measured the same
             const int p = run + (j * T + tid) * 4;
-            if (quads) {
-                const float4 v = __ldcg(reinterpret_cast<const float4 *>(scores + min(p, (n - 1) & ~3)));
-                raw[4 * j] = v.x;
-                raw[4 * j + 1] = v.y;
-                raw[4 * j + 2] = v.z;
-                raw[4 * j + 3] = v.w;
-            } else {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) raw[4 * j + e] = __ldcg(scores + min(p + e, n - 1));
-            }
+            for (int e = 0; e < 4; ++e) raw[4 * j + e] = __ldcg(scores + min(p + e, n - 1));
         }
         auto position = [&](int i) { return run + ((i / 4) * T + tid) * 4 + i % 4; };
         auto candidate = [&](int p) { return p >= first && p < last; };
@@ -319,15 +309,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
         for (int p = n + rank * T + tid; p < P.budget; p += ranks * T) kept[p] = -1;
     }
     // Zeros behind the kept scores (read by every CTA, see above), shared out between the CTAs.
-    int64_t tail = m;
-    if (quads) {
-        tail = min((static_cast<int64_t>(m) + 3) & ~static_cast<int64_t>(3), P.capacity);
-        if (rank == 0 && m + tid < tail) out[m + tid] = 0.f;
-        for (int64_t p = tail + 4 * (rank * T + tid); p < P.capacity; p += 4 * ranks * T)
-            *reinterpret_cast<float4 *>(out + p) = make_float4(0.f, 0.f, 0.f, 0.f);
-    } else {
-        for (int64_t p = tail + rank * T + tid; p < P.capacity; p += ranks * T) out[p] = 0.f;
-    }
+    for (int64_t p = static_cast<int64_t>(m) + rank * T + tid; p < P.capacity; p += ranks * T) out[p] = 0.f;
     cluster_arrive();  // no CTA's shared memory goes while another may read it
     cluster_wait();
 }
@@ -484,7 +466,6 @@ extern "C" PKV_API int pkv_evict(void *k_cache, void *v_cache, int32_t *kept, fl
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    p.quads = score_capacity % 4 == 0 && pkv_internal::aligned16(scores) && pkv_internal::aligned16(new_scores);
     // Eight CTAs to a row as long as a thread has four scores left; more than 32 a thread only past 131072.
     const int64_t runs = (cap + kSelThreads - 1) / kSelThreads;  // scores per thread of a single CTA
     p.select_cluster = runs <= 4 ? 1 : (runs <= 8 ? 2 : (runs <= 16 ? 4 : 8));
