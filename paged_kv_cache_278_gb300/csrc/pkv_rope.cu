@@ -13,7 +13,10 @@
 // modulo one turn, exact to 2^-65 p turns.  Its upper 32 bits, signed, are a fraction in [-1/2, 1/2)
 // turns, and sincospif takes them from there.
 //
-// What bounds it: memory (every row is read once and written once; 3 flops an element).  One CTA
+// What bounds it: memory (every row is read once and written once; 3 flops an element): 8192 tokens of 48
+// rows, half of each head rotated in interleaved pairs, 201 MB in 35.6 us, 5.65 TB/s, 85 % of what a plain copy
+// reaches; 4099 tokens of 64 rows out of a fused projection, 134 MB in 23.3 us, 86 %.  The issue slots are half
+// busy beside it.  A decode step's 16 tokens take 2.2 us (back to back in a graph).  One CTA
 // takes one token (and, when tokens are few, a slice of its rows, so that the call spreads over the
 // SMs): its rows' first loads are in flight while rotary_dim / 2 of its threads compute the angles
 // once for all heads into shared memory.  A thread's unit is 32 bytes (two 16-byte pieces): pieces c
@@ -85,7 +88,8 @@ __device__ __forceinline__ void rotate_unit(uint4 &x, uint4 &y, const float4 *cs
     y = make_uint4(b[0], b[1], b[2], b[3]);
 }
 
-// UNITS: units per row where known at compile time (8: heads of 128 dims), else 0.
+// UNITS: units per row where known at compile time (8: heads of 128 dims, whose 8192-token append takes 35.6 us
+// that way and 35.9 the other), else 0.
 template <int UNITS>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams P) {
     // (cos, sin) of pair i = 8 u + 2 j + e at float4 j * (rotary / 16) + u: neighbouring units' reads
@@ -191,7 +195,8 @@ int launch_rope(RopeParams p, int num_tokens, pkv_stream_t stream) {
     const int units = (p.num_q_heads + p.num_kv_heads + (p.v ? p.num_kv_heads : 0)) * (p.head_dim / 16);
     // One CTA per token and kRopePrefetch units a thread are one pass; with few tokens a token's rows
     // are cut into slices of one unit a thread, so that a decode step's call is one round of loads on
-    // many SMs instead of three on few.
+    // many SMs instead of three on few (48 rows, in a graph: 16 tokens 2.2 us sliced and 2.6 whole, 304 tokens 2.9
+    // both, 512 tokens 4.4 and 3.4).
     const int per_cta = num_tokens <= 304 ? kRopeThreads : ((units + kRopeThreads - 1) / kRopeThreads) * kRopeThreads;
     const int64_t slices = (units + per_cta - 1) / per_cta;
     if (slices > 65535) return PKV_ERR_UNSUPPORTED;
