@@ -1056,10 +1056,10 @@ __global__ void __launch_bounds__(kJoinThreads, BATCH == 8 ? 4 : 2) prompt_join_
 // until a chunk is so small that reading K bounds it.  The last 256 tokens of 2 x 16384 (32 heads, G = 4): 200
 // million pairs in 60 us, the tensor cores and the special-function units 40 % busy each (27 and 22 us alone): each
 // of the 13 items of an SM starts with loads and ends with its sums.
-//   warps 0-3, 4-7  the even and odd row tiles of an item, each with two S^T buffers of 128 TMEM columns
+//   warps 0-3, 4-7  a key tile each, or the even and odd row tiles of one, with two S^T buffers of 128 TMEM columns
 //   warp 8          issues the MMAs
-//   warps 9, 10     issue the tensor copies of K tiles (two stages) and of Q tiles (ring of four)
-//   warp 11         finds the items (a 128-key tile of one request and kv head), a few ahead
+//   warps 9, 10     issue the tensor copies of K tiles and of Q tiles, each through a ring
+//   warp 11         finds the items (two neighbouring 128-key tiles of one request and kv head, or one), a few ahead
 struct ChunkWeightParams {
     PromptParams p;
     const float *lse;
@@ -1067,7 +1067,7 @@ struct ChunkWeightParams {
     int64_t capacity;
 };
 
-constexpr int kKeyStages = 2, kRowRing = 4;
+constexpr int kKeyStages = 4, kRowRing = 2;
 
 struct ChunkWeightSmem {
     static constexpr int keys = 0;
@@ -1078,29 +1078,34 @@ struct ChunkWeightSmem {
     static constexpr int n_bars = 2 * kKeyStages + 2 * kRowRing + 8 + 3 * kItems + 1;
     static constexpr int tmem_slot = bars + n_bars * 8;
     static constexpr int items = (tmem_slot + 4 + 15) / 16 * 16;
-    static constexpr int total = items + kItems * 32;
+    static constexpr int total = items + kItems * 48;
 };
 constexpr int kWKeyFull = 0, kWKeyEmpty = kKeyStages, kWRowFull = 2 * kKeyStages, kWRowEmpty = kWRowFull + kRowRing,
               kWS = kWRowEmpty + kRowRing, kWSFree = kWS + 4, kWItemFull = kWSFree + 4, kWItemEmpty = kWItemFull + kItems,
               kWSum = kWItemEmpty + kItems, kWDrain = kWSum + kItems;
 
-// A 128-key tile of one request and kv head, and the row tiles [first, count) that see some of it.
+// Key tiles of one request and kv head, and the row tiles that see some of them.  Group g takes the row tiles from
+// first[g] on: all of them for key tile `tile` + g, or where the groups share one key tile every second one.
 struct alignas(16) KeyItem {
-    int seq, kvh, tile, start, tokens, keys, first, count;
+    int seq, kvh, tile, start;
+    int tokens, keys, count, shared;
+    int first[2];
 };
-static_assert(sizeof(KeyItem) == 32, "read as two 16-byte pieces");
+static_assert(sizeof(KeyItem) == 48, "read as 16-byte pieces");
 
-__device__ KeyItem find_key_item(const PromptParams &P, int64_t index, int lane) {
+// Item `index`; `pair`: 1 for two key tiles an item, 0 for one.
+__device__ KeyItem find_key_item(const PromptParams &P, uint32_t index, int pair, int lane) {
     KeyItem it{};
     it.seq = -1;
-    it.kvh = static_cast<int>(index % P.num_kv_heads);
-    int64_t rank = index / P.num_kv_heads;
+    const uint32_t heads = P.num_kv_heads;
+    int rank = static_cast<int>(index / heads);
+    it.kvh = static_cast<int>(index - rank * heads);
     for (int b0 = 0; b0 < P.num_seqs; b0 += 32) {
         const int b = b0 + lane;
         int tiles = 0;
         if (b < P.num_seqs) {
             const Request r = request_of(P, b, false);
-            tiles = r.tokens > 0 ? (r.keys + kTileRows - 1) / kTileRows : 0;
+            tiles = r.tokens > 0 ? ((r.keys + kTileRows - 1) / kTileRows + pair) >> pair : 0;
         }
         int upto = tiles;
 #pragma unroll
@@ -1115,7 +1120,7 @@ __device__ KeyItem find_key_item(const PromptParams &P, int64_t index, int lane)
         }
         const int who = __ffs(__ballot_sync(pkv::kFullMask, rank < upto)) - 1;
         it.seq = b0 + who;
-        it.tile = static_cast<int>(rank) - __shfl_sync(pkv::kFullMask, upto - tiles, who);
+        it.tile = (rank - __shfl_sync(pkv::kFullMask, upto - tiles, who)) << pair;
         break;
     }
     if (it.seq < 0) return it;
@@ -1123,9 +1128,15 @@ __device__ KeyItem find_key_item(const PromptParams &P, int64_t index, int lane)
     it.start = r.start;
     it.tokens = r.tokens;
     it.keys = r.keys;
-    const int skip = max(it.tile * kTileRows - (r.keys - r.tokens), 0);  // tokens before the tile's first key
-    it.first = (skip << P.group_log2) / kTileRows;
+    it.shared = pair ^ 1;
     it.count = ((r.tokens << P.group_log2) + kTileRows - 1) / kTileRows;
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+        const int key0 = (it.tile + (pair & g)) * kTileRows;
+        const int skip = max(key0 - (r.keys - r.tokens), 0);  // tokens before the tile's first key
+        const int first = (skip << P.group_log2) / kTileRows;
+        it.first[g] = pair ? (key0 < r.keys ? first : it.count) : first + ((first & 1) != g);
+    }
     return it;
 }
 
@@ -1175,26 +1186,32 @@ __global__ void __launch_bounds__(kPromptThreads, 1) chunk_weights_kernel(const 
             const int slot = k % kItems;
             if (!wait(kWItemFull + slot, k / kItems)) return false;
             uint4 *d = reinterpret_cast<uint4 *>(&it);
-            d[0] = lds128v(base + L::items + slot * sizeof(KeyItem));
-            d[1] = lds128v(base + L::items + slot * sizeof(KeyItem) + 16);
+#pragma unroll
+            for (int i = 0; i < 3; ++i) d[i] = lds128v(base + L::items + slot * sizeof(KeyItem) + 16 * i);
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kWItemEmpty + slot));
             return true;
         };
         if (warp == kItemWarp) {
             // ---------------------------------------------------------------- work items, up to kItems ahead
-            int tiles = 0;
+            int tiles = 0, pairs = 0;
             for (int b = lane; b < P.num_seqs; b += 32) {
                 const Request r = request_of(P, b, blockIdx.x == 0);
-                tiles += r.tokens > 0 ? (r.keys + kTileRows - 1) / kTileRows : 0;
+                const int n = r.tokens > 0 ? (r.keys + kTileRows - 1) / kTileRows : 0;
+                tiles += n;
+                pairs += (n + 1) / 2;
             }
-            const uint32_t n_items = static_cast<uint32_t>(__reduce_add_sync(pkv::kFullMask, tiles)) * P.num_kv_heads;
+            tiles = __reduce_add_sync(pkv::kFullMask, tiles);
+            pairs = __reduce_add_sync(pkv::kFullMask, pairs);
+            // Two key tiles an item read Q half as often; one where that leaves SMs idle.
+            const int pair = static_cast<int64_t>(tiles) * P.num_kv_heads > gridDim.x ? 1 : 0;
+            const uint32_t n_items = static_cast<uint32_t>(pair ? pairs : tiles) * P.num_kv_heads;
             bool ok = true;
             for (uint32_t k = 0; ok; ++k) {
                 const uint32_t index = k * gridDim.x + blockIdx.x;
                 KeyItem it{};
                 it.seq = -1;
-                if (index < n_items) it = find_key_item(P, index, lane);
+                if (index < n_items) it = find_key_item(P, index, pair, lane);
                 const int slot = k % kItems;
                 if (!(ok = wait(kWItemEmpty + slot, k / kItems + 1))) break;
                 if (lane == 0) {
@@ -1209,32 +1226,35 @@ __global__ void __launch_bounds__(kPromptThreads, 1) chunk_weights_kernel(const 
             }
         } else if (warp == kLoadWarp) {
             // ---------------------------------------------------------------- K tiles
-            uint32_t k = 0;
+            uint32_t loaded = 0;
             bool ok = true;
-            for (; ok; ++k) {
+            for (uint32_t k = 0; ok; ++k) {
                 KeyItem it;
                 if (!(ok = take(k, it)) || it.seq < 0) break;
-                const int key = it.tile * kTileRows + (lane >> 1) * P.box_rows;
-                int32_t id = 0;
-                if (lane < 2 * boxes_per_tile && key < it.keys)
-                    id = __ldg(P.block_tables + static_cast<int64_t>(it.seq) * P.max_blocks + key / P.block_size);
-                if (id < 0 || id >= P.num_blocks) {
-                    pkv::record_error(&g_prompt_error, PKV_DEV_BAD_BLOCK_ID);
-                    id = 0;
+                const int end = it.tile + (it.shared || it.first[1] >= it.count ? 1 : 2);
+                for (int tile = it.tile; tile < end; ++tile, ++loaded) {
+                    const int key = tile * kTileRows + (lane >> 1) * P.box_rows;
+                    int32_t id = 0;
+                    if (lane < 2 * boxes_per_tile && key < it.keys)
+                        id = __ldg(P.block_tables + static_cast<int64_t>(it.seq) * P.max_blocks + key / P.block_size);
+                    if (id < 0 || id >= P.num_blocks) {
+                        pkv::record_error(&g_prompt_error, PKV_DEV_BAD_BLOCK_ID);
+                        id = 0;
+                    }
+                    const int64_t row = (static_cast<int64_t>(id) * P.num_kv_heads + it.kvh) * P.block_size + key % P.block_size;
+                    const int ks = loaded % kKeyStages;
+                    if (!(ok = wait(kWKeyEmpty + ks, loaded / kKeyStages + 1))) break;
+                    const int boxes = (min(kTileRows, it.keys - tile * kTileRows) + P.box_rows - 1) / P.box_rows;
+                    if (lane == 0) pkv::mbar_arrive_expect_tx(bar(kWKeyFull + ks), boxes * P.box_rows * 256);
+                    __syncwarp();
+                    if (lane < 2 * boxes)
+                        pkv::tma_load_2d(base + L::keys + ks * kOperand + (lane & 1) * kSlab + (lane >> 1) * P.box_rows * 128, &P.tmap_k,
+                                         64 * (lane & 1), static_cast<int>(row), bar(kWKeyFull + ks));
+                    __syncwarp();
                 }
-                const int64_t row = (static_cast<int64_t>(id) * P.num_kv_heads + it.kvh) * P.block_size + key % P.block_size;
-                const int ks = k % kKeyStages;
-                if (!(ok = wait(kWKeyEmpty + ks, k / kKeyStages + 1))) break;
-                const int boxes = (min(kTileRows, it.keys - it.tile * kTileRows) + P.box_rows - 1) / P.box_rows;
-                if (lane == 0) pkv::mbar_arrive_expect_tx(bar(kWKeyFull + ks), boxes * P.box_rows * 256);
-                __syncwarp();
-                if (lane < 2 * boxes)
-                    pkv::tma_load_2d(base + L::keys + ks * kOperand + (lane & 1) * kSlab + (lane >> 1) * P.box_rows * 128, &P.tmap_k,
-                                     64 * (lane & 1), static_cast<int>(row), bar(kWKeyFull + ks));
-                __syncwarp();
             }
             if (!ok)  // copies still in flight land before the CTA's memory goes (bounded)
-                for (uint32_t s = k > kKeyStages ? k - kKeyStages : 0; s < k; ++s)
+                for (uint32_t s = loaded > kKeyStages ? loaded - kKeyStages : 0; s < loaded; ++s)
                     wait_phase(bar(kWKeyFull + s % kKeyStages), (s / kKeyStages) & 1);
         } else if (warp == kValueWarp) {
             // ---------------------------------------------------------------- Q tiles
@@ -1243,7 +1263,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) chunk_weights_kernel(const 
             for (uint32_t k = 0; ok; ++k) {
                 KeyItem it;
                 if (!(ok = take(k, it)) || it.seq < 0) break;
-                for (int i = it.first; i < it.count; ++i) {
+                for (int i = min(it.first[0], it.first[1]); i < it.count; ++i) {
                     const int st = rows % kRowRing;
                     if (!(ok = wait(kWRowEmpty + st, rows / kRowRing + 1))) break;
                     ++rows;
@@ -1260,42 +1280,55 @@ __global__ void __launch_bounds__(kPromptThreads, 1) chunk_weights_kernel(const 
                 for (uint32_t s = rows > kRowRing ? rows - kRowRing : 0; s < rows; ++s)
                     wait_phase(bar(kWRowFull + s % kRowRing), (s / kRowRing) & 1);
         } else if (warp == kMmaWarp) {
-            uint32_t rows = 0;
-            uint32_t used[4] = {0, 0, 0, 0};  // times each S^T buffer has been filled
+            uint32_t rows = 0, tiles = 0, fills[2] = {0, 0};  // Q and K tiles taken, each group's S^T filled
             bool ok = true;
             for (uint32_t k = 0; ok; ++k) {
                 const int slot = k % kItems;
                 if (!(ok = wait(kWItemFull + slot, k / kItems))) break;
-                const int seq = uniform(slots[slot].seq), first = uniform(slots[slot].first), count = uniform(slots[slot].count);
+                const int seq = uniform(slots[slot].seq), count = uniform(slots[slot].count);
+                const int first[2] = {uniform(slots[slot].first[0]), uniform(slots[slot].first[1])};
+                const bool shared = uniform(slots[slot].shared) != 0;
                 const int all_rows = uniform(slots[slot].tokens) << glog;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(kWItemEmpty + slot));
                 if (seq < 0) break;
-                const int ks = k % kKeyStages;
-                if (!(ok = wait(kWKeyFull + ks, k / kKeyStages))) break;
-                for (int i = first; i < count; ++i, ++rows) {
-                    const int st = rows % kRowRing, buf = i & 3;
+                const bool two = !shared && first[1] < count;  // key tiles
+                if (!(ok = wait(kWKeyFull + tiles % kKeyStages, tiles / kKeyStages))) break;
+                for (int i = min(first[0], first[1]); i < count && ok; ++i, ++rows) {
+                    const int st = rows % kRowRing;
                     if (!(ok = wait(kWRowFull + st, rows / kRowRing))) break;
-                    uint32_t fills = 0;
-    #pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        if (u == buf) fills = used[u]++;
-                    if (!(ok = wait(kWSFree + buf, fills + 1))) break;
-                    pkv::tmem_fence_after_sync();
-                    if (elected()) {
-                        const uint32_t a = base + L::keys + ks * kOperand, b = base + L::rows + st * kOperand;
-                        const uint32_t idesc = pkv::umma_idesc_f16_f32(kTileRows, (min(kTileRows, all_rows - i * kTileRows) + 15) / 16 * 16);
-    #pragma unroll
-                        for (int x = 0; x < kDim / 16; ++x) {
-                            const uint32_t off = (x >> 2) * kSlab + (x & 3) * 32;
-                            pkv::umma_f16(tmem + buf * kTileRows, pkv::umma_desc_k_sw128(a + off), pkv::umma_desc_k_sw128(b + off), idesc, x > 0);
+                    const uint32_t idesc = pkv::umma_idesc_f16_f32(kTileRows, (min(kTileRows, all_rows - i * kTileRows) + 15) / 16 * 16);
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        if (i < first[g] || (shared && ((i ^ first[g]) & 1))) continue;
+                        const uint32_t ks = (tiles + (shared ? 0 : g)) % kKeyStages;
+                        if (g == 1 && two && i == first[1] && !(ok = wait(kWKeyFull + ks, (tiles + 1) / kKeyStages))) break;
+                        const int buf = 2 * g + (fills[g] & 1);
+                        if (!(ok = wait(kWSFree + buf, (fills[g] >> 1) + 1))) break;
+                        ++fills[g];
+                        pkv::tmem_fence_after_sync();
+                        if (elected()) {
+                            const uint32_t a = base + L::keys + ks * kOperand, b = base + L::rows + st * kOperand;
+#pragma unroll
+                            for (int x = 0; x < kDim / 16; ++x) {
+                                const uint32_t off = (x >> 2) * kSlab + (x & 3) * 32;
+                                pkv::umma_f16(tmem + buf * kTileRows, pkv::umma_desc_k_sw128(a + off), pkv::umma_desc_k_sw128(b + off), idesc, x > 0);
+                            }
+                            pkv::umma_commit(bar(kWS + buf));
                         }
-                        pkv::umma_commit(bar(kWS + buf));
+                        __syncwarp();
+                    }
+                    if (!ok) break;
+                    if (elected()) {
                         pkv::umma_commit(bar(kWRowEmpty + st));
-                        if (i + 1 == count) pkv::umma_commit(bar(kWKeyEmpty + ks));
+                        if (i + 1 == count) {
+                            pkv::umma_commit(bar(kWKeyEmpty + tiles % kKeyStages));
+                            if (two) pkv::umma_commit(bar(kWKeyEmpty + (tiles + 1) % kKeyStages));
+                        }
                     }
                     __syncwarp();
                 }
+                tiles += two ? 2 : 1;
             }
             if (!ok) {  // MMAs in flight end before tensor memory is freed (bounded)
                 if (elected()) pkv::umma_commit(bar(kWDrain));
@@ -1311,20 +1344,24 @@ __global__ void __launch_bounds__(kPromptThreads, 1) chunk_weights_kernel(const 
         float4 *s_lse = reinterpret_cast<float4 *>(smem + L::lse) + warp * 32;  // this warp's own copy: no other warp waits for it
         float *s_sum = reinterpret_cast<float *>(smem + L::sums);
         const float sc = P.q_scale;
-        uint32_t seen[2] = {0, 0};  // times this group's two buffers have been read
+        uint32_t seen = 0;  // S^T tiles this group has read
         bool ok = true;
         for (uint32_t k = 0; ok; ++k) {
             const int slot = k % kItems;
             if (!(ok = wait(kWItemFull + slot, k / kItems))) break;
-            const uint4 i0 = lds128v(base + L::items + slot * sizeof(KeyItem)), i1 = lds128v(base + L::items + slot * sizeof(KeyItem) + 16);
-            const int seq = i0.x, kvh = i0.y, tile = i0.z, start = i0.w, tokens = i1.x, keys = i1.y, first = i1.z, count = i1.w;
+            const uint4 i0 = lds128v(base + L::items + slot * sizeof(KeyItem)), i1 = lds128v(base + L::items + slot * sizeof(KeyItem) + 16),
+                        i2 = lds128v(base + L::items + slot * sizeof(KeyItem) + 32);
+            const int seq = i0.x, kvh = i0.y, start = i0.w, tokens = i1.x, keys = i1.y, count = i1.z;
+            const bool shared = i1.w != 0;
+            const int tile = static_cast<int>(i0.z) + (shared ? 0 : grp), step = shared ? 2 : 1;
             if (seq < 0) break;
             const int key = tile * kTileRows + key_lane;
             const int rows = tokens << glog;
             float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
             // What scores holds, in flight through the whole item.
             float *const at = W.scores + (static_cast<int64_t>(seq) * P.num_kv_heads + kvh) * W.capacity + key;
-            const float before = grp == 0 && key < keys ? __ldcg(at) : 0.f;
+            const bool writes = (grp == 0 || !shared) && key < keys;
+            const float before = writes ? __ldcg(at) : 0.f;
             // minus the lse of four neighbouring columns of row tile i, log2 units (of one token with 4 heads or more)
             const float *const lse = W.lse + static_cast<int64_t>(start) * P.num_q_heads + (kvh << glog);
             auto column_lse = [&](int i) {
@@ -1344,18 +1381,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1) chunk_weights_kernel(const 
                 }
                 return make_float4(z.x * -kLog2e, z.y * -kLog2e, z.z * -kLog2e, z.w * -kLog2e);
             };
-            int i = first + ((first & 1) != grp);
+            int i = grp ? i2.y : i2.x;
             float4 z = column_lse(i);
-            for (; i < count; i += 2) {
-                const int buf = i & 3, which = buf >> 1;
+            for (; i < count; i += step) {
+                const int buf = 2 * grp + (seen & 1);
                 __syncwarp();
                 s_lse[lane] = z;
-                z = column_lse(i + 2);
-                uint32_t fills = 0;
-#pragma unroll
-                for (int u = 0; u < 2; ++u)
-                    if (u == which) fills = seen[u]++;
-                if (!(ok = wait(kWS + buf, fills))) break;
+                z = column_lse(i + step);
+                if (!(ok = wait(kWS + buf, seen >> 1))) break;
+                ++seen;
                 pkv::tmem_fence_after_sync();
                 uint32_t s0[64], s1[64];
                 tmem_ld64(tmem + lanes + buf * kTileRows, s0);
@@ -1396,15 +1430,19 @@ __global__ void __launch_bounds__(kPromptThreads, 1) chunk_weights_kernel(const 
             }
             if (!ok) break;
             const float total = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-            if (grp == 1) {  // the slot's sums are read before the slot's next item is published
-                s_sum[slot * kTileRows + key_lane] = total;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(kWSum + slot));
-            } else {
-                if (!(ok = wait(kWSum + slot, k / kItems))) break;
-                if (key < keys) *at = before + (total + s_sum[slot * kTileRows + key_lane]);
-                __syncwarp();
+            float other = 0.f;
+            if (shared) {  // the slot's sums are read before the slot's next item is published
+                if (grp == 1) {
+                    s_sum[slot * kTileRows + key_lane] = total;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(kWSum + slot));
+                } else {
+                    if (!(ok = wait(kWSum + slot, k / kItems))) break;
+                    other = s_sum[slot * kTileRows + key_lane];
+                }
             }
+            if (writes) *at = before + (total + other);
+            __syncwarp();
             if (lane == 0) mbar_arrive(bar(kWItemEmpty + slot));
         }
     }
