@@ -1054,8 +1054,8 @@ __global__ void __launch_bounds__(kJoinThreads, BATCH == 8 ? 4 : 2) prompt_join_
 // key's weights over all columns in its own registers and one thread adds them to scores: no exchange,
 // no atomics, a fixed order.  Bound by the exponentials, one per (row, key) pair (2 x 128 tensor flops),
 // until a chunk is so small that reading K bounds it.  The last 256 tokens of 2 x 16384 (32 heads, G = 4): 200
-// million pairs in 60 us, the tensor cores and the special-function units 40 % busy each (27 and 22 us alone): each
-// of the 13 items of an SM starts with loads and ends with its sums.
+// million pairs in 57 us, where the exponentials alone would take 22 and the MMAs 27: a group's chain per 128 x 128 tile,
+// from S^T's arrival through its load to the sums, is some 2100 cycles, of which 1100 are arithmetic.
 //   warps 0-3, 4-7  a key tile each, or the even and odd row tiles of one, with two S^T buffers of 128 TMEM columns
 //   warp 8          issues the MMAs
 //   warps 9, 10     issue the tensor copies of K tiles and of Q tiles, each through a ring
@@ -1067,7 +1067,7 @@ struct ChunkWeightParams {
     int64_t capacity;
 };
 
-constexpr int kKeyStages = 4, kRowRing = 2;
+constexpr int kKeyStages = 4, kRowRing = 2;  // three and three: 70 us where this takes 67
 
 struct ChunkWeightSmem {
     static constexpr int keys = 0;
@@ -1203,7 +1203,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) chunk_weights_kernel(const 
             }
             tiles = __reduce_add_sync(pkv::kFullMask, tiles);
             pairs = __reduce_add_sync(pkv::kFullMask, pairs);
-            // Two key tiles an item read Q half as often; one where that leaves SMs idle.
+            // Two key tiles an item read Q half as often; one where that leaves SMs idle.  (256 rows of 2 x 16384 keys: 67 us
+            // from cold caches against 78, 32 rows of 32768 29 against 34.)
             const int pair = static_cast<int64_t>(tiles) * P.num_kv_heads > gridDim.x ? 1 : 0;
             const uint32_t n_items = static_cast<uint32_t>(pair ? pairs : tiles) * P.num_kv_heads;
             bool ok = true;
