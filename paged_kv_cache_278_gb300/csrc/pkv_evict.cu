@@ -37,7 +37,8 @@ constexpr int kSelThreads = 512;
 constexpr int kBins = 512, kPasses = 4;  // digits of 9, 8, 8 and 7 bits
 constexpr int kMoveThreads = 256;
 constexpr int kRowLanes = PKV_HEAD_DIM * 2 / 16;  // threads that move one row, 16 bytes each
-constexpr int kMoveBatch = 4;                     // rows in flight per thread (2 and 8 measured 15 and 13 % slower on 4 x 32k -> 4k)
+constexpr int kMoveBatch = 4;                     // rows in flight per thread (2 and 8 measured 15 and 13 % slower on 4 x 32k -> 4k; the
+                                                  // next step's rows read ahead too take 72 registers, and 16 x 3.9k -> 1k 50 us, not 41)
 constexpr int kMoveRows = kMoveThreads / kRowLanes * kMoveBatch;  // rows of a CTA's step
 
 struct EvictParams {
