@@ -796,8 +796,9 @@ PKV_API int pkv_prefill_attention_paged(void *out, float *lse, const void *q, in
  * least max_blocks_per_seq * block_size.  Entries at or past context_lens[b] are left as they are. */
 
 /* Bytes of workspace pkv_decode_attention_weights needs for contexts up to max_context (the table's
- * capacity max_blocks_per_seq * block_size).  Zero-filled once by the caller; every call leaves
- * its counters zero.  Calls that may run at the same time need one each.  0: a bad argument. */
+ * capacity max_blocks_per_seq * block_size).  No initial contents, and nothing kept in it from one call
+ * to the next: calls of any sizes may take turns on one that is large enough for each.  Calls that may run
+ * at the same time need one each.  0: a bad argument. */
 PKV_API size_t pkv_weights_workspace_size(int num_seqs, int num_q_heads, int head_dim, int max_context);
 
 /* pkv_decode_attention, and scores[b][h][t] += the step's weights on position t.  A request with

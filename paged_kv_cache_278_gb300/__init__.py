@@ -874,12 +874,12 @@ def prefill_attention_paged(out: torch.Tensor, q: torch.Tensor, k_cache: torch.T
 # ---------------------------------------------------------------- accumulated attention weights, eviction
 
 def make_weights_workspace(num_seqs: int, num_q_heads: int, max_context: int, device) -> torch.Tensor:
-    """Zero-filled workspace for decode_attention_weights; max_context is the table's capacity
-    (entries * block_size).  One per call in flight."""
+    """Workspace for decode_attention_weights; max_context is the table's capacity (entries * block_size).  One per
+    call in flight; calls that need less may use it too."""
     n = int(_L().pkv_weights_workspace_size(num_seqs, num_q_heads, PKV_HEAD_DIM, max_context))
     if n == 0:
         raise ValueError("invalid weights workspace request")
-    return torch.zeros(n, dtype=torch.uint8, device=device)
+    return torch.empty(n, dtype=torch.uint8, device=device)
 
 
 def _need_scores(scores, name, b, hkv, capacity, device):

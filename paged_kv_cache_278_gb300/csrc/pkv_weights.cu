@@ -11,15 +11,18 @@
 //
 //   * attention pass: one CTA per (request, kv head, 1024-token partition), four warps each with a private
 //     ring of 16-token chunks (tensor copies, 128-byte swizzle), the tensor-core engine of the
-//     decode kernels with one 8-byte store per lane and token pair added; the last partition to
-//     finish merges.  Bound by HBM, as the decode kernels are: 90 us for the 538 MB of 64 x 2049 tokens alone on
-//     cold caches, what the plain decode kernel takes there; with the weights pass 97 us, 84 % of the copy bandwidth
-//     (4 x up to 32k tokens 64 us, 80 %).
+//     decode kernels with one 8-byte store per lane and token pair added; contexts past one partition
+//     leave a partial output each.  Bound by HBM, as the decode kernels are: 90 us for the 538 MB of 64 x 2049 tokens alone on
+//     cold caches, what the plain decode kernel takes there; with the weights pass 97 us, 85 % of the copy bandwidth
+//     (4 x up to 32k tokens 62 us, 83 %).
 //   * weights pass: one CTA per (request, kv head, 1024 tokens): the partitions' (m, l) give the
 //     group's log-sum-exps, then one exponential per (token, head) and one read-modify-write of
-//     scores per token, by exactly one thread: no atomics, a fixed order.  Bound by latency (7-10 us alone): its
-//     loads are issued together, those of scores while the attention pass still runs.  Done by the merging CTA
-//     instead, the call took 97.5 us against 97.2.
+//     scores per token, by exactly one thread: no atomics, a fixed order.  Its CTAs of a (request, kv head) join the
+//     partial outputs too, each a share of the dims: no counter has to survive from one call to the next, so any calls
+//     may take turns on one workspace, whatever it held.  Bound by latency (7-10 us alone): its
+//     loads are issued together, those of scores while the attention pass still runs.  The join
+//     by the last partition to arrive, with a counter, took as long or longer: 97.1 us against 96.9 (64 x 2049), 63.4
+//     against 61.8 (4 x up to 32k).
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -42,7 +45,7 @@ constexpr int kPart = PKV_DEFAULT_PARTITION;
 constexpr int kWeightThreads = 256;
 
 struct WeightParams {
-    DecodeParams d;  // its maps, split buffers and counters
+    DecodeParams d;  // its maps and split buffers
     float *raw;      // [B][Hkv][cap][G] scaled dot products, log2 units
     float *scores;   // [B][Hkv][capacity]
     int64_t capacity;
@@ -115,7 +118,7 @@ __global__ void __launch_bounds__(kThreads, PKV_DECODE_MIN_CTAS)
     unsigned char *scratch = smem + L::probs + warp * L::probs_per_warp(G);
     const uint32_t bar0 = pkv::smem_addr(smem + L::bars) + warp * kStages * kBarsPerStage * 8;
     const uint32_t stage0 = pkv::smem_addr(smem + L::stages) + warp * kStages * L::stage;
-    // The 128-byte swizzle needs 1 KB-aligned tiles; a CTA without them stages no tokens but still counts.
+    // The 128-byte swizzle needs 1 KB-aligned tiles; a CTA without them stages no tokens.
     const bool smem_ok = (pkv::smem_addr(smem) & 1023) == 0;
     if (!smem_ok && threadIdx.x == 0) pkv::record_error(&g_weights_error, PKV_DEV_SMEM_MISALIGNED);
     if (lane == 0) {
@@ -234,22 +237,13 @@ __global__ void __launch_bounds__(kThreads, PKV_DECODE_MIN_CTAS)
             P.l_part[prow] = S;
         }
     }
-    if (direct) return;
-    // ---- the last partition of (b, kv head) to finish merges them all
-    __shared__ int s_last;
-    __syncthreads();
-    int *counter = P.counters + static_cast<int64_t>(b) * P.num_kv_heads + kvh;
-    if (threadIdx.x == 0) s_last = pkv::atomic_add_acq_rel_gpu(counter, 1) == n_parts - 1;
-    __syncthreads();
-    if (!s_last) return;
-    merge_group<G, L::stage_bytes>(P, HeadRows{head_row}, n_parts, smem);
-    if (threadIdx.x == 0) *counter = 0;
 }
 
 template <int G>
 __global__ void __launch_bounds__(kWeightThreads) accumulate_weights_kernel(const __grid_constant__ WeightParams W) {
     const DecodeParams &P = W.d;
-    __shared__ float s_lse[G];
+    __shared__ float s_lse[G], s_top[G], s_inv[G];
+    __shared__ float4 s_join[kWeightThreads];
     const int part = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
     const int ctx = context_of(P, b, false);
     const int start = part * kPart;
@@ -291,6 +285,22 @@ __global__ void __launch_bounds__(kWeightThreads) accumulate_weights_kernel(cons
             for (int k = 0; k < G; ++k) s[i][k] = __ldcg(at + k);
         }
     }
+    // The partial outputs: this CTA joins `share` of the group's G x 32 pieces of four dims, n_parts threads (or as many
+    // as there are, in turn) to a piece.
+    const int share = (G * (kD / 4) + n_parts - 1) / n_parts, joiners = min(kWeightThreads / share, n_parts);
+    const int joiner = static_cast<int>(threadIdx.x) / share, piece = part * share + static_cast<int>(threadIdx.x) % share;
+    const int head_of = piece / (kD / 4);
+    const int64_t head_row = static_cast<int64_t>(b) * P.num_q_heads + kvh * G;
+    const int64_t part_row = (head_row + head_of) * P.max_partitions;
+    const bool joins = n_parts > 1 && joiner < joiners && piece < G * (kD / 4);
+    auto partial = [&](int p, float &m, float &l) {
+        m = __ldcg(P.m_part + part_row + p);
+        l = __ldcg(P.l_part + part_row + p);
+        return __ldcg(reinterpret_cast<const float4 *>(P.o_part + (part_row + p) * kD) + piece % (kD / 4));
+    };
+    float m0 = 0.f, l0 = 0.f;
+    float4 o0 = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (joins) o0 = partial(joiner, m0, l0);
     if (warp < G) {  // one warp per head: its log-sum-exp in log2 units from the partitions' (m, l)
         const int64_t row = (static_cast<int64_t>(b) * P.num_q_heads + kvh * G + warp) * P.max_partitions;
         float M = -INFINITY, S = 0.f;
@@ -300,7 +310,11 @@ __global__ void __launch_bounds__(kWeightThreads) accumulate_weights_kernel(cons
         for (int p = lane; p < n_parts; p += 32) S += __ldcg(P.l_part + row + p) * expf(__ldcg(P.m_part + row + p) - M);
 #pragma unroll
         for (int sh = 16; sh >= 1; sh >>= 1) S += __shfl_xor_sync(pkv::kFullMask, S, sh);
-        if (lane == 0) s_lse[warp] = fmaf(M, kLog2e, log2f(S));
+        if (lane == 0) {
+            s_lse[warp] = fmaf(M, kLog2e, log2f(S));
+            s_top[warp] = M;
+            s_inv[warp] = 1.f / S;
+        }
     }
     __syncthreads();
 #pragma unroll
@@ -311,13 +325,43 @@ __global__ void __launch_bounds__(kWeightThreads) accumulate_weights_kernel(cons
         for (int k = 0; k < G; ++k) w += pkv::exp2_approx(s[i][k] - s_lse[k]);
         if (t < end) scores[t] = before[i] + w;
     }
+    if (n_parts == 1) return;  // the attention pass wrote the output
+    if (joins) {
+        const float top = s_top[head_of];
+        float w = l0 * expf(m0 - top);
+        float4 o = make_float4(w * o0.x, w * o0.y, w * o0.z, w * o0.w);
+        for (int p = joiner + joiners; p < n_parts; p += joiners) {
+            const float4 x = partial(p, m0, l0);
+            w = l0 * expf(m0 - top);
+            o.x = fmaf(w, x.x, o.x);
+            o.y = fmaf(w, x.y, o.y);
+            o.z = fmaf(w, x.z, o.z);
+            o.w = fmaf(w, x.w, o.w);
+        }
+        s_join[threadIdx.x] = o;
+    }
+    __syncthreads();
+    if (joins && joiner == 0) {
+        float4 o = s_join[threadIdx.x];
+        for (int j = 1; j < joiners; ++j) {
+            const float4 x = s_join[j * share + threadIdx.x];
+            o.x += x.x;
+            o.y += x.y;
+            o.z += x.z;
+            o.w += x.w;
+        }
+        const float inv = s_inv[head_of];
+        const __half2 lo = __floats2half2_rn(o.x * inv, o.y * inv), hi = __floats2half2_rn(o.z * inv, o.w * inv);
+        *reinterpret_cast<uint2 *>(P.out + (head_row + head_of) * kD + 4 * (piece % (kD / 4))) =
+            make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+    }
 }
 
 using pkv_internal::align256;
 
-// Workspace: o_part | m_part | l_part | counters | raw, each 256-byte aligned.
+// Workspace: o_part | m_part | l_part | raw, each 256-byte aligned.  Every call writes what it reads.
 struct WeightsLayout {
-    size_t m, l, counters, raw, total;
+    size_t m, l, raw, total;
     int parts;
 };
 WeightsLayout weights_layout(int num_seqs, int num_q_heads, int64_t cap) {
@@ -326,8 +370,7 @@ WeightsLayout weights_layout(int num_seqs, int num_q_heads, int64_t cap) {
     const size_t rows = static_cast<size_t>(num_seqs) * num_q_heads * w.parts;
     w.m = w.parts > 1 ? align256(rows * kD * sizeof(float)) : 0;
     w.l = w.m + align256(rows * sizeof(float));
-    w.counters = w.l + align256(rows * sizeof(float));
-    w.raw = w.counters + align256(static_cast<size_t>(num_seqs) * num_q_heads * sizeof(int));
+    w.raw = w.l + align256(rows * sizeof(float));
     w.total = w.raw + align256(static_cast<size_t>(num_seqs) * num_q_heads * cap * sizeof(float));
     return w;
 }
@@ -398,7 +441,6 @@ extern "C" PKV_API int pkv_decode_attention_weights(void *out, float *scores, in
     p.o_part = reinterpret_cast<float *>(ws);
     p.m_part = reinterpret_cast<float *>(ws + lay.m);
     p.l_part = reinterpret_cast<float *>(ws + lay.l);
-    p.counters = reinterpret_cast<int *>(ws + lay.counters);
     p.max_blocks_per_seq = max_blocks_per_seq;
     p.num_q_heads = num_q_heads;
     p.num_kv_heads = num_kv_heads;

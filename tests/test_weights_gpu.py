@@ -94,6 +94,23 @@ def test_steps_accumulate_and_leave_the_workspace_clean():
     assert np.abs(sums[:2] - 4).max() < 4 * 1e-4 and (sums[2] == 0).all()
 
 
+def test_one_workspace_for_calls_of_other_sizes():
+    """A batch that shrinks and grows again, tables that get narrower and wider, other head counts: one workspace, as large
+    as the largest call needs and filled with anything."""
+    long, less = [2100, 1025, 1100, 40, 1500, 1030], [1300, 1025, 1100, 40, 1290]
+    wide = workloads.random_case(920, [6000, 1040], 8, 2, block_size=16)
+    cases = [workloads.random_case(921, long, 8, 2, block_size=16), workloads.random_case(922, long[:5], 8, 2, block_size=16), wide,
+             workloads.random_case(923, less, 8, 2, block_size=16), workloads.random_case(924, less, 4, 1, block_size=48),
+             workloads.random_case(925, long, 2, 2, block_size=32)]
+    sizes = [pkv.make_weights_workspace(c.num_seqs, c.num_q_heads, c.max_blocks_per_seq * c.block_size, "cuda").numel() for c in cases]
+    ws = torch.zeros(max(sizes), dtype=torch.uint8, device="cuda")
+    for i in (0, 1, 0, 2, 0, 3, 4, 5, 1, 0, 2):
+        run(cases[i], seed=i, ws=ws)
+    ws.fill_(255)
+    for i in (0, 3, 2):
+        run(cases[i], seed=i, ws=ws)
+
+
 def test_stale_rows_past_the_context():
     """Positions past a context hold whatever they held, infinities and NaN included."""
     case = workloads.random_case(912, [21, 1030], 4, 1, block_size=32)
