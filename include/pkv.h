@@ -756,9 +756,9 @@ PKV_API int pkv_rope_append(void *q_out, int64_t q_out_stride, const void *q, in
  * (DEVICE int32 [num_seqs + 1]; empty ranges allowed, overlapping ones not); rows outside every range are
  * left as they were.
  * A range that is negative, longer than max_query_len or past total_q is skipped and recorded as
- * PKV_DEV_BAD_CONTEXT.  Weights are rounded to fp16 for the product with V; sums and the
- * accumulator are float32.  What lies past a context never enters a result; infinities and NaN in a
- * position's K or V reach the rows that see the position and no others. */
+ * PKV_DEV_BAD_CONTEXT.  Weights are rounded to fp16 for the product with V, by at most 2^-11 of the weight
+ * or 2^-32 of the row's largest; sums and the accumulator are float32.  What lies past a context never enters
+ * a result; infinities and NaN in a position's K or V reach the rows that see the position and no others. */
 
 /* Bytes of workspace the two calls need (0: none).  max_context: the longest context the call may meet
  * (max_seq_len, or max_blocks_per_seq * block_size).  Grows with max_context, but not with total_q or

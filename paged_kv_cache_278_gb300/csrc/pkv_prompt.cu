@@ -23,7 +23,10 @@
 //   warps 0-3, 4-7  softmax of tile A, B: one thread per row, its 128 scores in registers; online max
 //       with lazy rescaling (O is rescaled only when a score exceeds the reference max by more than
 //       2^8, then by the row's own thread), row sums in fp32 of the unrounded weights.  P is rounded to
-//       fp16 once (2^-11 relative, as the output's own rounding), which keeps P V at the fp16 rate.
+//       fp16 once, which keeps P V at the fp16 rate (the decode kernels, bound by HBM, carry a second fp16 part).
+//       The weights are taken 2^7 too large, and so are the sums: fp16's range up to 2^15 is used, and a weight keeps its
+//       11 bits down to 2^-21 of the row's largest, some of them down to 2^-32, instead of 2^-14 and 2^-25: the
+//       tail behind one dominant key counts in P V as it does in the sum.
 //   warp 8  issues every tcgen05.mma (one lane).
 //   warps 9, 10  issue the tensor copies: Q (64 KB) once per item and the K tiles of 128 keys, and the V tiles,
 //       each through a ring of two 32 KB stages.  Two warps: with 16-token blocks a tile is 16 copies of 2 KB, and
@@ -65,6 +68,7 @@ constexpr int kSoftmaxRegs = 200, kOtherRegs = 88;  // launch: 384 x 168 = 64,51
 constexpr int kMmaWarp = kSoftmaxWarps, kLoadWarp = kSoftmaxWarps + 1, kValueWarp = kSoftmaxWarps + 2,
               kItemWarp = kSoftmaxWarps + 3;
 constexpr float kLazy = 8.0f;              // log2 units
+constexpr float kLift = 7.0f;              // P is at most 2^(kLazy + kLift) = 2^15, in fp16's range
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kMaxSplits = 64;
 constexpr int64_t kMaxContext = 1 << 30;  // positions and their sums with a tile's stay in 32 bits
@@ -732,7 +736,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
             if (seq < 0) break;
             const int pos = tile_pos + min(tok, live - 1);  // rows past the last token: computed like it, never stored
             const int n_kv = key_tiles(shared, n, n_of_other), keys = i1.w;
-            float m_ref = -INFINITY, l = 0.f;
+            float m_ref = -INFINITY, l = 0.f;  // what weights are relative to: kLift below a score, so that they reach 2^kLift
             for (int j = 0; j < n; ++j) {
                 const int key0 = (first + (shared ? 2 * j + t : j)) * kTileRows;
                 // A tile that some row of the item does not see to its end is cleaned first, while S is on its way.  Its V
@@ -780,8 +784,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                 for (int c = 0; c < 64; c += 2)
                     mx[(c >> 1) & 3] = fmaxf(fmaxf(mx[(c >> 1) & 3], __uint_as_float(s1[c])), __uint_as_float(s1[c + 1]));
                 const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
-                if (__any_sync(pkv::kFullMask, top > m_ref + kLazy)) {
-                    const float m_new = top > m_ref + kLazy ? top : m_ref;
+                if (__any_sync(pkv::kFullMask, top > m_ref + (kLift + kLazy))) {
+                    const float m_new = top > m_ref + (kLift + kLazy) ? top - kLift : m_ref;
                     const float a = m_ref == -INFINITY ? 0.f : exp2f(m_ref - m_new);
                     const float f = m_new == m_ref ? 1.f : a;
                     l *= f;

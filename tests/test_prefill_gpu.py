@@ -204,6 +204,59 @@ def test_paged_equals_the_multi_call():
     assert (out.float() - other.float()).abs().max() <= 4e-3  # twice the decode tests' bound
 
 
+def one_key_above(n, hkv, nats, at, seed):
+    """Keys of which the one at position `at` scores `nats` above all others for every row; its V is zero, the others' are
+    all positive, so that the output is what the tail gives: (q [n, 4 hkv, 128], k, v [n, hkv, 128])."""
+    rng = np.random.default_rng(seed)
+    q, k = np.zeros((n, 4 * hkv, 128), np.float16), np.zeros((n, hkv, 128), np.float16)
+    q[..., 0], k[at, :, 0] = 16.0, nats / (16.0 * SCALE)
+    v = rng.uniform(16.0, 64.0, (n, hkv, 128)).astype(np.float16)
+    v[at] = 0
+    return q, k, v
+
+
+def check_tail(out, lse, q, k, v, at):
+    """A weight of w relative to the row's largest is held in fp16 at 2^7 w or more: half a step is 2^-11 of it, or 2^-25 where that
+    is subnormal, so at most 2^-32 / w of itself.  All values and weights of the tail are positive: the output is off by no more
+    than the weights are, whatever the number of keys, but for the float32 sums: a step of 2^-23 per matrix instruction of 16 keys
+    and tile of 128.  The scores are one product each, a few steps of 2^-23 times their size."""
+    c, n = q.shape[0], k.shape[0]
+    p, z = ref.weights(q, k, SCALE)
+    o = np.einsum("chn,nhd->chd", p, np.repeat(v.astype(np.float64), 4, axis=1))
+    w = np.exp(-SCALE * 16.0 * float(k[at, 0, 0]))
+    sees = (np.arange(n - c, n) >= at)[:, None, None]
+    off = np.where(sees, max(2.0 ** -11, 2.0 ** -32 / w), 2.0 ** -11)
+    tol = o * (off + 2.0 ** -11 + (64 + n / 16 + n / 128) * 2.0 ** -23) + 2.0 ** -25
+    err = np.abs(out.astype(np.float64) - o)
+    assert (err <= tol).all(), (err.max(), o.max(), np.argwhere(~(err <= tol))[:4])
+    assert (np.abs(lse - z) <= 64 * 2.0 ** -23 * (1 + np.abs(z))).all()
+
+
+@pytest.mark.parametrize("nats", [12.0, 18.0, 19.5])
+@pytest.mark.parametrize("n,c,at", [(700, 700, 0), (700, 200, 130), (5000, 37, 0), (5000, 129, 4899), (20000, 3, 7)])
+def test_a_long_tail_below_one_key(nats, n, c, at):
+    """One key far above a long tail (an attention sink): what the tail's values give is there, in whole and split rows."""
+    q, k, v = one_key_above(n, 1, nats, at, 5)
+    q = q[n - c:]
+    t = lambda x: torch.from_numpy(x).cuda()  # noqa: E731
+    bs, nb = 16, -(-n // 16)
+    table = torch.randperm(nb, generator=torch.Generator().manual_seed(2)).to(torch.int32).view(1, -1)
+    kc, vc = (torch.zeros((nb, 1, bs, 128), dtype=torch.float16, device="cuda") for _ in range(2))
+    slots = pkv.slot_mapping(table.expand(n, -1).contiguous(), torch.arange(n, dtype=torch.int32), bs).cuda()
+    pkv.append(kc, vc, slots, t(k), t(v))
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    out, z = torch.full((c, 4, 128), float("nan"), dtype=torch.float16, device="cuda"), torch.full((c, 4), float("nan"), device="cuda")
+    ws = pkv.make_prefill_workspace(1, c, 4, 1, nb * bs, "cuda")
+    pkv.prefill_attention_paged(out, t(q), kc, vc, table.cuda(), i32(n), i32(0, c), c, SCALE, lse=z, workspace=ws)
+    check_tail(out.float().cpu().numpy(), z.cpu().numpy(), q, k, v, at)
+    if c == n:
+        o2, z2 = torch.empty_like(out), torch.empty_like(z)
+        pkv.prefill_attention(o2, t(q), t(k), t(v), i32(0, n), n, SCALE, lse=z2,
+                              workspace=pkv.make_prefill_workspace(1, n, 4, 1, n, "cuda"))
+        check_tail(o2.float().cpu().numpy(), z2.cpu().numpy(), q, k, v, at)
+    assert_no_device_error()
+
+
 def test_bad_requests_are_skipped_and_recorded():
     out, z, args, ws = run_paged([300, 200, 100], [20, 30, 40], 4, 2, 16, 80)
     q, kc, vc, bt, cl, qs, n, scale = args
