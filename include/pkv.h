@@ -837,8 +837,9 @@ PKV_API int pkv_prefill_attention_weights(float *scores, int64_t score_capacity,
  *                block_tables entry of the same index (compaction in place; the blocks must not be shared
  *                with another request) or a block that no block_tables row of the call names (a shared
  *                block's rows are copied out).  May be block_tables itself.
- * A context past its table is cut and recorded as PKV_DEV_BAD_CONTEXT, as is a new table too short;
- * a bad block id skips its rows and is recorded as PKV_DEV_BAD_BLOCK_ID.  recent + sinks <= budget;
+ * A context past its table is cut and recorded as PKV_DEV_BAD_CONTEXT.  So is what a new table too short has no
+ * room for: only the first max_new_blocks * block_size kept positions are moved, and kept, new_scores and new_lens
+ * describe those.  A bad block id skips its rows and is recorded as PKV_DEV_BAD_BLOCK_ID.  recent + sinks <= budget;
  * a table covers at most PKV_MAX_EVICT_CONTEXT positions.  head_dim is PKV_HEAD_DIM.
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 #define PKV_MAX_EVICT_CONTEXT 262144

@@ -74,6 +74,9 @@ __device__ __forceinline__ int cached(const EvictParams &P, int b, bool report) 
     return max(n, 0);
 }
 
+// Of the kept positions, those that the new table has room for.
+__device__ __forceinline__ int moved(const EvictParams &P, int kept) { return min(kept, P.max_new_blocks * P.block_size); }
+
 // Exclusive prefix sum over the CTA's threads, and the total.
 template <int W>
 __device__ __forceinline__ int block_scan(int v, int *s, int &total) {
@@ -142,7 +145,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
     float *out = P.new_scores + row * P.capacity;
     int32_t *kept = P.kept + row * P.budget;
     const int n = cached(P, b, tid == 0 && blockIdx.x == 0);
-    const int m = min(n, P.budget);
+    const int m = min(n, P.budget), room_for = moved(P, m);
     const int run = rank * kRun;      // the CTA's first position
 
     if (n > P.budget) {  // (the whole cluster)
@@ -299,19 +302,21 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
             const uint32_t bits = s_above[w];
             if ((bits >> (p & 31)) & 1u) {
                 const int to = static_cast<int>(s_at[w]) + __popc(bits & ((1u << (p & 31)) - 1u));
-                kept[to] = p;
-                out[to] = raw[i];
+                if (to < room_for) {
+                    kept[to] = p;
+                    out[to] = raw[i];
+                }
             }
         }
     } else {
-        for (int p = rank * T + tid; p < n; p += ranks * T) {
+        for (int p = rank * T + tid; p < room_for; p += ranks * T) {
             kept[p] = p;
             if (out != scores) out[p] = __ldcg(scores + p);
         }
-        for (int p = n + rank * T + tid; p < P.budget; p += ranks * T) kept[p] = -1;
     }
+    for (int p = room_for + rank * T + tid; p < P.budget; p += ranks * T) kept[p] = -1;
     // Zeros behind the kept scores (read by every CTA, see above), shared out between the CTAs.
-    for (int64_t p = static_cast<int64_t>(m) + rank * T + tid; p < P.capacity; p += ranks * T) out[p] = 0.f;
+    for (int64_t p = static_cast<int64_t>(room_for) + rank * T + tid; p < P.capacity; p += ranks * T) out[p] = 0.f;
     cluster_arrive();  // no CTA's shared memory goes while another may read it
     cluster_wait();
 }
@@ -324,11 +329,8 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constan
     const int rank = blockIdx.x % P.cluster, h = blockIdx.y, b = blockIdx.z;
     unsigned char *cache = static_cast<int>(blockIdx.x) < P.cluster ? P.k_cache : P.v_cache;
     const int n = cached(P, b, false);
-    int m = min(n, P.budget);
-    if (m > P.max_new_blocks * P.block_size) {
-        if (tid == 0 && blockIdx.x == 0 && h == 0) pkv::record_error(&g_evict_error, PKV_DEV_BAD_CONTEXT);
-        m = P.max_new_blocks * P.block_size;
-    }
+    const int m = moved(P, min(n, P.budget));
+    if (m < min(n, P.budget) && tid == 0 && blockIdx.x == 0 && h == 0) pkv::record_error(&g_evict_error, PKV_DEV_BAD_CONTEXT);
     const int32_t *kept = P.kept + (static_cast<int64_t>(b) * P.num_kv_heads + h) * P.budget;
     const int32_t *from = P.block_tables + static_cast<int64_t>(b) * P.max_blocks;
     const int32_t *to = P.new_tables + static_cast<int64_t>(b) * P.max_new_blocks;
@@ -386,8 +388,8 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constan
             if (dst[u] != nullptr) *reinterpret_cast<uint4 *>(dst[u] + byte) = x[u];
         __syncthreads();  // the next step's rows are located
     }
-    // new_lens may be context_lens: the other CTAs' min(n, budget) is the same from either value
-    if (tid == 0 && blockIdx.x == 0 && h == 0) P.new_lens[b] = min(n, P.budget);
+    // new_lens may be context_lens: the other CTAs' m is the same from either value
+    if (tid == 0 && blockIdx.x == 0 && h == 0) P.new_lens[b] = m;
 }
 
 template <int KPT>

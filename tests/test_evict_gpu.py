@@ -143,6 +143,28 @@ def test_bad_indices_are_recorded():
     assert pkv.device_error() == pkv.PKV_DEV_OK
 
 
+@pytest.mark.parametrize("alias", [False, True])
+def test_short_new_table(alias):
+    """A new table too short for what is kept: recorded, and everything the call writes describes the rows that were moved."""
+    k, v, s, old, fresh, lens = state([100, 30, 70], 2, 16, 12)
+    want = ref.evict(k, v, s, old, np.pad(fresh, ((0, 0), (0, 1)), constant_values=0), lens, 50, 5, 2)
+    d = [torch.from_numpy(x.copy()).cuda() for x in (k, v, s, old, np.ascontiguousarray(fresh[:, :2]), lens)]
+    kept = torch.full((3, 2, 50), -7, dtype=torch.int32, device="cuda")
+    ns, nl = (d[2], d[5]) if alias else (torch.full_like(d[2], 9.0), torch.full_like(d[5], -7))
+    pkv.evict(d[0], d[1], kept, ns, nl, d[2], d[3], d[5], 50, recent=5, sinks=2, new_tables=d[4])
+    assert pkv.device_error() == pkv.PKV_DEV_BAD_CONTEXT
+    assert nl.tolist() == [32, 30, 32]  # two blocks of 16
+    kept, ns = kept.cpu().numpy(), ns.cpu().numpy()
+    for b, n in enumerate([32, 30, 32]):
+        assert np.array_equal(kept[b, :, :n], want[2][b, :, :n]) and (kept[b, :, n:] == -1).all()
+        assert np.array_equal(bits(ns[b, :, :n].copy()), bits(want[3][b, :, :n].copy())) and (ns[b, :, n:] == 0).all()
+        for h in range(2):
+            for c, x in ((d[0], k), (d[1], v)):
+                got = ref.rows_of(c.cpu().numpy(), fresh[b], n)[:, h]
+                assert np.array_equal(got, ref.rows_of(x, old[b], int(lens[b]))[kept[b, h, :n], h])
+    assert pkv.device_error() == pkv.PKV_DEV_OK
+
+
 def test_graph_replay_follows_the_inputs():
     k, v, s, old, fresh, lens = state([300, 200], 2, 16, 4)
     d = [torch.from_numpy(x.copy()).cuda() for x in (k, v, s, old, fresh, lens)]
