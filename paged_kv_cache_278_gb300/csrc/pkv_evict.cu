@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
             if (out != scores) out[p] = __ldcg(scores + p);
         }
     }
-    for (int p = room_for + rank * T + tid; p < P.budget; p += ranks * T) kept[p] = -1;
+    for (int64_t p = static_cast<int64_t>(room_for) + rank * T + tid; p < P.budget; p += ranks * T) kept[p] = -1;
     // Zeros behind the kept scores (read by every CTA, see above), shared out between the CTAs.
     for (int64_t p = static_cast<int64_t>(room_for) + rank * T + tid; p < P.capacity; p += ranks * T) out[p] = 0.f;
     cluster_arrive();  // no CTA's shared memory goes while another may read it

@@ -165,6 +165,21 @@ def test_short_new_table(alias):
     assert pkv.device_error() == pkv.PKV_DEV_OK
 
 
+def test_largest_budget():
+    """A budget near the end of 32 bits: everything is kept, and -1 behind it to the last entry."""
+    k, v, s, old, fresh, lens = state([40], 1, 16, 13)
+    d = [torch.from_numpy(x.copy()).cuda() for x in (k, v, s, old, fresh, lens)]
+    budget = 2 ** 31 - 1
+    kept = torch.zeros((1, 1, budget), dtype=torch.int32, device="cuda")  # 8.6 GB
+    ns, nl = torch.empty_like(d[2]), torch.empty_like(d[5])
+    pkv.evict(d[0], d[1], kept, ns, nl, d[2], d[3], d[5], budget, recent=2 ** 30, sinks=2 ** 30 - 1, new_tables=d[4])
+    assert nl.tolist() == [40] and kept[0, 0, :40].tolist() == list(range(40))
+    for part in kept[0, 0, 40:].split(1 << 28):
+        assert int(part.max()) == -1 == int(part.min())
+    assert np.array_equal(ref.rows_of(d[0].cpu().numpy(), fresh[0], 40), ref.rows_of(k, old[0], 40))
+    assert_no_device_error()
+
+
 def test_graph_replay_follows_the_inputs():
     k, v, s, old, fresh, lens = state([300, 200], 2, 16, 4)
     d = [torch.from_numpy(x.copy()).cuda() for x in (k, v, s, old, fresh, lens)]
