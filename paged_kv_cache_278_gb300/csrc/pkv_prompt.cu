@@ -851,7 +851,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                 total = l * w_own + o.y * w_other;
             }
             const int n_other = shared ? n_of_other : 0;
-            const float inv = total == 0.f ? 0.f : 1.f / total;
+            // A split may hold none of the row's keys.  A whole row sees one at least, so only scores of minus infinity make its
+            // sum 0: it has no softmax, and becomes NaN here (0 x inf) and in the joining launch alike.
+            const float inv = total == 0.f && split >= 0 ? 0.f : 1.f / total;
             w_own *= inv;
             w_other *= inv;
             const int64_t row = q_row * P.num_q_heads + (kvh << glog) + (r & ((1 << glog) - 1));

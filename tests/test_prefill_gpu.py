@@ -257,6 +257,41 @@ def test_a_long_tail_below_one_key(nats, n, c, at):
     assert_no_device_error()
 
 
+@pytest.mark.parametrize("n,c", [(6, 6), (300, 300), (2500, 5)])
+def test_scores_of_minus_infinity(n, c):
+    """A key whose scores are minus infinity takes no part, and a row that sees no other has no softmax: NaN, and a log-sum-exp of
+    minus infinity, whether its keys are split or not."""
+    g = torch.Generator(device="cuda").manual_seed(n)
+    q = torch.rand((c, 4, 128), generator=g, device="cuda").half() + 0.5
+    k, v = (torch.randn((n, 1, 128), generator=g, device="cuda").half() for _ in range(2))
+    gone = n - c + 1  # all that the first row of the chunk sees, and one key more
+    k[:gone] = float("-inf")
+    k[gone + 2] = float("-inf")
+    bs, nb = 16, -(-n // 16)
+    kc, vc = (torch.zeros((nb, 1, bs, 128), dtype=torch.float16, device="cuda") for _ in range(2))
+    pkv.append(kc, vc, torch.arange(n, device="cuda"), k, v)
+    table = torch.arange(nb, dtype=torch.int32, device="cuda").view(1, -1)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    ws = pkv.make_prefill_workspace(1, c, 4, 1, nb * bs, "cuda")
+    assert (ws is not None) == (n == 2500)
+    out, z = torch.zeros_like(q), torch.zeros((c, 4), device="cuda")
+    pkv.prefill_attention_paged(out, q, kc, vc, table, i32(n), i32(0, c), c, SCALE, lse=z, workspace=ws)
+    assert torch.isnan(out[0]).all() and (z[0] == float("-inf")).all()
+    rows = [i for i in range(gone, n) if i != gone + 2]
+    qn, kn, vn = (x.float().cpu().numpy().astype(np.float64) for x in (q, k, v))
+    for t in range(1, c):
+        seen = [i for i in rows if i <= n - c + t]
+        s = np.einsum("hd,nd->hn", qn[t], kn[seen, 0]) * SCALE
+        p = np.exp(s - s.max(-1, keepdims=True))
+        want = (p / p.sum(-1, keepdims=True)) @ vn[seen, 0]
+        assert np.abs(out[t].float().cpu().numpy() - want).max() <= 2e-3
+    if n == c:
+        o2, z2 = torch.zeros_like(out), torch.zeros_like(z)
+        pkv.prefill_attention(o2, q, k, v, i32(0, n), n, SCALE, lse=z2)
+        assert torch.isnan(o2[0]).all() and torch.equal(o2[1:], out[1:]) and torch.equal(z2, z)
+    assert_no_device_error()
+
+
 def test_bad_requests_are_skipped_and_recorded():
     out, z, args, ws = run_paged([300, 200, 100], [20, 30, 40], 4, 2, 16, 80)
     q, kc, vc, bt, cl, qs, n, scale = args
