@@ -766,6 +766,7 @@ def rope(q_out: torch.Tensor, k_out: torch.Tensor, q: torch.Tensor, k: torch.Ten
     rest is copied.  Rows may be slices of a fused projection (any token stride); an output may be its input."""
     dev = _device_of(q, "q")
     qs = _need_rows(q, "q", dev)
+    _device_of(k, "k")
     ks = _need_rows(k, "k", dev, (q.shape[0], k.shape[1], q.shape[2]) if k.dim() == 3 else None)
     qos = _need_rows(q_out, "q_out", dev, q.shape)
     kos = _need_rows(k_out, "k_out", dev, k.shape)

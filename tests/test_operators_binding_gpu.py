@@ -58,6 +58,27 @@ def test_prefill(x):
         refused(pkv.prefill_attention_paged, *good[:i], bad, *good[i + 1:])
 
 
+def test_arguments_that_are_no_tensors(x):
+    """Every tensor argument of every call, one after the other: a TypeError that names it, nothing else."""
+    kept = torch.empty((2, 2, 8), dtype=torch.int32, device="cuda")
+    ws = pkv.make_weights_workspace(2, 8, 32, "cuda")
+    calls = [(pkv.rope, [x["out"], torch.empty_like(x["k"]), x["q"], x["k"], x["pos"], x["freq"]]),
+             (pkv.rope_append, [x["out"], x["q"], x["k"], x["v"], x["kc"], x["vc"], x["slots"], x["pos"], x["freq"]]),
+             (pkv.prefill_attention, [x["out"], x["q"], x["k"], x["v"], x["qs"], 4, 0.1]),
+             (pkv.prefill_attention_paged, [x["out"], x["q"], x["kc"], x["vc"], x["bt"], x["cl"], x["qs"], 4, 0.1]),
+             (pkv.decode_attention_weights, [x["out"][:2], x["scores"], x["q"][:2], x["kc"], x["vc"], x["bt"], x["cl"], 0.1, ws]),
+             (pkv.prefill_attention_weights, [x["scores"], x["q"], x["lse"], x["kc"], x["bt"], x["cl"], x["qs"], 4, 0.1]),
+             (pkv.evict, [x["kc"], x["vc"], kept, torch.empty_like(x["scores"]), torch.empty_like(x["cl"]), x["scores"], x["bt"],
+                          x["cl"], 8])]
+    for f, good in calls:
+        for i, a in enumerate(good):
+            if isinstance(a, torch.Tensor):
+                for bad in (None, [1.0]):
+                    with pytest.raises(TypeError, match="must be a torch.Tensor"):
+                        f(*good[:i], bad, *good[i + 1:])
+    assert_no_device_error()
+
+
 def test_weights_and_evict(x):
     ws = pkv.make_weights_workspace(2, 8, 32, "cuda")
     good = [x["out"][:2], x["scores"], x["q"][:2], x["kc"], x["vc"], x["bt"], x["cl"], 0.1, ws]
