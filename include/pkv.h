@@ -762,8 +762,8 @@ PKV_API int pkv_rope_append(void *q_out, int64_t q_out_stride, const void *q, in
 
 /* Bytes of workspace the two calls need (0: none).  max_context: the longest context the call may meet
  * (max_seq_len, or max_blocks_per_seq * block_size).  Grows with max_context, but not with total_q or
- * num_seqs, as few rows are split over more CTAs: ask for the call's own.  No initial contents.
- * Calls that may run at the same time need one each. */
+ * num_seqs, as few rows are split over more CTAs: ask for the call's own, or give every call 81 MB (81 * 10^6
+ * bytes), which no call's need exceeds.  No initial contents.  Calls that may run at the same time need one each. */
 PKV_API size_t pkv_prefill_workspace_size(int num_seqs, int total_q, int num_q_heads, int num_kv_heads, int head_dim,
                                           int max_context);
 

@@ -804,8 +804,8 @@ def rope_append(q_out: torch.Tensor, q: torch.Tensor, k_new: torch.Tensor, v_new
 def make_prefill_workspace(num_seqs: int, total_q: int, num_q_heads: int, num_kv_heads: int, max_context: int,
                            device) -> torch.Tensor | None:
     """Workspace for prefill_attention (max_context: its max_seq_len) and prefill_attention_paged (the table's
-    entries * block_size); None when the call needs none.  For this num_seqs and total_q: fewer rows can need more.
-    One per call in flight."""
+    entries * block_size); None when the call needs none.  For this num_seqs and total_q: fewer rows can need more
+    (81 * 10**6 bytes are enough for any call).  One per call in flight."""
     n = int(_L().pkv_prefill_workspace_size(num_seqs, total_q, num_q_heads, num_kv_heads, PKV_HEAD_DIM, max_context))
     return torch.empty(n, dtype=torch.uint8, device=device) if n else None
 

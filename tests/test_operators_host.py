@@ -169,6 +169,20 @@ def test_prefill_workspace(lib):
         assert f(*bad) == 0
 
 
+def test_prefill_workspace_bound(lib):
+    """What the header promises to a program that allocates once: never more than 81 MB, whatever the call's sizes."""
+    most = 0
+    for hkv in (1, 2, 3, 8, 31, 50, 101, 102):
+        for group in (1, 2, 4, 8):
+            for seqs in (1, 2, 7, 20, 101, 5000):
+                for rows in [2 ** i + d for i in range(15) for d in (-1, 0, 1)]:
+                    for context in (1, 300, 4096, 40000, 1 << 20, 1 << 30):
+                        if rows > 0:
+                            most = max(most, lib.pkv_prefill_workspace_size(seqs, rows, hkv * group, hkv, 128, context))
+    # 608 / items splits at most of the 256 rows of each item: 155,648 partial rows of 128 + 2 floats, and alignment
+    assert 0 < most <= 608 * 256 * 130 * 4 + 3 * 256 < 81 * 10 ** 6
+
+
 def test_long_tables_are_refused(lib):
     wide = dict(width=(1 << 30) // 16 + 1, seqs=1, nb=1000)
     assert call(lib, "pkv_prefill_attention_paged", dict(PAGED, **wide)) == UNSUPPORTED

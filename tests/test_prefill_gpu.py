@@ -166,6 +166,31 @@ def run_paged(ctxs, chunks, group, hkv, bs, seed, peaky=0.0, poison=False):
     return out, z, args, ws
 
 
+def test_long_prompt():
+    """Rows of a long prompt at and around tile borders, and of short ones packed beside it."""
+    lens = [300, 16384, 5]
+    q, k, v, start = packed(lens, 8, 2, 90)
+    out, z = torch.full((q.shape[0], 8, 128), float("nan"), dtype=torch.float16, device="cuda"), torch.zeros((q.shape[0], 8), device="cuda")
+    pkv.prefill_attention(out, q, k, v, torch.tensor(start, dtype=torch.int32, device="cuda"), max(lens), SCALE, lse=z,
+                          workspace=pkv.make_prefill_workspace(3, q.shape[0], 8, 2, max(lens), "cuda"))
+    assert_no_device_error()
+    assert torch.isfinite(out).all()
+    o, zz, h = out.float().cpu().numpy(), z.cpu().numpy(), [x.float().cpu().numpy() for x in (q, k, v)]
+    rows = [(b, t) for b, some in ((0, (0, 299)), (1, (0, 31, 32, 127, 128, 4095, 8191, 8192, 12345, 16351, 16352, 16383)), (2, (4,)))
+            for t in some]
+    check(o, zz, [(slice(start[b] + t, start[b] + t + 1), h[0][start[b] + t:start[b] + t + 1],
+                   *(x[start[b]:start[b] + t + 1].astype(np.float64) for x in h[1:])) for b, t in rows])
+
+
+def test_many_decode_rows_beside_a_chunk():
+    """One call with hundreds of requests of one new token each and one chunk of many, as continuous batching makes it."""
+    ctxs = [(53 * i) % 190 + 1 for i in range(420)]
+    chunks = [1] * 420
+    ctxs[200], chunks[200] = 1700, 900
+    chunks[17] = 0
+    run_paged(ctxs, chunks, 4, 2, 16, 91)
+
+
 @pytest.mark.parametrize("group", [1, 2, 4, 8])
 @pytest.mark.parametrize("bs", [16, 48, 64, 256])
 def test_paged_ragged(group, bs):

@@ -72,6 +72,10 @@ def test_long_and_peaky():
     run(case)
 
 
+def test_contexts_of_many_partitions():
+    run(workloads.random_case(926, [32768, 20001, 1024], 8, 2, block_size=32))
+
+
 def test_steps_accumulate_and_leave_the_workspace_clean():
     case = workloads.random_case(911, [1500, 40, 0], 8, 2, block_size=16)
     _, first, ws, prior = run(case, seed=1)
@@ -215,6 +219,10 @@ def test_chunk_ragged(group, bs):
 @pytest.mark.parametrize("ctxs,chunks,group,hkv,bs", [([5000], [600], 4, 1, 16), ([1300, 64], [1300, 64], 2, 3, 64), ([700] * 40, [1] * 40, 8, 1, 16)])
 def test_chunk_sizes(ctxs, chunks, group, hkv, bs):
     run_chunk(ctxs, chunks, group, hkv, bs, 60)
+
+
+def test_chunk_behind_long_contexts():
+    run_chunk([16384, 8193], [64, 33], 4, 1, 16, 62)
 
 
 def test_chunk_follows_the_attention():
