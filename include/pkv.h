@@ -316,6 +316,10 @@ PKV_API size_t pkv_decode_workspace_size(int num_seqs, int num_q_heads, int head
  * block_size, PKV_DEFAULT_PARTITION) bytes of 256-byte-aligned workspace whose
  * counter region is zero when the workspace is first used (zero-fill a new
  * workspace once, e.g. cudaMemsetAsync); every call leaves the counters zero.
+ * They lie behind the partials, at an offset that follows num_seqs, num_q_heads
+ * and the table's width: zero-fill a workspace again before a call of other sizes
+ * than its last one's, or keep one per size (every pkv_decode_* call with a
+ * zero-filled workspace).
  * Calls that share a workspace must be ordered (one stream).
  * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */
 PKV_API int pkv_decode_attention(void *out, const void *q, const void *k_cache,
@@ -695,8 +699,9 @@ PKV_API int pkv_get_device_error(pkv_stream_t stream, int *code);
  *     y_a = m (x_a cos - x_b sin),  y_b = m (x_b cos + x_a sin),
  * the pair being dims (i, i + rotary_dim / 2), or (2i, 2i + 1) with interleaved != 0;
  * dims past rotary_dim are copied unchanged.  float32 arithmetic, one rounding to fp16.
- * The frequencies are fixed-point: f_i / 2 pi in units of 2^-64 turns, so the phase
- * is exact at any int32 position (negative ones turn backwards). */
+ * The frequencies are fixed-point: f_i / 2 pi in units of 2^-64 turns.  The phase is their exact
+ * product with any int32 position (negative ones turn backwards) modulo one turn; the frequencies themselves
+ * carry float64's rounding, some 2^-55 turns per position for the fastest pairs. */
 
 /* How the frequencies are derived from the base. */
 #define PKV_ROPE_PLAIN 0  /* f_i = base^(-2i / d) */
@@ -837,6 +842,8 @@ PKV_API int pkv_prefill_attention_weights(float *scores, int64_t score_capacity,
  *                block_tables entry of the same index (compaction in place; the blocks must not be shared
  *                with another request) or a block that no block_tables row of the call names (a shared
  *                block's rows are copied out).  May be block_tables itself.
+ * It writes the cache (and context_lens, if that is new_lens): a step call issued right behind it on the same cache
+ * must not set PKV_STEP_OVERLAP.
  * A context past its table is cut and recorded as PKV_DEV_BAD_CONTEXT.  So is what a new table too short has no
  * room for: only the first max_new_blocks * block_size kept positions are moved, and kept, new_scores and new_lens
  * describe those.  A bad block id skips its rows and is recorded as PKV_DEV_BAD_BLOCK_ID.  recent + sinks <= budget;

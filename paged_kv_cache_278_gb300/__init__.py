@@ -142,7 +142,8 @@ def decode_workspace_size(num_seqs: int, num_q_heads: int, max_context: int,
 
 def make_workspace(num_seqs: int, num_q_heads: int, max_context: int, device) -> torch.Tensor | None:
     """Allocate (with torch) the zero-filled workspace decode_attention needs; None when it needs
-    none.  Its completion counters start at zero and every call leaves them zero."""
+    none.  Its completion counters start at zero and every call leaves them zero; they lie where the call's sizes put
+    them, so a call of other sizes needs a workspace of its own (or this one zeroed again)."""
     n = decode_workspace_size(num_seqs, num_q_heads, max_context)
     if n == 0:
         return None

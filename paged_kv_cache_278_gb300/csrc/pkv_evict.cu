@@ -13,8 +13,8 @@
 //     bits) that the CTAs add up through distributed shared memory; counts do not depend on the
 //     order of the atomics that made them.  The kept set is then a bitmap over the positions (above the
 //     border, the lowest ties, sinks, recent); prefix popcounts of its words give every kept position
-//     its place.  Bound by latency, four meetings of the cluster in a row: 20 us alone, of 43 in all, for 32 rows of
-//     32768 scores, 14 of 41 for 128 rows of 3900.
+//     its place.  Bound by latency, four meetings of the cluster in a row: 20 us alone, of 42 in all, for 32 rows of
+//     16385 to 32768 scores, 14 of 41 for 128 rows of 1951 to 3900.
 //   * move: bound by HBM (each kept row is read once and written once): 134 MB in 23 us into new blocks, 29 us where
 //     the clusters meet at every step.  In a block that both tables
 //     name, a row's place may be the source of a row placed earlier, so rows move in order: a cluster
@@ -37,8 +37,8 @@ constexpr int kSelThreads = 512;
 constexpr int kBins = 512, kPasses = 4;  // digits of 9, 8, 8 and 7 bits
 constexpr int kMoveThreads = 256;
 constexpr int kRowLanes = PKV_HEAD_DIM * 2 / 16;  // threads that move one row, 16 bytes each
-constexpr int kMoveBatch = 4;                     // rows in flight per thread (2 and 8 measured 15 and 13 % slower on 4 x 32k -> 4k; the
-                                                  // next step's rows read ahead too take 72 registers, and 16 x 3.9k -> 1k 50 us, not 41)
+constexpr int kMoveBatch = 4;                     // rows in flight per thread (2 and 8 measured 15 and 13 % slower on 4 x 32768 -> 4096; the
+                                                  // next step's rows read ahead too take 72 registers, and 16 x 3900 -> 1024 in place 50 us, not 41)
 constexpr int kMoveRows = kMoveThreads / kRowLanes * kMoveBatch;  // rows of a CTA's step
 
 struct EvictParams {
@@ -461,8 +461,9 @@ extern "C" PKV_API int pkv_evict(void *k_cache, void *v_cache, int32_t *kept, fl
     p.recent = recent;
     p.sinks = sinks;
     // CTAs per cluster: doubled, to at most eight, while the grid has fewer than three CTAs per SM and
-    // the kept rows fill a step of the larger cluster.  (Whole call, one CTA against this rule: 4 x 32k -> 4k 148 and
-    // 48 us, in place 215 and 56; always eight against it: 64 x 2k -> 512 76 and 72.)
+    // the kept rows fill a step of the larger cluster.  (Whole call alone between flushes, 8 kv heads, all requests equally
+    // long, uniform scores, into new blocks, one CTA against this rule: 4 x 32768 -> 4096 148 and 48 us, in place 215 and
+    // 56; always eight against it: 64 x 2048 -> 512 76 and 72.)
     p.cluster = 1;
     while (p.cluster < 8 && static_cast<int64_t>(num_seqs) * num_kv_heads * 2 * p.cluster < 3 * sms &&
            budget >= 2 * p.cluster * kMoveRows)
@@ -471,9 +472,9 @@ extern "C" PKV_API int pkv_evict(void *k_cache, void *v_cache, int32_t *kept, fl
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    // Eight CTAs to a row as long as a thread has four scores left; more than 32 a thread only past 131072.  (Whole
-    // call, one CTA against this rule: 4 x 32k -> 4k 66 and 48 us, 1 x 32k -> 8k 67 and 46, 8 x 8k -> 2k 43 and 41,
-    // 16 x 3.9k -> 1k 41 both.)
+    // Eight CTAs to a row as long as a thread has four scores left; more than 32 a thread only past 131072.  (Timed
+    // like the clusters above, one CTA against this rule: 4 x 32768 -> 4096 66 and 48 us, 1 x 32768 -> 8192 67 and 46,
+    // 8 x 8192 -> 2048 43 and 41, 16 x 3900 -> 1024 41 both.)
     const int64_t runs = (cap + kSelThreads - 1) / kSelThreads;  // scores per thread of a single CTA
     p.select_cluster = runs <= 4 ? 1 : (runs <= 8 ? 2 : (runs <= 16 ? 4 : 8));
     const int64_t each = (runs + p.select_cluster - 1) / p.select_cluster;

@@ -11,9 +11,9 @@
 // behind (128 x 128 pairs: 1024 tensor cycles, 512 or more of the special-function units).  The two tiles
 // take turns: while the tensor cores run tile A's P V and next Q K^T, tile B's warps do their softmax.
 // Measured: one prompt of 16384 tokens (32 heads, G = 4) 1.52 ms, 1.45 PFLOP/s, 76 % of the measured bf16 rate (the
-// same MMAs without the softmax arithmetic: 1.34 ms); four chunks of 2048 tokens, each at the end of 8192 cached ones in 16-token
-// blocks, 0.53 ms, 1.3 PFLOP/s; 2 x 37 tokens behind 32k 60 us, 3.4 TB/s of K and V; sixteen prompts of 17 to 1000
-// tokens 71 us: a pair there is three key tiles long, and its start, its border tile, the last P V and the epilogue
+// same MMAs without the softmax arithmetic: 1.34 ms); four chunks of 2039 to 2048 tokens that end at 8192, 6827, 5462 and 4097
+// cached ones in 16-token blocks 0.53 ms, 1.3 PFLOP/s; 37 and 34 tokens that end at 32768 and 16385 in 64-token blocks
+// 60 us, 3.4 TB/s of K and V; sixteen prompts of 17 to 1000 tokens 71 us: a pair there is three key tiles long, and its start, its border tile, the last P V and the epilogue
 // (some 7000 cycles together) outweigh them.
 //
 //   TMEM (512 columns): S_A | S_B | O_A | O_B, 128 fp32 columns each.  P (fp16, two per column) replaces
@@ -23,14 +23,15 @@
 //   warps 0-3, 4-7  softmax of tile A, B: one thread per row, its 128 scores in registers; online max
 //       with lazy rescaling (O is rescaled only when a score exceeds the reference max by more than
 //       2^8, then by the row's own thread), row sums in fp32 of the unrounded weights.  P is rounded to
-//       fp16 once, which keeps P V at the fp16 rate (the decode kernels, bound by HBM, carry a second fp16 part).
+//       fp16 once, which keeps P V at the fp16 rate (the decode kernels, bound by HBM, carry a second fp16 part): beside
+//       the output's own rounding, 2.0e-4 of its norm, that adds 1.5e-4 to 2.0e-4.
 //       The weights are taken 2^7 too large, and so are the sums: fp16's range up to 2^15 is used, and a weight keeps its
 //       11 bits down to 2^-21 of the row's largest, some of them down to 2^-32, instead of 2^-14 and 2^-25: the
 //       tail behind one dominant key counts in P V as it does in the sum.
 //   warp 8  issues every tcgen05.mma (one lane).
 //   warps 9, 10  issue the tensor copies: Q (64 KB) once per item and the K tiles of 128 keys, and the V tiles,
 //       each through a ring of two 32 KB stages.  Two warps: with 16-token blocks a tile is 16 copies of 2 KB, and
-//       one warp issuing both K's and V's held the MMAs up (chunks of 2048 tokens 632 us against 551).
+//       one warp issuing both K's and V's held the MMAs up (the four chunks 632 us against 551 then).
 //
 // Work items are (pair of tiles, kv head, split of the keys), dealt to one persistent CTA per SM,
 // the longest first and in alternating direction, so that CTAs end together: warp 11 finds them, a few
@@ -304,9 +305,9 @@ __device__ __forceinline__ int most_tiles(const PromptParams &P, int lane) {
 // Splits of each item's keys, from the call's actual pairs and contexts, which the host does not know; the
 // same in every CTA and in the joining launch.  Two items per SM (the longer ones come first) where the
 // items are fewer than half of the SMs; up to two thirds of them, three splits make two rounds of a third of the
-// work; past that the rounds cost what the splits save.  (G = 4, 8 kv heads, whole against split: 2 x 37 tokens behind
-// 32k 419 and 84 us, 37 behind 4k 66 and 26, 4 x 100 behind 8k 117 and 88, 8 x 64 behind 4k 70 and 66; two
-// splits of 128 items 119 and 146.)
+// work; past that the rounds cost what the splits save.  (G = 4, 8 kv heads, 16-token blocks, one call alone between
+// flushes, all requests equally long, whole against split: 2 x 37 tokens ending at 32768 419 and 84 us, 37 at 4096 66 and 26,
+// 4 x 100 at 8192 117 and 88, 8 x 64 at 4096 70 and 66; two splits of 128 items 119 and 146.)
 __device__ __forceinline__ int split_count(const PromptParams &P, int pairs, int tiles) {
     if (P.splits <= 1) return 1;
     const int items = max(pairs * P.num_kv_heads, 1);
@@ -983,8 +984,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
 
 // Joins the splits of each (token, head) row: one warp per row, four dims a lane, BATCH splits' loads in flight.
 // Sixteen take 120 registers, two CTAs per SM; where those hold fewer rows than there are, eight loads a lane and
-// four CTAs do better (512 tokens behind 7680, three splits: 90 -> 87 us in all; 2 x 37 tokens behind 32k the other
-// way, 89 -> 84).
+// four CTAs do better (one call alone between flushes: 512 tokens ending at 8192, three splits, 90 -> 87 us in all;
+// 2 x 37 tokens ending at 32768 each the other way, 89 -> 84).
 constexpr int kJoinThreads = 256;
 template <int BATCH>
 __global__ void __launch_bounds__(kJoinThreads, BATCH == 8 ? 4 : 2) prompt_join_kernel(const __grid_constant__ PromptParams P) {
@@ -1059,8 +1060,8 @@ __global__ void __launch_bounds__(kJoinThreads, BATCH == 8 ? 4 : 2) prompt_join_
 // 128 keys of a tile as M (one TMEM lane, one thread each) and 128 packed rows as N; a thread adds up its
 // key's weights over all columns in its own registers and one thread adds them to scores: no exchange,
 // no atomics, a fixed order.  Bound by the exponentials, one per (row, key) pair (2 x 128 tensor flops),
-// until a chunk is so small that reading K bounds it.  The last 256 tokens of 2 x 16384 (32 heads, G = 4): 200
-// million pairs in 57 us, where the exponentials alone would take 22 and the MMAs 27: a group's chain per 128 x 128 tile,
+// until a chunk is so small that reading K bounds it.  The last 256 and 253 tokens of 16384 and 8193 (32 heads, G = 4):
+// 200 million pairs in 57 us, where the exponentials alone would take 22 and the MMAs 27: a group's chain per 128 x 128 tile,
 // from S^T's arrival through its load to the sums, is some 2100 cycles, of which 1100 are arithmetic.
 //   warps 0-3, 4-7  a key tile each, or the even and odd row tiles of one, with two S^T buffers of 128 TMEM columns
 //   warp 8          issues the MMAs
@@ -1073,7 +1074,7 @@ struct ChunkWeightParams {
     int64_t capacity;
 };
 
-constexpr int kKeyStages = 4, kRowRing = 2;  // three and three: 70 us where this takes 67
+constexpr int kKeyStages = 4, kRowRing = 2;  // three and three: 70 us where this takes 67 (2 x 256 tokens over 16384 keys each, alone)
 
 struct ChunkWeightSmem {
     static constexpr int keys = 0;
@@ -1209,8 +1210,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) chunk_weights_kernel(const 
             }
             tiles = __reduce_add_sync(pkv::kFullMask, tiles);
             pairs = __reduce_add_sync(pkv::kFullMask, pairs);
-            // Two key tiles an item read Q half as often; one where that leaves SMs idle.  (256 rows of 2 x 16384 keys: 67 us
-            // from cold caches against 78, 32 rows of 32768 29 against 34.)
+            // Two key tiles an item read Q half as often; one where that leaves SMs idle.  (One call alone between flushes:
+            // 2 x 256 tokens over 16384 keys each 67 us against 78, 32 tokens over 32768 29 against 34.)
             const int pair = static_cast<int64_t>(tiles) * P.num_kv_heads > gridDim.x ? 1 : 0;
             const uint32_t n_items = static_cast<uint32_t>(pair ? pairs : tiles) * P.num_kv_heads;
             bool ok = true;
@@ -1502,8 +1503,8 @@ int encode_rows(CUtensorMap *map, const void *base, int64_t rows, int64_t cols, 
 
 
 // Key tiles that a split is worth: the joining launch costs by the rows, so one per 1024 rows, two at least and
-// eight at most.  (37 tokens x 32 heads over 1000 keys: 22.5 us with two tiles, 27 with four, 27.5 whole; 160 over
-// 4096: 42 with two or four, 34 with five; 512 over 2048: 49 with four, 41 whole.)
+// eight at most.  (One call alone between flushes, 37 tokens x 32 heads over 1000 keys: 22.5 us with two tiles, 27 with
+// four, 27.5 whole; 160 over 4096: 42 with two or four, 34 with five; 512 over 2048: 49 with four, 41 whole.)
 int split_tiles(int total_q, int num_q_heads) {
     const int64_t t = static_cast<int64_t>(total_q) * num_q_heads / 1024;
     return t < 2 ? 2 : (t > 8 ? 8 : static_cast<int>(t));

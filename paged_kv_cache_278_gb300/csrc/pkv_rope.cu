@@ -10,7 +10,9 @@
 // The angle.  p f_i reaches 10^6 radians, where a float32 product has lost every bit of the phase and
 // float64 runs at a thousandth of the float32 rate here.  The frequencies are therefore fixed-point:
 // f_i / 2 pi in units of 2^-64 turns, and p x frequency in wrapping 64-bit integers is the phase
-// modulo one turn, exact to 2^-65 p turns.  Its upper 32 bits, signed, are a fraction in [-1/2, 1/2)
+// modulo one turn, exactly.  What is rounded is the frequency: computed in float64, it is off by some 2^-53 of itself (and
+// by 2^-65 turns, half a unit), so the phase by some 2^-55 p turns for the fastest pairs: 2^-24 turns at the largest
+// position, 2^-35 at a million.  Its upper 32 bits, signed, are a fraction in [-1/2, 1/2)
 // turns, and sincospif takes them from there.
 //
 // What bounds it: memory (every row is read once and written once; 3 flops an element): 8192 tokens of 48

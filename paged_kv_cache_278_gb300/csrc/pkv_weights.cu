@@ -13,16 +13,16 @@
 //     ring of 16-token chunks (tensor copies, 128-byte swizzle), the tensor-core engine of the
 //     decode kernels with one 8-byte store per lane and token pair added; contexts past one partition
 //     leave a partial output each.  Bound by HBM, as the decode kernels are: 90 us for the 538 MB of 64 x 2049 tokens alone on
-//     cold caches, what the plain decode kernel takes there; with the weights pass 97 us, 85 % of the copy bandwidth
-//     (4 x up to 32k tokens 62 us, 83 %).
+//     cold caches, what the plain decode kernel takes there; with the weights pass 97 us, 84 % of the copy bandwidth
+//     (32768, 24577, 16385 and 8193 tokens 62 us, 82 %).
 //   * weights pass: one CTA per (request, kv head, 1024 tokens): the partitions' (m, l) give the
 //     group's log-sum-exps, then one exponential per (token, head) and one read-modify-write of
 //     scores per token, by exactly one thread: no atomics, a fixed order.  Its CTAs of a (request, kv head) join the
 //     partial outputs too, each a share of the dims: no counter has to survive from one call to the next, so any calls
-//     may take turns on one workspace, whatever it held.  Bound by latency (7-10 us alone): its
+//     may take turns on one workspace, whatever it held.  Bound by latency (10-12 us alone): its
 //     loads are issued together, those of scores while the attention pass still runs.  The join
-//     by the last partition to arrive, with a counter, took as long or longer: 97.1 us against 96.9 (64 x 2049), 63.4
-//     against 61.8 (4 x up to 32k).
+//     by the last partition to arrive, with a counter, took as long or longer: 97.1 us against 96.9 (64 x 2049) and 63.4
+//     against 61.8 (the four contexts).
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
