@@ -76,6 +76,12 @@ def test_contexts_of_many_partitions():
     run(workloads.random_case(926, [32768, 20001, 1024], 8, 2, block_size=32))
 
 
+@pytest.mark.parametrize("group", [1, 8])
+def test_more_partitions_than_pieces_and_threads(group):
+    """264 partitions: more than the 32 pieces of one head's row, and than a CTA has threads."""
+    run(workloads.random_case(927, [270000, 40000], group, 1, block_size=256))
+
+
 def test_steps_accumulate_and_leave_the_workspace_clean():
     case = workloads.random_case(911, [1500, 40, 0], 8, 2, block_size=16)
     _, first, ws, prior = run(case, seed=1)
