@@ -3,7 +3,7 @@
  *
  * One decode step of a transformer layer over a paged KV cache, for one GPU
  * (NVIDIA GB300, sm_103a), and what a server runs around it (rotary positions, attention of
- * prompts and chunks, accumulated attention weights, eviction: the sections at the end).
+ * prompts and chunks, trees of drafted tokens, accumulated attention weights, eviction: the sections at the end).
  * The step:
  *
  *   1. the new token's K and V are written in place into their cache slots
@@ -91,6 +91,8 @@ extern "C" {
 #define PKV_DEV_WAIT_TIMEOUT 4   /* an asynchronous copy did not complete in time */
 #define PKV_DEV_PREFIX_MISMATCH 5 /* a block table does not start with the shared prefix's blocks */
 #define PKV_DEV_SMEM_MISALIGNED 6 /* dynamic shared memory not 1024-byte aligned (the CTA skipped its tokens) */
+#define PKV_DEV_BAD_AXIS 7       /* an axis outside [0, num_axes) (axis 0 was taken) */
+#define PKV_DEV_BAD_PATH 8       /* a tree's parent or path that does not go from node to later node */
 
 /* Defaults and limits of the decode kernels. */
 #define PKV_HEAD_DIM 128             /* the only head_dim the decode kernels take */
@@ -751,6 +753,56 @@ PKV_API int pkv_rope_append(void *q_out, int64_t q_out_stride, const void *q, in
                             int block_size, int64_t num_blocks, int interleaved, float magnitude,
                             pkv_stream_t stream);
 
+/* ---- norms of q and k per head, positions of several axes -------------------
+ * pkv_rope and pkv_rope_append with two additions in the same pass.  Each row x of q (k) is first divided by
+ * sqrt(mean(x^2) + eps) and multiplied by q_weight (k_weight), float32 [head_dim], 16-byte aligned; a NULL weight
+ * leaves those rows as they are.  And a token has num_axes positions (1 .. PKV_MAX_ROPE_AXES; time, height and
+ * width of a picture's patch, say):
+ *   positions : DEVICE int32 [num_tokens][num_axes]
+ *   axes      : DEVICE int32 [rotary_dim / 2], the axis that turns each pair (may be NULL with one axis); an entry
+ *               outside [0, num_axes) counts as 0 and is recorded as PKV_DEV_BAD_AXIS
+ * float32 arithmetic from the row to the rotated row, one rounding.  eps >= 0.  Other arguments, in-place use and
+ * errors as pkv_rope's and pkv_rope_append's. */
+#define PKV_MAX_ROPE_AXES 4
+
+PKV_API int pkv_norm_rope(void *q_out, int64_t q_out_stride, void *k_out, int64_t k_out_stride, const void *q,
+                          int64_t q_stride, const void *k, int64_t k_stride, const int32_t *positions,
+                          const int32_t *axes, int num_axes, const int64_t *frequencies, const float *q_weight,
+                          const float *k_weight, float eps, int num_tokens, int num_q_heads, int num_kv_heads,
+                          int head_dim, int rotary_dim, int interleaved, float magnitude, pkv_stream_t stream);
+
+PKV_API int pkv_norm_rope_append(void *q_out, int64_t q_out_stride, const void *q, int64_t q_stride, const void *k_new,
+                                 int64_t k_stride, const void *v_new, int64_t v_stride, void *k_cache, void *v_cache,
+                                 const int64_t *slot_mapping, const int32_t *positions, const int32_t *axes,
+                                 int num_axes, const int64_t *frequencies, const float *q_weight,
+                                 const float *k_weight, float eps, int num_tokens, int num_q_heads, int num_kv_heads,
+                                 int head_dim, int rotary_dim, int block_size, int64_t num_blocks, int interleaved,
+                                 float magnitude, pkv_stream_t stream);
+
+/* pkv_norm_rope_append into the fp8 K + V cache: k and v rows are quantised by pkv_append_fp8kv's rule, k from the
+ * float32 rotated row (not from its fp16 rounding).  head_dim PKV_HEAD_DIM.  Scales 4-byte aligned.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+PKV_API int pkv_norm_rope_append_fp8kv(void *q_out, int64_t q_out_stride, const void *q, int64_t q_stride,
+                                       const void *k_new, int64_t k_stride, const void *v_new, int64_t v_stride,
+                                       void *k_codes, float *k_scale, void *v_codes, float *v_scale,
+                                       const int64_t *slot_mapping, const int32_t *positions, const int32_t *axes,
+                                       int num_axes, const int64_t *frequencies, const float *q_weight,
+                                       const float *k_weight, float eps, int num_tokens, int num_q_heads,
+                                       int num_kv_heads, int head_dim, int rotary_dim, int block_size,
+                                       int64_t num_blocks, int interleaved, float magnitude, pkv_stream_t stream);
+
+/* ================================================================ reading the fp8 cache back
+ * Whole blocks of an fp8 K + V cache into blocks of an fp16 cache of the same heads and block size, for the calls
+ * that read fp16 (prompt, tree and weight attention):
+ *   k_cache[dst_ids[i]] <- k_codes[src_ids[i]] x k_scale[src_ids[i]], and V likewise, i < n,
+ * the product in float32, rounded once to fp16.  src_ids and dst_ids are DEVICE int32 arrays; a destination must not
+ * appear twice.  num_blocks is the fp16 cache's, src_num_blocks the fp8 one's; a pair with an id outside its cache is
+ * skipped and recorded as PKV_DEV_BAD_BLOCK_ID.  head_dim PKV_HEAD_DIM.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+PKV_API int pkv_read_blocks_fp8kv(void *k_cache, void *v_cache, int64_t num_blocks, const void *k_codes,
+                                  const float *k_scale, const void *v_codes, const float *v_scale,
+                                  int64_t src_num_blocks, const int32_t *src_ids, const int32_t *dst_ids, int n,
+                                  int num_kv_heads, int head_dim, int block_size, pkv_stream_t stream);
+
 /* ================================================================ prompts and chunks
  * Causal attention of many new tokens per request:
  *     out[t][hq] = softmax over the positions at or before t's (scale q[t][hq] . K) . V
@@ -792,6 +844,59 @@ PKV_API int pkv_prefill_attention_paged(void *out, float *lse, const void *q, in
                                         int total_q, int max_query_len, int max_blocks_per_seq, int num_q_heads,
                                         int num_kv_heads, int head_dim, int block_size, int64_t num_blocks,
                                         float scale, void *workspace, size_t workspace_bytes, pkv_stream_t stream);
+
+/* ================================================================ trees of drafted tokens
+ * A speculative step that drafts a tree instead of a line: request b's n_b = query_start[b + 1] - query_start[b]
+ * nodes lie behind its context, appended like any tokens (node i at cached position context_lens[b] - n_b + i; its
+ * rotary position is the one its depth gives).  Node i's row attends to every cached position before the tree and to
+ * the nodes whose bits its mask has:
+ *   tree_mask : DEVICE int32 [total_q][mask_words], bit j % 32 of word j / 32 of row query_start[b] + i set when the row
+ *               sees node j of request b (itself too, if its own bit is set).  mask_words * 32 >= max_query_len; bits
+ *               from n_b on are not read.
+ * Any mask is allowed, not only a tree's.  A row that sees nothing (no context before the tree and no bit) is a
+ * zero row with an lse of minus infinity.  max_query_len <= PKV_MAX_QUERY_LEN.  Rows, ranges, bad requests, lse,
+ * rounding and what reaches a result as in "prompts and chunks". */
+
+/* Bytes of workspace (0: none) for tables of max_context = max_blocks_per_seq * block_size positions; 41 MB at most.  No
+ * initial contents, and nothing kept in it from one call to the next.  Calls that may run at the same time need one
+ * each. */
+PKV_API size_t pkv_tree_workspace_size(int num_seqs, int total_q, int max_query_len, int num_q_heads, int num_kv_heads,
+                                       int head_dim, int max_context);
+
+/* Attention of every request's tree over its paged cache, on the 5th-generation tensor cores.
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */
+PKV_API int pkv_decode_attention_tree(void *out, float *lse, const void *q, int64_t q_stride, const void *k_cache,
+                                      const void *v_cache, const int32_t *block_tables, const int32_t *context_lens,
+                                      const int32_t *query_start, const int32_t *tree_mask, int mask_words,
+                                      int num_seqs, int total_q, int max_query_len, int max_blocks_per_seq,
+                                      int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                                      int64_t num_blocks, float scale, void *workspace, size_t workspace_bytes,
+                                      pkv_stream_t stream);
+
+/* The masks of trees from their parents: parents is DEVICE int32 [total_q], parents[query_start[b] + i] the node
+ * above node i of request b (below i: a parent comes before its children) or negative for a node that follows the
+ * context directly.  Row i of tree_mask (all mask_words of it) receives the bits of i and of every node above it;
+ * depths, if not NULL, int32 [total_q], the number of nodes above it: its rotary position is the context before the
+ * tree plus that.  A parent at or behind its node ends the walk there and is recorded as PKV_DEV_BAD_PATH.
+ * Rows of no request stay as they are.  Errors: INVALID_ARG, UNSUPPORTED (max_query_len), CUDA. */
+PKV_API int pkv_tree_masks(int32_t *tree_mask, int32_t *depths, const int32_t *parents, const int32_t *query_start,
+                           int num_seqs, int total_q, int max_query_len, int mask_words, pkv_stream_t stream);
+
+/* Keeps the accepted path of each request's tree: node path[b][i]'s rows of K and V move to position base + i,
+ * base = context_lens[b] - n_b, for i < path_lens[b].
+ *   path      : DEVICE int32 [num_seqs][max_path], a request's accepted nodes in ascending order
+ *   path_lens : DEVICE int32 [num_seqs], 0 .. min(n_b, max_path)
+ *   new_lens  : DEVICE int32 [num_seqs], base + path_lens[b]; may be NULL (every layer's cache but the last's), may
+ *               be context_lens itself
+ * It writes the blocks from position base on, which must not be shared with another request.  A path that does not
+ * ascend within its tree, or is too long, is recorded as PKV_DEV_BAD_PATH, a context shorter than its tree or
+ * past its table as PKV_DEV_BAD_CONTEXT: nothing of that request moves and its length stays.  A bad block id skips its row
+ * and is recorded as PKV_DEV_BAD_BLOCK_ID.  It writes the cache: a step call issued right behind it on the same cache
+ * must not set PKV_STEP_OVERLAP.  head_dim PKV_HEAD_DIM.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+PKV_API int pkv_keep_path(void *k_cache, void *v_cache, int32_t *new_lens, const int32_t *block_tables,
+                          const int32_t *context_lens, const int32_t *query_start, const int32_t *path,
+                          const int32_t *path_lens, int num_seqs, int max_blocks_per_seq, int max_path,
+                          int num_kv_heads, int head_dim, int block_size, int64_t num_blocks, pkv_stream_t stream);
 
 /* ================================================================ accumulated attention weights
  * scores is float32 [num_seqs][num_kv_heads][score_capacity], row (b, h) holding for each cached

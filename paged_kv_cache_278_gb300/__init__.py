@@ -12,7 +12,9 @@ and streams only.
                          context_lens, scale, workspace=ws)
     o, m, l = ...; pkv.decode_partition(o, m, l, q, ...); pkv.merge(out, o, m, l, context_lens, 512)
 
-Around the step: rope / rope_append (rotary positions, alone or fused with the append), prefill_attention and
+Around the step: rope / rope_append (rotary positions, alone or fused with the append), norm_rope / norm_rope_append /
+norm_rope_append_fp8kv (the same with norms per head and positions of several axes), read_blocks_fp8kv (an fp8 cache's blocks
+as fp16), tree_masks, decode_attention_tree and keep_path (drafted trees and their accepted paths), prefill_attention and
 prefill_attention_paged (whole prompts, chunks behind a cache), decode_attention_weights and
 prefill_attention_weights (the attention each cached position received), evict (cut a cache to a budget by it).
 
@@ -27,7 +29,7 @@ import torch
 from . import _lib
 from ._lib import (PKV_MAX_QUERY_LEN, PKV_DEFAULT_PARTITION, PKV_DEV_BAD_BLOCK_ID, PKV_DEV_BAD_CONTEXT, PKV_DEV_BAD_SLOT,
                    PKV_DEV_OK, PKV_DEV_PREFIX_MISMATCH, PKV_DEV_SMEM_MISALIGNED, PKV_DEV_WAIT_TIMEOUT, PKV_HEAD_DIM, PKV_MAX_PARTITION,
-                   PKV_STEP_OVERLAP, PKV_MAX_STEP_QUERY_LEN, PkvError)
+                   PKV_DEV_BAD_AXIS, PKV_DEV_BAD_PATH, PKV_STEP_OVERLAP, PKV_MAX_STEP_QUERY_LEN, PkvError)
 
 __all__ = [
     "append", "decode_attention", "decode_partition", "merge", "decode_workspace_size", "make_workspace",
@@ -39,10 +41,12 @@ __all__ = [
     "rope_frequencies", "rope_magnitude", "rope", "rope_append", "make_prefill_workspace", "prefill_attention",
     "prefill_attention_paged", "make_weights_workspace", "decode_attention_weights",
     "prefill_attention_weights", "evict",
+    "rope_axes", "norm_rope", "norm_rope_append", "norm_rope_append_fp8kv", "read_blocks_fp8kv", "tree_masks",
+    "make_tree_workspace", "decode_attention_tree", "keep_path",
     "device_error", "slot_mapping", "BlockPool", "PkvError", "library_path",
     "PKV_DEFAULT_PARTITION", "PKV_MAX_PARTITION", "PKV_HEAD_DIM",
     "PKV_DEV_OK", "PKV_DEV_BAD_BLOCK_ID", "PKV_DEV_BAD_CONTEXT", "PKV_DEV_BAD_SLOT", "PKV_DEV_WAIT_TIMEOUT",
-    "PKV_DEV_SMEM_MISALIGNED", "PKV_STEP_OVERLAP", "PKV_MAX_STEP_QUERY_LEN",
+    "PKV_DEV_SMEM_MISALIGNED", "PKV_DEV_BAD_AXIS", "PKV_DEV_BAD_PATH", "PKV_STEP_OVERLAP", "PKV_MAX_STEP_QUERY_LEN",
 ]
 
 
@@ -800,6 +804,123 @@ def rope_append(q_out: torch.Tensor, q: torch.Tensor, k_new: torch.Tensor, v_new
           frequencies.data_ptr(), t, q.shape[1], hkv, d, r, bs, nb, int(bool(interleaved)), float(magnitude))
 
 
+# ---------------------------------------------------------------- norms with the rotation, several axes
+
+def rope_axes(sections, device="cuda") -> torch.Tensor:
+    """The axis that turns each pair where every axis has one section of them: sections [pairs of axis 0, of axis
+    1, ...] as int32 [sum(sections)].  (norm_rope takes any other assignment too.)"""
+    return torch.tensor([a for a, n in enumerate(sections) for _ in range(n)], dtype=torch.int32, device=device)
+
+
+def _norm_inputs(q, positions, frequencies, q_weight, k_weight, axes, device):
+    """The checked arguments the norm_rope calls share: axes' pointer, number of axes, weights' pointers, rotary_dim."""
+    if not isinstance(positions, torch.Tensor):
+        raise TypeError("positions must be a torch.Tensor")
+    _need(positions, "positions", torch.int32, 2 if positions.dim() == 2 else 1, device)
+    _need(frequencies, "frequencies", torch.int64, 1, device)
+    t, _, d = q.shape
+    if positions.shape[0] != t:
+        raise ValueError("positions must have one entry (or row) per token")
+    n = positions.shape[1] if positions.dim() == 2 else 1
+    if axes is not None:
+        _need(axes, "axes", torch.int32, 1, device)
+        if axes.shape[0] != frequencies.shape[0]:
+            raise ValueError("axes must have one entry per pair")
+    elif n != 1:
+        raise ValueError("positions of several axes need axes")
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _need(w, name, torch.float32, 1, device)
+            if w.shape[0] != d:
+                raise ValueError(f"{name} must be [{d}]")
+    pointer = lambda x: None if x is None else x.data_ptr()  # noqa: E731
+    return pointer(axes), n, pointer(q_weight), pointer(k_weight), 2 * frequencies.shape[0]
+
+
+def norm_rope(q_out: torch.Tensor, k_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor,
+              frequencies: torch.Tensor, q_weight: torch.Tensor | None, k_weight: torch.Tensor | None, eps: float,
+              axes: torch.Tensor | None = None, interleaved: bool = False, magnitude: float = 1.0, stream=None) -> None:
+    """rope with a norm per head before it: each row of q [T, Hq, D] is x / sqrt(mean(x^2) + eps) * q_weight (float32 [D];
+    None: as it is) and then turned, k likewise.  positions [T], or [T, A] with axes (int32, one entry per
+    pair: the axis whose position turns it)."""
+    dev = _device_of(q, "q")
+    qs = _need_rows(q, "q", dev)
+    _device_of(k, "k")
+    ks = _need_rows(k, "k", dev, (q.shape[0], k.shape[1], q.shape[2]) if k.dim() == 3 else None)
+    qos = _need_rows(q_out, "q_out", dev, q.shape)
+    kos = _need_rows(k_out, "k_out", dev, k.shape)
+    ax, n, qw, kw, r = _norm_inputs(q, positions, frequencies, q_weight, k_weight, axes, dev)
+    _call("pkv_norm_rope", dev, stream, q_out.data_ptr(), qos, k_out.data_ptr(), kos, q.data_ptr(), qs, k.data_ptr(), ks,
+          positions.data_ptr(), ax, n, frequencies.data_ptr(), qw, kw, float(eps), q.shape[0], q.shape[1], k.shape[1],
+          q.shape[2], r, int(bool(interleaved)), float(magnitude))
+
+
+def _norm_append_rows(q_out, q, k_new, v_new, slot_mapping, hkv, d, dev):
+    qs = _need_rows(q, "q", dev)
+    t = q.shape[0]
+    if q.shape[2] != d:
+        raise ValueError("q head_dim differs from the cache's")
+    qos = _need_rows(q_out, "q_out", dev, q.shape)
+    ks = _need_rows(k_new, "k_new", dev, (t, hkv, d))
+    vs = _need_rows(v_new, "v_new", dev, (t, hkv, d))
+    _need(slot_mapping, "slot_mapping", torch.int64, 1, dev)
+    if slot_mapping.shape[0] != t:
+        raise ValueError("slot_mapping must have one entry per token")
+    return (q_out.data_ptr(), qos, q.data_ptr(), qs, k_new.data_ptr(), ks, v_new.data_ptr(), vs), t
+
+
+def norm_rope_append(q_out: torch.Tensor, q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, k_cache: torch.Tensor,
+                     v_cache: torch.Tensor, slot_mapping: torch.Tensor, positions: torch.Tensor, frequencies: torch.Tensor,
+                     q_weight: torch.Tensor | None, k_weight: torch.Tensor | None, eps: float,
+                     axes: torch.Tensor | None = None, interleaved: bool = False, magnitude: float = 1.0, stream=None) -> None:
+    """norm_rope and append in one launch: q into q_out (which may be q), k_new into the cache slots slot_mapping [T]
+    (int64; -1 = skip), v_new copied there.  Rows as rope's."""
+    nb, hkv, bs, d = _cache_shape(k_cache, v_cache)
+    dev = k_cache.device
+    rows, t = _norm_append_rows(q_out, q, k_new, v_new, slot_mapping, hkv, d, dev)
+    ax, n, qw, kw, r = _norm_inputs(q, positions, frequencies, q_weight, k_weight, axes, dev)
+    _call("pkv_norm_rope_append", dev, stream, *rows, k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(),
+          positions.data_ptr(), ax, n, frequencies.data_ptr(), qw, kw, float(eps), t, q.shape[1], hkv, d, r, bs, nb,
+          int(bool(interleaved)), float(magnitude))
+
+
+def norm_rope_append_fp8kv(q_out: torch.Tensor, q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
+                           k_codes: torch.Tensor, k_scale: torch.Tensor, v_codes: torch.Tensor, v_scale: torch.Tensor,
+                           slot_mapping: torch.Tensor, positions: torch.Tensor, frequencies: torch.Tensor,
+                           q_weight: torch.Tensor | None, k_weight: torch.Tensor | None, eps: float,
+                           axes: torch.Tensor | None = None, interleaved: bool = False, magnitude: float = 1.0,
+                           stream=None) -> None:
+    """norm_rope_append into the fp8 cache (as empty_fp8kv_cache makes it): k quantised from the float32 rotated row, v
+    as append_fp8kv does it."""
+    nb, hkv, bs, d = _int8kv_shape(k_codes, k_scale, v_codes, v_scale, torch.uint8)
+    dev = k_codes.device
+    rows, t = _norm_append_rows(q_out, q, k_new, v_new, slot_mapping, hkv, d, dev)
+    ax, n, qw, kw, r = _norm_inputs(q, positions, frequencies, q_weight, k_weight, axes, dev)
+    _call("pkv_norm_rope_append_fp8kv", dev, stream, *rows, k_codes.data_ptr(), k_scale.data_ptr(), v_codes.data_ptr(),
+          v_scale.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(), ax, n, frequencies.data_ptr(), qw, kw,
+          float(eps), t, q.shape[1], hkv, d, r, bs, nb, int(bool(interleaved)), float(magnitude))
+
+
+def read_blocks_fp8kv(k_cache: torch.Tensor, v_cache: torch.Tensor, k_codes: torch.Tensor, k_scale: torch.Tensor,
+                      v_codes: torch.Tensor, v_scale: torch.Tensor, src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
+    """k_cache[dst[i]] <- k_codes[src[i]] x k_scale[src[i]] and V likewise: blocks of an fp8 cache into blocks of an
+    fp16 one of the same heads and block size (src, dst: CUDA int32 [n], no destination twice)."""
+    nb, hkv, bs, d = _cache_shape(k_cache, v_cache)
+    dev = k_cache.device
+    src_nb, *geometry = _int8kv_shape(k_codes, k_scale, v_codes, v_scale, torch.uint8)
+    if geometry != [hkv, bs, d]:
+        raise ValueError("the fp8 and the fp16 cache differ in kv heads, block size or head_dim")
+    if k_codes.device != dev:
+        raise ValueError(f"k_codes is on {k_codes.device}, expected {dev}")
+    _need(src, "src", torch.int32, 1, dev)
+    _need(dst, "dst", torch.int32, 1, dev)
+    if src.shape != dst.shape:
+        raise ValueError("src and dst must have the same length")
+    _call("pkv_read_blocks_fp8kv", dev, stream, k_cache.data_ptr(), v_cache.data_ptr(), nb, k_codes.data_ptr(),
+          k_scale.data_ptr(), v_codes.data_ptr(), v_scale.data_ptr(), src_nb, src.data_ptr(), dst.data_ptr(),
+          src.shape[0], hkv, d, bs)
+
+
 # ---------------------------------------------------------------- prompts and chunks
 
 def make_prefill_workspace(num_seqs: int, total_q: int, num_q_heads: int, num_kv_heads: int, max_context: int,
@@ -871,6 +992,92 @@ def prefill_attention_paged(out: torch.Tensor, q: torch.Tensor, k_cache: torch.T
           query_start.data_ptr(), b, q.shape[0], int(max_query_len), block_tables.shape[1], q.shape[1], hkv, d, bs,
           nb, float(scale), ws_ptr, ws_bytes)
     return out
+
+
+# ---------------------------------------------------------------- trees of drafted tokens
+
+def tree_masks(mask: torch.Tensor, depths: torch.Tensor | None, parents: torch.Tensor, query_start: torch.Tensor,
+               max_query_len: int, stream=None) -> None:
+    """The masks [T, words] (int32, 32 * words >= max_query_len) of trees from their parents [T] (int32: the node above,
+    by its index in its request's tree and below the node's own, or -1): the bits of each node and of all above it.
+    depths [T] int32 (or None) receives the number of nodes above."""
+    _need(mask, "mask", torch.int32, 2)
+    dev = mask.device
+    _need(parents, "parents", torch.int32, 1, dev)
+    _need(query_start, "query_start", torch.int32, 1, dev)
+    t = parents.shape[0]
+    if mask.shape[0] != t or query_start.shape[0] < 1:
+        raise ValueError("mask [T, words], parents [T] and query_start [B + 1] disagree")
+    if depths is not None:
+        _need(depths, "depths", torch.int32, 1, dev)
+        if depths.shape[0] != t:
+            raise ValueError("depths must have one entry per node")
+    _call("pkv_tree_masks", dev, stream, mask.data_ptr(), None if depths is None else depths.data_ptr(), parents.data_ptr(),
+          query_start.data_ptr(), query_start.shape[0] - 1, t, int(max_query_len), mask.shape[1])
+
+
+def make_tree_workspace(num_seqs: int, total_q: int, max_query_len: int, num_q_heads: int, num_kv_heads: int,
+                        max_context: int, device) -> torch.Tensor | None:
+    """Workspace for decode_attention_tree (max_context: the table's entries * block_size); None when the call needs
+    none, 41 * 10**6 bytes at most.  One per call in flight; calls that need less may use it too."""
+    n = int(_L().pkv_tree_workspace_size(num_seqs, total_q, max_query_len, num_q_heads, num_kv_heads, PKV_HEAD_DIM,
+                                         max_context))
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def decode_attention_tree(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                          block_tables: torch.Tensor, context_lens: torch.Tensor, query_start: torch.Tensor,
+                          tree_mask: torch.Tensor, max_query_len: int, scale: float, lse: torch.Tensor | None = None,
+                          workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """decode_attention_multi for drafted trees: request b's nodes (q rows query_start[b] .. query_start[b + 1] - 1,
+    already appended, so context_lens counts them) each attend to the cache before the tree and to the nodes whose
+    bits tree_mask [T, words] (int32, 32 * words >= max_query_len) has.  q may have any token stride; lse as
+    prefill_attention's.  A row that sees nothing is zero."""
+    nb, hkv, bs, d = _cache_shape(k_cache, v_cache)
+    dev = k_cache.device
+    qs = _need_rows(q, "q", dev)
+    if q.shape[2] != d:
+        raise ValueError("q head_dim differs from the cache's")
+    _need(block_tables, "block_tables", torch.int32, 2, dev)
+    _need(context_lens, "context_lens", torch.int32, 1, dev)
+    _need(query_start, "query_start", torch.int32, 1, dev)
+    _need(tree_mask, "tree_mask", torch.int32, 2, dev)
+    b = context_lens.shape[0]
+    if block_tables.shape[0] != b or query_start.shape[0] != b + 1:
+        raise ValueError("block_tables [B, ...], context_lens [B] and query_start [B + 1] disagree")
+    if tree_mask.shape[0] != q.shape[0]:
+        raise ValueError("tree_mask must have one row per node")
+    ws_ptr, ws_bytes = _prompt_outputs(out, lse, q, workspace, dev)
+    _call("pkv_decode_attention_tree", dev, stream, out.data_ptr(), None if lse is None else lse.data_ptr(), q.data_ptr(),
+          qs, k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(),
+          query_start.data_ptr(), tree_mask.data_ptr(), tree_mask.shape[1], b, q.shape[0], int(max_query_len),
+          block_tables.shape[1], q.shape[1], hkv, d, bs, nb, float(scale), ws_ptr, ws_bytes)
+    return out
+
+
+def keep_path(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
+              query_start: torch.Tensor, path: torch.Tensor, path_lens: torch.Tensor,
+              new_lens: torch.Tensor | None = None, stream=None) -> None:
+    """Keep the accepted nodes of each request's tree: rows of node path[b, i] (int32 [B, P], ascending) move to the i-th
+    position behind the context before the tree, for i < path_lens[b] (int32 [B]).  new_lens [B] (or None; may be
+    context_lens) receives that context's length plus path_lens.  The blocks must not be shared."""
+    nb, hkv, bs, d = _cache_shape(k_cache, v_cache)
+    dev = k_cache.device
+    _need(block_tables, "block_tables", torch.int32, 2, dev)
+    _need(context_lens, "context_lens", torch.int32, 1, dev)
+    _need(query_start, "query_start", torch.int32, 1, dev)
+    _need(path, "path", torch.int32, 2, dev)
+    _need(path_lens, "path_lens", torch.int32, 1, dev)
+    b = context_lens.shape[0]
+    if block_tables.shape[0] != b or query_start.shape[0] != b + 1 or path.shape[0] != b or path_lens.shape[0] != b:
+        raise ValueError("block_tables, context_lens, path and path_lens [B, ...] and query_start [B + 1] disagree")
+    if new_lens is not None:
+        _need(new_lens, "new_lens", torch.int32, 1, dev)
+        if new_lens.shape[0] != b:
+            raise ValueError("new_lens must have one entry per request")
+    _call("pkv_keep_path", dev, stream, k_cache.data_ptr(), v_cache.data_ptr(), None if new_lens is None else new_lens.data_ptr(),
+          block_tables.data_ptr(), context_lens.data_ptr(), query_start.data_ptr(), path.data_ptr(), path_lens.data_ptr(),
+          b, block_tables.shape[1], path.shape[1], hkv, d, bs, nb)
 
 
 # ---------------------------------------------------------------- accumulated attention weights, eviction

@@ -32,6 +32,8 @@ PKV_DEV_BAD_SLOT = 3
 PKV_DEV_WAIT_TIMEOUT = 4
 PKV_DEV_PREFIX_MISMATCH = 5
 PKV_DEV_SMEM_MISALIGNED = 6
+PKV_DEV_BAD_AXIS = 7
+PKV_DEV_BAD_PATH = 8
 
 PKV_HEAD_DIM = 128
 PKV_DEFAULT_PARTITION = 1024
@@ -44,6 +46,7 @@ PKV_NOALLOC_SCRATCH_BYTES = 16 << 20
 # how rotary frequencies are derived (PKV_ROPE_*)
 ROPE_METHODS = {"none": 0, "linear": 1, "base": 2, "bands": 3, "ramp": 4}
 PKV_MAX_ROPE_HEAD_DIM = 256
+PKV_MAX_ROPE_AXES = 4
 PKV_MAX_EVICT_CONTEXT = 262144
 
 
@@ -124,6 +127,19 @@ SIGNATURES = {
     "pkv_rope": (c_int, [c_void_p, c_int64] * 4 + [c_void_p] * 2 + [c_int] * 6 + [c_float, c_void_p]),
     "pkv_rope_append": (c_int, [c_void_p, c_int64] * 4 + [c_void_p] * 5 + [c_int] * 6 + [c_int64, c_int, c_float,
                                                                                           c_void_p]),
+    "pkv_norm_rope": (c_int, [c_void_p, c_int64] * 4 + [c_void_p] * 2 + [c_int] + [c_void_p] * 3 + [c_float] + [c_int] * 6 +
+                      [c_float, c_void_p]),
+    "pkv_norm_rope_append": (c_int, [c_void_p, c_int64] * 4 + [c_void_p] * 5 + [c_int] + [c_void_p] * 3 + [c_float] +
+                             [c_int] * 6 + [c_int64, c_int, c_float, c_void_p]),
+    "pkv_norm_rope_append_fp8kv": (c_int, [c_void_p, c_int64] * 4 + [c_void_p] * 7 + [c_int] + [c_void_p] * 3 + [c_float] +
+                                   [c_int] * 6 + [c_int64, c_int, c_float, c_void_p]),
+    "pkv_read_blocks_fp8kv": (c_int, [c_void_p] * 2 + [c_int64] + [c_void_p] * 4 + [c_int64] + [c_void_p] * 2 +
+                              [c_int] * 4 + [c_void_p]),
+    "pkv_tree_workspace_size": (c_size_t, [c_int] * 7),
+    "pkv_decode_attention_tree": (c_int, [c_void_p] * 3 + [c_int64] + [c_void_p] * 6 + [c_int] * 9 +
+                                  [c_int64, c_float, c_void_p, c_size_t, c_void_p]),
+    "pkv_tree_masks": (c_int, [c_void_p] * 4 + [c_int] * 4 + [c_void_p]),
+    "pkv_keep_path": (c_int, [c_void_p] * 8 + [c_int] * 6 + [c_int64, c_void_p]),
     "pkv_prefill_workspace_size": (c_size_t, [c_int] * 6),
     "pkv_prefill_attention": (c_int, [c_void_p] * 2 + [c_void_p, c_int64] * 3 + [c_void_p] + [c_int] * 6 +
                               [c_float, c_void_p, c_size_t, c_void_p]),

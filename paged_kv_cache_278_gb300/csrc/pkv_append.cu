@@ -169,6 +169,62 @@ __global__ void __launch_bounds__(kAppendThreads)
     (is_v ? dst_v : dst_k)[d * pieces_per_block + piece] = (is_v ? src_v : src_k)[s * pieces_per_block + piece];
 }
 
+// Blocks read back from the fp8 cache: fp16 row = value(code) x row scale, one rounding.  Memory bound: 132 bytes
+// read and 256 written per row.  A thread takes kReadAhead pieces of 16 codes, their loads in flight together.
+constexpr int kReadAhead = 4;
+constexpr int kReadPerCta = kReadAhead * kAppendThreads;
+
+__global__ void __launch_bounds__(kAppendThreads)
+    read_blocks_fp8kv_kernel(uint4 *__restrict__ dst_k, uint4 *__restrict__ dst_v, int64_t dst_blocks,
+                             const uint4 *__restrict__ k_codes, const float *__restrict__ k_scale,
+                             const uint4 *__restrict__ v_codes, const float *__restrict__ v_scale, int64_t src_blocks,
+                             const int32_t *__restrict__ src, const int32_t *__restrict__ dst, int pieces_per_block, int n) {
+    const bool is_v = blockIdx.y != 0;
+    const uint4 *codes = is_v ? v_codes : k_codes;
+    const float *scale = is_v ? v_scale : k_scale;
+    uint4 *out = is_v ? dst_v : dst_k;
+    const int64_t begin = static_cast<int64_t>(blockIdx.x) * kReadPerCta;  // of the call's pieces
+    const int64_t pair0 = begin / pieces_per_block;
+    const uint32_t rest = static_cast<uint32_t>(begin - pair0 * pieces_per_block) + threadIdx.x;  // (a block has under 2^31 pieces)
+    int64_t to[kReadAhead];
+    uint4 w[kReadAhead];
+    float s[kReadAhead];
+#pragma unroll
+    for (int i = 0; i < kReadAhead; ++i) {
+        const uint32_t at = rest + i * kAppendThreads, skip = at / static_cast<uint32_t>(pieces_per_block);
+        const uint32_t piece = at - skip * static_cast<uint32_t>(pieces_per_block);
+        const int64_t pair = pair0 + skip;
+        to[i] = -1;
+        if (pair >= n) continue;
+        const int32_t from = __ldg(src + pair), into = __ldg(dst + pair);
+        if (from < 0 || from >= src_blocks || into < 0 || into >= dst_blocks) {
+            if (piece == 0 && !is_v) pkv::record_error(&g_append_error, PKV_DEV_BAD_BLOCK_ID);
+            continue;
+        }
+        const int64_t at_src = static_cast<int64_t>(from) * pieces_per_block + piece;
+        to[i] = static_cast<int64_t>(into) * pieces_per_block + piece;
+        w[i] = __ldg(codes + at_src);
+        s[i] = __ldg(scale + (at_src >> 3));  // eight pieces a row
+    }
+#pragma unroll
+    for (int i = 0; i < kReadAhead; ++i) {
+        if (to[i] < 0) continue;
+        const uint32_t c[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+        uint32_t h[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t lo, hi;
+            pkv::e4m3x4_to_h2x2(c[j], lo, hi);
+            const float2 x = pkv::half2_bits_to_float2(lo), y = pkv::half2_bits_to_float2(hi);
+            const __half2 a = __floats2half2_rn(x.x * s[i], x.y * s[i]), b = __floats2half2_rn(y.x * s[i], y.y * s[i]);
+            h[2 * j] = *reinterpret_cast<const uint32_t *>(&a);
+            h[2 * j + 1] = *reinterpret_cast<const uint32_t *>(&b);
+        }
+        out[2 * to[i]] = make_uint4(h[0], h[1], h[2], h[3]);
+        out[2 * to[i] + 1] = make_uint4(h[4], h[5], h[6], h[7]);
+    }
+}
+
 int launch_copy_blocks(void *dst_k, void *dst_v, int64_t dst_blocks, const void *src_k, const void *src_v,
                        int64_t src_blocks, const int32_t *src, const int32_t *dst, int n, int num_kv_heads,
                        int head_dim, int block_size, pkv_stream_t stream) {
@@ -204,6 +260,30 @@ extern "C" PKV_API int pkv_copy_blocks_between(void *dst_k, void *dst_v, int64_t
                                                int block_size, pkv_stream_t stream) {
     return launch_copy_blocks(dst_k, dst_v, dst_num_blocks, src_k, src_v, src_num_blocks, src_ids, dst_ids, n,
                               num_kv_heads, head_dim, block_size, stream);
+}
+
+extern "C" PKV_API int pkv_read_blocks_fp8kv(void *k_cache, void *v_cache, int64_t num_blocks, const void *k_codes,
+                                             const float *k_scale, const void *v_codes, const float *v_scale,
+                                             int64_t src_num_blocks, const int32_t *src_ids, const int32_t *dst_ids, int n,
+                                             int num_kv_heads, int head_dim, int block_size, pkv_stream_t stream) {
+    if (!k_cache || !v_cache || !k_codes || !k_scale || !v_codes || !v_scale || (n > 0 && (!src_ids || !dst_ids)))
+        return PKV_ERR_INVALID_ARG;
+    if (n < 0 || num_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 || num_blocks <= 0 || src_num_blocks <= 0)
+        return PKV_ERR_INVALID_ARG;
+    if (head_dim != PKV_HEAD_DIM) return PKV_ERR_UNSUPPORTED;
+    if (!pkv_internal::aligned16(k_cache) || !pkv_internal::aligned16(v_cache) || !pkv_internal::aligned16(k_codes) ||
+        !pkv_internal::aligned16(v_codes) || !pkv_internal::aligned(k_scale, 4) || !pkv_internal::aligned(v_scale, 4) ||
+        (n > 0 && (!pkv_internal::aligned(src_ids, 4) || !pkv_internal::aligned(dst_ids, 4))))
+        return PKV_ERR_INVALID_ARG;
+    if (n == 0) return PKV_OK;
+    const int64_t pieces = static_cast<int64_t>(num_kv_heads) * block_size * (PKV_HEAD_DIM / 16);
+    if (pieces >= (1LL << 30)) return PKV_ERR_UNSUPPORTED;  // 32-bit positions inside a block
+    const int64_t ctas = (pieces * n + kReadPerCta - 1) / kReadPerCta;
+    if (ctas > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
+    read_blocks_fp8kv_kernel<<<dim3(static_cast<unsigned>(ctas), 2), kAppendThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+        static_cast<uint4 *>(k_cache), static_cast<uint4 *>(v_cache), num_blocks, static_cast<const uint4 *>(k_codes), k_scale,
+        static_cast<const uint4 *>(v_codes), v_scale, src_num_blocks, src_ids, dst_ids, static_cast<int>(pieces), n);
+    return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
 extern "C" PKV_API int pkv_append_int8k(void *k_codes, float *k_scale, void *v_cache, const int64_t *slot_mapping,

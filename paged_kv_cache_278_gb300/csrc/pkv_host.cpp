@@ -241,7 +241,8 @@ PKV_API int pkv_get_device_error(pkv_stream_t stream, int *code) {
     int (*const take[])(int *) = {pkv_internal::append_take_error,  pkv_internal::decode_take_error,
                                   pkv_internal::prefix_take_error,  pkv_internal::rope_take_error,
                                   pkv_internal::weights_take_error, pkv_internal::evict_take_error,
-                                  pkv_internal::prompt_take_error};
+                                  pkv_internal::prompt_take_error,  pkv_internal::norm_rope_take_error,
+                                  pkv_internal::tree_take_error};
     for (auto *take_error : take) {
         int value = 0;
         const int st = take_error(&value);

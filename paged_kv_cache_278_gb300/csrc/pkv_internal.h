@@ -18,6 +18,8 @@ int rope_take_error(int *code);
 int weights_take_error(int *code);
 int evict_take_error(int *code);
 int prompt_take_error(int *code);
+int norm_rope_take_error(int *code);
+int tree_take_error(int *code);
 
 inline size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 

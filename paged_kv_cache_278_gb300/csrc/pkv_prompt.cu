@@ -90,6 +90,9 @@ struct PromptParams {
     float q_scale;                // scale * log2(e)
     const __half *v;   // V as the maps read it: [rows][128], rows v_stride elements apart where packed
     int64_t v_stride;
+    // A tree's call: split counts slots (0: no item is split), their partial results [slot][slot_rows](x 128).
+    const uint32_t *tree_mask;  // [total_q][mask_words]
+    int mask_words, grid, slot_rows;
     CUtensorMap tmap_q, tmap_k, tmap_v;
 };
 
@@ -393,6 +396,142 @@ __device__ Item find_item(const PromptParams &P, int64_t index, int splits, int 
     return it;
 }
 
+// ---- trees of drafted tokens
+// Every row of a request goes over all of its key tiles, so an item (pair of tiles, kv head) is its key tiles in a row,
+// and all items' in a row are cut into one even stretch per CTA: at most two pieces of a CTA are parts of items.
+// A piece that begins an item leaves its part in slot 2 c + 1, one that goes on with an item in slot 2 c; a whole
+// item is written at once.  The stretch counts an item's start and end as kItemUnits tiles beside its own.
+constexpr int kItemUnits = 2;
+constexpr int kLeastUnits = 6;  // of a CTA's stretch
+
+struct TreePlan {
+    int64_t units;
+    int ctas;  // that take part
+};
+
+__device__ __forceinline__ int tree_tiles(const Request &r) { return (r.keys + kTileRows - 1) / kTileRows; }
+__device__ __forceinline__ int tree_pairs(const PromptParams &P, const Request &r) {
+    const int pair_tokens = 2 * kTileRows >> P.group_log2;
+    return (r.tokens + pair_tokens - 1) / pair_tokens;
+}
+__device__ __forceinline__ int64_t tree_units(const PromptParams &P, const Request &r) {
+    return r.tokens > 0 ? static_cast<int64_t>(tree_pairs(P, r)) * P.num_kv_heads * (tree_tiles(r) + kItemUnits) : 0;
+}
+// The units of requests begin .. end - 1 (all lanes get the sum).
+__device__ __forceinline__ int64_t tree_units_of(const PromptParams &P, int begin, int end, int lane, bool report) {
+    long long n = 0;
+    for (int b = begin + lane; b < end; b += 32) n += tree_units(P, request_of(P, b, report));
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) n += __shfl_xor_sync(pkv::kFullMask, n, d);
+    return n;
+}
+__device__ __forceinline__ TreePlan tree_plan(const PromptParams &P, int64_t units) {
+    const int64_t most = units / kLeastUnits;
+    return {units, static_cast<int>(most < 1 ? 1 : (most < P.grid ? most : P.grid))};
+}
+__device__ __forceinline__ int64_t tree_begin(const TreePlan &p, int cta) { return p.units * cta / p.ctas; }
+// The CTA whose stretch holds a unit: the last one that begins at or before it.
+__device__ __forceinline__ int tree_owner(const TreePlan &p, int64_t unit) { return static_cast<int>(((unit + 1) * p.ctas - 1) / p.units); }
+
+// Goes through one CTA's stretch, piece by piece (one warp, the same in all lanes).
+struct TreeWalk {
+    TreePlan plan;
+    int64_t at, end, begin_of_seq, end_of_seq;
+    int seq;
+    Request r;
+
+    __device__ TreeWalk(const PromptParams &P, int lane) {
+        plan = tree_plan(P, tree_units_of(P, 0, P.num_seqs, lane, blockIdx.x == 0));
+        const int cta = blockIdx.x;
+        at = cta < plan.ctas ? tree_begin(plan, cta) : 0;
+        end = cta < plan.ctas ? tree_begin(plan, cta + 1) : 0;
+        seq = -1;
+        begin_of_seq = end_of_seq = 0;
+    }
+    // The request that unit `at` belongs to, from the one behind the present one on.
+    __device__ void seek(const PromptParams &P, int lane) {
+        int64_t before = end_of_seq;
+        for (int b0 = seq + 1; b0 < P.num_seqs; b0 += 32) {
+            long long own = b0 + lane < P.num_seqs ? tree_units(P, request_of(P, b0 + lane, false)) : 0, upto = own;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const long long y = __shfl_up_sync(pkv::kFullMask, upto, d);
+                if (lane >= d) upto += y;
+            }
+            const unsigned past = __ballot_sync(pkv::kFullMask, before + upto > at);
+            if (past) {
+                const int who = __ffs(past) - 1;
+                seq = b0 + who;
+                end_of_seq = before + __shfl_sync(pkv::kFullMask, upto, who);
+                begin_of_seq = end_of_seq - __shfl_sync(pkv::kFullMask, own, who);
+                r = request_of(P, seq, false);
+                return;
+            }
+            before += __shfl_sync(pkv::kFullMask, upto, 31);
+        }
+        at = end;  // (not reached: `at` lies before the call's last unit)
+    }
+    __device__ Item next(const PromptParams &P, int lane) {
+        const int tile_tokens = kTileRows >> P.group_log2;
+        Item it{};
+        it.seq = -1;
+        while (at < end) {
+            if (at >= end_of_seq) {
+                seek(P, lane);
+                continue;
+            }
+            const int tiles = tree_tiles(r), pairs = tree_pairs(P, r), units = tiles + kItemUnits;
+            const int item = static_cast<int>((at - begin_of_seq) / units);
+            const int from = static_cast<int>(at - begin_of_seq - static_cast<int64_t>(item) * units);
+            const int to = static_cast<int>(min(static_cast<int64_t>(units), from + (end - at)));
+            at += to - from;
+            const int first = max(from - kItemUnits, 0);
+            int past = to - kItemUnits;
+            if (P.splits == 0) {  // an item belongs to the CTA of its first tile
+                if (first > 0) continue;
+                past = past > 0 ? tiles : 0;
+            }
+            if (past <= first) continue;
+            it.seq = seq;
+            it.kvh = item / pairs;
+            const int t0 = (item - it.kvh * pairs) * 2 * tile_tokens;
+            const int cta = static_cast<int>(blockIdx.x);
+            it.split = first > 0 ? 2 * cta : (past < tiles ? 2 * cta + 1 : -1);
+            it.row0 = r.start + t0;
+            it.pos0 = r.keys - r.tokens - 1;  // the last position that all rows see
+            it.keys = r.keys;
+            it.kv_first = first;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                it.live[t] = min(max(r.tokens - t0 - t * tile_tokens, 0), tile_tokens);
+                it.kv_count[t] = it.live[t] > 0 ? past - first : 0;
+            }
+            it.shared = it.live[1] == 0;
+            if (it.shared) {
+                it.live[1] = it.live[0];
+                it.kv_count[1] = it.kv_count[0] / 2;
+                it.kv_count[0] -= it.kv_count[1];
+            }
+            return it;
+        }
+        return it;
+    }
+};
+
+// Word `i` of a node's mask: all ones before the tree, nothing behind its last node.
+__device__ __forceinline__ uint32_t tree_word(const uint32_t *mask, int i, int tokens) {
+    if (i < 0) return 0xffffffffu;
+    const int left = tokens - 32 * i;
+    if (left <= 0) return 0u;
+    return __ldg(mask + i) & (left >= 32 ? 0xffffffffu : (1u << left) - 1u);
+}
+// Whether a row of a tree sees nothing at all.
+__device__ __forceinline__ bool tree_blind(const uint32_t *mask, int base, int tokens) {
+    uint32_t any = base > 0;
+    for (int i = 0; i * 32 < tokens; ++i) any |= tree_word(mask, i, tokens);
+    return any == 0;
+}
+
 // V rows of a tile that not every row of the item may see: weights there can be 0, and 0 x inf is NaN.  A group's
 // four warps (`part` 0-3) go over the tile before its weights are delivered: rows past the context become
 // zeros (whatever lies there), and infinities and NaN of cached rows too, with the item marked: its epilogue gives
@@ -436,7 +575,7 @@ __device__ __forceinline__ void clean_values(uint32_t v, int valid, int part, in
 // Key tiles that an item's groups go through: the same ones, or each its own.
 __device__ __forceinline__ int key_tiles(bool shared, int a, int b) { return shared ? a + b : max(a, b); }
 
-template <bool PAGED>
+template <bool PAGED, bool TREE>
 __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_constant__ PromptParams P) {
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t base = pkv::smem_addr(smem);
@@ -510,19 +649,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
         };
         if (warp == kItemWarp) {
             // ---------------------------------------------------------------- work items, up to kItems ahead
-            const int pairs = pairs_from(P, 0, 2 * tile_tokens, lane, blockIdx.x == 0);
-            const int tiles = most_tiles(P, lane);
-            const int splits = split_count(P, pairs, tiles);
-            const uint32_t n_items = static_cast<uint32_t>(pairs) * P.num_kv_heads * splits;  // (bounded by the host)
-            bool ok = true;
-            for (uint32_t k = 0; ok; ++k) {
-                // the rounds go in alternating direction: a CTA's items are not always the longest of their round
-                const uint32_t index = k * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-                Item it{};
-                it.seq = -1;
-                if (index < n_items) it = find_item(P, index, splits, tiles, lane);
+            auto publish = [&](const Item &it, uint32_t k) {
                 const int slot = k % kItems;
-                if (!(ok = wait(kBarItemEmpty + slot, k / kItems + 1))) break;
+                if (!wait(kBarItemEmpty + slot, k / kItems + 1)) return false;
                 if (lane == 0) {
                     volatile int *d = reinterpret_cast<volatile int *>(slots + slot);
                     const int *s = reinterpret_cast<const int *>(&it);
@@ -531,7 +660,25 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                     mbar_arrive(bar(kBarItemFull + slot));
                 }
                 __syncwarp();
-                if (it.seq < 0) break;
+                return it.seq >= 0;
+            };
+            if constexpr (TREE) {
+                TreeWalk walk(P, lane);
+                for (uint32_t k = 0; publish(walk.next(P, lane), k); ++k) {
+                }
+            } else {
+                const int pairs = pairs_from(P, 0, 2 * tile_tokens, lane, blockIdx.x == 0);
+                const int tiles = most_tiles(P, lane);
+                const int splits = split_count(P, pairs, tiles);
+                const uint32_t n_items = static_cast<uint32_t>(pairs) * P.num_kv_heads * splits;  // (bounded by the host)
+                for (uint32_t k = 0;; ++k) {
+                    // the rounds go in alternating direction: a CTA's items are not always the longest of their round
+                    const uint32_t index = k * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+                    Item it{};
+                    it.seq = -1;
+                    if (index < n_items) it = find_item(P, index, splits, tiles, lane);
+                    if (!publish(it, k)) break;
+                }
             }
         } else if (warp == kLoadWarp) {
             // ---------------------------------------------------------------- Q and K
@@ -736,6 +883,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
             if (lane == 0) mbar_arrive(bar(kBarItemEmpty + slot));
             if (seq < 0) break;
             const int pos = tile_pos + min(tok, live - 1);  // rows past the last token: computed like it, never stored
+            // of a tree: the row's mask, the tree's nodes
+            const uint32_t *const row_mask =
+                TREE ? P.tree_mask + (static_cast<int64_t>(slot_row0) + tile * tile_tokens + min(tok, live - 1)) * P.mask_words : nullptr;
+            const int nodes = TREE ? static_cast<int>(i1.w) - pos0 - 1 : 0;
             const int n_kv = key_tiles(shared, n, n_of_other), keys = i1.w;
             float m_ref = -INFINITY, l = 0.f;  // what weights are relative to: kLift below a score, so that they reach 2^kLift
             for (int j = 0; j < n; ++j) {
@@ -748,6 +899,17 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                 const uint32_t vs = v_stage + (shared ? 2 * j + t : j);
                 const uint32_t v = base + PromptSmem::values + (vs % kRing) * kOperand;
                 bool cleaned = !border;
+                uint32_t seen[4];  // of a tree's row: the tile's keys that it sees
+                if (TREE && border) {
+                    const int from = key0 - pos0 - 1;  // the node at the tile's first key
+                    uint32_t lo = tree_word(row_mask, from >> 5, nodes);
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const uint32_t hi = tree_word(row_mask, (from >> 5) + w + 1, nodes);
+                        seen[w] = __funnelshift_r(lo, hi, from & 31);
+                        lo = hi;
+                    }
+                }
 #pragma unroll 1
                 for (int step = 0; step < 2; ++step) {
                     if (step == 1) {
@@ -766,11 +928,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                 tmem_ld64(t_s, s0);
                 tmem_landed(s0);
                 tmem_ld64(t_s + 64, s1);
-                const bool masked = key0 + kTileRows - 1 > tile_pos;  // the causal border, or the context's end
+                const bool masked = TREE ? border : key0 + kTileRows - 1 > tile_pos;  // the causal border, or the context's end
                 const int lim = pos - key0;
                 if (masked) {
 #pragma unroll
-                    for (int c = 0; c < 64; ++c) s0[c] = c <= lim ? s0[c] : 0xff800000u;
+                    for (int c = 0; c < 64; ++c) s0[c] = (TREE ? (seen[c >> 5] >> (c & 31) & 1) != 0 : c <= lim) ? s0[c] : 0xff800000u;
                 }
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -779,7 +941,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                 tmem_landed(s1);
                 if (masked) {
 #pragma unroll
-                    for (int c = 0; c < 64; ++c) s1[c] = 64 + c <= lim ? s1[c] : 0xff800000u;
+                    for (int c = 0; c < 64; ++c)
+                        s1[c] = (TREE ? (seen[2 + (c >> 5)] >> (c & 31) & 1) != 0 : 64 + c <= lim) ? s1[c] : 0xff800000u;
                 }
 #pragma unroll
                 for (int c = 0; c < 64; c += 2)
@@ -852,9 +1015,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                 total = l * w_own + o.y * w_other;
             }
             const int n_other = shared ? n_of_other : 0;
-            // A split may hold none of the row's keys.  A whole row sees one at least, so only scores of minus infinity make its
-            // sum 0: it has no softmax, and becomes NaN here (0 x inf) and in the joining launch alike.
-            const float inv = total == 0.f && split >= 0 ? 0.f : 1.f / total;
+            // A split may hold none of the row's keys.  A whole row sees one at least (but for a tree's blind one, a zero row), so
+            // only scores of minus infinity make its sum 0: it has no softmax, and becomes NaN here (0 x inf) and in the joining
+            // launch alike.
+            const bool nothing = total == 0.f && (split >= 0 || (TREE && tree_blind(row_mask, pos0 + 1, nodes)));
+            const float inv = nothing ? 0.f : 1.f / total;
             w_own *= inv;
             w_other *= inv;
             const int64_t row = q_row * P.num_q_heads + (kvh << glog) + (r & ((1 << glog) - 1));
@@ -864,17 +1029,19 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                 // ^ (x % 8).  Lane's share of a line: piece lane % 8 of rows 4 i + lane / 8.
                 const bool whole = split < 0;
                 const uint32_t lines = base + PromptSmem::staging + warp * 4096, mine = lines + lane * 128;
-                const uint32_t row_bytes = whole ? kDim * 2 : P.splits * kDim * 4;
+                const bool in_slot = TREE && !whole;  // a slot's rows lie one behind another
+                const uint32_t row_bytes = whole ? kDim * 2 : (TREE ? 1 : P.splits) * kDim * 4;
                 const int group_mask = (1 << glog) - 1;
+                const int64_t first_row = in_slot ? static_cast<int64_t>(split) * P.slot_rows + tile * kTileRows
+                                                  : (static_cast<int64_t>(slot_row0) + tile * tile_tokens) * P.num_q_heads + (kvh << glog);
                 unsigned char *const dst = reinterpret_cast<unsigned char *>(whole ? static_cast<void *>(P.out) : static_cast<void *>(P.o_part)) +
-                                           ((static_cast<int64_t>(slot_row0) + tile * tile_tokens) * P.num_q_heads + (kvh << glog)) * row_bytes +
-                                           (whole ? 0 : split * kDim * 4) + (lane & 7) * 16;
+                                           first_row * row_bytes + (whole || TREE ? 0 : split * kDim * 4) + (lane & 7) * 16;
                 uint32_t offset[8];  // of the lane's rows, from the tile's first (under 2^32: 128 tokens' rows)
                 bool keep[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int x = (warp & 3) * 32 + 4 * i + (lane >> 3);
-                    offset[i] = ((x >> glog) * P.num_q_heads + (x & group_mask)) * row_bytes;
+                    offset[i] = (in_slot ? x : (x >> glog) * P.num_q_heads + (x & group_mask)) * row_bytes;
                     keep[i] = (x >> glog) < live;
                 }
                 auto store_line = [&](int line) {
@@ -917,7 +1084,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                     if (dirty[k % kItems] == k + 1) {
                         // Infinities and NaN that were taken out of V: every row that sees their key gets them whole
                         // (an infinity times a weight above 0 is one; a weight that underflowed is taken for one above 0).
-                        for (int key = max(pos0 / kTileRows, first) * kTileRows; key <= pos && key < (first + n_kv) * kTileRows; ++key) {
+                        const int last = TREE ? static_cast<int>(i1.w) - 1 : pos;
+                        for (int key = max(pos0 / kTileRows, first) * kTileRows; key <= last && key < (first + n_kv) * kTileRows; ++key) {
+                            if (TREE && key > pos0 && !(tree_word(row_mask, (key - pos0 - 1) >> 5, nodes) >> ((key - pos0 - 1) & 31) & 1)) continue;
                             const __half *row_v;
                             if (PAGED) {
                                 const int32_t id = __ldg(P.block_tables + static_cast<int64_t>(i0.x) * P.max_blocks + key / P.block_size);
@@ -960,8 +1129,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
             }
             if (store && (t == 0 || !shared)) {
                 if (split >= 0) {
-                    P.m_part[row * P.splits + split] = total == 0.f ? -INFINITY : m;
-                    P.l_part[row * P.splits + split] = total;
+                    const int64_t part = TREE ? static_cast<int64_t>(split) * P.slot_rows + tile * kTileRows + r : row * P.splits + split;
+                    P.m_part[part] = total == 0.f ? -INFINITY : m;
+                    P.l_part[part] = total;
                 } else if (P.lse != nullptr) {
                     P.lse[row] = (m + log2f(total)) * kLn2;
                 }
@@ -1051,6 +1221,64 @@ __global__ void __launch_bounds__(kJoinThreads, BATCH == 8 ? 4 : 2) prompt_join_
         *reinterpret_cast<uint2 *>(P.out + row * kDim + 4 * lane) =
             make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
         if (lane == 0 && P.lse != nullptr) P.lse[row] = (top + log2f(total)) * kLn2;
+    }
+}
+
+// Joins the parts of each (token, head) row of the items that were split: one warp per row, four dims a lane.
+__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_constant__ PromptParams P) {
+    __shared__ int64_t s_units, s_before;
+    const int lane = threadIdx.x & 31;
+    if (threadIdx.x < 32) {
+        const int64_t before = tree_units_of(P, 0, blockIdx.y, lane, false);
+        const int64_t behind = tree_units_of(P, blockIdx.y, P.num_seqs, lane, false);
+        if (lane == 0) {
+            s_units = before + behind;
+            s_before = before;
+        }
+    }
+    __syncthreads();
+    const Request r = request_of(P, blockIdx.y, false);
+    const TreePlan plan = tree_plan(P, s_units);
+    // So far only the call's inputs; the attention launch's parts from here on.
+    pkv::pdl_wait_primary();
+    pkv::pdl_launch_dependents();
+    const int tile_tokens = kTileRows >> P.group_log2, pairs = tree_pairs(P, r), units = tree_tiles(r) + kItemUnits;
+    const int64_t rows = static_cast<int64_t>(r.tokens) * P.num_q_heads;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * (kJoinThreads / 32) + (threadIdx.x >> 5); i < rows;
+         i += static_cast<int64_t>(gridDim.x) * (kJoinThreads / 32)) {
+        const int token = static_cast<int>(i / P.num_q_heads), head = static_cast<int>(i - static_cast<int64_t>(token) * P.num_q_heads);
+        const int pair = token / (2 * tile_tokens), in_pair = token - pair * 2 * tile_tokens;
+        const int64_t begin = s_before + (static_cast<int64_t>(head >> P.group_log2) * pairs + pair) * units;
+        const int c0 = tree_owner(plan, begin + kItemUnits), c1 = tree_owner(plan, begin + units - 1);
+        if (c0 == c1) continue;  // written whole
+        const int row = (in_pair << P.group_log2) + (head & ((1 << P.group_log2) - 1));
+        auto part_of = [&](int c) { return static_cast<int64_t>(c == c0 ? 2 * c + 1 : 2 * c) * P.slot_rows + row; };
+        float top = -INFINITY;
+        for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, __ldcg(P.m_part + part_of(c)));
+#pragma unroll
+        for (int sh = 16; sh >= 1; sh >>= 1) top = fmaxf(top, __shfl_xor_sync(pkv::kFullMask, top, sh));
+        float total = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = c0; c <= c1; ++c) {
+            const int64_t part = part_of(c);
+            const float l = __ldcg(P.l_part + part);
+            if (l == 0.f) continue;  // none of the row's keys
+            const float w = l * exp2f(__ldcg(P.m_part + part) - top);
+            const float4 o = __ldcg(reinterpret_cast<const float4 *>(P.o_part + part * kDim) + lane);
+            total += w;
+            acc.x = fmaf(w, o.x, acc.x);
+            acc.y = fmaf(w, o.y, acc.y);
+            acc.z = fmaf(w, o.z, acc.z);
+            acc.w = fmaf(w, o.w, acc.w);
+        }
+        const int64_t token_row = static_cast<int64_t>(r.start) + token;
+        const bool blind = total == 0.f && tree_blind(P.tree_mask + token_row * P.mask_words, r.keys - r.tokens, r.tokens);
+        const float inv = blind ? 0.f : 1.f / total;
+        const __half2 lo = __floats2half2_rn(acc.x * inv, acc.y * inv), hi = __floats2half2_rn(acc.z * inv, acc.w * inv);
+        const int64_t out_row = token_row * P.num_q_heads + head;
+        *reinterpret_cast<uint2 *>(P.out + out_row * kDim + 4 * lane) =
+            make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+        if (lane == 0 && P.lse != nullptr) P.lse[out_row] = (top + log2f(total)) * kLn2;
     }
 }
 
@@ -1538,6 +1766,56 @@ bool group_ok(int num_q_heads, int num_kv_heads) {
     return g == 1 || g == 2 || g == 4 || g == 8;
 }
 
+// The launch of prompt_kernel's instance on one CTA per SM, or on `most`.
+template <bool PAGED, bool TREE>
+int launch_prompt_kernel(const PromptParams &p, unsigned grid, pkv_stream_t stream) {
+    auto kernel = prompt_kernel<PAGED, TREE>;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
+    static std::atomic<uint64_t> configured{0};  // one bit per device
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(configured.load(std::memory_order_acquire) & bit)) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PromptSmem::total) != cudaSuccess)
+            return PKV_ERR_CUDA;
+        configured.fetch_or(bit, std::memory_order_acq_rel);
+    }
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kPromptThreads);
+    cfg.dynamicSmemBytes = PromptSmem::total;
+    cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+// The joining launch behind it: CTAs of eight rows, all rows of a request in one round or four CTAs per SM.
+template <typename Kernel>
+int launch_join(Kernel kernel, const PromptParams &p, int sms, pkv_stream_t stream) {
+    const int64_t rows = static_cast<int64_t>(p.max_query_len < p.total_q ? p.max_query_len : p.total_q) * p.num_q_heads;
+    const int64_t by_rows = (rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32), by_sms = (4 * sms + p.num_seqs - 1) / p.num_seqs;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(by_rows < by_sms ? by_rows : by_sms), p.num_seqs);
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+int sm_count(int *sms) {
+    int dev = 0;
+    return cudaGetDevice(&dev) == cudaSuccess && cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess
+               ? PKV_OK
+               : PKV_ERR_CUDA;
+}
+
 template <bool PAGED>
 int launch_prompt(PromptParams p, int max_context, void *workspace, size_t workspace_bytes, pkv_stream_t stream) {
     p.splits = plan_splits(p.num_seqs, p.total_q, p.num_q_heads, p.num_kv_heads, max_context);
@@ -1551,39 +1829,35 @@ int launch_prompt(PromptParams p, int max_context, void *workspace, size_t works
         p.m_part = reinterpret_cast<float *>(ws + align256(rows * kDim * sizeof(float)));
         p.l_part = reinterpret_cast<float *>(ws + align256(rows * kDim * sizeof(float)) + align256(rows * sizeof(float)));
     }
-    auto kernel = prompt_kernel<PAGED>;
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return PKV_ERR_CUDA;
-    static std::atomic<uint64_t> configured{0};  // one bit per device
-    const uint64_t bit = 1ull << (dev & 63);
-    if (!(configured.load(std::memory_order_acquire) & bit)) {
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PromptSmem::total) != cudaSuccess)
-            return PKV_ERR_CUDA;
-        configured.fetch_or(bit, std::memory_order_acq_rel);
-    }
+    int sms = 0;
+    if (sm_count(&sms) != PKV_OK) return PKV_ERR_CUDA;
     const int pair_tokens = 2 * kTileRows >> p.group_log2;
     const int64_t most = (static_cast<int64_t>(p.total_q) / pair_tokens + p.num_seqs) * p.num_kv_heads * p.splits;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(most < sms ? most : sms));
-    cfg.blockDim = dim3(kPromptThreads);
-    cfg.dynamicSmemBytes = PromptSmem::total;
-    cfg.stream = reinterpret_cast<cudaStream_t>(stream);
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kernel, p) != cudaSuccess) return PKV_ERR_CUDA;
-    if (p.splits == 1) return PKV_OK;
-    const int64_t rows = static_cast<int64_t>(p.max_query_len < p.total_q ? p.max_query_len : p.total_q) * p.num_q_heads;
-    const int64_t by_rows = (rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32), by_sms = (4 * sms + p.num_seqs - 1) / p.num_seqs;
+    const int st = launch_prompt_kernel<PAGED, false>(p, static_cast<unsigned>(most < sms ? most : sms), stream);
+    if (st != PKV_OK || p.splits == 1) return st;
     const bool many = static_cast<int64_t>(p.total_q) * p.num_q_heads > 2 * sms * (kJoinThreads / 32);
-    cfg.gridDim = dim3(static_cast<unsigned>(by_rows < by_sms ? by_rows : by_sms), p.num_seqs);
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, many ? prompt_join_kernel<8> : prompt_join_kernel<16>, p) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+    return launch_join(many ? prompt_join_kernel<8> : prompt_join_kernel<16>, p, sms, stream);
+}
+
+// A tree's call: the CTAs that take part (with their two slots each) at most, and the rows of a slot.  0 slots: no item
+// is split, as none has more key tiles than a joining launch is worth.
+struct TreeSizes {
+    int ctas, slot_rows;
+    bool split;
+};
+constexpr int kWholeTiles = 4;
+TreeSizes tree_sizes(int num_seqs, int total_q, int max_query_len, int num_q_heads, int num_kv_heads, int64_t max_context) {
+    const int tile_tokens = kTileRows / (num_q_heads / num_kv_heads);
+    const int64_t tiles = (max_context + kTileRows - 1) / kTileRows;
+    const int64_t pairs = static_cast<int64_t>(total_q) / (2 * tile_tokens) + num_seqs;
+    const bool split = tiles > kWholeTiles;
+    const int64_t most = pairs * num_kv_heads * (split ? tiles : 1);
+    return {static_cast<int>(most < kPlannedSms ? most : kPlannedSms), max_query_len > tile_tokens ? 2 * kTileRows : kTileRows, split};
+}
+size_t tree_workspace(const TreeSizes &t) {
+    if (!t.split) return 0;
+    const size_t rows = static_cast<size_t>(2 * t.ctas) * t.slot_rows;
+    return rows * (kDim + 2) * sizeof(float);
 }
 
 int log2_of(int g) { return g == 1 ? 0 : (g == 2 ? 1 : (g == 4 ? 2 : 3)); }
@@ -1606,6 +1880,51 @@ int check_prompt(const float *lse, const void *q, int64_t q_stride, const int32_
         return PKV_ERR_INVALID_ARG;
     if (q_stride % 8 != 0 || q_stride < static_cast<int64_t>(num_q_heads) * head_dim) return PKV_ERR_INVALID_ARG;
     return PKV_OK;
+}
+
+// What the calls over a paged cache check and hand to the kernel; PKV_OK with *done set when there is nothing to do.
+int paged_params(PromptParams *params, void *out, float *lse, const void *q, int64_t q_stride, const void *k_cache,
+                 const void *v_cache, const int32_t *block_tables, const int32_t *context_lens, const int32_t *query_start,
+                 int num_seqs, int total_q, int max_query_len, int max_blocks_per_seq, int num_q_heads, int num_kv_heads,
+                 int head_dim, int block_size, int64_t num_blocks, float scale, bool *done) {
+    int st = pkv_internal::check_decode_args(q, k_cache, v_cache, block_tables, context_lens, num_seqs, max_blocks_per_seq,
+                                             num_q_heads, num_kv_heads, head_dim, block_size, num_blocks);
+    if (st != PKV_OK) return st;
+    st = check_prompt(lse, q, q_stride, query_start, num_seqs, total_q, max_query_len, num_q_heads, num_kv_heads, head_dim,
+                      scale, done);
+    if (st != PKV_OK || *done) return st;
+    if (!out || !pkv_internal::aligned16(out)) return PKV_ERR_INVALID_ARG;
+    const int64_t rows = num_blocks * num_kv_heads * block_size;
+    if (rows >= 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;  // box row coordinates are signed 32-bit
+    if (static_cast<int64_t>(max_blocks_per_seq) * block_size > kMaxContext) return PKV_ERR_UNSUPPORTED;
+    PromptParams &p = *params;
+    p.out = static_cast<__half *>(out);
+    p.lse = lse;
+    p.v = static_cast<const __half *>(v_cache);
+    p.query_start = query_start;
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.num_seqs = num_seqs;
+    p.total_q = total_q;
+    p.max_query_len = max_query_len;
+    p.max_blocks = max_blocks_per_seq;
+    p.num_q_heads = num_q_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.block_size = block_size;
+    p.num_blocks = num_blocks;
+    p.group_log2 = log2_of(num_q_heads / num_kv_heads);
+    p.q_scale = scale * kLog2e;
+    p.box_rows = kTileRows;
+    while (block_size % p.box_rows != 0) p.box_rows /= 2;  // a box never leaves its block: 16 at least
+    return PKV_OK;
+}
+
+int encode_paged(PromptParams *p, const void *q, int64_t q_stride, const void *k_cache, const void *v_cache) {
+    const int64_t rows = p->num_blocks * p->num_kv_heads * p->block_size;
+    int st = encode_query(&p->tmap_q, q, q_stride, p->total_q, p->num_q_heads, p->num_q_heads / p->num_kv_heads);
+    if (st == PKV_OK) st = encode_rows(&p->tmap_k, k_cache, rows, kDim, kDim, p->box_rows);
+    if (st == PKV_OK) st = encode_rows(&p->tmap_v, v_cache, rows, kDim, kDim, p->box_rows);
+    return st;
 }
 
 }  // namespace
@@ -1659,42 +1978,63 @@ extern "C" PKV_API int pkv_prefill_attention_paged(void *out, float *lse, const 
                                                    int num_kv_heads, int head_dim, int block_size, int64_t num_blocks,
                                                    float scale, void *workspace, size_t workspace_bytes,
                                                    pkv_stream_t stream) {
-    int st = pkv_internal::check_decode_args(q, k_cache, v_cache, block_tables, context_lens, num_seqs, max_blocks_per_seq,
-                                             num_q_heads, num_kv_heads, head_dim, block_size, num_blocks);
-    if (st != PKV_OK) return st;
-    bool done = false;
-    st = check_prompt(lse, q, q_stride, query_start, num_seqs, total_q, max_query_len, num_q_heads, num_kv_heads, head_dim,
-                      scale, &done);
-    if (st != PKV_OK || done) return st;
-    if (!out || !pkv_internal::aligned16(out)) return PKV_ERR_INVALID_ARG;
-    const int64_t rows = num_blocks * num_kv_heads * block_size;
-    if (rows >= 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;  // box row coordinates are signed 32-bit
-    if (static_cast<int64_t>(max_blocks_per_seq) * block_size > kMaxContext) return PKV_ERR_UNSUPPORTED;
     PromptParams p{};
-    p.out = static_cast<__half *>(out);
-    p.lse = lse;
-    p.v = static_cast<const __half *>(v_cache);
-    p.query_start = query_start;
-    p.block_tables = block_tables;
-    p.context_lens = context_lens;
-    p.num_seqs = num_seqs;
-    p.total_q = total_q;
-    p.max_query_len = max_query_len;
-    p.max_blocks = max_blocks_per_seq;
-    p.num_q_heads = num_q_heads;
-    p.num_kv_heads = num_kv_heads;
-    p.block_size = block_size;
-    p.num_blocks = num_blocks;
-    p.group_log2 = log2_of(num_q_heads / num_kv_heads);
-    p.q_scale = scale * kLog2e;
-    p.box_rows = kTileRows;
-    while (block_size % p.box_rows != 0) p.box_rows /= 2;  // a box never leaves its block: 16 at least
-    st = encode_query(&p.tmap_q, q, q_stride, total_q, num_q_heads, num_q_heads / num_kv_heads);
-    if (st == PKV_OK) st = encode_rows(&p.tmap_k, k_cache, rows, kDim, kDim, p.box_rows);
-    if (st == PKV_OK) st = encode_rows(&p.tmap_v, v_cache, rows, kDim, kDim, p.box_rows);
+    bool done = false;
+    int st = paged_params(&p, out, lse, q, q_stride, k_cache, v_cache, block_tables, context_lens, query_start, num_seqs, total_q,
+                                max_query_len, max_blocks_per_seq, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, scale,
+                                &done);
+    if (st != PKV_OK || done) return st;
+    st = encode_paged(&p, q, q_stride, k_cache, v_cache);
     if (st != PKV_OK) return st;
     return launch_prompt<true>(p, static_cast<int>(static_cast<int64_t>(max_blocks_per_seq) * block_size), workspace, workspace_bytes,
                                stream);
+}
+
+extern "C" PKV_API size_t pkv_tree_workspace_size(int num_seqs, int total_q, int max_query_len, int num_q_heads,
+                                                  int num_kv_heads, int head_dim, int max_context) {
+    if (num_seqs <= 0 || total_q <= 0 || max_query_len <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 ||
+        num_q_heads % num_kv_heads != 0 || head_dim != kDim || max_context <= 0 || !group_ok(num_q_heads, num_kv_heads))
+        return 0;
+    return tree_workspace(tree_sizes(num_seqs, total_q, max_query_len, num_q_heads, num_kv_heads, max_context));
+}
+
+extern "C" PKV_API int pkv_decode_attention_tree(void *out, float *lse, const void *q, int64_t q_stride, const void *k_cache,
+                                                 const void *v_cache, const int32_t *block_tables,
+                                                 const int32_t *context_lens, const int32_t *query_start,
+                                                 const int32_t *tree_mask, int mask_words, int num_seqs, int total_q,
+                                                 int max_query_len, int max_blocks_per_seq, int num_q_heads,
+                                                 int num_kv_heads, int head_dim, int block_size, int64_t num_blocks,
+                                                 float scale, void *workspace, size_t workspace_bytes, pkv_stream_t stream) {
+    PromptParams p{};
+    bool done = false;
+    int st = paged_params(&p, out, lse, q, q_stride, k_cache, v_cache, block_tables, context_lens, query_start, num_seqs, total_q,
+                          max_query_len, max_blocks_per_seq, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, scale, &done);
+    if (st != PKV_OK) return st;
+    if (max_query_len > PKV_MAX_QUERY_LEN) return PKV_ERR_UNSUPPORTED;
+    if (mask_words < 0 || static_cast<int64_t>(mask_words) * 32 < max_query_len) return PKV_ERR_INVALID_ARG;
+    if (done) return PKV_OK;
+    if (!tree_mask || !pkv_internal::aligned(tree_mask, 4)) return PKV_ERR_INVALID_ARG;
+    const TreeSizes sizes = tree_sizes(num_seqs, total_q, max_query_len, num_q_heads, num_kv_heads,
+                                       static_cast<int64_t>(max_blocks_per_seq) * block_size);
+    if (sizes.split) {
+        if (!workspace || workspace_bytes < tree_workspace(sizes) || !pkv_internal::aligned(workspace, 256)) return PKV_ERR_WORKSPACE;
+        const size_t rows = static_cast<size_t>(2 * sizes.ctas) * sizes.slot_rows;
+        p.o_part = static_cast<float *>(workspace);
+        p.m_part = p.o_part + rows * kDim;
+        p.l_part = p.m_part + rows;
+    }
+    p.tree_mask = reinterpret_cast<const uint32_t *>(tree_mask);
+    p.mask_words = mask_words;
+    p.slot_rows = sizes.slot_rows;
+    p.splits = sizes.split ? 2 * sizes.ctas : 0;
+    st = encode_paged(&p, q, q_stride, k_cache, v_cache);
+    if (st != PKV_OK) return st;
+    int sms = 0;
+    if (sm_count(&sms) != PKV_OK) return PKV_ERR_CUDA;
+    p.grid = sizes.ctas < sms ? sizes.ctas : sms;
+    st = launch_prompt_kernel<true, true>(p, static_cast<unsigned>(p.grid), stream);
+    if (st != PKV_OK || !sizes.split) return st;
+    return launch_join(tree_join_kernel, p, sms, stream);
 }
 
 extern "C" PKV_API int pkv_prefill_attention_weights(float *scores, int64_t score_capacity, const void *q, int64_t q_stride,
