@@ -15,10 +15,16 @@
 //
 // A row's 16-element units lie in LANES neighbouring lanes of a warp (8 for heads of 128 dims), so that a row's
 // sums are log2(LANES) shuffles and a lane keeps one unit for all the rows it meets: its eight (cos, sin) pairs
-// stay in registers.  A unit is 32 bytes (two 16-byte pieces): pieces c and c + rotary_dim / 16 hold both
-// halves of eight half-layout pairs, two neighbouring pieces eight interleaved pairs.  One CTA takes one token
-// (and, when tokens are few, a slice of its rows): the first rows' loads are in flight while rotary_dim / 2 of
-// its threads compute the angles once for all heads.
+// and its weights stay in registers.  A unit is 32 bytes (two 16-byte pieces): pieces c and c + rotary_dim / 16 hold
+// both halves of eight half-layout pairs, two neighbouring pieces eight interleaved pairs.  The lanes compute a token's
+// angles, one or two sincospi each, and share them by shuffles.
+//
+// A pass is 32 / LANES rows of one kind (q, k or v) of one token; up to kBatch passes of a kind are a batch.  Each warp has an even
+// stretch of the call's batches and a ring of kStages batches of shared memory, which bulk copies fill ahead of it: what
+// is in flight costs no registers.  Two passes are worked on at a time: with 16 warps on an SM it is the chains of
+// dependent instructions that the kernel waits for, more than memory (8192 tokens of 48 rows, three axes: 37 us, 39 one
+// pass at a time, 41 with a warp per batch that loads into registers, 47 with a CTA per token; 29.7 at the rate of a
+// plain copy).  With few tokens a warp takes one pass straight from global memory: one round of loads on many SMs.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -33,8 +39,16 @@ namespace {
 __device__ int g_norm_error;
 
 constexpr int kNormThreads = 128;
-constexpr int kNormAhead = 3;  // rows a lane keeps in flight: 48 rows of 128 dims per CTA
+constexpr int kNormWarps = kNormThreads / 32;
+constexpr int kBatch = 4;    // passes: 16 rows of 128 dims
+constexpr int kStages = 2;
+constexpr int kBatchBytes = kBatch * 32 * 32;  // a lane's unit is 32 bytes
 constexpr int kMaxHeadDim = PKV_MAX_ROPE_HEAD_DIM;
+// Up to one pass for each of the warps that 152 SMs hold of the other kernel, a warp takes one pass straight from global
+// memory (48 rows a token, in a graph: 64 tokens 2.6 us so and 3.4 from the ring, 150 tokens 2.8 and 3.4, 300 tokens
+// 4.0 and 3.9, 600 tokens 5.9 and 4.5).
+constexpr int kFewPasses = 152 * 16;
+constexpr int kNormCtas = 4;  // per SM
 
 struct NormParams {
     uint4 *q_out;
@@ -53,191 +67,487 @@ struct NormParams {
     int num_q_heads, num_kv_heads, head_dim, rotary_dim, block_size, num_axes;
     int interleaved;
     float magnitude, eps, inv_dim;
-    int rows_per_cta;
+    int num_tokens, q_passes, k_passes, passes;  // of a token: passes of q rows, of k rows, of all
+    int batches;                                 // of a token
 };
 
-__device__ __forceinline__ void unpack(const uint4 &p, float *x) {
+// Two float32 in a register pair, and arithmetic on both at once, each lane rounded as the scalar form.
+using Pair = uint64_t;
+__device__ __forceinline__ Pair pair(float lo, float hi) {
+    Pair d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
+__device__ __forceinline__ float2 halves(Pair p) {
+    float2 d;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(p));
+    return d;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+    Pair d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+    Pair d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ Pair twice(float x) { return pair(x, x); }
+
+__device__ __forceinline__ void unpack(const uint4 &p, Pair (&x)[8], int from) {
     const uint32_t w[4] = {p.x, p.y, p.z, p.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float2 f = pkv::half2_bits_to_float2(w[i]);
-        x[2 * i] = f.x;
-        x[2 * i + 1] = f.y;
+        x[from + i] = pair(f.x, f.y);
     }
 }
-__device__ __forceinline__ uint4 pack(const float *x) {
+__device__ __forceinline__ uint4 pack(const Pair (&x)[8], int from) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+        const float2 f = halves(x[from + i]);
+        const __half2 h = __floats2half2_rn(f.x, f.y);
         w[i] = *reinterpret_cast<const uint32_t *>(&h);
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
-__device__ __forceinline__ uint2 pack_e4m3(const float *x, float s) {
-    return make_uint2(pkv::quantize_e4m3x2(x[0], x[1], s) | (pkv::quantize_e4m3x2(x[2], x[3], s) << 16),
-                      pkv::quantize_e4m3x2(x[4], x[5], s) | (pkv::quantize_e4m3x2(x[6], x[7], s) << 16));
+
+// E4M3 codes of a row's unit for the row scale s = max|x| / 448, as pkv::quantize_e4m3x2 gives them.  The quotient is the
+// IEEE one: with r the reciprocal of s rounded to nearest, x r corrected once by its remainder over s is the
+// correctly rounded x / s (P. Markstein, "Computation of elementary functions on the IBM RISC System/6000
+// processor", 1990) where nothing leaves the normal range, and nothing does for quotients of 2^-11 to 448 (smaller
+// ones have code 0 either way) with s in [2^-90, 2^100]: other scales are brought there, with x, by a power of two.
+// Three packed operations for two quotients, where the division takes some twenty.
+struct Quantiser {
+    Pair r, minus_s;
+    bool zero;
+
+    __device__ __forceinline__ Quantiser(float s, Pair (&x)[8]) : zero(s == 0.f) {
+        if (s < 0x1p-90f || s > 0x1p100f) {
+            const float k = s < 1.f ? 0x1p100f : 0x1p-60f;
+            s *= k;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = mul2(x[e], twice(k));
+        }
+        r = twice(__frcp_rn(s));
+        minus_s = twice(s == INFINITY ? 0.f : -s);  // (of an infinite scale x r is the quotient: 0, or NaN of an infinity)
+    }
+    __device__ __forceinline__ uint2 codes(const Pair (&x)[8], int from) const {
+        uint32_t c[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const Pair q0 = mul2(x[from + i], r);
+            const float2 q = halves(fma2(fma2(q0, minus_s, x[from + i]), r, q0));
+            uint16_t h;
+            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(q.y), "f"(q.x));
+            c[i] = h;
+        }
+        return zero ? make_uint2(0u, 0u) : make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+    }
+};
+
+__device__ __forceinline__ uint4 lds128_now(uint32_t addr) {  // ordered behind the barrier that published it
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
 }
 
-template <int LANES, bool FP8>
-__global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const __grid_constant__ NormParams P) {
-    constexpr int kRows = kNormThreads / LANES;  // rows of one pass
-    // (cos, sin) of pair i = 8 u + 2 j + e at float4 j * LANES + u, weights of element 4 j + e of unit u likewise:
-    // a row's lanes read neighbouring float4s.
-    __shared__ float4 s_cs[4 * LANES], s_weight[2][4 * LANES];
-    pkv::pdl_wait_primary();  // by every thread: the next kernel may rely on it
-    pkv::pdl_launch_dependents();
-    const int64_t t = blockIdx.x;
-    const int units = P.head_dim / 16, r16 = P.rotary_dim / 16;
-    const int u = threadIdx.x % LANES;
-    const bool in_row = u < units;
-    const int begin = blockIdx.y * P.rows_per_cta;
-    const int rows = P.num_q_heads + P.num_kv_heads + (P.v ? P.num_kv_heads : 0);
-    const int end = min(rows, begin + P.rows_per_cta);
+// One warp's view of a token at a time.  Kinds of rows: 0 q, 1 k, 2 v.
+template <int LANES, bool FP8, bool INTERLEAVED>
+struct RowWarp {
+    static constexpr int kRows = 32 / LANES;                     // rows of one pass
+    static constexpr int kShare = kRows >= 8 ? 1 : 8 / kRows;    // of a unit's eight pairs: angles a lane computes
+    const NormParams &P;
+    int lane, u, g, units, half0, half1;
+    bool turns;
+    int64_t t, slot, next_slot, cache_row;
+    // of the angles this lane computes
+    int axis[kShare], next_position[kShare];
+    uint64_t frequency[kShare];
+    Pair co[INTERLEAVED ? 8 : 4], si[INTERLEAVED ? 8 : 4], back[INTERLEAVED ? 1 : 4];  // as rotate takes them
 
-    int64_t slot = -1, cache_row = 0;
-    if (P.v) {
-        slot = __ldg(P.slot_mapping + t);
-        if (slot >= P.num_slots) {
-            if (threadIdx.x == 0 && blockIdx.y == 0) pkv::record_error(&g_norm_error, PKV_DEV_BAD_SLOT);
+    __device__ __forceinline__ explicit RowWarp(const NormParams &params) : P(params), t(-1), slot(-1), next_slot(-1), cache_row(0) {
+        lane = threadIdx.x & 31;
+        u = lane % LANES;
+        g = lane / LANES;
+        units = P.head_dim / 16;
+        const int r16 = P.rotary_dim / 16;
+        turns = u < r16;
+        half0 = turns && !INTERLEAVED ? u : 2 * u;
+        half1 = turns && !INTERLEAVED ? u + r16 : 2 * u + 1;
+    }
+    // The axes and frequencies of the angles this lane computes.
+    __device__ __forceinline__ void load_axes() {
+#pragma unroll
+        for (int e = 0; e < kShare; ++e) {
+            const int i = 8 * u + g * kShare + e;
+            if (!turns || g * kShare >= 8) continue;
+            axis[e] = P.axes ? __ldg(P.axes + i) : 0;
+            if (axis[e] < 0 || axis[e] >= P.num_axes) {
+                pkv::record_error(&g_norm_error, PKV_DEV_BAD_AXIS);
+                axis[e] = 0;
+            }
+            frequency[e] = static_cast<uint64_t>(__ldg(P.frequencies + i));
+        }
+    }
+    __device__ __forceinline__ int heads_of(int kind) const { return kind == 0 ? P.num_q_heads : P.num_kv_heads; }
+    __device__ __forceinline__ const uint4 *rows_of(int kind, int64_t token) const {
+        return kind == 0 ? P.q + token * P.q_stride : (kind == 1 ? P.k + token * P.k_stride : P.v + token * P.v_stride);
+    }
+    // The lane's two pieces of a row of this kind.
+    __device__ __forceinline__ int piece0(int kind) const { return kind == 2 ? 2 * u : half0; }
+    __device__ __forceinline__ int piece1(int kind) const { return kind == 2 ? 2 * u + 1 : half1; }
+
+    // What begin() needs of a token, on its way.
+    __device__ __forceinline__ void fetch(int64_t token) {
+#pragma unroll
+        for (int e = 0; e < kShare; ++e)
+            if (turns && g * kShare < 8) next_position[e] = __ldg(P.positions + token * P.num_axes + axis[e]);
+        if (P.v) next_slot = __ldg(P.slot_mapping + token);
+    }
+    // The fetched token's slot and angles.
+    __device__ __forceinline__ void begin(int64_t token) {
+        t = token;
+        slot = next_slot;
+        if (P.v && slot >= P.num_slots) {
+            if (lane == 0) pkv::record_error(&g_norm_error, PKV_DEV_BAD_SLOT);
             slot = -1;
         }
-        if (slot >= 0) {
-            const int64_t block = slot / P.block_size;
+        float2 own[kShare];
+#pragma unroll
+        for (int e = 0; e < kShare; ++e) {
+            own[e] = make_float2(0.f, 0.f);
+            if (!turns || g * kShare >= 8) continue;
+            const uint64_t phase = static_cast<uint64_t>(static_cast<int64_t>(next_position[e])) * frequency[e] + (1ull << 31);
+            const float x = static_cast<float>(static_cast<int32_t>(phase >> 32)) * (1.f / 2147483648.f);
+            float s, c;
+            sincospif(x, &s, &c);
+            own[e] = make_float2(c * P.magnitude, s * P.magnitude);
+        }
+        float c[8], s[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int from = (j / kShare) * LANES + u;
+            c[j] = __shfl_sync(pkv::kFullMask, own[j % kShare].x, from);
+            s[j] = __shfl_sync(pkv::kFullMask, own[j % kShare].y, from);
+        }
+        if constexpr (INTERLEAVED) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                co[j] = twice(c[j]);
+                si[j] = pair(-s[j], s[j]);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                co[j] = pair(c[2 * j], c[2 * j + 1]);
+                si[j] = pair(s[2 * j], s[2 * j + 1]);
+                back[j] = pair(-s[2 * j], -s[2 * j + 1]);
+            }
+        }
+        if (P.v && slot >= 0) {
+            const int64_t block = slot < 0x7fffffff ? static_cast<int>(slot) / P.block_size : slot / P.block_size;
             cache_row = block * P.num_kv_heads * P.block_size + (slot - block * P.block_size);
         }
     }
-    // Row `row` of the token: 0 q, 1 k, 2 v.
-    auto kind_of = [&](int row) { return row < P.num_q_heads ? 0 : (row < P.num_q_heads + P.num_kv_heads ? 1 : 2); };
-    auto live = [&](int row) { return in_row && row < end && (kind_of(row) == 0 || !P.v || slot >= 0); };
-    // The two pieces of the lane's unit, in its row.
-    auto first_of = [&](int kind) { return kind < 2 && u < r16 && !P.interleaved ? u : 2 * u; };
-    auto second_of = [&](int kind) { return kind < 2 && u < r16 && !P.interleaved ? u + r16 : 2 * u + 1; };
-    uint4 a[kNormAhead], b[kNormAhead];
-    auto fetch = [&](int base) {
+
+    // (a, b) -> (a c - b s, b c + a s) for the unit's pairs.
+    __device__ __forceinline__ void rotate(Pair (&x)[8]) const {
+        if constexpr (INTERLEAVED) {
 #pragma unroll
-        for (int i = 0; i < kNormAhead; ++i) {
-            const int row = base + i * kRows;
-            a[i] = b[i] = make_uint4(0, 0, 0, 0);
-            if (!live(row)) continue;
-            const int kind = kind_of(row);
-            const uint4 *src = kind == 0   ? P.q + t * P.q_stride + static_cast<int64_t>(row) * (2 * units)
-                               : kind == 1 ? P.k + t * P.k_stride + static_cast<int64_t>(row - P.num_q_heads) * (2 * units)
-                                           : P.v + t * P.v_stride + static_cast<int64_t>(row - P.num_q_heads - P.num_kv_heads) * (2 * units);
-            a[i] = src[first_of(kind)];
-            b[i] = src[second_of(kind)];
+            for (int j = 0; j < 8; ++j) {
+                const float2 f = halves(x[j]);
+                x[j] = fma2(x[j], co[j], mul2(pair(f.y, f.x), si[j]));
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const Pair lo = x[j], hi = x[4 + j];
+                x[j] = fma2(lo, co[j], mul2(hi, back[j]));
+                x[4 + j] = fma2(hi, co[j], mul2(lo, si[j]));
+            }
+        }
+    }
+
+    // Passes of one kind: rows head0 + g, head0 + g + kRows, ... of the token's `count` passes, N at a time for
+    // their chains to overlap.  `source` gives a pass's pieces (zeros where a row or the lane's unit is none), `weights`
+    // the unit's four float4s as they lie in its pieces.
+    template <int KIND, int N, typename Source, typename Weights>
+    __device__ __forceinline__ void run(int head0, int count, const Source &source, const Weights &weights) {
+        const int heads = heads_of(KIND), pieces = 2 * units;
+        const bool normed = KIND == 0 ? P.q_weight != nullptr : (KIND == 1 && P.k_weight != nullptr);
+        const bool goes = u < units && (KIND == 0 || !P.v || slot >= 0);
+        int head = head0 + g;
+        // where the first row goes, and what lies between passes
+        int64_t step = static_cast<int64_t>(kRows) * pieces, row = 0;
+        uint4 *dst = nullptr;
+        if (KIND == 0) {
+            dst = P.q_out + t * P.q_out_stride + head * pieces;
+        } else if (!P.v) {
+            dst = P.k_out + t * P.k_out_stride + head * pieces;
+        } else {
+            row = cache_row + static_cast<int64_t>(head) * P.block_size;
+            step *= P.block_size;
+            if (!FP8) dst = P.k_cache + row * pieces;
+        }
+        uint2 *codes = FP8 && KIND > 0 ? (KIND == 1 ? P.k_codes : P.v_codes) + row * pieces : nullptr;
+        float *scale = FP8 && KIND > 0 ? (KIND == 1 ? P.k_scale : P.v_scale) + row : nullptr;
+        const int64_t scale_step = static_cast<int64_t>(kRows) * P.block_size;
+        const int at0 = piece0(KIND), at1 = piece1(KIND);
+#pragma unroll 1
+        for (int i = 0; i < count; i += N, head += N * kRows) {
+            uint4 raw[N][2];
+            bool writes[N];
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                const bool there = u < units && head + n * kRows < heads && i + n < count;
+                writes[n] = goes && there;
+                source(i + n, there, at0, at1, raw[n][0], raw[n][1]);
+            }
+            Pair x[N][8];
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                unpack(raw[n][0], x[n], 0);
+                unpack(raw[n][1], x[n], 4);
+            }
+            if constexpr (KIND < 2) {
+                if (normed) {
+                    float square[N];
+#pragma unroll
+                    for (int n = 0; n < N; ++n) {
+                        Pair sum = mul2(x[n][0], x[n][0]), sum1 = mul2(x[n][1], x[n][1]);
+#pragma unroll
+                        for (int e = 2; e < 8; e += 2) {
+                            sum = fma2(x[n][e], x[n][e], sum);
+                            sum1 = fma2(x[n][e + 1], x[n][e + 1], sum1);
+                        }
+                        const float2 p = halves(sum), q = halves(sum1);
+                        square[n] = (p.x + p.y) + (q.x + q.y);
+                    }
+#pragma unroll
+                    for (int d = LANES / 2; d >= 1; d >>= 1)
+#pragma unroll
+                        for (int n = 0; n < N; ++n) square[n] += __shfl_xor_sync(pkv::kFullMask, square[n], d);
+#pragma unroll
+                    for (int n = 0; n < N; ++n) {
+                        const Pair r = twice(rsqrtf(fmaf(square[n], P.inv_dim, P.eps)));
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) x[n][e] = mul2(x[n][e], r);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float4 f = weights(j);
+#pragma unroll
+                        for (int n = 0; n < N; ++n) {
+                            x[n][2 * j] = mul2(x[n][2 * j], pair(f.x, f.y));
+                            x[n][2 * j + 1] = mul2(x[n][2 * j + 1], pair(f.z, f.w));
+                        }
+                    }
+                }
+                if (turns) {
+#pragma unroll
+                    for (int n = 0; n < N; ++n) rotate(x[n]);
+                }
+            }
+            if constexpr (FP8 && KIND > 0) {
+                float most[N];
+#pragma unroll
+                for (int n = 0; n < N; ++n) {
+                    most[n] = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float2 f = halves(x[n][e]);
+                        most[n] = fmaxf(most[n], fmaxf(fabsf(f.x), fabsf(f.y)));
+                    }
+                }
+#pragma unroll
+                for (int d = LANES / 2; d >= 1; d >>= 1)
+#pragma unroll
+                    for (int n = 0; n < N; ++n) most[n] = fmaxf(most[n], __shfl_xor_sync(pkv::kFullMask, most[n], d));
+#pragma unroll
+                for (int n = 0; n < N; ++n) {
+                    if (writes[n]) {
+                        const float s = __fdiv_rn(most[n], 448.f);
+                        const Quantiser quantiser(s, x[n]);
+                        codes[at0] = quantiser.codes(x[n], 0);
+                        codes[at1] = quantiser.codes(x[n], 4);
+                        if (u == 0) *scale = s;
+                    }
+                    codes += step;
+                    scale += scale_step;
+                }
+            } else {
+#pragma unroll
+                for (int n = 0; n < N; ++n) {
+                    if (writes[n]) {
+                        dst[at0] = pack(x[n], 0);
+                        dst[at1] = pack(x[n], 4);
+                    }
+                    dst += step;
+                }
+            }
+        }
+    }
+    // The same of v into the fp16 cache: its rows as they are.
+    template <int N, typename Source>
+    __device__ __forceinline__ void copy(int head0, int count, const Source &source) {
+        const bool goes = u < units && slot >= 0;
+        int head = head0 + g;
+        const int64_t step = static_cast<int64_t>(kRows) * P.block_size * (2 * units);
+        uint4 *dst = P.v_cache + (cache_row + static_cast<int64_t>(head) * P.block_size) * (2 * units) + 2 * u;
+#pragma unroll 1
+        for (int i = 0; i < count; i += N, head += N * kRows) {
+            uint4 raw[N][2];
+            bool there[N];
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                there[n] = u < units && head + n * kRows < P.num_kv_heads && i + n < count;
+                source(i + n, there[n], 2 * u, 2 * u + 1, raw[n][0], raw[n][1]);
+            }
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                if (goes && there[n]) {
+                    dst[0] = raw[n][0];
+                    dst[1] = raw[n][1];
+                }
+                dst += step;
+            }
+        }
+    }
+    template <int N, typename Source, typename Weights>
+    __device__ __forceinline__ void run_kind(int kind, int head0, int count, const Source &source, const Weights &weights) {
+        if (kind == 0)
+            run<0, N>(head0, count, source, weights);
+        else if (kind == 1)
+            run<1, N>(head0, count, source, weights);
+        else if constexpr (FP8)
+            run<2, N>(head0, count, source, weights);
+        else
+            copy<N>(head0, count, source);
+    }
+};
+
+// One pass a warp, straight from global memory.
+template <int LANES, bool FP8, bool INTERLEAVED>
+__global__ void __launch_bounds__(kNormThreads) norm_rope_few_kernel(const __grid_constant__ NormParams P) {
+    pkv::pdl_wait_primary();  // by every thread: the next kernel may rely on it
+    pkv::pdl_launch_dependents();
+    RowWarp<LANES, FP8, INTERLEAVED> rows(P);
+    const int at = blockIdx.x * kNormWarps + threadIdx.x / 32;
+    if (at >= P.num_tokens * P.passes) return;
+    const int token = at / P.passes, pass = at - token * P.passes;
+    const int kind = pass < P.q_passes ? 0 : (pass < P.q_passes + P.k_passes ? 1 : 2);
+    const int head0 = (pass - (kind == 0 ? 0 : P.q_passes + (kind == 2 ? P.k_passes : 0))) * rows.kRows;
+    uint4 a = make_uint4(0, 0, 0, 0), b = a;
+    if (rows.u < rows.units && head0 + rows.g < rows.heads_of(kind)) {
+        const uint4 *src = rows.rows_of(kind, token) + (head0 + rows.g) * 2 * rows.units;
+        a = src[rows.piece0(kind)];
+        b = src[rows.piece1(kind)];
+    }
+    const float4 *weight = reinterpret_cast<const float4 *>(kind == 0 ? P.q_weight : P.k_weight);
+    float4 w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        w[j] = kind < 2 && weight && rows.u < rows.units ? __ldg(weight + 2 * (j < 2 ? rows.half0 : rows.half1) + (j & 1)) : make_float4(1.f, 1.f, 1.f, 1.f);
+    rows.load_axes();
+    rows.fetch(token);
+    rows.begin(token);
+    rows.template run_kind<1>(
+        kind, head0, 1,
+        [&](int, bool, int, int, uint4 &x, uint4 &y) {
+            x = a;
+            y = b;
+        },
+        [&](int j) { return w[j]; });
+}
+
+template <int LANES, bool FP8, bool INTERLEAVED>
+__global__ void __launch_bounds__(kNormThreads, kNormCtas) norm_rope_kernel(const __grid_constant__ NormParams P) {
+    __shared__ __align__(128) unsigned char s_ring[kNormWarps][kStages][kBatchBytes];
+    __shared__ uint64_t s_full[kNormWarps][kStages];
+    __shared__ float4 s_weight[2][4 * LANES];  // float4 j of unit u at j * LANES + u: a row's lanes read neighbouring ones
+    const int warp = threadIdx.x / 32;
+    const uint32_t ring = pkv::smem_addr(s_ring[warp]), full = pkv::smem_addr(s_full[warp]);
+    if (threadIdx.x % 32 == 0) {
+        for (int i = 0; i < kStages; ++i) pkv::mbar_init(full + 8 * i, 1);
+        pkv::fence_mbar_init();
+    }
+    __syncwarp();
+    pkv::pdl_wait_primary();
+    pkv::pdl_launch_dependents();
+    RowWarp<LANES, FP8, INTERLEAVED> rows(P);
+    const int64_t all = static_cast<int64_t>(P.num_tokens) * P.batches, warps = static_cast<int64_t>(gridDim.x) * kNormWarps;
+    const int64_t own = static_cast<int64_t>(blockIdx.x) * kNormWarps + warp;
+    const int64_t first = all * own / warps;
+    const int count = static_cast<int>(all * (own + 1) / warps - first);
+    int64_t load_token = first / P.batches, token = load_token;
+    int load_batch = static_cast<int>(first - load_token * P.batches), batch = load_batch, loaded = 0;
+    const int q_batches = (P.q_passes + kBatch - 1) / kBatch, k_batches = (P.k_passes + kBatch - 1) / kBatch;
+    const int row_bytes = P.head_dim * 2;
+    // A token's batch: rows of one kind, from head0 on.
+    auto kind_of = [&](int n) { return n < q_batches ? 0 : (n < q_batches + k_batches ? 1 : 2); };
+    auto head0_of = [&](int n, int kind) { return (n - (kind == 0 ? 0 : q_batches + (kind == 2 ? k_batches : 0))) * (kBatch * rows.kRows); };
+    // Fills stage loaded % kStages.
+    auto load = [&]() {
+        if (rows.lane == 0) {
+            const int kind = kind_of(load_batch), head0 = head0_of(load_batch, kind);
+            const uint32_t bar = full + 8 * (loaded % kStages);
+            const uint32_t bytes = min(rows.heads_of(kind) - head0, kBatch * rows.kRows) * row_bytes;
+            pkv::mbar_arrive_expect_tx(bar, bytes);
+            pkv::bulk_copy_g2s(ring + (loaded % kStages) * kBatchBytes, rows.rows_of(kind, load_token) + head0 * 2 * rows.units, bytes, bar);
+        }
+        ++loaded;
+        if (++load_batch == P.batches) {
+            load_batch = 0;
+            ++load_token;
         }
     };
-    const int row0 = begin + static_cast<int>(threadIdx.x) / LANES;
-    fetch(row0);
-
-    for (int i = threadIdx.x; i < P.rotary_dim / 2; i += kNormThreads) {
-        int axis = P.axes ? __ldg(P.axes + i) : 0;
-        if (axis < 0 || axis >= P.num_axes) {
-            pkv::record_error(&g_norm_error, PKV_DEV_BAD_AXIS);
-            axis = 0;
-        }
-        const uint64_t pos = static_cast<uint64_t>(static_cast<int64_t>(__ldg(P.positions + t * P.num_axes + axis)));
-        const uint64_t turns = pos * static_cast<uint64_t>(__ldg(P.frequencies + i)) + (1ull << 31);
-        const float x = static_cast<float>(static_cast<int32_t>(turns >> 32)) * (1.f / 2147483648.f);
-        float si, co;
-        sincospif(x, &si, &co);
-        reinterpret_cast<float2 *>(s_cs)[(((i & 7) >> 1) * LANES + (i >> 3)) * 2 + (i & 1)] = make_float2(co * P.magnitude, si * P.magnitude);
+    for (int i = 0; i < kStages && i < count; ++i) load();
+    if (count > 0) {
+        rows.load_axes();
+        rows.fetch(token);
     }
-    for (int i = threadIdx.x; i < P.head_dim / 2; i += kNormThreads) {  // float4 i of q's weight, then of k's
-        const bool is_k = i >= P.head_dim / 4;
-        const float *w = is_k ? P.k_weight : P.q_weight;
-        const int f = is_k ? i - P.head_dim / 4 : i, piece = f >> 1;
-        const bool split = !P.interleaved && piece < 2 * r16;  // the halves' pieces: unit piece % r16
-        const int unit = split ? (piece < r16 ? piece : piece - r16) : piece >> 1;
-        const int second = split ? piece >= r16 : piece & 1;
-        if (w) s_weight[is_k][(2 * second + (f & 1)) * LANES + unit] = __ldg(reinterpret_cast<const float4 *>(w) + f);
+    for (int i = threadIdx.x; i < 8 * LANES; i += kNormThreads) {
+        const int kind = i / (4 * LANES), j = i / LANES % 4, unit = i % LANES;
+        const float4 *w = reinterpret_cast<const float4 *>(kind == 0 ? P.q_weight : P.k_weight);
+        const int r16 = P.rotary_dim / 16;
+        const bool split = unit < r16 && !INTERLEAVED;  // the unit's pieces, as in RowWarp
+        const int piece = split ? (j < 2 ? unit : unit + r16) : 2 * unit + (j >= 2);
+        if (w && unit < rows.units) s_weight[kind][j * LANES + unit] = __ldg(w + 2 * piece + (j & 1));
     }
     __syncthreads();
-    float4 cs[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) cs[j] = u < r16 ? s_cs[j * LANES + u] : make_float4(0.f, 0.f, 0.f, 0.f);
-
-    for (int base = row0; base - row0 < end - begin; base += kNormAhead * kRows) {  // (the same passes in all lanes)
-        if (base != row0) fetch(base);
-#pragma unroll
-        for (int i = 0; i < kNormAhead; ++i) {
-            const int row = base + i * kRows, kind = kind_of(row);
-            if (i > 0 && base - row0 + i * kRows >= end - begin) break;  // (in all lanes)
-            float x[16];  // zeros where the lane holds nothing
-            unpack(a[i], x);
-            unpack(b[i], x + 8);
-            const bool normed = kind == 0 ? P.q_weight != nullptr : kind == 1 && P.k_weight != nullptr;
-            float2 sum = {0.f, 0.f};
-#pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-                sum.x = fmaf(x[e], x[e], sum.x);
-                sum.y = fmaf(x[e + 1], x[e + 1], sum.y);
-            }
-            float square = sum.x + sum.y;
-#pragma unroll
-            for (int d = LANES / 2; d >= 1; d >>= 1) square += __shfl_xor_sync(pkv::kFullMask, square, d);
-            if (normed && in_row) {
-                const float r = rsqrtf(fmaf(square, P.inv_dim, P.eps));
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float4 w = s_weight[kind][j * LANES + u];
-                    x[4 * j] *= r * w.x;
-                    x[4 * j + 1] *= r * w.y;
-                    x[4 * j + 2] *= r * w.z;
-                    x[4 * j + 3] *= r * w.w;
-                }
-            }
-            if (kind < 2 && u < r16) {
-                if (P.interleaved) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float c0 = x[4 * j], c1 = x[4 * j + 1], c2 = x[4 * j + 2], c3 = x[4 * j + 3];
-                        x[4 * j] = c0 * cs[j].x - c1 * cs[j].y;
-                        x[4 * j + 1] = c1 * cs[j].x + c0 * cs[j].y;
-                        x[4 * j + 2] = c2 * cs[j].z - c3 * cs[j].w;
-                        x[4 * j + 3] = c3 * cs[j].z + c2 * cs[j].w;
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float a0 = x[2 * j], a1 = x[2 * j + 1], b0 = x[8 + 2 * j], b1 = x[9 + 2 * j];
-                        x[2 * j] = a0 * cs[j].x - b0 * cs[j].y;
-                        x[8 + 2 * j] = b0 * cs[j].x + a0 * cs[j].y;
-                        x[2 * j + 1] = a1 * cs[j].z - b1 * cs[j].w;
-                        x[9 + 2 * j] = b1 * cs[j].z + a1 * cs[j].w;
-                    }
-                }
-            }
-            const int first = first_of(kind), second = second_of(kind);
-            if (FP8) {
-                float most = 0.f;
-#pragma unroll
-                for (int e = 0; e < 16; ++e) most = fmaxf(most, fabsf(x[e]));
-#pragma unroll
-                for (int d = LANES / 2; d >= 1; d >>= 1) most = fmaxf(most, __shfl_xor_sync(pkv::kFullMask, most, d));
-                if (kind != 0 && live(row)) {
-                    const float s = __fdiv_rn(most, 448.f);
-                    const int kvh = row - P.num_q_heads - (kind == 2 ? P.num_kv_heads : 0);
-                    const int64_t to = cache_row + static_cast<int64_t>(kvh) * P.block_size;
-                    uint2 *codes = (kind == 2 ? P.v_codes : P.k_codes) + to * (2 * units);
-                    codes[first] = pack_e4m3(x, s);
-                    codes[second] = pack_e4m3(x + 8, s);
-                    if (u == 0) (kind == 2 ? P.v_scale : P.k_scale)[to] = s;
-                    continue;
-                }
-            }
-            if (!live(row)) continue;
-            uint4 *dst;
-            if (kind == 0) {
-                dst = P.q_out + t * P.q_out_stride + static_cast<int64_t>(row) * (2 * units);
-            } else {
-                const int kvh = row - P.num_q_heads - (kind == 2 ? P.num_kv_heads : 0);
-                dst = P.v ? (kind == 2 ? P.v_cache : P.k_cache) + (cache_row + static_cast<int64_t>(kvh) * P.block_size) * (2 * units)
-                          : P.k_out + t * P.k_out_stride + static_cast<int64_t>(kvh) * (2 * units);
-            }
-            dst[first] = pack(x);
-            dst[second] = pack(x + 8);
+    for (int n = 0; n < count; ++n) {
+        if (token != rows.t) {
+            rows.begin(token);
+            if (token + 1 < P.num_tokens) rows.fetch(token + 1);
+        }
+        const int stage = n % kStages;
+        if (!__all_sync(pkv::kFullMask, pkv::mbar_wait_bounded(full + 8 * stage, (n / kStages) & 1))) {
+            if (rows.lane == 0) pkv::record_error(&g_norm_error, PKV_DEV_WAIT_TIMEOUT);
+            for (int i = n + 1; i < loaded; ++i)  // copies in flight land before the CTA's memory goes (bounded)
+                pkv::mbar_wait_bounded(full + 8 * (i % kStages), (i / kStages) & 1);
+            return;
+        }
+        const int kind = kind_of(batch), head0 = head0_of(batch, kind);
+        const int passes = min(kBatch, (rows.heads_of(kind) - head0 + rows.kRows - 1) / rows.kRows);
+        rows.template run_kind<2>(
+            kind, head0, passes,
+            [&](int i, bool there, int at0, int at1, uint4 &x, uint4 &y) {
+                const uint32_t at = ring + stage * kBatchBytes + (i * rows.kRows + rows.g) * row_bytes;
+                x = there ? lds128_now(at + 16 * at0) : make_uint4(0, 0, 0, 0);
+                y = there ? lds128_now(at + 16 * at1) : make_uint4(0, 0, 0, 0);
+            },
+            [&](int j) { return s_weight[kind & 1][j * LANES + rows.u]; });
+        __syncwarp();  // every lane has read the stage
+        if (loaded < count) {
+            pkv::fence_proxy_async_smem();
+            load();
+        }
+        if (++batch == P.batches) {
+            batch = 0;
+            ++token;
         }
     }
 }
@@ -248,25 +558,41 @@ bool stride_ok(int64_t stride, int heads, int head_dim, int num_tokens) {
     return num_tokens <= 1 || stride >= static_cast<int64_t>(heads) * head_dim;
 }
 
+using NormKernel = void (*)(NormParams);
+template <int LANES, bool FP8>
+NormKernel kernel_of(bool few, bool interleaved) {
+    if (few) return interleaved ? norm_rope_few_kernel<LANES, FP8, true> : norm_rope_few_kernel<LANES, FP8, false>;
+    return interleaved ? norm_rope_kernel<LANES, FP8, true> : norm_rope_kernel<LANES, FP8, false>;
+}
+
 template <bool FP8>
 int launch_norm_rope(NormParams p, int num_tokens, pkv_stream_t stream) {
     const int units = p.head_dim / 16;
     const int lanes = units <= 1 ? 1 : (units <= 2 ? 2 : (units <= 4 ? 4 : (units <= 8 ? 8 : 16)));
-    const int pass = kNormThreads / lanes, rows = p.num_q_heads + p.num_kv_heads + (p.v ? p.num_kv_heads : 0);
-    // One CTA per token; with few tokens a token's rows are cut into single passes, so that a decode step's call
-    // is one round of loads on many SMs instead of three on few.
-    p.rows_per_cta = num_tokens <= 304 ? pass : (rows + pass - 1) / pass * pass;
+    const int rows = 32 / lanes;
+    p.num_tokens = num_tokens;
+    p.q_passes = (p.num_q_heads + rows - 1) / rows;
+    p.k_passes = (p.num_kv_heads + rows - 1) / rows;
+    p.passes = p.q_passes + (p.v ? 2 : 1) * p.k_passes;
+    p.batches = (p.q_passes + kBatch - 1) / kBatch + (p.v ? 2 : 1) * ((p.k_passes + kBatch - 1) / kBatch);
     p.inv_dim = 1.f / static_cast<float>(p.head_dim);
-    const int64_t slices = (rows + p.rows_per_cta - 1) / p.rows_per_cta;
-    if (slices > 65535) return PKV_ERR_UNSUPPORTED;
-    auto kernel = FP8            ? norm_rope_kernel<8, FP8>
-                  : lanes == 1   ? norm_rope_kernel<1, false>
-                  : lanes == 2   ? norm_rope_kernel<2, false>
-                  : lanes == 4   ? norm_rope_kernel<4, false>
-                  : lanes == 8   ? norm_rope_kernel<8, false>
-                                 : norm_rope_kernel<16, false>;
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return PKV_ERR_CUDA;
+    const int64_t passes = static_cast<int64_t>(num_tokens) * p.passes;
+    const bool few = passes <= kFewPasses;
+    const int64_t warps = few ? passes : static_cast<int64_t>(num_tokens) * p.batches;
+    int64_t ctas = (warps + kNormWarps - 1) / kNormWarps;
+    if (!few && ctas > static_cast<int64_t>(sms) * kNormCtas) ctas = static_cast<int64_t>(sms) * kNormCtas;
+    const bool i = p.interleaved != 0;
+    const NormKernel kernel = FP8          ? kernel_of<8, FP8>(few, i)
+                              : lanes == 1 ? kernel_of<1, false>(few, i)
+                              : lanes == 2 ? kernel_of<2, false>(few, i)
+                              : lanes == 4 ? kernel_of<4, false>(few, i)
+                              : lanes == 8 ? kernel_of<8, false>(few, i)
+                                           : kernel_of<16, false>(few, i);
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(num_tokens), static_cast<unsigned>(slices));
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
     cfg.blockDim = dim3(kNormThreads);
     cfg.stream = reinterpret_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr{};

@@ -61,7 +61,6 @@ constexpr int kDim = PKV_HEAD_DIM;
 constexpr int kTileRows = 128;             // query rows per tile (M) and keys per K/V tile (N)
 constexpr int kSlab = kTileRows * 128;     // 128 rows x 64 fp16 dims, 128-byte swizzle
 constexpr int kOperand = 2 * kSlab;        // a whole 128 x 128 fp16 operand tile
-constexpr int kRing = 2;                   // stages of K, and of V
 constexpr int kItems = 4;                  // work items found ahead
 constexpr int kSoftmaxWarps = 8;
 constexpr int kPromptThreads = 32 * (kSoftmaxWarps + 4);  // three warpgroups
@@ -74,6 +73,14 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kMaxSplits = 64;
 constexpr int64_t kMaxContext = 1 << 30;  // positions and their sums with a tile's stay in 32 bits
 constexpr int kPlannedSms = 152;  // the split plan, and with it the workspace, is the same on every device
+
+// Of a tree's call: the item that a CTA's stretch begins but does not finish, for the joining launch.
+struct alignas(16) TreePart {
+    int last;  // the CTA that finishes it; -1: there is no such item
+    int row0, tokens, kvh;
+    int base, nodes, pad[2];  // the tree's
+};
+static_assert(sizeof(TreePart) == 32, "read as two 16-byte pieces");
 
 struct PromptParams {
     __half *out;
@@ -92,6 +99,7 @@ struct PromptParams {
     int64_t v_stride;
     // A tree's call: split counts slots (0: no item is split), their partial results [slot][slot_rows](x 128).
     const uint32_t *tree_mask;  // [total_q][mask_words]
+    TreePart *tree_parts;       // [grid]
     int mask_words, grid, slot_rows;
     CUtensorMap tmap_q, tmap_k, tmap_v;
 };
@@ -110,12 +118,19 @@ struct alignas(16) Item {
 };
 static_assert(sizeof(Item) == 48, "read as three 16-byte pieces");
 
-struct PromptSmem {
-    static constexpr int q = 0;                              // two operand tiles
-    static constexpr int ring = 2 * kOperand;
-    static constexpr int values = ring + kRing * kOperand;   // ring: K stages, values: V stages
-    static constexpr int bars = values + kRing * kOperand;
-    static constexpr int n_bars = 4 * kRing + 2 + 2 * kItems + 8 + 2 + 1;
+// Shared memory and barriers of an instance: `q` operand tiles of Q, rings of `ks` K and `vs` V stages.
+template <int QS, int KS, int VS, bool TREE>
+struct PromptLayout {
+    static constexpr bool tree = TREE;
+    static constexpr int k_ring = KS, v_ring = VS;
+    static constexpr int q = 0;
+    static constexpr int ring = QS * kOperand;
+    static constexpr int values = ring + KS * kOperand;   // ring: K stages, values: V stages
+    static constexpr int bars = values + VS * kOperand;
+    // barriers by index
+    static constexpr int k_full = 0, k_empty = KS, v_full = 2 * KS, v_empty = v_full + VS, q_full = v_empty + VS, q_empty = q_full + 1,
+                         item_full = q_empty + 1, item_empty = item_full + kItems, s = item_empty + kItems, p = s + 2, o = p + 4,
+                         state_bar = o + 2, joined = state_bar + 1, drain = joined + 1, n_bars = drain + 1;
     static constexpr int tmem_slot = bars + n_bars * 8;
     static constexpr int items = (tmem_slot + 4 + 15) / 16 * 16;
     static constexpr int state = items + kItems * static_cast<int>(sizeof(Item));  // [2 groups][128 rows] (m, l)
@@ -124,11 +139,9 @@ struct PromptSmem {
     static constexpr int total = staging + kSoftmaxWarps * 32 * 128;
     static_assert(total <= 227 * 1024, "a CTA's shared memory");
 };
-
-// Barriers by index.
-constexpr int kBarKFull = 0, kBarKEmpty = kRing, kBarVFull = 2 * kRing, kBarVEmpty = 3 * kRing, kBarQFull = 4 * kRing, kBarQEmpty = kBarQFull + 1,
-              kBarItemFull = kBarQEmpty + 1, kBarItemEmpty = kBarItemFull + kItems, kBarS = kBarItemEmpty + kItems, kBarP = kBarS + 2,
-              kBarO = kBarP + 4, kBarState = kBarO + 2, kBarJoined = kBarState + 1, kBarDrain = kBarJoined + 1;
+using CausalLayout = PromptLayout<2, 2, 2, false>;
+using TreeLayout = PromptLayout<2, 2, 2, true>;
+using SmallTreeLayout = PromptLayout<1, 2, 3, true>;  // trees of one tile
 
 // ---- TMEM moves (one row per lane, consecutive 32-bit columns)
 // The load is asynchronous: its registers may be used after tmem_landed on them.
@@ -439,6 +452,7 @@ struct TreeWalk {
     int64_t at, end, begin_of_seq, end_of_seq;
     int seq;
     Request r;
+    TreePart part;
 
     __device__ TreeWalk(const PromptParams &P, int lane) {
         plan = tree_plan(P, tree_units_of(P, 0, P.num_seqs, lane, blockIdx.x == 0));
@@ -447,6 +461,8 @@ struct TreeWalk {
         end = cta < plan.ctas ? tree_begin(plan, cta + 1) : 0;
         seq = -1;
         begin_of_seq = end_of_seq = 0;
+        part = TreePart{};
+        part.last = -1;
     }
     // The request that unit `at` belongs to, from the one behind the present one on.
     __device__ void seek(const PromptParams &P, int lane) {
@@ -512,6 +528,15 @@ struct TreeWalk {
                 it.kv_count[1] = it.kv_count[0] / 2;
                 it.kv_count[0] -= it.kv_count[1];
             }
+            if (first == 0 && past < tiles) {  // the stretch's last
+                const int64_t end_of_item = begin_of_seq + static_cast<int64_t>(item + 1) * units;
+                part.last = tree_owner(plan, end_of_item - 1);
+                part.row0 = it.row0;
+                part.tokens = it.live[0] + (it.shared ? 0 : it.live[1]);
+                part.kvh = it.kvh;
+                part.base = r.keys - r.tokens;
+                part.nodes = r.tokens;
+            }
             return it;
         }
         return it;
@@ -575,19 +600,24 @@ __device__ __forceinline__ void clean_values(uint32_t v, int valid, int part, in
 // Key tiles that an item's groups go through: the same ones, or each its own.
 __device__ __forceinline__ int key_tiles(bool shared, int a, int b) { return shared ? a + b : max(a, b); }
 
-template <bool PAGED, bool TREE>
+template <bool PAGED, typename L>
 __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_constant__ PromptParams P) {
+    constexpr bool TREE = L::tree;
+    constexpr int kKRing = L::k_ring, kVRing = L::v_ring;
+    constexpr int kBarKFull = L::k_full, kBarKEmpty = L::k_empty, kBarVFull = L::v_full, kBarVEmpty = L::v_empty, kBarQFull = L::q_full,
+                  kBarQEmpty = L::q_empty, kBarItemFull = L::item_full, kBarItemEmpty = L::item_empty, kBarS = L::s, kBarP = L::p, kBarO = L::o,
+                  kBarState = L::state_bar, kBarJoined = L::joined, kBarDrain = L::drain;
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t base = pkv::smem_addr(smem);
     const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
-    const uint32_t bars = base + PromptSmem::bars;
+    const uint32_t bars = base + L::bars;
     auto bar = [bars](int i) { return bars + 8 * i; };
-    volatile Item *slots = reinterpret_cast<volatile Item *>(smem + PromptSmem::items);
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + PromptSmem::tmem_slot);
+    volatile Item *slots = reinterpret_cast<volatile Item *>(smem + L::items);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::tmem_slot);
 
     const bool aligned = (base & 1023) == 0;  // the swizzled operand tiles need it (the same in every CTA)
     if (threadIdx.x == 0) {
-        for (int i = 0; i < PromptSmem::n_bars; ++i) {
+        for (int i = 0; i < L::n_bars; ++i) {
             uint32_t count = 1;
             if (i >= kBarItemEmpty && i < kBarItemEmpty + kItems) count = kSoftmaxWarps + 3;
             if (i >= kBarP && i < kBarP + 4) count = 4;  // one arrival per softmax warp of the tile
@@ -596,7 +626,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
         }
         pkv::fence_mbar_init();
     }
-    volatile uint32_t *dirty = reinterpret_cast<volatile uint32_t *>(smem + PromptSmem::dirty);
+    volatile uint32_t *dirty = reinterpret_cast<volatile uint32_t *>(smem + L::dirty);
     if (threadIdx.x < kItems) dirty[threadIdx.x] = 0;
     if (warp == kMmaWarp && aligned) pkv::tmem_alloc(pkv::smem_addr(tmem_slot), 512);
     pkv::tmem_fence_before_sync();
@@ -666,6 +696,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                 TreeWalk walk(P, lane);
                 for (uint32_t k = 0; publish(walk.next(P, lane), k); ++k) {
                 }
+                if (P.splits > 0 && lane == 0) P.tree_parts[blockIdx.x] = walk.part;
             } else {
                 const int pairs = pairs_from(P, 0, 2 * tile_tokens, lane, blockIdx.x == 0);
                 const int tiles = most_tiles(P, lane);
@@ -689,7 +720,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                 if (!(ok = wait(kBarItemFull + slot, k / kItems))) break;
                 Item it;
                 {
-                    const uint32_t at = base + PromptSmem::items + slot * sizeof(Item);
+                    const uint32_t at = base + L::items + slot * sizeof(Item);
                     uint4 *d = reinterpret_cast<uint4 *>(&it);
                     d[0] = lds128v(at);
                     d[1] = lds128v(at + 16);
@@ -701,10 +732,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                 const int n_kv = key_tiles(it.shared, it.kv_count[0], it.kv_count[1]);
                 int row = box_row(it.seq, it.kvh, it.keys, it.kv_first);
                 for (int j = 0; j < n_kv; ++j, ++stage) {
-                    const int tile = it.kv_first + j, st = stage % kRing;
+                    const int tile = it.kv_first + j, st = stage % kKRing;
                     const int ahead = j + 1 < n_kv ? box_row(it.seq, it.kvh, it.keys, tile + 1) : 0;
-                    if (!(ok = wait(kBarKEmpty + st, stage / kRing + 1))) break;
-                    copy_tile(&P.tmap_k, base + PromptSmem::ring + st * kOperand, bar(kBarKFull + st), it.keys, it.kvh, tile,
+                    if (!(ok = wait(kBarKEmpty + st, stage / kKRing + 1))) break;
+                    copy_tile(&P.tmap_k, base + L::ring + st * kOperand, bar(kBarKFull + st), it.keys, it.kvh, tile,
                               it.row0 - it.pos0, row);
                     row = ahead;
                     if (j > 0) continue;
@@ -719,7 +750,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                         pkv::mbar_arrive_expect_tx(bar(kBarQFull), tiles * kOperand);
                         for (int t = 0; t < tiles; ++t)
                             for (int half = 0; half < 2; ++half)
-                                pkv::tma_load_3d(base + PromptSmem::q + t * kOperand + half * kSlab, &P.tmap_q, 64 * half, it.kvh << glog,
+                                pkv::tma_load_3d(base + L::q + t * kOperand + half * kSlab, &P.tmap_q, 64 * half, it.kvh << glog,
                                                  it.row0 + t * tile_tokens, bar(kBarQFull));
                     }
                     __syncwarp();
@@ -727,8 +758,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
             }
             if (!ok) {  // copies still in flight land before the CTA's memory goes (bounded)
                 if (loaded) wait_phase(bar(kBarQFull), (loaded - 1) & 1);
-                for (uint32_t s = stage > kRing ? stage - kRing : 0; s < stage; ++s)
-                    wait_phase(bar(kBarKFull + s % kRing), (s / kRing) & 1);
+                for (uint32_t s = stage > kKRing ? stage - kKRing : 0; s < stage; ++s)
+                    wait_phase(bar(kBarKFull + s % kKRing), (s / kKRing) & 1);
             }
         } else if (warp == kValueWarp) {
             // ---------------------------------------------------------------- V
@@ -745,16 +776,16 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                 if (seq < 0) break;
                 int row = n_kv > 0 ? box_row(seq, kvh, keys, first) : 0;
                 for (int j = 0; j < n_kv; ++j, ++stage) {
-                    const int tile = first + j, st = stage % kRing;
+                    const int tile = first + j, st = stage % kVRing;
                     const int ahead = j + 1 < n_kv ? box_row(seq, kvh, keys, tile + 1) : 0;
-                    if (!(ok = wait(kBarVEmpty + st, stage / kRing + 1))) break;
-                    copy_tile(&P.tmap_v, base + PromptSmem::values + st * kOperand, bar(kBarVFull + st), keys, kvh, tile, first_row, row);
+                    if (!(ok = wait(kBarVEmpty + st, stage / kVRing + 1))) break;
+                    copy_tile(&P.tmap_v, base + L::values + st * kOperand, bar(kBarVFull + st), keys, kvh, tile, first_row, row);
                     row = ahead;
                 }
             }
             if (!ok)
-                for (uint32_t s = stage > kRing ? stage - kRing : 0; s < stage; ++s)
-                    wait_phase(bar(kBarVFull + s % kRing), (s / kRing) & 1);
+                for (uint32_t s = stage > kVRing ? stage - kVRing : 0; s < stage; ++s)
+                    wait_phase(bar(kBarVFull + s % kVRing), (s / kVRing) & 1);
         } else if (warp == kMmaWarp) {
             // ---------------------------------------------------------------- tensor-core issue
             constexpr uint32_t kIdescPV = pkv::umma_idesc_f16_f32(kTileRows, kDim) | (1u << 16);  // V: MN-major
@@ -775,7 +806,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                 auto groups_of = [&](int j) { return (min(kTileRows, keys - (first + j) * kTileRows) + 15) / 16; };
                 auto qk = [&](int t, uint32_t st, int groups) {
                     if (elected()) {
-                        const uint32_t q = base + PromptSmem::q + (shared ? 0 : t) * kOperand, kk = base + PromptSmem::ring + (st % kRing) * kOperand;
+                        const uint32_t q = base + L::q + (shared ? 0 : t) * kOperand, kk = base + L::ring + (st % kKRing) * kOperand;
                         const uint32_t idesc = pkv::umma_idesc_f16_f32(kTileRows, groups * 16);
     #pragma unroll
                         for (int ks = 0; ks < kDim / 16; ++ks) {
@@ -811,7 +842,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                     ++p_count[t];
                     return true;
                 };
-                auto k_landed = [&]() { return wait(kBarKFull + k_stage % kRing, k_stage / kRing); };
+                auto k_landed = [&]() { return wait(kBarKFull + k_stage % kKRing, k_stage / kKRing); };
                 // Q K^T of the first key tile for both groups, or of the first two for one each
                 const int firsts = shared ? min(2, n_kv) : 1;
                 for (int x = 0; x < firsts && ok; ++x) {
@@ -819,7 +850,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                     pkv::tmem_fence_after_sync();
                     for (int t = 0; t < 2; ++t)
                         if (shared ? t == x : n[t] > 0) qk(t, k_stage, groups_of(x));
-                    commit(kBarKEmpty + k_stage % kRing);
+                    commit(kBarKEmpty + k_stage % kKRing);
                     ++k_stage;
                 }
                 if (!ok) break;
@@ -827,8 +858,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                 for (int j = 0; j < n_kv && ok; ++j) {
                     const int k_tile = j + (shared ? 2 : 1);
                     const bool more = k_tile < n_kv;
-                    if (!(ok = wait(kBarVFull + v_stage % kRing, v_stage / kRing))) break;
-                    const uint32_t v = base + PromptSmem::values + (v_stage % kRing) * kOperand;
+                    if (!(ok = wait(kBarVFull + v_stage % kVRing, v_stage / kVRing))) break;
+                    const uint32_t v = base + L::values + (v_stage % kVRing) * kOperand;
                     const int groups = groups_of(j), local = shared ? j >> 1 : j;
                     bool k_here = false;
                     for (int t = 0; t < 2; ++t) {
@@ -841,10 +872,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                         }
                     }
                     if (!ok) break;
-                    commit(kBarVEmpty + v_stage % kRing);
+                    commit(kBarVEmpty + v_stage % kVRing);
                     ++v_stage;
                     if (more) {  // (some group always takes the next K tile)
-                        commit(kBarKEmpty + k_stage % kRing);
+                        commit(kBarKEmpty + k_stage % kKRing);
                         ++k_stage;
                         if (k_tile + 1 == n_kv) commit(kBarQEmpty);  // the item's last Q K^T has been issued
                     }
@@ -865,13 +896,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
         const int r = (warp & 3) * 32 + lane, tok = r >> glog;
         const float sc = P.q_scale;
         uint32_t s_count = 0, o_count = 0, joins = 0, v_stage = 0;  // v_stage: V stages of the items so far
-        float2 *s_state = reinterpret_cast<float2 *>(smem + PromptSmem::state);
+        float2 *s_state = reinterpret_cast<float2 *>(smem + L::state);
         bool ok = true;
         for (uint32_t k = 0; ok; ++k) {
             const int slot = k % kItems;
             if (!(ok = wait(kBarItemFull + slot, k / kItems))) break;
-            const uint4 i0 = lds128v(base + PromptSmem::items + slot * sizeof(Item)), i1 = lds128v(base + PromptSmem::items + slot * sizeof(Item) + 16),
-                        i2 = lds128v(base + PromptSmem::items + slot * sizeof(Item) + 32);
+            const uint4 i0 = lds128v(base + L::items + slot * sizeof(Item)), i1 = lds128v(base + L::items + slot * sizeof(Item) + 16),
+                        i2 = lds128v(base + L::items + slot * sizeof(Item) + 32);
             const int seq = i0.x, kvh = i0.y, split = i0.z, slot_row0 = i0.w;
             const int live = t ? i1.y : i1.x, pos0 = i1.z, first = i2.x;
             const int n = t ? i2.z : i2.y, n_of_other = t ? i2.y : i2.z;
@@ -897,7 +928,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                 // already, and for shared rows and split keys once S is there, which was issued behind it.
                 const bool border = key0 + kTileRows - 1 > pos0, early = split < 0 && !shared;
                 const uint32_t vs = v_stage + (shared ? 2 * j + t : j);
-                const uint32_t v = base + PromptSmem::values + (vs % kRing) * kOperand;
+                const uint32_t v = base + L::values + (vs % kVRing) * kOperand;
                 bool cleaned = !border;
                 uint32_t seen[4];  // of a tree's row: the tile's keys that it sees
                 if (TREE && border) {
@@ -917,7 +948,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                         ++s_count;
                     }
                     if (!cleaned && (early || step == 1)) {
-                        if (!(ok = wait(kBarVFull + vs % kRing, vs / kRing))) break;
+                        if (!(ok = wait(kBarVFull + vs % kVRing, vs / kVRing))) break;
                         clean_values(v, min(kTileRows, keys - key0), warp & 3, lane, dirty + k % kItems, k + 1);
                         cleaned = true;
                     }
@@ -1028,7 +1059,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                 // warp's own 4 KB, so that eight lanes store a whole line.  The 16-byte pieces of row x lie at piece
                 // ^ (x % 8).  Lane's share of a line: piece lane % 8 of rows 4 i + lane / 8.
                 const bool whole = split < 0;
-                const uint32_t lines = base + PromptSmem::staging + warp * 4096, mine = lines + lane * 128;
+                const uint32_t lines = base + L::staging + warp * 4096, mine = lines + lane * 128;
                 const bool in_slot = TREE && !whole;  // a slot's rows lie one behind another
                 const uint32_t row_bytes = whole ? kDim * 2 : (TREE ? 1 : P.splits) * kDim * 4;
                 const int group_mask = (1 << glog) - 1;
@@ -1224,58 +1255,57 @@ __global__ void __launch_bounds__(kJoinThreads, BATCH == 8 ? 4 : 2) prompt_join_
     }
 }
 
-// Joins the parts of each (token, head) row of the items that were split: one warp per row, four dims a lane.
+// Joins the parts of a tree's split items: kJoinCtas CTAs for the item that CTA blockIdx.y began, one warp per row,
+// four dims a lane, eight parts' loads in flight.
+constexpr int kJoinCtas = 16;
 __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_constant__ PromptParams P) {
-    __shared__ int64_t s_units, s_before;
-    const int lane = threadIdx.x & 31;
-    if (threadIdx.x < 32) {
-        const int64_t before = tree_units_of(P, 0, blockIdx.y, lane, false);
-        const int64_t behind = tree_units_of(P, blockIdx.y, P.num_seqs, lane, false);
-        if (lane == 0) {
-            s_units = before + behind;
-            s_before = before;
-        }
-    }
-    __syncthreads();
-    const Request r = request_of(P, blockIdx.y, false);
-    const TreePlan plan = tree_plan(P, s_units);
-    // So far only the call's inputs; the attention launch's parts from here on.
     pkv::pdl_wait_primary();
     pkv::pdl_launch_dependents();
-    const int tile_tokens = kTileRows >> P.group_log2, pairs = tree_pairs(P, r), units = tree_tiles(r) + kItemUnits;
-    const int64_t rows = static_cast<int64_t>(r.tokens) * P.num_q_heads;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * (kJoinThreads / 32) + (threadIdx.x >> 5); i < rows;
-         i += static_cast<int64_t>(gridDim.x) * (kJoinThreads / 32)) {
-        const int token = static_cast<int>(i / P.num_q_heads), head = static_cast<int>(i - static_cast<int64_t>(token) * P.num_q_heads);
-        const int pair = token / (2 * tile_tokens), in_pair = token - pair * 2 * tile_tokens;
-        const int64_t begin = s_before + (static_cast<int64_t>(head >> P.group_log2) * pairs + pair) * units;
-        const int c0 = tree_owner(plan, begin + kItemUnits), c1 = tree_owner(plan, begin + units - 1);
-        if (c0 == c1) continue;  // written whole
-        const int row = (in_pair << P.group_log2) + (head & ((1 << P.group_log2) - 1));
-        auto part_of = [&](int c) { return static_cast<int64_t>(c == c0 ? 2 * c + 1 : 2 * c) * P.slot_rows + row; };
-        float top = -INFINITY;
-        for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, __ldcg(P.m_part + part_of(c)));
+    const int lane = threadIdx.x & 31, c0 = blockIdx.y;
+    const uint4 d0 = __ldcg(reinterpret_cast<const uint4 *>(P.tree_parts + c0)), d1 = __ldcg(reinterpret_cast<const uint4 *>(P.tree_parts + c0) + 1);
+    const int last = d0.x, row0 = d0.y, rows = static_cast<int>(d0.z) << P.group_log2, kvh = d0.w, parts = last - c0 + 1;
+    if (last < 0) return;
+    for (int row = blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5); row < rows; row += kJoinCtas * (kJoinThreads / 32)) {
+        auto part_of = [&](int i) { return static_cast<int64_t>(i == 0 ? 2 * c0 + 1 : 2 * (c0 + i)) * P.slot_rows + row; };
+        float top = -INFINITY, m = -INFINITY, l = 0.f;
+        for (int i = lane; i < parts; i += 32) {
+            m = __ldcg(P.m_part + part_of(i));
+            l = __ldcg(P.l_part + part_of(i));
+            top = fmaxf(top, m);
+        }
 #pragma unroll
         for (int sh = 16; sh >= 1; sh >>= 1) top = fmaxf(top, __shfl_xor_sync(pkv::kFullMask, top, sh));
         float total = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int c = c0; c <= c1; ++c) {
-            const int64_t part = part_of(c);
-            const float l = __ldcg(P.l_part + part);
-            if (l == 0.f) continue;  // none of the row's keys
-            const float w = l * exp2f(__ldcg(P.m_part + part) - top);
-            const float4 o = __ldcg(reinterpret_cast<const float4 *>(P.o_part + part * kDim) + lane);
-            total += w;
-            acc.x = fmaf(w, o.x, acc.x);
-            acc.y = fmaf(w, o.y, acc.y);
-            acc.z = fmaf(w, o.z, acc.z);
-            acc.w = fmaf(w, o.w, acc.w);
+        for (int i0 = 0; i0 < parts; i0 += 32) {
+            if (parts > 32) {
+                const bool here = i0 + lane < parts;
+                m = here ? __ldcg(P.m_part + part_of(i0 + lane)) : -INFINITY;
+                l = here ? __ldcg(P.l_part + part_of(i0 + lane)) : 0.f;
+            }
+            const float weight = l == 0.f ? 0.f : l * exp2f(m - top);  // (0 past the last part, and where a part holds none of the row's keys)
+            const int here = min(32, parts - i0);
+            for (int j0 = 0; j0 < here; j0 += 8) {
+                float4 o[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) o[j] = __ldcg(reinterpret_cast<const float4 *>(P.o_part + part_of(i0 + min(j0 + j, here - 1)) * kDim) + lane);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float w = __shfl_sync(pkv::kFullMask, weight, j0 + j);
+                    if (j0 + j >= here || w == 0.f) continue;
+                    total += w;
+                    acc.x = fmaf(w, o[j].x, acc.x);
+                    acc.y = fmaf(w, o[j].y, acc.y);
+                    acc.z = fmaf(w, o[j].z, acc.z);
+                    acc.w = fmaf(w, o[j].w, acc.w);
+                }
+            }
         }
-        const int64_t token_row = static_cast<int64_t>(r.start) + token;
-        const bool blind = total == 0.f && tree_blind(P.tree_mask + token_row * P.mask_words, r.keys - r.tokens, r.tokens);
+        const int64_t token = static_cast<int64_t>(row0) + (row >> P.group_log2);
+        const bool blind = total == 0.f && tree_blind(P.tree_mask + token * P.mask_words, static_cast<int>(d1.x), static_cast<int>(d1.y));
         const float inv = blind ? 0.f : 1.f / total;
         const __half2 lo = __floats2half2_rn(acc.x * inv, acc.y * inv), hi = __floats2half2_rn(acc.z * inv, acc.w * inv);
-        const int64_t out_row = token_row * P.num_q_heads + head;
+        const int64_t out_row = token * P.num_q_heads + (kvh << P.group_log2) + (row & ((1 << P.group_log2) - 1));
         *reinterpret_cast<uint2 *>(P.out + out_row * kDim + 4 * lane) =
             make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
         if (lane == 0 && P.lse != nullptr) P.lse[out_row] = (top + log2f(total)) * kLn2;
@@ -1767,22 +1797,22 @@ bool group_ok(int num_q_heads, int num_kv_heads) {
 }
 
 // The launch of prompt_kernel's instance on one CTA per SM, or on `most`.
-template <bool PAGED, bool TREE>
+template <bool PAGED, typename L>
 int launch_prompt_kernel(const PromptParams &p, unsigned grid, pkv_stream_t stream) {
-    auto kernel = prompt_kernel<PAGED, TREE>;
+    auto kernel = prompt_kernel<PAGED, L>;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
     static std::atomic<uint64_t> configured{0};  // one bit per device
     const uint64_t bit = 1ull << (dev & 63);
     if (!(configured.load(std::memory_order_acquire) & bit)) {
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PromptSmem::total) != cudaSuccess)
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::total) != cudaSuccess)
             return PKV_ERR_CUDA;
         configured.fetch_or(bit, std::memory_order_acq_rel);
     }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kPromptThreads);
-    cfg.dynamicSmemBytes = PromptSmem::total;
+    cfg.dynamicSmemBytes = L::total;
     cfg.stream = reinterpret_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1792,13 +1822,11 @@ int launch_prompt_kernel(const PromptParams &p, unsigned grid, pkv_stream_t stre
     return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
-// The joining launch behind it: CTAs of eight rows, all rows of a request in one round or four CTAs per SM.
+// A joining launch behind it.
 template <typename Kernel>
-int launch_join(Kernel kernel, const PromptParams &p, int sms, pkv_stream_t stream) {
-    const int64_t rows = static_cast<int64_t>(p.max_query_len < p.total_q ? p.max_query_len : p.total_q) * p.num_q_heads;
-    const int64_t by_rows = (rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32), by_sms = (4 * sms + p.num_seqs - 1) / p.num_seqs;
+int launch_after(Kernel kernel, const PromptParams &p, dim3 grid, pkv_stream_t stream) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(by_rows < by_sms ? by_rows : by_sms), p.num_seqs);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = reinterpret_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr{};
@@ -1833,10 +1861,13 @@ int launch_prompt(PromptParams p, int max_context, void *workspace, size_t works
     if (sm_count(&sms) != PKV_OK) return PKV_ERR_CUDA;
     const int pair_tokens = 2 * kTileRows >> p.group_log2;
     const int64_t most = (static_cast<int64_t>(p.total_q) / pair_tokens + p.num_seqs) * p.num_kv_heads * p.splits;
-    const int st = launch_prompt_kernel<PAGED, false>(p, static_cast<unsigned>(most < sms ? most : sms), stream);
+    const int st = launch_prompt_kernel<PAGED, CausalLayout>(p, static_cast<unsigned>(most < sms ? most : sms), stream);
     if (st != PKV_OK || p.splits == 1) return st;
+    const int64_t rows = static_cast<int64_t>(p.max_query_len < p.total_q ? p.max_query_len : p.total_q) * p.num_q_heads;
+    const int64_t by_rows = (rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32), by_sms = (4 * sms + p.num_seqs - 1) / p.num_seqs;
     const bool many = static_cast<int64_t>(p.total_q) * p.num_q_heads > 2 * sms * (kJoinThreads / 32);
-    return launch_join(many ? prompt_join_kernel<8> : prompt_join_kernel<16>, p, sms, stream);
+    return launch_after(many ? prompt_join_kernel<8> : prompt_join_kernel<16>, p,
+                        dim3(static_cast<unsigned>(by_rows < by_sms ? by_rows : by_sms), p.num_seqs), stream);
 }
 
 // A tree's call: the CTAs that take part (with their two slots each) at most, and the rows of a slot.  0 slots: no item
@@ -1857,7 +1888,7 @@ TreeSizes tree_sizes(int num_seqs, int total_q, int max_query_len, int num_q_hea
 size_t tree_workspace(const TreeSizes &t) {
     if (!t.split) return 0;
     const size_t rows = static_cast<size_t>(2 * t.ctas) * t.slot_rows;
-    return rows * (kDim + 2) * sizeof(float);
+    return rows * (kDim + 2) * sizeof(float) + t.ctas * sizeof(TreePart);
 }
 
 int log2_of(int g) { return g == 1 ? 0 : (g == 2 ? 1 : (g == 4 ? 2 : 3)); }
@@ -2022,6 +2053,7 @@ extern "C" PKV_API int pkv_decode_attention_tree(void *out, float *lse, const vo
         p.o_part = static_cast<float *>(workspace);
         p.m_part = p.o_part + rows * kDim;
         p.l_part = p.m_part + rows;
+        p.tree_parts = reinterpret_cast<TreePart *>(p.l_part + rows);
     }
     p.tree_mask = reinterpret_cast<const uint32_t *>(tree_mask);
     p.mask_words = mask_words;
@@ -2032,9 +2064,10 @@ extern "C" PKV_API int pkv_decode_attention_tree(void *out, float *lse, const vo
     int sms = 0;
     if (sm_count(&sms) != PKV_OK) return PKV_ERR_CUDA;
     p.grid = sizes.ctas < sms ? sizes.ctas : sms;
-    st = launch_prompt_kernel<true, true>(p, static_cast<unsigned>(p.grid), stream);
+    st = sizes.slot_rows == kTileRows ? launch_prompt_kernel<true, SmallTreeLayout>(p, static_cast<unsigned>(p.grid), stream)
+                                      : launch_prompt_kernel<true, TreeLayout>(p, static_cast<unsigned>(p.grid), stream);
     if (st != PKV_OK || !sizes.split) return st;
-    return launch_join(tree_join_kernel, p, sms, stream);
+    return launch_after(tree_join_kernel, p, dim3(kJoinCtas, static_cast<unsigned>(p.grid)), stream);
 }
 
 extern "C" PKV_API int pkv_prefill_attention_weights(float *scores, int64_t score_capacity, const void *q, int64_t q_stride,

@@ -118,8 +118,8 @@ def test_tree_workspace(lib):
                 for n in (1, 16, 61, 1024):
                     for context in (1, 513, 4096, 1 << 20, 1 << 30):
                         most = max(most, f(seqs, seqs * n, n, hkv * group, hkv, 128, context))
-    # two slots of at most 256 rows of 128 + 2 floats for each of 152 CTAs
-    assert most == 2 * 152 * 256 * 130 * 4 < 41 * 10 ** 6
+    # two slots of at most 256 rows of 128 + 2 floats, and 32 bytes, for each of 152 CTAs
+    assert most == 152 * (2 * 256 * 130 * 4 + 32) < 41 * 10 ** 6
     for bad in ((0, 16, 16, 32, 8, 128, 4096), (1, 0, 16, 32, 8, 128, 4096), (1, 16, 0, 32, 8, 128, 4096), (1, 16, 16, 24, 8, 128, 4096),
                 (1, 16, 16, 32, 8, 64, 4096), (1, 16, 16, 32, 8, 128, 0)):
         assert f(*bad) == 0
