@@ -91,7 +91,7 @@ struct PromptParams {
     float *o_part, *m_part, *l_part;  // splits > 1: [total_q][Hq][splits](x 128), m in log2 units
     int num_seqs, total_q, max_query_len, max_blocks, num_q_heads, num_kv_heads, block_size;
     int64_t num_blocks;
-    int group_log2, box_rows;
+    int group_log2, box_rows, box_log2;
     int splits;       // at most; the kernels take split_count of it
     int split_tiles;  // key tiles that a split is worth
     float q_scale;                // scale * log2(e)
@@ -417,48 +417,54 @@ __device__ Item find_item(const PromptParams &P, int64_t index, int splits, int 
 constexpr int kItemUnits = 2;
 constexpr int kLeastUnits = 6;  // of a CTA's stretch
 
-struct TreePlan {
-    int64_t units;
-    int ctas;  // that take part
-};
-
 __device__ __forceinline__ int tree_tiles(const Request &r) { return (r.keys + kTileRows - 1) / kTileRows; }
 __device__ __forceinline__ int tree_pairs(const PromptParams &P, const Request &r) {
     const int pair_tokens = 2 * kTileRows >> P.group_log2;
     return (r.tokens + pair_tokens - 1) / pair_tokens;
 }
-__device__ __forceinline__ int64_t tree_units(const PromptParams &P, const Request &r) {
-    return r.tokens > 0 ? static_cast<int64_t>(tree_pairs(P, r)) * P.num_kv_heads * (tree_tiles(r) + kItemUnits) : 0;
+__device__ __forceinline__ uint32_t tree_units(const PromptParams &P, const Request &r) {  // (the host bounds their sum)
+    return r.tokens > 0 ? static_cast<uint32_t>(tree_pairs(P, r)) * P.num_kv_heads * (tree_tiles(r) + kItemUnits) : 0u;
 }
-// The units of requests begin .. end - 1 (all lanes get the sum).
-__device__ __forceinline__ int64_t tree_units_of(const PromptParams &P, int begin, int end, int lane, bool report) {
-    long long n = 0;
-    for (int b = begin + lane; b < end; b += 32) n += tree_units(P, request_of(P, b, report));
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) n += __shfl_xor_sync(pkv::kFullMask, n, d);
-    return n;
-}
-__device__ __forceinline__ TreePlan tree_plan(const PromptParams &P, int64_t units) {
-    const int64_t most = units / kLeastUnits;
-    return {units, static_cast<int>(most < 1 ? 1 : (most < P.grid ? most : P.grid))};
-}
-__device__ __forceinline__ int64_t tree_begin(const TreePlan &p, int cta) { return p.units * cta / p.ctas; }
-// The CTA whose stretch holds a unit: the last one that begins at or before it.
-__device__ __forceinline__ int tree_owner(const TreePlan &p, int64_t unit) { return static_cast<int>(((unit + 1) * p.ctas - 1) / p.units); }
+
+// CTA c's stretch begins at unit each * c + rest * c / ctas.
+struct TreePlan {
+    uint32_t units, ctas, each, rest;
+
+    __device__ __forceinline__ void make(const PromptParams &P, uint32_t sum) {
+        units = sum;
+        const uint32_t most = units / kLeastUnits;
+        ctas = most < 1 ? 1 : min(most, static_cast<uint32_t>(P.grid));
+        each = units / ctas;
+        rest = units - each * ctas;
+    }
+    __device__ __forceinline__ uint32_t begin(uint32_t cta) const { return each * cta + rest * cta / ctas; }
+    // The CTA whose stretch holds a unit: the last one that begins at or before it.
+    __device__ __forceinline__ uint32_t owner(uint32_t unit) const {
+        uint32_t c = unit / (each + 1);  // not past it
+        while (c + 1 < ctas && begin(c + 1) <= unit) ++c;
+        return c;
+    }
+};
 
 // Goes through one CTA's stretch, piece by piece (one warp, the same in all lanes).
 struct TreeWalk {
     TreePlan plan;
-    int64_t at, end, begin_of_seq, end_of_seq;
+    uint32_t at, end, begin_of_seq, end_of_seq;
     int seq;
     Request r;
     TreePart part;
 
-    __device__ TreeWalk(const PromptParams &P, int lane) {
-        plan = tree_plan(P, tree_units_of(P, 0, P.num_seqs, lane, blockIdx.x == 0));
-        const int cta = blockIdx.x;
-        at = cta < plan.ctas ? tree_begin(plan, cta) : 0;
-        end = cta < plan.ctas ? tree_begin(plan, cta + 1) : 0;
+    __device__ void start(const PromptParams &P, int lane) {
+        uint32_t sum = 0;
+#pragma unroll 2
+        for (int b = lane; b < P.num_seqs; b += 32) sum += tree_units(P, request_of(P, b, blockIdx.x == 0));
+        plan.make(P, __reduce_add_sync(pkv::kFullMask, sum));
+        const uint32_t cta = blockIdx.x;
+        at = end = 0;
+        if (cta < plan.ctas && plan.units > 0) {
+            at = plan.begin(cta);
+            end = plan.begin(cta + 1);
+        }
         seq = -1;
         begin_of_seq = end_of_seq = 0;
         part = TreePart{};
@@ -466,12 +472,15 @@ struct TreeWalk {
     }
     // The request that unit `at` belongs to, from the one behind the present one on.
     __device__ void seek(const PromptParams &P, int lane) {
-        int64_t before = end_of_seq;
+        uint32_t before = end_of_seq;
         for (int b0 = seq + 1; b0 < P.num_seqs; b0 += 32) {
-            long long own = b0 + lane < P.num_seqs ? tree_units(P, request_of(P, b0 + lane, false)) : 0, upto = own;
+            Request own{};
+            if (b0 + lane < P.num_seqs) own = request_of(P, b0 + lane, false);
+            const uint32_t units = tree_units(P, own);
+            uint32_t upto = units;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
-                const long long y = __shfl_up_sync(pkv::kFullMask, upto, d);
+                const uint32_t y = __shfl_up_sync(pkv::kFullMask, upto, d);
                 if (lane >= d) upto += y;
             }
             const unsigned past = __ballot_sync(pkv::kFullMask, before + upto > at);
@@ -479,8 +488,10 @@ struct TreeWalk {
                 const int who = __ffs(past) - 1;
                 seq = b0 + who;
                 end_of_seq = before + __shfl_sync(pkv::kFullMask, upto, who);
-                begin_of_seq = end_of_seq - __shfl_sync(pkv::kFullMask, own, who);
-                r = request_of(P, seq, false);
+                begin_of_seq = end_of_seq - __shfl_sync(pkv::kFullMask, units, who);
+                r.start = __shfl_sync(pkv::kFullMask, own.start, who);
+                r.tokens = __shfl_sync(pkv::kFullMask, own.tokens, who);
+                r.keys = __shfl_sync(pkv::kFullMask, own.keys, who);
                 return;
             }
             before += __shfl_sync(pkv::kFullMask, upto, 31);
@@ -498,8 +509,8 @@ struct TreeWalk {
             }
             const int tiles = tree_tiles(r), pairs = tree_pairs(P, r), units = tiles + kItemUnits;
             const int item = static_cast<int>((at - begin_of_seq) / units);
-            const int from = static_cast<int>(at - begin_of_seq - static_cast<int64_t>(item) * units);
-            const int to = static_cast<int>(min(static_cast<int64_t>(units), from + (end - at)));
+            const int from = static_cast<int>(at - begin_of_seq) - item * units;
+            const int to = min(units, from + static_cast<int>(end - at));
             at += to - from;
             const int first = max(from - kItemUnits, 0);
             int past = to - kItemUnits;
@@ -529,14 +540,17 @@ struct TreeWalk {
                 it.kv_count[0] -= it.kv_count[1];
             }
             if (first == 0 && past < tiles) {  // the stretch's last
-                const int64_t end_of_item = begin_of_seq + static_cast<int64_t>(item + 1) * units;
-                part.last = tree_owner(plan, end_of_item - 1);
+                part.last = static_cast<int>(plan.owner(begin_of_seq + static_cast<uint32_t>(item + 1) * units - 1));
                 part.row0 = it.row0;
                 part.tokens = it.live[0] + (it.shared ? 0 : it.live[1]);
                 part.kvh = it.kvh;
                 part.base = r.keys - r.tokens;
                 part.nodes = r.tokens;
             }
+            // its first tile's table entries, near by the time the copies need them
+            const int block = first * kTileRows / P.block_size + lane;
+            if (lane < 8 && block < P.max_blocks)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(P.block_tables + static_cast<int64_t>(seq) * P.max_blocks + block));
             return it;
         }
         return it;
@@ -597,6 +611,34 @@ __device__ __forceinline__ void clean_values(uint32_t v, int valid, int part, in
     __syncwarp();
 }
 
+// The same for a tree's tile: only its rows from `from` on, the first that not every row of the item may see, up to the
+// last 16-key group that the MMAs take.
+__device__ __forceinline__ void clean_tail(uint32_t v, int from, int valid, int part, int lane, volatile uint32_t *dirty, uint32_t mark) {
+    auto bad_of = [](uint32_t w) { return ((w & 0x7c007c00u) + 0x04000400u) & 0x80008000u; };  // exponent 31, per half
+    const int upto = (valid + 15) & ~15;
+#pragma unroll 1
+    for (int row = (from & ~3) + 4 * part + (lane >> 3); row - (lane >> 3) < upto; row += 16) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const uint32_t at = v + half * kSlab + row * 128 + (lane & 7) * 16;
+            if (row >= valid) {
+                sts128(at, 0u, 0u, 0u, 0u);
+                continue;
+            }
+            const uint4 x = lds128v(at);
+            const uint32_t b[4] = {bad_of(x.x), bad_of(x.y), bad_of(x.z), bad_of(x.w)};
+            if (b[0] | b[1] | b[2] | b[3]) {
+                *dirty = mark;
+                __threadfence_block();  // whoever finds the zeros finds the mark
+                sts128(at, x.x & ~((b[0] >> 15) * 0xffffu), x.y & ~((b[1] >> 15) * 0xffffu), x.z & ~((b[2] >> 15) * 0xffffu),
+                       x.w & ~((b[3] >> 15) * 0xffffu));
+            }
+        }
+    }
+    pkv::fence_proxy_async_smem();  // before the arrival that lets the MMA read the tile
+    __syncwarp();
+}
+
 // Key tiles that an item's groups go through: the same ones, or each its own.
 __device__ __forceinline__ int key_tiles(bool shared, int a, int b) { return shared ? a + b : max(a, b); }
 
@@ -629,6 +671,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
     volatile uint32_t *dirty = reinterpret_cast<volatile uint32_t *>(smem + L::dirty);
     if (threadIdx.x < kItems) dirty[threadIdx.x] = 0;
     if (warp == kMmaWarp && aligned) pkv::tmem_alloc(pkv::smem_addr(tmem_slot), 512);
+    TreeWalk walk;
+    if constexpr (TREE) {  // the first item and the copies' descriptors are looked for while the rest is set up
+        if (warp == kLoadWarp && lane < 3)
+            asm volatile("prefetch.tensormap [%0];" ::"l"(lane == 0 ? &P.tmap_q : lane == 1 ? &P.tmap_k : &P.tmap_v) : "memory");
+        if (warp == kItemWarp) {
+            pkv::pdl_wait_primary();
+            walk.start(P, lane);
+        }
+    }
     pkv::tmem_fence_before_sync();
     __syncthreads();
     pkv::tmem_fence_after_sync();
@@ -649,27 +700,61 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
 
     if (warp >= kSoftmaxWarps) {
         shrink_registers<kOtherRegs>();
-        // The cache row at which this lane's box of a key tile starts (lane = 2 x box + half).
-        const int boxes_per_tile = PAGED ? kTileRows / P.box_rows : 1;
-        auto box_row = [&](int seq, int kvh, int keys, int tile) -> int {
-            const int key = tile * kTileRows + (lane >> 1) * P.box_rows;
-            if (!PAGED || lane >= 2 * boxes_per_tile || key >= keys) return 0;
-            int32_t id = __ldg(P.block_tables + static_cast<int64_t>(seq) * P.max_blocks + key / P.block_size);
+        // Where this lane's boxes of an item's key tiles start (lane = 2 x box + half), tile by tile without a division; their
+        // table entries are asked for two tiles ahead and looked at when their tile is copied.
+        const int boxes_per_tile = PAGED ? kTileRows >> P.box_log2 : 1;
+        const int step_blocks = PAGED ? kTileRows / P.block_size : 0, step_rest = PAGED ? kTileRows - step_blocks * P.block_size : 0;
+        struct Boxes {
+            const int32_t *entry;  // of the tile after next, and its key and row in the block
+            int key, offset;
+            int32_t id[2];
+            int row[2];
+        };
+        auto ask = [&](Boxes &x, int keys) {
+            x.id[0] = x.id[1];
+            x.row[0] = x.row[1];
+            x.id[1] = lane < 2 * boxes_per_tile && x.key < keys ? __ldg(x.entry) : 0;
+            x.row[1] = x.offset;
+            x.key += kTileRows;
+            x.entry += step_blocks;
+            x.offset += step_rest;
+            if (x.offset >= P.block_size) {
+                x.offset -= P.block_size;
+                ++x.entry;
+            }
+        };
+        auto begin_boxes = [&](int seq, int keys, int tile) {
+            Boxes x{};
+            if (!PAGED) return x;
+            x.key = tile * kTileRows + ((lane >> 1) << P.box_log2);
+            const int block = x.key / P.block_size;
+            x.entry = P.block_tables + static_cast<int64_t>(seq) * P.max_blocks + block;
+            x.offset = x.key - block * P.block_size;
+            ask(x, keys);
+            ask(x, keys);
+            return x;
+        };
+        // The cache row of the present tile's box; the next one becomes the present one.
+        auto next_row = [&](Boxes &x, int kvh, int keys) -> int {
+            if (!PAGED) return 0;
+            int32_t id = x.id[0];
+            const int offset = x.row[0];
             if (id < 0 || id >= P.num_blocks) {
                 pkv::record_error(&g_prompt_error, PKV_DEV_BAD_BLOCK_ID);
                 id = 0;
             }
-            return static_cast<int>((static_cast<int64_t>(id) * P.num_kv_heads + kvh) * P.block_size + key % P.block_size);
+            ask(x, keys);
+            return static_cast<int>((static_cast<int64_t>(id) * P.num_kv_heads + kvh) * P.block_size + offset);
         };
         // Copies of one K or V tile into a stage (box by box where paged; packed, rows past the sequence are
         // the next one's, past the tensor zeros).
         auto copy_tile = [&](const void *map, uint32_t dst, uint32_t full, int keys, int kvh, int tile, int first_row, int row) {
             if (PAGED) {
-                const int boxes = (min(kTileRows, keys - tile * kTileRows) + P.box_rows - 1) / P.box_rows;
-                if (lane == 0) pkv::mbar_arrive_expect_tx(full, boxes * P.box_rows * 256);
+                const int boxes = (min(kTileRows, keys - tile * kTileRows) + (1 << P.box_log2) - 1) >> P.box_log2;
+                if (lane == 0) pkv::mbar_arrive_expect_tx(full, boxes << (P.box_log2 + 8));
                 __syncwarp();
                 if (lane < 2 * boxes)
-                    pkv::tma_load_2d(dst + (lane & 1) * kSlab + (lane >> 1) * P.box_rows * 128, map, 64 * (lane & 1), row, full);
+                    pkv::tma_load_2d(dst + (lane & 1) * kSlab + ((lane >> 1) << (P.box_log2 + 7)), map, 64 * (lane & 1), row, full);
             } else if (lane == 0) {
                 pkv::mbar_arrive_expect_tx(full, kOperand);
                 for (int half = 0; half < 2; ++half)
@@ -693,7 +778,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                 return it.seq >= 0;
             };
             if constexpr (TREE) {
-                TreeWalk walk(P, lane);
                 for (uint32_t k = 0; publish(walk.next(P, lane), k); ++k) {
                 }
                 if (P.splits > 0 && lane == 0) P.tree_parts[blockIdx.x] = walk.part;
@@ -730,20 +814,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                 if (lane == 0) mbar_arrive(bar(kBarItemEmpty + slot));
                 if (it.seq < 0) break;
                 const int n_kv = key_tiles(it.shared, it.kv_count[0], it.kv_count[1]);
-                int row = box_row(it.seq, it.kvh, it.keys, it.kv_first);
-                for (int j = 0; j < n_kv; ++j, ++stage) {
-                    const int tile = it.kv_first + j, st = stage % kKRing;
-                    const int ahead = j + 1 < n_kv ? box_row(it.seq, it.kvh, it.keys, tile + 1) : 0;
-                    if (!(ok = wait(kBarKEmpty + st, stage / kKRing + 1))) break;
-                    copy_tile(&P.tmap_k, base + L::ring + st * kOperand, bar(kBarKFull + st), it.keys, it.kvh, tile,
-                              it.row0 - it.pos0, row);
-                    row = ahead;
-                    if (j > 0) continue;
-                    // The first K tile is under way: now Q, once the last item's Q K^T are done (it is brought near meanwhile).
-                    if (lane < (it.shared ? 2 : 4))
-                        tma_prefetch_3d(&P.tmap_q, 64 * (lane & 1), it.kvh << glog, it.row0 + (lane >> 1) * tile_tokens);
-                    __syncwarp();
-                    if (!(ok = wait(kBarQEmpty, loaded + 1))) break;
+                auto load_q = [&]() {
+                    if (!wait(kBarQEmpty, loaded + 1)) return false;
                     ++loaded;
                     if (lane == 0) {
                         const int tiles = it.shared ? 1 : 2;
@@ -754,6 +826,22 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                                                  it.row0 + t * tile_tokens, bar(kBarQFull));
                     }
                     __syncwarp();
+                    return true;
+                };
+                Boxes boxes = begin_boxes(it.seq, it.keys, it.kv_first);
+                const bool q_first = loaded == 0;  // its buffer is free, and K's block ids are still on their way
+                if (q_first && n_kv > 0 && !(ok = load_q())) break;
+                for (int j = 0; j < n_kv; ++j, ++stage) {
+                    const int tile = it.kv_first + j, st = stage % kKRing;
+                    if (!(ok = wait(kBarKEmpty + st, stage / kKRing + 1))) break;
+                    copy_tile(&P.tmap_k, base + L::ring + st * kOperand, bar(kBarKFull + st), it.keys, it.kvh, tile,
+                              it.row0 - it.pos0, next_row(boxes, it.kvh, it.keys));
+                    if (j > 0 || q_first) continue;
+                    // The first K tile is under way: now Q, once the last item's Q K^T are done (it is brought near meanwhile).
+                    if (lane < (it.shared ? 2 : 4))
+                        tma_prefetch_3d(&P.tmap_q, 64 * (lane & 1), it.kvh << glog, it.row0 + (lane >> 1) * tile_tokens);
+                    __syncwarp();
+                    if (!(ok = load_q())) break;
                 }
             }
             if (!ok) {  // copies still in flight land before the CTA's memory goes (bounded)
@@ -774,13 +862,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(kBarItemEmpty + slot));
                 if (seq < 0) break;
-                int row = n_kv > 0 ? box_row(seq, kvh, keys, first) : 0;
+                Boxes boxes = begin_boxes(seq, keys, first);
                 for (int j = 0; j < n_kv; ++j, ++stage) {
                     const int tile = first + j, st = stage % kVRing;
-                    const int ahead = j + 1 < n_kv ? box_row(seq, kvh, keys, tile + 1) : 0;
                     if (!(ok = wait(kBarVEmpty + st, stage / kVRing + 1))) break;
-                    copy_tile(&P.tmap_v, base + L::values + st * kOperand, bar(kBarVFull + st), keys, kvh, tile, first_row, row);
-                    row = ahead;
+                    copy_tile(&P.tmap_v, base + L::values + st * kOperand, bar(kBarVFull + st), keys, kvh, tile, first_row,
+                              next_row(boxes, kvh, keys));
                 }
             }
             if (!ok)
@@ -918,6 +1005,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
             const uint32_t *const row_mask =
                 TREE ? P.tree_mask + (static_cast<int64_t>(slot_row0) + tile * tile_tokens + min(tok, live - 1)) * P.mask_words : nullptr;
             const int nodes = TREE ? static_cast<int>(i1.w) - pos0 - 1 : 0;
+            const bool dead = TREE && (warp & 3) * 32 >= live << glog;
             const int n_kv = key_tiles(shared, n, n_of_other), keys = i1.w;
             float m_ref = -INFINITY, l = 0.f;  // what weights are relative to: kLift below a score, so that they reach 2^kLift
             for (int j = 0; j < n; ++j) {
@@ -949,11 +1037,19 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                     }
                     if (!cleaned && (early || step == 1)) {
                         if (!(ok = wait(kBarVFull + vs % kVRing, vs / kVRing))) break;
-                        clean_values(v, min(kTileRows, keys - key0), warp & 3, lane, dirty + k % kItems, k + 1);
+                        if (TREE)
+                            clean_tail(v, max(pos0 + 1 - key0, 0), min(kTileRows, keys - key0), warp & 3, lane, dirty + k % kItems, k + 1);
+                        else
+                            clean_values(v, min(kTileRows, keys - key0), warp & 3, lane, dirty + k % kItems, k + 1);
                         cleaned = true;
                     }
                 }
                 if (!ok) break;
+                if (TREE && dead) {  // no row of this warp's is stored: whatever its lanes hold may stand for their weights
+                    if (lane < 2) mbar_arrive(bar(kBarP + 2 * t + lane));
+                    __syncwarp();
+                    continue;
+                }
                 pkv::tmem_fence_after_sync();
                 uint32_t s0[64], s1[64];
                 tmem_ld64(t_s, s0);
@@ -961,9 +1057,20 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                 tmem_ld64(t_s + 64, s1);
                 const bool masked = TREE ? border : key0 + kTileRows - 1 > tile_pos;  // the causal border, or the context's end
                 const int lim = pos - key0;
-                if (masked) {
+                // of a tree's tile, 32 keys that some row does not see
+                auto hide = [&](uint32_t(&x)[64], int c0, uint32_t bits) {
+                    if (__all_sync(pkv::kFullMask, bits == 0xffffffffu)) return;
 #pragma unroll
-                    for (int c = 0; c < 64; ++c) s0[c] = (TREE ? (seen[c >> 5] >> (c & 31) & 1) != 0 : c <= lim) ? s0[c] : 0xff800000u;
+                    for (int c = 0; c < 32; ++c) x[c0 + c] = bits & (1u << c) ? x[c0 + c] : 0xff800000u;
+                };
+                if (masked) {
+                    if constexpr (TREE) {
+                        hide(s0, 0, seen[0]);
+                        hide(s0, 32, seen[1]);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 64; ++c) s0[c] = c <= lim ? s0[c] : 0xff800000u;
+                    }
                 }
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -971,9 +1078,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                     mx[(c >> 1) & 3] = fmaxf(fmaxf(mx[(c >> 1) & 3], __uint_as_float(s0[c])), __uint_as_float(s0[c + 1]));
                 tmem_landed(s1);
                 if (masked) {
+                    if constexpr (TREE) {
+                        hide(s1, 0, seen[2]);
+                        hide(s1, 32, seen[3]);
+                    } else {
 #pragma unroll
-                    for (int c = 0; c < 64; ++c)
-                        s1[c] = (TREE ? (seen[2 + (c >> 5)] >> (c & 31) & 1) != 0 : 64 + c <= lim) ? s1[c] : 0xff800000u;
+                        for (int c = 0; c < 64; ++c) s1[c] = 64 + c <= lim ? s1[c] : 0xff800000u;
+                    }
                 }
 #pragma unroll
                 for (int c = 0; c < 64; c += 2)
@@ -1054,25 +1165,102 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
             w_own *= inv;
             w_other *= inv;
             const int64_t row = q_row * P.num_q_heads + (kvh << glog) + (r & ((1 << glog) - 1));
-            if (n > 0 || n_other > 0) {
+            if constexpr (TREE) {
+                // 128 bytes of each row at a time (64 fp16 dims, or 32 float32 ones of a partial result) through the warp's own
+                // 4 KB, as below, in code as short as it can be: it is run once an item, and instructions that have left the
+                // caches meanwhile cost more than they do.
+                if (!dead) {
+                    const bool whole = split < 0;
+                    const uint32_t lines = base + L::staging + warp * 4096, mine = lines + lane * 128;
+                    const int row_bytes = whole ? kDim * 2 : kDim * 4, group_mask = (1 << glog) - 1;
+                    unsigned char *const dst =
+                        whole ? reinterpret_cast<unsigned char *>(P.out) +
+                                    ((static_cast<int64_t>(slot_row0) + tile * tile_tokens) * P.num_q_heads + (kvh << glog)) * row_bytes
+                              : reinterpret_cast<unsigned char *>(P.o_part) + (static_cast<int64_t>(split) * P.slot_rows + tile * kTileRows) * row_bytes;
+                    const int c_begin = shared ? t * (kDim / 2) : 0, c_end = shared ? c_begin + kDim / 2 : kDim;
+                    const uint32_t t_other = tmem + lanes + 2 * kTileRows + (t ^ 1) * kDim;
+#pragma unroll 1
+                    for (int c = c_begin; c < c_end; c += 32) {
+                        uint32_t o[32];
+                        if (n > 0) pkv::tmem_ld32(t_o + c, o);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = n > 0 ? __float_as_uint(__uint_as_float(o[i]) * w_own) : 0u;
+                        if (n_other > 0) {
+                            uint32_t q[32];
+                            pkv::tmem_ld32(t_other + c, q);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(fmaf(__uint_as_float(q[i]), w_other, __uint_as_float(o[i])));
+                        }
+                        if (whole) {
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) {
+                                uint32_t w[4];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    const __half2 v = __floats2half2_rn(__uint_as_float(o[8 * u + 2 * i]), __uint_as_float(o[8 * u + 2 * i + 1]));
+                                    w[i] = *reinterpret_cast<const uint32_t *>(&v);
+                                }
+                                sts128(mine + ((((c >> 3) & 4) + u) ^ (lane & 7)) * 16, w[0], w[1], w[2], w[3]);
+                            }
+                            if (!(c & 32)) continue;  // (c_begin is a multiple of 64)
+                        } else {
+#pragma unroll
+                            for (int u = 0; u < 8; ++u) sts128(mine + ((u ^ (lane & 7)) << 4), o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+                        }
+                        __syncwarp();
+                        const int from = whole ? (c & 64) * 2 : c * 4;  // of the row's bytes
+#pragma unroll 4
+                        for (int i = 0; i < 8; ++i) {
+                            const int x = 4 * i + (lane >> 3), in_tile = (warp & 3) * 32 + x;
+                            const uint4 v = lds128v(lines + x * 128 + (((lane & 7) ^ (x & 7)) << 4));
+                            const int to = whole ? (in_tile >> glog) * P.num_q_heads + (in_tile & group_mask) : in_tile;
+                            if ((in_tile >> glog) < live) *reinterpret_cast<uint4 *>(dst + static_cast<int64_t>(to) * row_bytes + from + (lane & 7) * 16) = v;
+                        }
+                        __syncwarp();
+                    }
+                    if (dirty[k % kItems] == k + 1 && store) {
+                        // Infinities and NaN that were taken out of V: every row that sees their key gets them whole (an infinity times
+                        // a weight above 0 is one; a weight that underflowed is taken for one above 0).
+                        const int to = whole ? tok * P.num_q_heads + (r & group_mask) : r;
+                        for (int key = max(pos0 / kTileRows, first) * kTileRows; key < min(static_cast<int>(i1.w), (first + n_kv) * kTileRows); ++key) {
+                            const int node = key - pos0 - 1;
+                            if (node >= 0 && !(tree_word(row_mask, node >> 5, nodes) >> (node & 31) & 1)) continue;
+                            const int32_t id = __ldg(P.block_tables + static_cast<int64_t>(i0.x) * P.max_blocks + key / P.block_size);
+                            const __half *const row_v = P.v + ((static_cast<int64_t>(id < 0 || id >= P.num_blocks ? 0 : id) * P.num_kv_heads + kvh) * P.block_size +
+                                                               key % P.block_size) * kDim;
+#pragma unroll 1
+                            for (int i = c_begin; i < c_end; ++i) {
+                                const float x = __half2float(row_v[i]);
+                                if (isfinite(x)) continue;
+                                unsigned char *const at = dst + static_cast<int64_t>(to) * row_bytes;
+                                if (whole) {
+                                    __half *const h = reinterpret_cast<__half *>(at) + i;
+                                    *h = __float2half_rn(__half2float(*h) + x);
+                                } else {
+                                    reinterpret_cast<float *>(at)[i] += x;
+                                }
+                            }
+                        }
+                    }
+                }
+                pkv::tmem_fence_before_sync();  // O read before the next item's first P V (ordered by its weights' arrival)
+            } else if (n > 0 || n_other > 0) {
                 // 128 bytes of each row at a time (64 fp16 dims, or 32 float32 ones of a partial result) through the
                 // warp's own 4 KB, so that eight lanes store a whole line.  The 16-byte pieces of row x lie at piece
                 // ^ (x % 8).  Lane's share of a line: piece lane % 8 of rows 4 i + lane / 8.
                 const bool whole = split < 0;
                 const uint32_t lines = base + L::staging + warp * 4096, mine = lines + lane * 128;
-                const bool in_slot = TREE && !whole;  // a slot's rows lie one behind another
-                const uint32_t row_bytes = whole ? kDim * 2 : (TREE ? 1 : P.splits) * kDim * 4;
+                const uint32_t row_bytes = whole ? kDim * 2 : P.splits * kDim * 4;
                 const int group_mask = (1 << glog) - 1;
-                const int64_t first_row = in_slot ? static_cast<int64_t>(split) * P.slot_rows + tile * kTileRows
-                                                  : (static_cast<int64_t>(slot_row0) + tile * tile_tokens) * P.num_q_heads + (kvh << glog);
                 unsigned char *const dst = reinterpret_cast<unsigned char *>(whole ? static_cast<void *>(P.out) : static_cast<void *>(P.o_part)) +
-                                           first_row * row_bytes + (whole || TREE ? 0 : split * kDim * 4) + (lane & 7) * 16;
+                                           ((static_cast<int64_t>(slot_row0) + tile * tile_tokens) * P.num_q_heads + (kvh << glog)) * row_bytes +
+                                           (whole ? 0 : split * kDim * 4) + (lane & 7) * 16;
                 uint32_t offset[8];  // of the lane's rows, from the tile's first (under 2^32: 128 tokens' rows)
                 bool keep[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int x = (warp & 3) * 32 + 4 * i + (lane >> 3);
-                    offset[i] = (in_slot ? x : (x >> glog) * P.num_q_heads + (x & group_mask)) * row_bytes;
+                    offset[i] = ((x >> glog) * P.num_q_heads + (x & group_mask)) * row_bytes;
                     keep[i] = (x >> glog) < live;
                 }
                 auto store_line = [&](int line) {
@@ -1115,9 +1303,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                     if (dirty[k % kItems] == k + 1) {
                         // Infinities and NaN that were taken out of V: every row that sees their key gets them whole
                         // (an infinity times a weight above 0 is one; a weight that underflowed is taken for one above 0).
-                        const int last = TREE ? static_cast<int>(i1.w) - 1 : pos;
-                        for (int key = max(pos0 / kTileRows, first) * kTileRows; key <= last && key < (first + n_kv) * kTileRows; ++key) {
-                            if (TREE && key > pos0 && !(tree_word(row_mask, (key - pos0 - 1) >> 5, nodes) >> ((key - pos0 - 1) & 31) & 1)) continue;
+                        for (int key = max(pos0 / kTileRows, first) * kTileRows; key <= pos && key < (first + n_kv) * kTileRows; ++key) {
                             const __half *row_v;
                             if (PAGED) {
                                 const int32_t id = __ldg(P.block_tables + static_cast<int64_t>(i0.x) * P.max_blocks + key / P.block_size);
@@ -1946,7 +2132,11 @@ int paged_params(PromptParams *params, void *out, float *lse, const void *q, int
     p.group_log2 = log2_of(num_q_heads / num_kv_heads);
     p.q_scale = scale * kLog2e;
     p.box_rows = kTileRows;
-    while (block_size % p.box_rows != 0) p.box_rows /= 2;  // a box never leaves its block: 16 at least
+    p.box_log2 = 7;
+    while (block_size % p.box_rows != 0) {  // a box never leaves its block: 16 at least
+        p.box_rows /= 2;
+        --p.box_log2;
+    }
     return PKV_OK;
 }
 
@@ -2045,6 +2235,12 @@ extern "C" PKV_API int pkv_decode_attention_tree(void *out, float *lse, const vo
     if (mask_words < 0 || static_cast<int64_t>(mask_words) * 32 < max_query_len) return PKV_ERR_INVALID_ARG;
     if (done) return PKV_OK;
     if (!tree_mask || !pkv_internal::aligned(tree_mask, 4)) return PKV_ERR_INVALID_ARG;
+    {  // the call's stretch of key tiles is counted in 32 bits
+        const int pair_tokens = 2 * kTileRows >> p.group_log2;
+        const int64_t tiles = (static_cast<int64_t>(max_blocks_per_seq) * block_size + kTileRows - 1) / kTileRows;
+        const int64_t items = static_cast<int64_t>(num_seqs) * ((max_query_len + pair_tokens - 1) / pair_tokens) * num_kv_heads;
+        if (items >= (1LL << 31) / (tiles + kItemUnits)) return PKV_ERR_UNSUPPORTED;
+    }
     const TreeSizes sizes = tree_sizes(num_seqs, total_q, max_query_len, num_q_heads, num_kv_heads,
                                        static_cast<int64_t>(max_blocks_per_seq) * block_size);
     if (sizes.split) {
