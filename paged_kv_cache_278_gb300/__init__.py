@@ -488,6 +488,16 @@ def decode_step_int8k(out: torch.Tensor, q: torch.Tensor, k_new: torch.Tensor, v
 # ---------------------------------------------------------------- int8 keys and values
 
 def _int8kv_shape(k_codes, k_scale, v_codes, v_scale, codes=torch.int8):
+    try:
+        shape, at = k_codes.shape, k_codes.get_device()
+        if (len(shape) == 4 and v_codes.shape == shape and k_scale.shape == shape[:3] == v_scale.shape and at >= 0
+                and k_codes.dtype is codes and v_codes.dtype is codes and k_scale.dtype is torch.float32
+                and v_scale.dtype is torch.float32 and v_codes.get_device() == at and k_scale.get_device() == at
+                and v_scale.get_device() == at and k_codes.is_contiguous() and v_codes.is_contiguous()
+                and k_scale.is_contiguous() and v_scale.is_contiguous()):
+            return shape
+    except AttributeError:
+        pass
     _need(k_codes, "k_codes", codes, 4)
     dev = k_codes.device
     _need(v_codes, "v_codes", codes, 4, dev)
@@ -733,8 +743,9 @@ def _device_of(t: torch.Tensor, name: str) -> torch.device:
 def _need_rows(t: torch.Tensor, name: str, device, shape=None):
     """fp16 [tokens, heads, dim] whose heads lie together; returns the elements between tokens."""
     try:
-        if t.dtype is torch.float16 and t.get_device() == device.index and (t.dim() == 3 if shape is None else t.shape == shape):
-            n, h, d = t.shape
+        own = t.shape
+        if t.dtype is torch.float16 and t.get_device() == device.index and (len(own) == 3 if shape is None else own == shape):
+            n, h, d = own
             s0, s1, s2 = t.stride()
             if s2 == 1 and s1 == d:
                 return s0 if n > 1 else h * d
@@ -812,29 +823,37 @@ def rope_axes(sections, device="cuda") -> torch.Tensor:
     return torch.tensor([a for a, n in enumerate(sections) for _ in range(n)], dtype=torch.int32, device=device)
 
 
-def _norm_inputs(q, positions, frequencies, q_weight, k_weight, axes, device):
-    """The checked arguments the norm_rope calls share: axes' pointer, number of axes, weights' pointers, rotary_dim."""
+def _norm_inputs(t, d, positions, frequencies, q_weight, k_weight, axes, device):
+    """The checked arguments the norm_rope calls share for t tokens: positions', axes', frequencies' and weights' pointers,
+    the number of axes, rotary_dim."""
     if not isinstance(positions, torch.Tensor):
         raise TypeError("positions must be a torch.Tensor")
-    _need(positions, "positions", torch.int32, 2 if positions.dim() == 2 else 1, device)
+    ndim = positions.dim()
+    _need(positions, "positions", torch.int32, 2 if ndim == 2 else 1, device)
     _need(frequencies, "frequencies", torch.int64, 1, device)
-    t, _, d = q.shape
-    if positions.shape[0] != t:
+    if positions.size(0) != t:
         raise ValueError("positions must have one entry (or row) per token")
-    n = positions.shape[1] if positions.dim() == 2 else 1
+    pairs, n, ax, qw, kw = frequencies.numel(), 1, None, None, None
+    if ndim == 2:
+        n = positions.size(1)
     if axes is not None:
         _need(axes, "axes", torch.int32, 1, device)
-        if axes.shape[0] != frequencies.shape[0]:
+        if axes.numel() != pairs:
             raise ValueError("axes must have one entry per pair")
+        ax = axes.data_ptr()
     elif n != 1:
         raise ValueError("positions of several axes need axes")
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _need(w, name, torch.float32, 1, device)
-            if w.shape[0] != d:
-                raise ValueError(f"{name} must be [{d}]")
-    pointer = lambda x: None if x is None else x.data_ptr()  # noqa: E731
-    return pointer(axes), n, pointer(q_weight), pointer(k_weight), 2 * frequencies.shape[0]
+    if q_weight is not None:
+        _need(q_weight, "q_weight", torch.float32, 1, device)
+        if q_weight.numel() != d:
+            raise ValueError(f"q_weight must be [{d}]")
+        qw = q_weight.data_ptr()
+    if k_weight is not None:
+        _need(k_weight, "k_weight", torch.float32, 1, device)
+        if k_weight.numel() != d:
+            raise ValueError(f"k_weight must be [{d}]")
+        kw = k_weight.data_ptr()
+    return positions.data_ptr(), ax, n, frequencies.data_ptr(), qw, kw, 2 * pairs
 
 
 def norm_rope(q_out: torch.Tensor, k_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor,
@@ -849,24 +868,26 @@ def norm_rope(q_out: torch.Tensor, k_out: torch.Tensor, q: torch.Tensor, k: torc
     ks = _need_rows(k, "k", dev, (q.shape[0], k.shape[1], q.shape[2]) if k.dim() == 3 else None)
     qos = _need_rows(q_out, "q_out", dev, q.shape)
     kos = _need_rows(k_out, "k_out", dev, k.shape)
-    ax, n, qw, kw, r = _norm_inputs(q, positions, frequencies, q_weight, k_weight, axes, dev)
+    t, hq, d = q.shape
+    *shared, r = _norm_inputs(t, d, positions, frequencies, q_weight, k_weight, axes, dev)
     _call("pkv_norm_rope", dev, stream, q_out.data_ptr(), qos, k_out.data_ptr(), kos, q.data_ptr(), qs, k.data_ptr(), ks,
-          positions.data_ptr(), ax, n, frequencies.data_ptr(), qw, kw, float(eps), q.shape[0], q.shape[1], k.shape[1],
-          q.shape[2], r, int(bool(interleaved)), float(magnitude))
+          *shared, eps, t, hq, k.shape[1], d, r, 1 if interleaved else 0, magnitude)
 
 
 def _norm_append_rows(q_out, q, k_new, v_new, slot_mapping, hkv, d, dev):
     qs = _need_rows(q, "q", dev)
-    t = q.shape[0]
-    if q.shape[2] != d:
+    shape = q.shape
+    t, hq, dq = shape
+    if dq != d:
         raise ValueError("q head_dim differs from the cache's")
-    qos = _need_rows(q_out, "q_out", dev, q.shape)
-    ks = _need_rows(k_new, "k_new", dev, (t, hkv, d))
-    vs = _need_rows(v_new, "v_new", dev, (t, hkv, d))
+    qos = _need_rows(q_out, "q_out", dev, shape)
+    new = (t, hkv, d)
+    ks = _need_rows(k_new, "k_new", dev, new)
+    vs = _need_rows(v_new, "v_new", dev, new)
     _need(slot_mapping, "slot_mapping", torch.int64, 1, dev)
-    if slot_mapping.shape[0] != t:
+    if slot_mapping.numel() != t:
         raise ValueError("slot_mapping must have one entry per token")
-    return (q_out.data_ptr(), qos, q.data_ptr(), qs, k_new.data_ptr(), ks, v_new.data_ptr(), vs), t
+    return (q_out.data_ptr(), qos, q.data_ptr(), qs, k_new.data_ptr(), ks, v_new.data_ptr(), vs), t, hq
 
 
 def norm_rope_append(q_out: torch.Tensor, q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, k_cache: torch.Tensor,
@@ -877,11 +898,10 @@ def norm_rope_append(q_out: torch.Tensor, q: torch.Tensor, k_new: torch.Tensor, 
     (int64; -1 = skip), v_new copied there.  Rows as rope's."""
     nb, hkv, bs, d = _cache_shape(k_cache, v_cache)
     dev = k_cache.device
-    rows, t = _norm_append_rows(q_out, q, k_new, v_new, slot_mapping, hkv, d, dev)
-    ax, n, qw, kw, r = _norm_inputs(q, positions, frequencies, q_weight, k_weight, axes, dev)
+    rows, t, hq = _norm_append_rows(q_out, q, k_new, v_new, slot_mapping, hkv, d, dev)
+    *shared, r = _norm_inputs(t, d, positions, frequencies, q_weight, k_weight, axes, dev)
     _call("pkv_norm_rope_append", dev, stream, *rows, k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(),
-          positions.data_ptr(), ax, n, frequencies.data_ptr(), qw, kw, float(eps), t, q.shape[1], hkv, d, r, bs, nb,
-          int(bool(interleaved)), float(magnitude))
+          *shared, eps, t, hq, hkv, d, r, bs, nb, 1 if interleaved else 0, magnitude)
 
 
 def norm_rope_append_fp8kv(q_out: torch.Tensor, q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
@@ -894,11 +914,11 @@ def norm_rope_append_fp8kv(q_out: torch.Tensor, q: torch.Tensor, k_new: torch.Te
     as append_fp8kv does it."""
     nb, hkv, bs, d = _int8kv_shape(k_codes, k_scale, v_codes, v_scale, torch.uint8)
     dev = k_codes.device
-    rows, t = _norm_append_rows(q_out, q, k_new, v_new, slot_mapping, hkv, d, dev)
-    ax, n, qw, kw, r = _norm_inputs(q, positions, frequencies, q_weight, k_weight, axes, dev)
+    rows, t, hq = _norm_append_rows(q_out, q, k_new, v_new, slot_mapping, hkv, d, dev)
+    *shared, r = _norm_inputs(t, d, positions, frequencies, q_weight, k_weight, axes, dev)
     _call("pkv_norm_rope_append_fp8kv", dev, stream, *rows, k_codes.data_ptr(), k_scale.data_ptr(), v_codes.data_ptr(),
-          v_scale.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(), ax, n, frequencies.data_ptr(), qw, kw,
-          float(eps), t, q.shape[1], hkv, d, r, bs, nb, int(bool(interleaved)), float(magnitude))
+          v_scale.data_ptr(), slot_mapping.data_ptr(), *shared, eps, t, hq, hkv, d, r, bs, nb, 1 if interleaved else 0,
+          magnitude)
 
 
 def read_blocks_fp8kv(k_cache: torch.Tensor, v_cache: torch.Tensor, k_codes: torch.Tensor, k_scale: torch.Tensor,
