@@ -52,6 +52,7 @@
 #include "pkv.h"
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
+#include "pkv_tree.cuh"
 
 namespace {
 
@@ -419,8 +420,8 @@ constexpr int kLeastUnits = 6;  // of a CTA's stretch
 
 __device__ __forceinline__ int tree_tiles(const Request &r) { return (r.keys + kTileRows - 1) / kTileRows; }
 __device__ __forceinline__ int tree_pairs(const PromptParams &P, const Request &r) {
-    const int pair_tokens = 2 * kTileRows >> P.group_log2;
-    return (r.tokens + pair_tokens - 1) / pair_tokens;
+    const int pair_log2 = 8 - P.group_log2;  // of the tokens in 256 rows
+    return (r.tokens + (1 << pair_log2) - 1) >> pair_log2;
 }
 __device__ __forceinline__ uint32_t tree_units(const PromptParams &P, const Request &r) {  // (the host bounds their sum)
     return r.tokens > 0 ? static_cast<uint32_t>(tree_pairs(P, r)) * P.num_kv_heads * (tree_tiles(r) + kItemUnits) : 0u;
@@ -446,57 +447,89 @@ struct TreePlan {
     }
 };
 
-// Goes through one CTA's stretch, piece by piece (one warp, the same in all lanes).
+// Goes through one CTA's stretch, piece by piece (one warp, the same in all lanes).  A window is 128 requests, four
+// neighbouring ones a lane, whose loads are all on their way at once; most calls have one.
+constexpr int kWindow = 128;
 struct TreeWalk {
     TreePlan plan;
     uint32_t at, end, begin_of_seq, end_of_seq;
     int seq;
     Request r;
     TreePart part;
+    int window;          // the window's first request
+    uint32_t own[4];     // the lane's requests' units
+    uint32_t upto;       // units of the window up to the lane's last request
+    uint32_t before;     // units before the window
 
-    __device__ void start(const PromptParams &P, int lane) {
+    __device__ void read(const PromptParams &P, int first, int lane, bool report) {
+        window = first;
         uint32_t sum = 0;
-#pragma unroll 2
-        for (int b = lane; b < P.num_seqs; b += 32) sum += tree_units(P, request_of(P, b, blockIdx.x == 0));
-        plan.make(P, __reduce_add_sync(pkv::kFullMask, sum));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int b = first + 4 * lane + i;
+            own[i] = b < P.num_seqs ? tree_units(P, request_of(P, b, report)) : 0;
+            sum += own[i];
+        }
+        upto = sum;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint32_t y = __shfl_up_sync(pkv::kFullMask, upto, d);
+            if (lane >= d) upto += y;
+        }
+    }
+    __device__ void start(const PromptParams &P, int lane) {
+        before = 0;
+        read(P, 0, lane, blockIdx.x == 0);
+        uint32_t sum = __shfl_sync(pkv::kFullMask, upto, 31);
+        if (P.num_seqs > kWindow) {
+            for (int first = kWindow; first < P.num_seqs; first += kWindow) {
+                read(P, first, lane, blockIdx.x == 0);
+                sum += __shfl_sync(pkv::kFullMask, upto, 31);
+            }
+            read(P, 0, lane, false);
+        }
+        plan.make(P, sum);
         const uint32_t cta = blockIdx.x;
         at = end = 0;
         if (cta < plan.ctas && plan.units > 0) {
             at = plan.begin(cta);
             end = plan.begin(cta + 1);
         }
-        seq = -1;
         begin_of_seq = end_of_seq = 0;
         part = TreePart{};
         part.last = -1;
     }
-    // The request that unit `at` belongs to, from the one behind the present one on.
+    // The request that unit `at` belongs to, in this window or a later one.
     __device__ void seek(const PromptParams &P, int lane) {
-        uint32_t before = end_of_seq;
-        for (int b0 = seq + 1; b0 < P.num_seqs; b0 += 32) {
-            Request own{};
-            if (b0 + lane < P.num_seqs) own = request_of(P, b0 + lane, false);
-            const uint32_t units = tree_units(P, own);
-            uint32_t upto = units;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const uint32_t y = __shfl_up_sync(pkv::kFullMask, upto, d);
-                if (lane >= d) upto += y;
-            }
+        for (;;) {
             const unsigned past = __ballot_sync(pkv::kFullMask, before + upto > at);
             if (past) {
                 const int who = __ffs(past) - 1;
-                seq = b0 + who;
-                end_of_seq = before + __shfl_sync(pkv::kFullMask, upto, who);
-                begin_of_seq = end_of_seq - __shfl_sync(pkv::kFullMask, units, who);
-                r.start = __shfl_sync(pkv::kFullMask, own.start, who);
-                r.tokens = __shfl_sync(pkv::kFullMask, own.tokens, who);
-                r.keys = __shfl_sync(pkv::kFullMask, own.keys, who);
+                end_of_seq = before + __shfl_sync(pkv::kFullMask, upto, who);  // (of the lane's last request, so far)
+                int i = 3;
+                uint32_t units = __shfl_sync(pkv::kFullMask, own[3], who);
+#pragma unroll
+                for (int k = 2; k >= 0; --k) {
+                    const uint32_t less = __shfl_sync(pkv::kFullMask, own[k], who);
+                    if (i == k + 1 && end_of_seq - units > at) {
+                        end_of_seq -= units;
+                        units = less;
+                        i = k;
+                    }
+                }
+                begin_of_seq = end_of_seq - units;
+                seq = window + 4 * who + i;
+                r = request_of(P, seq, false);
                 return;
             }
-            before += __shfl_sync(pkv::kFullMask, upto, 31);
+            const uint32_t all = __shfl_sync(pkv::kFullMask, upto, 31);
+            if (window + kWindow >= P.num_seqs) {
+                at = end;  // (not reached: `at` lies before the call's last unit)
+                return;
+            }
+            before += all;
+            read(P, window + kWindow, lane, false);
         }
-        at = end;  // (not reached: `at` lies before the call's last unit)
     }
     __device__ Item next(const PromptParams &P, int lane) {
         const int tile_tokens = kTileRows >> P.group_log2;
@@ -508,7 +541,7 @@ struct TreeWalk {
                 continue;
             }
             const int tiles = tree_tiles(r), pairs = tree_pairs(P, r), units = tiles + kItemUnits;
-            const int item = static_cast<int>((at - begin_of_seq) / units);
+            const int item = static_cast<int>((at - begin_of_seq) / static_cast<uint32_t>(units));
             const int from = static_cast<int>(at - begin_of_seq) - item * units;
             const int to = min(units, from + static_cast<int>(end - at));
             at += to - from;
@@ -520,7 +553,7 @@ struct TreeWalk {
             }
             if (past <= first) continue;
             it.seq = seq;
-            it.kvh = item / pairs;
+            it.kvh = pairs == 1 ? item : item / pairs;
             const int t0 = (item - it.kvh * pairs) * 2 * tile_tokens;
             const int cta = static_cast<int>(blockIdx.x);
             it.split = first > 0 ? 2 * cta : (past < tiles ? 2 * cta + 1 : -1);
@@ -547,29 +580,11 @@ struct TreeWalk {
                 part.base = r.keys - r.tokens;
                 part.nodes = r.tokens;
             }
-            // its first tile's table entries, near by the time the copies need them
-            const int block = first * kTileRows / P.block_size + lane;
-            if (lane < 8 && block < P.max_blocks)
-                asm volatile("prefetch.global.L2 [%0];" ::"l"(P.block_tables + static_cast<int64_t>(seq) * P.max_blocks + block));
             return it;
         }
         return it;
     }
 };
-
-// Word `i` of a node's mask: all ones before the tree, nothing behind its last node.
-__device__ __forceinline__ uint32_t tree_word(const uint32_t *mask, int i, int tokens) {
-    if (i < 0) return 0xffffffffu;
-    const int left = tokens - 32 * i;
-    if (left <= 0) return 0u;
-    return __ldg(mask + i) & (left >= 32 ? 0xffffffffu : (1u << left) - 1u);
-}
-// Whether a row of a tree sees nothing at all.
-__device__ __forceinline__ bool tree_blind(const uint32_t *mask, int base, int tokens) {
-    uint32_t any = base > 0;
-    for (int i = 0; i * 32 < tokens; ++i) any |= tree_word(mask, i, tokens);
-    return any == 0;
-}
 
 // V rows of a tile that not every row of the item may see: weights there can be 0, and 0 x inf is NaN.  A group's
 // four warps (`part` 0-3) go over the tile before its weights are delivered: rows past the context become
@@ -1001,11 +1016,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
             if (lane == 0) mbar_arrive(bar(kBarItemEmpty + slot));
             if (seq < 0) break;
             const int pos = tile_pos + min(tok, live - 1);  // rows past the last token: computed like it, never stored
-            // of a tree: the row's mask, the tree's nodes
-            const uint32_t *const row_mask =
-                TREE ? P.tree_mask + (static_cast<int64_t>(slot_row0) + tile * tile_tokens + min(tok, live - 1)) * P.mask_words : nullptr;
-            const int nodes = TREE ? static_cast<int>(i1.w) - pos0 - 1 : 0;
-            const bool dead = TREE && (warp & 3) * 32 >= live << glog;
+            // Of a tree: the row's mask and the tree's nodes.  (Made anew where they are used: the registers of the loop over
+            // the tiles are all taken.)
+            auto row_mask = [&]() {
+                return P.tree_mask + (static_cast<int64_t>(slot_row0) + tile * tile_tokens + min(tok, live - 1)) * P.mask_words;
+            };
+            auto nodes = [&]() { return static_cast<int>(i1.w) - pos0 - 1; };
+            auto dead = [&]() { return TREE && (warp & 3) * 32 >= live << glog; };
             const int n_kv = key_tiles(shared, n, n_of_other), keys = i1.w;
             float m_ref = -INFINITY, l = 0.f;  // what weights are relative to: kLift below a score, so that they reach 2^kLift
             for (int j = 0; j < n; ++j) {
@@ -1021,10 +1038,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                 uint32_t seen[4];  // of a tree's row: the tile's keys that it sees
                 if (TREE && border) {
                     const int from = key0 - pos0 - 1;  // the node at the tile's first key
-                    uint32_t lo = tree_word(row_mask, from >> 5, nodes);
+                    const uint32_t *const mask = row_mask();
+                    uint32_t lo = pkv::tree_word(mask, from >> 5, nodes());
 #pragma unroll
                     for (int w = 0; w < 4; ++w) {
-                        const uint32_t hi = tree_word(row_mask, (from >> 5) + w + 1, nodes);
+                        const uint32_t hi = pkv::tree_word(mask, (from >> 5) + w + 1, nodes());
                         seen[w] = __funnelshift_r(lo, hi, from & 31);
                         lo = hi;
                     }
@@ -1045,7 +1063,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                     }
                 }
                 if (!ok) break;
-                if (TREE && dead) {  // no row of this warp's is stored: whatever its lanes hold may stand for their weights
+                if (TREE && dead()) {  // no row of this warp's is stored: whatever its lanes hold may stand for their weights
                     if (lane < 2) mbar_arrive(bar(kBarP + 2 * t + lane));
                     __syncwarp();
                     continue;
@@ -1160,7 +1178,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
             // A split may hold none of the row's keys.  A whole row sees one at least (but for a tree's blind one, a zero row), so
             // only scores of minus infinity make its sum 0: it has no softmax, and becomes NaN here (0 x inf) and in the joining
             // launch alike.
-            const bool nothing = total == 0.f && (split >= 0 || (TREE && tree_blind(row_mask, pos0 + 1, nodes)));
+            const bool nothing = total == 0.f && (split >= 0 || (TREE && pkv::tree_blind(row_mask(), pos0 + 1, nodes())));
             const float inv = nothing ? 0.f : 1.f / total;
             w_own *= inv;
             w_other *= inv;
@@ -1169,7 +1187,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                 // 128 bytes of each row at a time (64 fp16 dims, or 32 float32 ones of a partial result) through the warp's own
                 // 4 KB, as below, in code as short as it can be: it is run once an item, and instructions that have left the
                 // caches meanwhile cost more than they do.
-                if (!dead) {
+                if (!dead()) {
                     const bool whole = split < 0;
                     const uint32_t lines = base + L::staging + warp * 4096, mine = lines + lane * 128;
                     const int row_bytes = whole ? kDim * 2 : kDim * 4, group_mask = (1 << glog) - 1;
@@ -1224,7 +1242,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                         const int to = whole ? tok * P.num_q_heads + (r & group_mask) : r;
                         for (int key = max(pos0 / kTileRows, first) * kTileRows; key < min(static_cast<int>(i1.w), (first + n_kv) * kTileRows); ++key) {
                             const int node = key - pos0 - 1;
-                            if (node >= 0 && !(tree_word(row_mask, node >> 5, nodes) >> (node & 31) & 1)) continue;
+                            if (node >= 0 && !(pkv::tree_word(row_mask(), node >> 5, nodes()) >> (node & 31) & 1)) continue;
                             const int32_t id = __ldg(P.block_tables + static_cast<int64_t>(i0.x) * P.max_blocks + key / P.block_size);
                             const __half *const row_v = P.v + ((static_cast<int64_t>(id < 0 || id >= P.num_blocks ? 0 : id) * P.num_kv_heads + kvh) * P.block_size +
                                                                key % P.block_size) * kDim;
@@ -1441,9 +1459,9 @@ __global__ void __launch_bounds__(kJoinThreads, BATCH == 8 ? 4 : 2) prompt_join_
     }
 }
 
-// Joins the parts of a tree's split items: kJoinCtas CTAs for the item that CTA blockIdx.y began, one warp per row,
+// Joins the parts of a tree's split items: some CTAs for the item that CTA blockIdx.y began, one warp per row,
 // four dims a lane, eight parts' loads in flight.
-constexpr int kJoinCtas = 16;
+constexpr int kJoinRows = 16;  // of a slot, per CTA
 __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_constant__ PromptParams P) {
     pkv::pdl_wait_primary();
     pkv::pdl_launch_dependents();
@@ -1451,7 +1469,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
     const uint4 d0 = __ldcg(reinterpret_cast<const uint4 *>(P.tree_parts + c0)), d1 = __ldcg(reinterpret_cast<const uint4 *>(P.tree_parts + c0) + 1);
     const int last = d0.x, row0 = d0.y, rows = static_cast<int>(d0.z) << P.group_log2, kvh = d0.w, parts = last - c0 + 1;
     if (last < 0) return;
-    for (int row = blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5); row < rows; row += kJoinCtas * (kJoinThreads / 32)) {
+    for (int row = blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5); row < rows; row += gridDim.x * (kJoinThreads / 32)) {
         auto part_of = [&](int i) { return static_cast<int64_t>(i == 0 ? 2 * c0 + 1 : 2 * (c0 + i)) * P.slot_rows + row; };
         float top = -INFINITY, m = -INFINITY, l = 0.f;
         for (int i = lane; i < parts; i += 32) {
@@ -1488,7 +1506,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
             }
         }
         const int64_t token = static_cast<int64_t>(row0) + (row >> P.group_log2);
-        const bool blind = total == 0.f && tree_blind(P.tree_mask + token * P.mask_words, static_cast<int>(d1.x), static_cast<int>(d1.y));
+        const bool blind = total == 0.f && pkv::tree_blind(P.tree_mask + token * P.mask_words, static_cast<int>(d1.x), static_cast<int>(d1.y));
         const float inv = blind ? 0.f : 1.f / total;
         const __half2 lo = __floats2half2_rn(acc.x * inv, acc.y * inv), hi = __floats2half2_rn(acc.z * inv, acc.w * inv);
         const int64_t out_row = token * P.num_q_heads + (kvh << P.group_log2) + (row & ((1 << P.group_log2) - 1));
@@ -2241,6 +2259,11 @@ extern "C" PKV_API int pkv_decode_attention_tree(void *out, float *lse, const vo
         const int64_t items = static_cast<int64_t>(num_seqs) * ((max_query_len + pair_tokens - 1) / pair_tokens) * num_kv_heads;
         if (items >= (1LL << 31) / (tiles + kItemUnits)) return PKV_ERR_UNSUPPORTED;
     }
+    const pkv_internal::TreeCall call{out,           lse,         q,         k_cache,       v_cache,     block_tables, context_lens,
+                                      query_start,   reinterpret_cast<const uint32_t *>(tree_mask), q_stride, num_blocks, mask_words,
+                                      num_seqs,      total_q,     max_query_len, max_blocks_per_seq, num_q_heads, num_kv_heads,
+                                      block_size,    p.group_log2, p.q_scale};
+    if (pkv_internal::tree_is_short(call)) return pkv_internal::tree_short(call, stream);
     const TreeSizes sizes = tree_sizes(num_seqs, total_q, max_query_len, num_q_heads, num_kv_heads,
                                        static_cast<int64_t>(max_blocks_per_seq) * block_size);
     if (sizes.split) {
@@ -2263,7 +2286,7 @@ extern "C" PKV_API int pkv_decode_attention_tree(void *out, float *lse, const vo
     st = sizes.slot_rows == kTileRows ? launch_prompt_kernel<true, SmallTreeLayout>(p, static_cast<unsigned>(p.grid), stream)
                                       : launch_prompt_kernel<true, TreeLayout>(p, static_cast<unsigned>(p.grid), stream);
     if (st != PKV_OK || !sizes.split) return st;
-    return launch_after(tree_join_kernel, p, dim3(kJoinCtas, static_cast<unsigned>(p.grid)), stream);
+    return launch_after(tree_join_kernel, p, dim3(static_cast<unsigned>(p.slot_rows / kJoinRows), static_cast<unsigned>(p.grid)), stream);
 }
 
 extern "C" PKV_API int pkv_prefill_attention_weights(float *scores, int64_t score_capacity, const void *q, int64_t q_stride,

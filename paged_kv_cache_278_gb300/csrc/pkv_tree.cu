@@ -1,20 +1,26 @@
 // pkv_tree.cu -- a tree of drafted tokens around its attention: the ancestor masks and depths that go with its
-// parents, and the accepted path moved together in the cache.  (The attention itself is in pkv_prompt.cu.)
+// parents, the accepted path moved together in the cache, and the attention itself over short contexts (long ones and
+// large batches: pkv_prompt.cu).
 //
 // A request's n_b drafted tokens lie behind its context in any order that puts a node behind its parent, node i
 // at position base + i (base = context_lens[b] - n_b).  A node's mask has the bit of every node it attends to.
 //
-// Both kernels are bound by latency.  keep_path moves a few rows per request: all of a kept row's K and V pieces
+// tree_masks and keep_path are bound by latency.  keep_path moves a few rows per request: all of a kept row's K and V pieces
 // are columns of 16 bytes, a column belongs to one thread, and the thread goes up the path with eight rows in
 // flight.  Path entries ascend, so path[j] >= j: a row is read before anything is written over it.  What comes before
 // the rows, the sizes, the path and its blocks, is three loads in a row, each of them all at once (with every thread
 // looking up its own rows: 256 paths of 1-12 nodes 9.7 us).
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdint.h>
+
+#include <atomic>
 
 #include "pkv.h"
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
+#include "pkv_tree.cuh"
 
 namespace {
 
@@ -151,6 +157,233 @@ __global__ void __launch_bounds__(kKeepThreads) keep_path_kernel(const __grid_co
     if (teller && P.new_lens) P.new_lens[b] = error == PKV_DEV_OK ? base + len : ctx;
 }
 
+// ---------------------------------------------------------------- attention over short contexts
+// Where a call has few rows and few keys, the time of the tensor-memory kernel is its start: barriers, tensor memory,
+// copies' descriptors.  Here one CTA takes 16 (token, head) rows of one kv head, its eight warps a 16-key chunk each in
+// turn, everything from global memory straight into registers, and one meeting at the end.  Bound by latency: 8 nodes over
+// 300 keys (32 heads, 8 kv heads) 8.4 us where the other
+// kernel takes 14.4.
+//
+// m16n8k16 products without shared memory.  A thread holds 32 neighbouring dims of a row (64 bytes, four loads), lane % 4
+// saying which 32, and gives the product's k index a meaning of its own: in step s its four k are dims 4 s .. 4 s + 3 of
+// its 32, for Q and K alike.  V's 8 x 8 blocks of (key, two of a lane's dims) are transposed by movmatrix, so that an
+// output tile's columns are two dims of each of the four lanes', and a lane ends up with the same 32 dims of its output rows.
+// Weights, lifted by 2^7 as in the other kernel, are rounded to fp16 for the product with V; sums are float32.
+constexpr int kShortWarps = 8;
+constexpr int kShortThreads = 32 * kShortWarps;
+constexpr int kShortSmem = kShortWarps * 16 * PKV_HEAD_DIM * 4;  // the warps' outputs
+constexpr float kShortLift = 7.0f;
+constexpr float kShortLn2 = 0.6931471805599453f;
+// It is taken where its CTAs are no more than the SMs and the tables no longer than 1024 positions (32 heads, 8 kv heads,
+// 16-token blocks, in a graph, this kernel and the other: 8 nodes over 300 keys 8.4 and 14.4 us, 61 over 300 8.6 and 19.7,
+// 4 x 16 over 300 8.4 and 14.6, 8 x 16 over 300 (256 CTAs) 14.1 and 14.9, 16 x 16 over 300 25.9 and 16.3; 8 over 1000 14.7 and
+// 17.2, 61 over 1000 16.2 and 25.0; 8 over 2000 24.1 and 16.5, 61 over 2000 26.3 and 25.0).
+constexpr int kShortCtas = 152, kShortContext = 1024;
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+// 32 dims of a row.
+__device__ __forceinline__ void load_dims(uint32_t (&r)[16], const __half *row) {
+    const uint4 *p = reinterpret_cast<const uint4 *>(row);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint4 v = __ldg(p + i);
+        r[4 * i] = v.x;
+        r[4 * i + 1] = v.y;
+        r[4 * i + 2] = v.z;
+        r[4 * i + 3] = v.w;
+    }
+}
+
+__global__ void __launch_bounds__(kShortThreads, 1) tree_short_kernel(const __grid_constant__ pkv_internal::TreeCall P) {
+    extern __shared__ __align__(16) float4 s_out[];  // [warp][16 rows][32 pieces], see piece_at
+    __shared__ float s_m[kShortWarps][16], s_l[kShortWarps][16];
+    pkv::pdl_wait_primary();
+    pkv::pdl_launch_dependents();
+    const int kvh = blockIdx.x, b = blockIdx.z, warp = threadIdx.x / 32, lane = threadIdx.x & 31, g = lane >> 2, quarter = lane & 3;
+    const int start = __ldg(P.query_start + b), n = __ldg(P.query_start + b + 1) - start, keys = __ldg(P.context_lens + b);
+    if (n < 0 || n > P.max_query_len || start < 0 || start > P.total_q - n || keys < n || keys > P.max_blocks * P.block_size) {
+        if (threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0) pkv::record_error(&g_tree_error, PKV_DEV_BAD_CONTEXT);
+        return;
+    }
+    const int rows = n << P.group_log2, row0 = blockIdx.y * 16, base = keys - n, group_mask = (1 << P.group_log2) - 1;
+    if (row0 >= rows) return;
+    // The thread's two rows (those past the last one are computed like it and not stored).
+    const uint32_t *mask[2];
+    uint32_t q[2][16];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        const int row = min(row0 + g + 8 * r, rows - 1), token = start + (row >> P.group_log2), head = (kvh << P.group_log2) + (row & group_mask);
+        mask[r] = P.mask + static_cast<int64_t>(token) * P.mask_words;
+        load_dims(q[r], static_cast<const __half *>(P.q) + token * P.q_stride + head * PKV_HEAD_DIM + quarter * 32);
+    }
+    const int32_t *table = P.block_tables + static_cast<int64_t>(b) * P.max_blocks;
+    // Element of the cache at which a chunk's rows begin (this lane's dims of its first row).
+    auto chunk_at = [&](int key0) -> int64_t {
+        const int block = key0 / P.block_size;
+        int32_t id = __ldg(table + block);
+        if (id < 0 || id >= P.num_blocks) {
+            if (lane == 0) pkv::record_error(&g_tree_error, PKV_DEV_BAD_BLOCK_ID);
+            id = 0;
+        }
+        return ((static_cast<int64_t>(id) * P.num_kv_heads + kvh) * P.block_size + (key0 - block * P.block_size)) * PKV_HEAD_DIM + quarter * 32;
+    };
+    const __half *const k_cache = static_cast<const __half *>(P.k_cache), *const v_cache = static_cast<const __half *>(P.v_cache);
+    uint32_t k[2][16], v[2][16];  // rows g and g + 8 of the chunk
+    auto load = [&](uint32_t(&x)[2][16], const __half *cache, int64_t at) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) load_dims(x[h], cache + at + (8 * h + g) * PKV_HEAD_DIM);
+    };
+    float o[16][4];
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // of rows g, g + 8 over this warp's chunks (l: this thread's keys)
+    int stripped = 0;
+    int key0 = warp * 16;
+    int64_t at = 0;
+    if (key0 < keys) {
+        at = chunk_at(key0);
+        load(k, k_cache, at);
+        load(v, v_cache, at);
+    }
+    for (; key0 < keys; key0 += 16 * kShortWarps) {
+        const int next = key0 + 16 * kShortWarps;
+        const bool more = next < keys;
+        const int64_t next_at = more ? chunk_at(next) : 0;
+        float s[2][4];  // keys 8 t + 2 quarter, + 1 of rows g (0, 1) and g + 8 (2, 3)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[t][e] = 0.f;
+#pragma unroll
+            for (int step = 0; step < 8; ++step) {
+                const uint32_t a[4] = {q[0][2 * step], q[1][2 * step], q[0][2 * step + 1], q[1][2 * step + 1]};
+                pkv::mma16816(s[t], a, k[t][2 * step], k[t][2 * step + 1]);
+            }
+        }
+        if (more) load(k, k_cache, next_at);
+        if (key0 + 15 >= base) {  // some rows may not see some of these keys
+            const int from = key0 - base;  // the node at the chunk's first key
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const uint32_t seen = __funnelshift_r(pkv::tree_word(mask[r], from >> 5, n), pkv::tree_word(mask[r], (from >> 5) + 1, n), from & 31);
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        if (!(seen >> (8 * t + 2 * quarter + e) & 1)) s[t][2 * r + e] = -INFINITY;
+            }
+            // weights there can be 0, and 0 x inf is NaN: past the context zeros, infinities and NaN of a node put aside
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int key = key0 + 8 * h + g;
+                if (key < base) continue;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const uint32_t bad = ((v[h][i] & 0x7c007c00u) + 0x04000400u) & 0x80008000u;  // exponent 31, per half
+                    if (key >= keys) {
+                        v[h][i] = 0;
+                    } else if (bad) {
+                        stripped = 1;
+                        v[h][i] &= ~((bad >> 15) * 0xffffu);
+                    }
+                }
+            }
+        }
+        uint32_t p[4];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            float top = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1])) * P.q_scale;
+            top = fmaxf(top, __shfl_xor_sync(pkv::kFullMask, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(pkv::kFullMask, top, 2));
+            const float m_new = fmaxf(m[r], top - kShortLift);
+            const float f = m[r] == -INFINITY ? 0.f : exp2f(m[r] - m_new), ms = m_new == -INFINITY ? 0.f : m_new;
+            m[r] = m_new;
+            l[r] *= f;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const float w0 = pkv::exp2_approx(fmaf(s[t][2 * r], P.q_scale, -ms)), w1 = pkv::exp2_approx(fmaf(s[t][2 * r + 1], P.q_scale, -ms));
+                l[r] += w0 + w1;
+                const __half2 pk = __floats2half2_rn(w0, w1);
+                p[2 * t + r] = *reinterpret_cast<const uint32_t *>(&pk);
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                o[i][2 * r] *= f;
+                o[i][2 * r + 1] *= f;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) pkv::mma16816(o[i], p, transpose8x8(v[0][i]), transpose8x8(v[1][i]));
+        if (more) load(v, v_cache, next_at);
+    }
+    // Outputs to shared memory: piece x (four dims) of quarter y's 32 dims of row z.
+    auto piece_at = [](int w, int z, int y, int x) { return (w * 16 + z) * 32 + y * 8 + (x ^ ((2 * y + z) & 7)); };
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+            s_out[piece_at(warp, g + 8 * r, quarter, x)] = make_float4(o[2 * x][2 * r], o[2 * x][2 * r + 1], o[2 * x + 1][2 * r], o[2 * x + 1][2 * r + 1]);
+        l[r] += __shfl_xor_sync(pkv::kFullMask, l[r], 1);
+        l[r] += __shfl_xor_sync(pkv::kFullMask, l[r], 2);
+        if (quarter == 0) {
+            s_m[warp][g + 8 * r] = m[r];
+            s_l[warp][g + 8 * r] = l[r];
+        }
+    }
+    const bool fix = __syncthreads_or(stripped);
+    // A thread per eight dims of a row.
+    const int z = threadIdx.x >> 4, y = (threadIdx.x >> 2) & 3, x0 = 2 * (threadIdx.x & 3), row = row0 + z;
+    if (row >= rows) return;
+    float top = -INFINITY, total = 0.f;
+#pragma unroll
+    for (int w = 0; w < kShortWarps; ++w) top = fmaxf(top, s_m[w][z]);
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < kShortWarps; ++w) {
+        const float f = s_m[w][z] == -INFINITY ? 0.f : exp2f(s_m[w][z] - top);
+        total = fmaf(s_l[w][z], f, total);
+        const float4 lo = s_out[piece_at(w, z, y, x0)], hi = s_out[piece_at(w, z, y, x0 + 1)];
+        const float part[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] = fmaf(part[i], f, acc[i]);
+    }
+    const int token = start + (row >> P.group_log2), head = (kvh << P.group_log2) + (row & group_mask), dim = 32 * y + 4 * x0;
+    const uint32_t *own_mask = P.mask + static_cast<int64_t>(token) * P.mask_words;
+    // A row that sees nothing is zero; one whose scores are all minus infinity has no softmax: NaN (0 x inf).
+    const float inv = total == 0.f && pkv::tree_blind(own_mask, base, n) ? 0.f : 1.f / total;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] *= inv;
+    if (fix) {  // every row that sees an infinity's or a NaN's key gets it whole
+        for (int node = 0; node < n; ++node) {
+            if (!(pkv::tree_word(own_mask, node >> 5, n) >> (node & 31) & 1)) continue;
+            const int key = base + node, block = key / P.block_size;
+            const int32_t id = __ldg(table + block);
+            const __half *row_v = v_cache + ((static_cast<int64_t>(id < 0 || id >= P.num_blocks ? 0 : id) * P.num_kv_heads + kvh) * P.block_size +
+                                             (key - block * P.block_size)) * PKV_HEAD_DIM + dim;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float value = __half2float(row_v[i]);
+                if (!isfinite(value)) acc[i] += value;
+            }
+        }
+    }
+    uint32_t h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __half2 pair = __floats2half2_rn(acc[2 * i], acc[2 * i + 1]);
+        h[i] = *reinterpret_cast<const uint32_t *>(&pair);
+    }
+    const int64_t out_row = static_cast<int64_t>(token) * P.num_q_heads + head;
+    *reinterpret_cast<uint4 *>(static_cast<__half *>(P.out) + out_row * PKV_HEAD_DIM + dim) = make_uint4(h[0], h[1], h[2], h[3]);
+    if ((threadIdx.x & 15) == 0 && P.lse != nullptr) P.lse[out_row] = (top + log2f(total)) * kShortLn2;
+}
+
 }  // namespace
 
 extern "C" PKV_API int pkv_tree_masks(int32_t *mask, int32_t *depths, const int32_t *parents, const int32_t *query_start,
@@ -216,6 +449,34 @@ extern "C" PKV_API int pkv_keep_path(void *k_cache, void *v_cache, int32_t *new_
 }
 
 namespace pkv_internal {
+
+bool tree_is_short(const TreeCall &c) {
+    const int64_t ctas = static_cast<int64_t>(c.num_seqs) * c.num_kv_heads * (((c.max_query_len << c.group_log2) + 15) / 16);
+    return ctas <= kShortCtas && static_cast<int64_t>(c.max_blocks) * c.block_size <= kShortContext;
+}
+
+int tree_short(const TreeCall &c, pkv_stream_t stream) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
+    static std::atomic<uint64_t> configured{0};  // one bit per device
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(configured.load(std::memory_order_acquire) & bit)) {
+        if (cudaFuncSetAttribute(tree_short_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kShortSmem) != cudaSuccess) return PKV_ERR_CUDA;
+        configured.fetch_or(bit, std::memory_order_acq_rel);
+    }
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(c.num_kv_heads), static_cast<unsigned>(((c.max_query_len << c.group_log2) + 15) / 16),
+                       static_cast<unsigned>(c.num_seqs));
+    cfg.blockDim = dim3(kShortThreads);
+    cfg.dynamicSmemBytes = kShortSmem;
+    cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, tree_short_kernel, c) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
 
 int tree_take_error(int *code) {
     int value = 0;

@@ -104,6 +104,37 @@ def test_ragged(group, hkv, bs):
     assert_no_device_error()
 
 
+@pytest.mark.parametrize("group", [1, 2, 4, 8])
+@pytest.mark.parametrize("lens,counts,hkv,bs", [([1], [1], 1, 16), ([16, 17, 300, 0, 33], [1, 16, 8, 0, 33], 2, 16), ([480, 129, 5], [61, 3, 1], 1, 48),
+                                                ([256, 500], [20, 31], 3, 256), ([512], [130], 1, 128)])
+def test_short_contexts(group, lens, counts, hkv, bs):
+    """Few rows over tables of up to 512 positions: one warp has no chunk or several, rows end inside a tile, trees start
+    inside a chunk."""
+    c = Call(lens, counts, group * hkv, hkv, bs, group + len(lens), before=2, behind=3, fused=group != 2)
+    assert c.ws is None
+    out, z = c.run()
+    c.check(out, z)
+    assert torch.equal(c.run()[0], out)
+    assert_no_device_error()
+
+
+def test_short_contexts_any_mask():
+    rng = np.random.default_rng(7)
+    lens, counts = [40, 40, 300, 33, 8], [40, 17, 40, 33, 8]
+    masks = [rng.random((n, n)) < 0.3 for n in counts]
+    masks[0][5] = masks[0][39] = False
+    masks[1][3] = False
+    masks[3][:] = False
+    masks[4][:] = True
+    c = Call(lens, counts, 8, 2, 16, 4, masks=masks, words=4)
+    out, z = c.run()
+    c.check(out, z)
+    assert (out[5] == 0).all() and torch.isneginf(z[5]).all()
+    assert (out[c.start[3]:c.start[4]] == 0).all()
+    c.check(out, c.run(lse=False)[1])
+    assert_no_device_error()
+
+
 @pytest.mark.parametrize("lens,counts,hq,hkv,bs", [([4000], [8], 8, 2, 16), ([9000], [37], 4, 1, 64), ([3000, 20, 5000], [61, 20, 7], 32, 8, 16),
                                                     ([2500, 2500], [300, 200], 16, 2, 32), ([1030] * 70, [3] * 70, 8, 1, 16),
                                                     ([700] * 40, [1] * 40, 8, 8, 16)])
