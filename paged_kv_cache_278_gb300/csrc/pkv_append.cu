@@ -170,24 +170,25 @@ __global__ void __launch_bounds__(kAppendThreads)
 }
 
 // Blocks read back from the fp8 cache: fp16 row = value(code) x row scale, one rounding.  Memory bound: 132 bytes
-// read and 256 written per row.  A thread takes kReadAhead pieces of 16 codes, their loads in flight together.
-constexpr int kReadAhead = 4;
+// read and 256 written per row.  A thread takes kReadAhead pieces of eight codes, their loads in flight together, so that
+// neighbouring lanes store neighbouring 16 bytes.
+constexpr int kReadAhead = 8;
 constexpr int kReadPerCta = kReadAhead * kAppendThreads;
 
 __global__ void __launch_bounds__(kAppendThreads)
     read_blocks_fp8kv_kernel(uint4 *__restrict__ dst_k, uint4 *__restrict__ dst_v, int64_t dst_blocks,
-                             const uint4 *__restrict__ k_codes, const float *__restrict__ k_scale,
-                             const uint4 *__restrict__ v_codes, const float *__restrict__ v_scale, int64_t src_blocks,
+                             const uint2 *__restrict__ k_codes, const float *__restrict__ k_scale,
+                             const uint2 *__restrict__ v_codes, const float *__restrict__ v_scale, int64_t src_blocks,
                              const int32_t *__restrict__ src, const int32_t *__restrict__ dst, int pieces_per_block, int n) {
     const bool is_v = blockIdx.y != 0;
-    const uint4 *codes = is_v ? v_codes : k_codes;
+    const uint2 *codes = is_v ? v_codes : k_codes;
     const float *scale = is_v ? v_scale : k_scale;
     uint4 *out = is_v ? dst_v : dst_k;
     const int64_t begin = static_cast<int64_t>(blockIdx.x) * kReadPerCta;  // of the call's pieces
     const int64_t pair0 = begin / pieces_per_block;
-    const uint32_t rest = static_cast<uint32_t>(begin - pair0 * pieces_per_block) + threadIdx.x;  // (a block has under 2^31 pieces)
+    const uint32_t rest = static_cast<uint32_t>(begin - pair0 * pieces_per_block) + threadIdx.x;  // (a block has under 2^30 pieces)
     int64_t to[kReadAhead];
-    uint4 w[kReadAhead];
+    uint2 w[kReadAhead];
     float s[kReadAhead];
 #pragma unroll
     for (int i = 0; i < kReadAhead; ++i) {
@@ -204,24 +205,21 @@ __global__ void __launch_bounds__(kAppendThreads)
         const int64_t at_src = static_cast<int64_t>(from) * pieces_per_block + piece;
         to[i] = static_cast<int64_t>(into) * pieces_per_block + piece;
         w[i] = __ldg(codes + at_src);
-        s[i] = __ldg(scale + (at_src >> 3));  // eight pieces a row
+        s[i] = __ldg(scale + (at_src >> 4));  // sixteen pieces a row
     }
 #pragma unroll
     for (int i = 0; i < kReadAhead; ++i) {
         if (to[i] < 0) continue;
-        const uint32_t c[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-        uint32_t h[8];
+        uint32_t h[4];
+        pkv::e4m3x4_to_h2x2(w[i].x, h[0], h[1]);
+        pkv::e4m3x4_to_h2x2(w[i].y, h[2], h[3]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            uint32_t lo, hi;
-            pkv::e4m3x4_to_h2x2(c[j], lo, hi);
-            const float2 x = pkv::half2_bits_to_float2(lo), y = pkv::half2_bits_to_float2(hi);
-            const __half2 a = __floats2half2_rn(x.x * s[i], x.y * s[i]), b = __floats2half2_rn(y.x * s[i], y.y * s[i]);
-            h[2 * j] = *reinterpret_cast<const uint32_t *>(&a);
-            h[2 * j + 1] = *reinterpret_cast<const uint32_t *>(&b);
+            const float2 x = pkv::half2_bits_to_float2(h[j]);
+            const __half2 y = __floats2half2_rn(x.x * s[i], x.y * s[i]);
+            h[j] = *reinterpret_cast<const uint32_t *>(&y);
         }
-        out[2 * to[i]] = make_uint4(h[0], h[1], h[2], h[3]);
-        out[2 * to[i] + 1] = make_uint4(h[4], h[5], h[6], h[7]);
+        out[to[i]] = make_uint4(h[0], h[1], h[2], h[3]);
     }
 }
 
@@ -276,13 +274,13 @@ extern "C" PKV_API int pkv_read_blocks_fp8kv(void *k_cache, void *v_cache, int64
         (n > 0 && (!pkv_internal::aligned(src_ids, 4) || !pkv_internal::aligned(dst_ids, 4))))
         return PKV_ERR_INVALID_ARG;
     if (n == 0) return PKV_OK;
-    const int64_t pieces = static_cast<int64_t>(num_kv_heads) * block_size * (PKV_HEAD_DIM / 16);
+    const int64_t pieces = static_cast<int64_t>(num_kv_heads) * block_size * (PKV_HEAD_DIM / 8);
     if (pieces >= (1LL << 30)) return PKV_ERR_UNSUPPORTED;  // 32-bit positions inside a block
     const int64_t ctas = (pieces * n + kReadPerCta - 1) / kReadPerCta;
     if (ctas > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
     read_blocks_fp8kv_kernel<<<dim3(static_cast<unsigned>(ctas), 2), kAppendThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
-        static_cast<uint4 *>(k_cache), static_cast<uint4 *>(v_cache), num_blocks, static_cast<const uint4 *>(k_codes), k_scale,
-        static_cast<const uint4 *>(v_codes), v_scale, src_num_blocks, src_ids, dst_ids, static_cast<int>(pieces), n);
+        static_cast<uint4 *>(k_cache), static_cast<uint4 *>(v_cache), num_blocks, static_cast<const uint2 *>(k_codes), k_scale,
+        static_cast<const uint2 *>(v_codes), v_scale, src_num_blocks, src_ids, dst_ids, static_cast<int>(pieces), n);
     return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 

@@ -15,9 +15,10 @@
 //
 // A row's 16-element units lie in LANES neighbouring lanes of a warp (8 for heads of 128 dims), so that a row's
 // sums are log2(LANES) shuffles and a lane keeps one unit for all the rows it meets: its eight (cos, sin) pairs
-// and its weights stay in registers.  A unit is 32 bytes (two 16-byte pieces): pieces c and c + rotary_dim / 16 hold
-// both halves of eight half-layout pairs, two neighbouring pieces eight interleaved pairs.  The lanes compute a token's
-// angles, one or two sincospi each, and share them by shuffles.
+// stay in registers.  A unit is two 16-byte pieces: pieces u and u + rotary_dim / 16 hold both halves of eight half-layout
+// pairs, any piece four interleaved pairs; neighbouring lanes' pieces are neighbours, so that each of a unit's two loads
+// and stores is one line for the row's lanes.  The lanes compute a token's angles, one or two sincospi each, and share
+// them by shuffles.
 //
 // A pass is 32 / LANES rows of one kind (q, k or v) of one token; up to kBatch passes of a kind are a batch.  Each warp has an even
 // stretch of the call's batches and a ring of kStages batches of shared memory, which bulk copies fill ahead of it: what
@@ -40,8 +41,8 @@ __device__ int g_norm_error;
 
 constexpr int kNormThreads = 128;
 constexpr int kNormWarps = kNormThreads / 32;
-constexpr int kBatch = 4;    // passes: 16 rows of 128 dims
-constexpr int kStages = 2;
+constexpr int kBatch = 2;    // passes: 8 rows of 128 dims
+constexpr int kStages = 3;
 constexpr int kBatchBytes = kBatch * 32 * 32;  // a lane's unit is 32 bytes
 constexpr int kMaxHeadDim = PKV_MAX_ROPE_HEAD_DIM;
 // Up to one pass for each of the warps that 152 SMs hold of the other kernel, a warp takes one pass straight from global
@@ -161,7 +162,7 @@ struct RowWarp {
     static constexpr int kShare = kRows >= 8 ? 1 : 8 / kRows;    // of a unit's eight pairs: angles a lane computes
     const NormParams &P;
     int lane, u, g, units, half0, half1;
-    bool turns;
+    bool turns0, turns1;  // whether the unit's pieces are rotated (together, in the half layout)
     int64_t t, slot, next_slot, cache_row;
     // of the angles this lane computes
     int axis[kShare], next_position[kShare];
@@ -174,16 +175,26 @@ struct RowWarp {
         g = lane / LANES;
         units = P.head_dim / 16;
         const int r16 = P.rotary_dim / 16;
-        turns = u < r16;
-        half0 = turns && !INTERLEAVED ? u : 2 * u;
-        half1 = turns && !INTERLEAVED ? u + r16 : 2 * u + 1;
+        half0 = first_piece(u, units, r16);
+        half1 = second_piece(u, units, r16);
+        turns0 = INTERLEAVED ? half0 < 2 * r16 : u < r16;
+        turns1 = INTERLEAVED ? half1 < 2 * r16 : u < r16;
+    }
+    // The two pieces of unit `unit` of a q or k row.
+    static __device__ __forceinline__ int first_piece(int unit, int units, int r16) { return INTERLEAVED || unit < r16 ? unit : unit + r16; }
+    static __device__ __forceinline__ int second_piece(int unit, int units, int r16) { return INTERLEAVED || unit >= r16 ? unit + units : unit + r16; }
+    // Angle e of this lane's share of the unit's eight: the pair it turns, or -1.
+    __device__ __forceinline__ int pair_of(int e) const {
+        const int j = g * kShare + e;
+        if (j >= 8 || !(INTERLEAVED && j >= 4 ? turns1 : turns0)) return -1;
+        return INTERLEAVED ? 4 * (j < 4 ? half0 : half1) + (j & 3) : 8 * u + j;
     }
     // The axes and frequencies of the angles this lane computes.
     __device__ __forceinline__ void load_axes() {
 #pragma unroll
         for (int e = 0; e < kShare; ++e) {
-            const int i = 8 * u + g * kShare + e;
-            if (!turns || g * kShare >= 8) continue;
+            const int i = pair_of(e);
+            if (i < 0) continue;
             axis[e] = P.axes ? __ldg(P.axes + i) : 0;
             if (axis[e] < 0 || axis[e] >= P.num_axes) {
                 pkv::record_error(&g_norm_error, PKV_DEV_BAD_AXIS);
@@ -197,14 +208,14 @@ struct RowWarp {
         return kind == 0 ? P.q + token * P.q_stride : (kind == 1 ? P.k + token * P.k_stride : P.v + token * P.v_stride);
     }
     // The lane's two pieces of a row of this kind.
-    __device__ __forceinline__ int piece0(int kind) const { return kind == 2 ? 2 * u : half0; }
-    __device__ __forceinline__ int piece1(int kind) const { return kind == 2 ? 2 * u + 1 : half1; }
+    __device__ __forceinline__ int piece0(int kind) const { return kind == 2 ? u : half0; }
+    __device__ __forceinline__ int piece1(int kind) const { return kind == 2 ? u + units : half1; }
 
     // What begin() needs of a token, on its way.
     __device__ __forceinline__ void fetch(int64_t token) {
 #pragma unroll
         for (int e = 0; e < kShare; ++e)
-            if (turns && g * kShare < 8) next_position[e] = __ldg(P.positions + token * P.num_axes + axis[e]);
+            if (pair_of(e) >= 0) next_position[e] = __ldg(P.positions + token * P.num_axes + axis[e]);
         if (P.v) next_slot = __ldg(P.slot_mapping + token);
     }
     // The fetched token's slot and angles.
@@ -219,7 +230,7 @@ struct RowWarp {
 #pragma unroll
         for (int e = 0; e < kShare; ++e) {
             own[e] = make_float2(0.f, 0.f);
-            if (!turns || g * kShare >= 8) continue;
+            if (pair_of(e) < 0) continue;
             const uint64_t phase = static_cast<uint64_t>(static_cast<int64_t>(next_position[e])) * frequency[e] + (1ull << 31);
             const float x = static_cast<float>(static_cast<int32_t>(phase >> 32)) * (1.f / 2147483648.f);
             float s, c;
@@ -259,7 +270,8 @@ struct RowWarp {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float2 f = halves(x[j]);
-                x[j] = fma2(x[j], co[j], mul2(pair(f.y, f.x), si[j]));
+                const Pair y = fma2(x[j], co[j], mul2(pair(f.y, f.x), si[j]));
+                x[j] = (j < 4 ? turns0 : turns1) ? y : x[j];
             }
         } else {
 #pragma unroll
@@ -346,7 +358,7 @@ struct RowWarp {
                         }
                     }
                 }
-                if (turns) {
+                if (turns0) {  // (a second piece is rotated only with the first)
 #pragma unroll
                     for (int n = 0; n < N; ++n) rotate(x[n]);
                 }
@@ -396,7 +408,7 @@ struct RowWarp {
         const bool goes = u < units && slot >= 0;
         int head = head0 + g;
         const int64_t step = static_cast<int64_t>(kRows) * P.block_size * (2 * units);
-        uint4 *dst = P.v_cache + (cache_row + static_cast<int64_t>(head) * P.block_size) * (2 * units) + 2 * u;
+        uint4 *dst = P.v_cache + (cache_row + static_cast<int64_t>(head) * P.block_size) * (2 * units) + u;
 #pragma unroll 1
         for (int i = 0; i < count; i += N, head += N * kRows) {
             uint4 raw[N][2];
@@ -404,13 +416,13 @@ struct RowWarp {
 #pragma unroll
             for (int n = 0; n < N; ++n) {
                 there[n] = u < units && head + n * kRows < P.num_kv_heads && i + n < count;
-                source(i + n, there[n], 2 * u, 2 * u + 1, raw[n][0], raw[n][1]);
+                source(i + n, there[n], u, u + units, raw[n][0], raw[n][1]);
             }
 #pragma unroll
             for (int n = 0; n < N; ++n) {
                 if (goes && there[n]) {
                     dst[0] = raw[n][0];
-                    dst[1] = raw[n][1];
+                    dst[units] = raw[n][1];
                 }
                 dst += step;
             }
@@ -512,9 +524,7 @@ __global__ void __launch_bounds__(kNormThreads, kNormCtas) norm_rope_kernel(cons
     for (int i = threadIdx.x; i < 8 * LANES; i += kNormThreads) {
         const int kind = i / (4 * LANES), j = i / LANES % 4, unit = i % LANES;
         const float4 *w = reinterpret_cast<const float4 *>(kind == 0 ? P.q_weight : P.k_weight);
-        const int r16 = P.rotary_dim / 16;
-        const bool split = unit < r16 && !INTERLEAVED;  // the unit's pieces, as in RowWarp
-        const int piece = split ? (j < 2 ? unit : unit + r16) : 2 * unit + (j >= 2);
+        const int piece = j < 2 ? rows.first_piece(unit, rows.units, P.rotary_dim / 16) : rows.second_piece(unit, rows.units, P.rotary_dim / 16);
         if (w && unit < rows.units) s_weight[kind][j * LANES + unit] = __ldg(w + 2 * piece + (j & 1));
     }
     __syncthreads();

@@ -206,6 +206,58 @@ def test_append_fp8kv(t, hq, hkv, bs, rotary, interleaved, normed):
     assert_no_device_error()
 
 
+@pytest.mark.parametrize("weight", [1e-30, 1e30, 3e36])
+@pytest.mark.parametrize("t", [3, 400])
+def test_fp8_scales_of_any_size(weight, t):
+    """Rows whose scale is far from one: the codes are still those of the quotient."""
+    hkv, bs = 2, 16
+    q, k, v, qw, kw, pos = make(t, 2, hkv, 128, 17)
+    kw = kw * weight
+    pos, freq, slots = pos[:, 0].contiguous(), pkv.rope_frequencies(128), torch.arange(t, device="cuda")
+    cache = pkv.empty_fp8kv_cache(-(-t // bs), hkv, bs, "cuda")
+    pkv.norm_rope_append_fp8kv(torch.empty_like(q), q, k, v, *cache, slots, pos, freq, qw, kw, EPS)
+    flat = lambda x: x.transpose(1, 2).reshape(-1, hkv, *x.shape[3:])[:t]  # noqa: E731
+    codes, scale = flat(cache[0]).view(F8).double().cpu().numpy(), host(flat(cache[1]))
+    z, size = want_of(k, kw, pos, None, 128)
+    err = error(size, True)
+    assert (np.abs(scale - np.abs(z).max(-1) / 448) <= err.max(-1) / 448 + 2.0 ** -23 * scale).all()
+    assert (np.abs(codes * scale[..., None] - z) <= 2.0 ** -4 * np.abs(z) * (1 + 1e-5) + 2.0 ** -10 * scale[..., None] * 1.001 + 2 * err).all()
+    assert_no_device_error()
+
+
+def test_fp8_codes_are_the_append_s():
+    """K rows that are neither normalised nor turned (position 0) have append_fp8kv's codes and scales, bit for bit: rows of
+    all sizes, infinities and NaN among them."""
+    t, hkv, bs = 700, 2, 16
+    g = torch.Generator(device="cuda").manual_seed(3)
+    k = (torch.randn((t, hkv, 128), generator=g, device="cuda") * torch.exp(4 * torch.randn((t, hkv, 1), generator=g, device="cuda"))).half()
+    k[5] = 0
+    k[6, 0] = 2.0 ** -24
+    k[7, 1, 3] = float("inf")
+    k[8, 0, 9] = float("nan")
+    k[9] = -k[9].abs()
+    k[10, :, 1:] = 0
+    q, slots = torch.zeros((t, 2, 128), dtype=torch.float16, device="cuda"), torch.arange(t, device="cuda")
+    a, b = pkv.empty_fp8kv_cache(-(-t // bs), hkv, bs, "cuda"), pkv.empty_fp8kv_cache(-(-t // bs), hkv, bs, "cuda")
+    pkv.append_fp8kv(*b, slots, k, k)
+    for n in (t, 20):  # both kernels
+        for x in a:
+            x.zero_()
+        pos = torch.zeros(n, dtype=torch.int32, device="cuda")
+        # 16 dims are turned by nothing, which makes NaN of what an infinity is paired with (inf x 0): of rows with an infinity or a
+        # NaN (some of the largest ones too) only V's codes are compared
+        pkv.norm_rope_append_fp8kv(torch.empty_like(q[:n]), q[:n], k[:n], k[:n], *a, slots[:n], pos, pkv.rope_frequencies(16), None, None, EPS)
+        flat = lambda x: x.transpose(1, 2).reshape(-1, hkv, *x.shape[3:])[:n]  # noqa: E731
+        rows = torch.isfinite(k[:n]).flatten(1).all(1)
+        assert rows.sum() > n // 2
+        got, want = flat(a[0])[rows], flat(b[0])[rows]
+        # The 16 dims that are turned by nothing keep their value, but not the sign of a zero: -0 x 1 - y x 0 is +0 for y < 0.
+        assert torch.equal(got[..., 16:], want[..., 16:]) and torch.equal(got[..., :16].view(F8).float(), want[..., :16].view(F8).float())
+        assert torch.equal(flat(a[1])[rows], flat(b[1])[rows])
+        assert torch.equal(flat(a[2]), flat(b[2])) and torch.equal(flat(a[3]).nan_to_num(7.0), flat(b[3]).nan_to_num(7.0))
+    assert_no_device_error()
+
+
 def test_bad_axis_is_recorded():
     q, k, _, qw, kw, pos = make(4, 2, 1, 128, 5, axes=2)
     axes = torch.zeros(64, dtype=torch.int32, device="cuda")
