@@ -76,7 +76,7 @@ constexpr int64_t kMaxContext = 1 << 30;  // positions and their sums with a til
 constexpr int kPlannedSms = 152;  // the split plan, and with it the workspace, is the same on every device
 
 // Of a tree's call: the item that a CTA's stretch begins but does not finish, for the joining launch.
-struct alignas(16) TreePart {
+struct alignas(16) TreePart {  // (kJoinThreads threads read kPlannedSms of them)
     int last;  // the CTA that finishes it; -1: there is no such item
     int row0, tokens, kvh;
     int base, nodes, pad[2];  // the tree's
@@ -101,7 +101,7 @@ struct PromptParams {
     // A tree's call: split counts slots (0: no item is split), their partial results [slot][slot_rows](x 128).
     const uint32_t *tree_mask;  // [total_q][mask_words]
     TreePart *tree_parts;       // [grid]
-    int mask_words, grid, slot_rows;
+    int mask_words, grid, slot_rows, read_once;
     CUtensorMap tmap_q, tmap_k, tmap_v;
 };
 
@@ -263,6 +263,20 @@ __device__ __forceinline__ bool elected() {
 __device__ __forceinline__ void tma_prefetch_3d(const void *tensor_map, int x, int y, int z) {
     asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global [%0, {%1, %2, %3}];" ::"l"(tensor_map), "r"(x), "r"(y), "r"(z)
                  : "memory");
+}
+
+// pkv::tma_load_2d with a cache policy.
+__device__ __forceinline__ void tma_load_2d_hint(uint32_t dst, const void *tensor_map, int x, int y, uint32_t bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(
+            dst),
+        "l"(tensor_map), "r"(x), "r"(y), "r"(bar), "l"(policy)
+        : "memory");
+}
+__device__ __forceinline__ uint64_t first_to_go_policy() {
+    uint64_t policy;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+    return policy;
 }
 
 __device__ __forceinline__ uint4 lds128v(uint32_t addr) {  // ordered behind the barrier that published it
@@ -768,8 +782,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                 const int boxes = (min(kTileRows, keys - tile * kTileRows) + (1 << P.box_log2) - 1) >> P.box_log2;
                 if (lane == 0) pkv::mbar_arrive_expect_tx(full, boxes << (P.box_log2 + 8));
                 __syncwarp();
-                if (lane < 2 * boxes)
-                    pkv::tma_load_2d(dst + (lane & 1) * kSlab + ((lane >> 1) << (P.box_log2 + 7)), map, 64 * (lane & 1), row, full);
+                if (lane < 2 * boxes) {
+                    const uint32_t to = dst + (lane & 1) * kSlab + ((lane >> 1) << (P.box_log2 + 7));
+                    if (TREE && P.read_once)  // leaves L2 first: what the next launches need stays there
+                        tma_load_2d_hint(to, map, 64 * (lane & 1), row, full, first_to_go_policy());
+                    else
+                        pkv::tma_load_2d(to, map, 64 * (lane & 1), row, full);
+                }
             } else if (lane == 0) {
                 pkv::mbar_arrive_expect_tx(full, kOperand);
                 for (int half = 0; half < 2; ++half)
@@ -888,6 +907,99 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
             if (!ok)
                 for (uint32_t s = stage > kVRing ? stage - kVRing : 0; s < stage; ++s)
                     wait_phase(bar(kBarVFull + s % kVRing), (s / kVRing) & 1);
+        } else if (TREE && warp == kMmaWarp) {
+            // ---------------------------------------------------------------- tensor-core issue, by one thread throughout
+            if (elected()) {
+                auto wait1 = [&](int b, uint32_t phase) {
+                    if (wait_phase(bar(b), phase & 1)) return true;
+                    pkv::record_error(&g_prompt_error, PKV_DEV_WAIT_TIMEOUT);
+                    return false;
+                };
+                constexpr uint32_t kIdescPV = pkv::umma_idesc_f16_f32(kTileRows, kDim) | (1u << 16);  // V: MN-major
+                constexpr uint32_t kIdescQK = pkv::umma_idesc_f16_f32(kTileRows, kTileRows);
+                uint32_t k_stage = 0, v_stage = 0, loaded = 0, p_count[2] = {0, 0};
+                bool ok = true;
+                for (uint32_t k = 0; ok; ++k) {
+                    const int slot = k % kItems;
+                    if (!(ok = wait1(kBarItemFull + slot, k / kItems))) break;
+                    const int seq = slots[slot].seq, keys = slots[slot].keys, first = slots[slot].kv_first;
+                    const int n[2] = {slots[slot].kv_count[0], slots[slot].kv_count[1]};
+                    const bool shared = slots[slot].shared != 0;
+                    mbar_arrive(bar(kBarItemEmpty + slot));
+                    if (seq < 0) break;
+                    const int n_kv = key_tiles(shared, n[0], n[1]);
+                    // 16-key groups of key tile j that hold cached keys
+                    auto groups_of = [&](int j) { return (min(kTileRows, keys - (first + j) * kTileRows) + 15) / 16; };
+                    auto qk = [&](int t, int groups) {
+                        const uint64_t q = pkv::umma_desc_k_sw128(base + L::q + (shared ? 0 : t) * kOperand);
+                        const uint64_t kk = pkv::umma_desc_k_sw128(base + L::ring + (k_stage % kKRing) * kOperand);
+                        const uint32_t idesc = groups == 8 ? kIdescQK : pkv::umma_idesc_f16_f32(kTileRows, groups * 16);
+#pragma unroll
+                        for (int ks = 0; ks < kDim / 16; ++ks) {
+                            const uint64_t off = ((ks >> 2) * kSlab + (ks & 3) * 32) >> 4;
+                            pkv::umma_f16(tmem + t * kTileRows, q + off, kk + off, idesc, ks > 0);
+                        }
+                        pkv::umma_commit(bar(kBarS + t));
+                    };
+                    // O of group t += P V of a key tile (the group's `local`-th)
+                    auto pv = [&](int t, int groups, int local) {
+                        const uint64_t v = pkv::umma_desc_mn_sw128(base + L::values + (v_stage % kVRing) * kOperand, kSlab, 1024);
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {  // keys 0-63 while the softmax finishes 64-127
+                            if (!wait1(kBarP + 2 * t + half, p_count[t])) return false;
+                            pkv::tmem_fence_after_sync();
+#pragma unroll
+                            for (int g = 4 * half; g < 4 * half + 4; ++g)
+                                if (g < groups)
+                                    umma_f16_ta(tmem + 2 * kTileRows + t * kDim, tmem + t * kTileRows + g * 8, v + g * (2048 >> 4), kIdescPV,
+                                                local > 0 || g > 0);
+                        }
+                        if (local + 1 == n[t]) pkv::umma_commit(bar(kBarO + t));
+                        ++p_count[t];
+                        return true;
+                    };
+                    auto k_landed = [&]() { return wait1(kBarKFull + k_stage % kKRing, k_stage / kKRing); };
+                    if (!(ok = wait1(kBarQFull, loaded))) break;
+                    ++loaded;
+                    // Q K^T of the first key tile for both groups, or of the first two for one each
+                    const int firsts = shared ? min(2, n_kv) : 1;
+                    for (int x = 0; x < firsts && ok; ++x) {
+                        if (!(ok = k_landed())) break;
+                        pkv::tmem_fence_after_sync();
+                        for (int t = 0; t < 2; ++t)
+                            if (shared ? t == x : n[t] > 0) qk(t, groups_of(x));
+                        pkv::umma_commit(bar(kBarKEmpty + k_stage % kKRing));
+                        ++k_stage;
+                    }
+                    if (!ok) break;
+                    if (n_kv == firsts) pkv::umma_commit(bar(kBarQEmpty));
+                    for (int j = 0; j < n_kv && ok; ++j) {
+                        const int k_tile = j + (shared ? 2 : 1);
+                        const bool more = k_tile < n_kv;
+                        if (!(ok = wait1(kBarVFull + v_stage % kVRing, v_stage / kVRing))) break;
+                        if (more && !(ok = k_landed())) break;
+                        const int groups = groups_of(j), next_groups = groups_of(k_tile), local = shared ? j >> 1 : j;
+                        for (int t = 0; t < 2; ++t) {
+                            if (shared ? t != (j & 1) : j >= n[t]) continue;
+                            if (!(ok = pv(t, groups, local))) break;
+                            if (local + 1 < n[t]) qk(t, next_groups);
+                        }
+                        if (!ok) break;
+                        pkv::umma_commit(bar(kBarVEmpty + v_stage % kVRing));
+                        ++v_stage;
+                        if (more) {  // (some group always takes the next K tile)
+                            pkv::umma_commit(bar(kBarKEmpty + k_stage % kKRing));
+                            ++k_stage;
+                            if (k_tile + 1 == n_kv) pkv::umma_commit(bar(kBarQEmpty));  // the item's last Q K^T has been issued
+                        }
+                    }
+                }
+                if (!ok) {  // MMAs in flight end before tensor memory is freed (bounded)
+                    pkv::umma_commit(bar(kBarDrain));
+                    wait_phase(bar(kBarDrain), 0);
+                }
+            }
+            __syncwarp();
         } else if (warp == kMmaWarp) {
             // ---------------------------------------------------------------- tensor-core issue
             constexpr uint32_t kIdescPV = pkv::umma_idesc_f16_f32(kTileRows, kDim) | (1u << 16);  // V: MN-major
@@ -1459,43 +1571,80 @@ __global__ void __launch_bounds__(kJoinThreads, BATCH == 8 ? 4 : 2) prompt_join_
     }
 }
 
-// Joins the parts of a tree's split items: some CTAs for the item that CTA blockIdx.y began, one warp per row,
-// four dims a lane, eight parts' loads in flight.
-constexpr int kJoinRows = 16;  // of a slot, per CTA
-__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_constant__ PromptParams P) {
+// Joins the parts of a tree's split items: one warp per row, four dims a lane.  What it takes is latency (20 MB of parts at
+// most), so there are two rounds of loads only: every CTA of one full round lists the split items with one load a record, and
+// a row's outputs are asked for together with what they weigh.  (Some CTAs for each stretch, four times too many for one round
+// and most without a part to join: 5 to 8 us more.)
+constexpr int kJoinRows = kJoinThreads / 32, kJoinBatch = 6;
+__global__ void __launch_bounds__(kJoinThreads, 4) tree_join_kernel(const __grid_constant__ PromptParams P) {
+    __shared__ TreePart s_part[kPlannedSms];
+    __shared__ int s_first[kPlannedSms], s_warp[kJoinRows];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pkv::pdl_wait_primary();
     pkv::pdl_launch_dependents();
-    const int lane = threadIdx.x & 31, c0 = blockIdx.y;
-    const uint4 d0 = __ldcg(reinterpret_cast<const uint4 *>(P.tree_parts + c0)), d1 = __ldcg(reinterpret_cast<const uint4 *>(P.tree_parts + c0) + 1);
-    const int last = d0.x, row0 = d0.y, rows = static_cast<int>(d0.z) << P.group_log2, kvh = d0.w, parts = last - c0 + 1;
-    if (last < 0) return;
-    for (int row = blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5); row < rows; row += gridDim.x * (kJoinThreads / 32)) {
-        auto part_of = [&](int i) { return static_cast<int64_t>(i == 0 ? 2 * c0 + 1 : 2 * (c0 + i)) * P.slot_rows + row; };
-        float top = -INFINITY, m = -INFINITY, l = 0.f;
-        for (int i = lane; i < parts; i += 32) {
-            m = __ldcg(P.m_part + part_of(i));
-            l = __ldcg(P.l_part + part_of(i));
-            top = fmaxf(top, m);
-        }
+    // The split items, in order: a thread reads the record of its stretch.
+    uint4 d0 = make_uint4(0xffffffffu, 0, 0, 0), d1 = make_uint4(0, 0, 0, 0);
+    if (static_cast<int>(threadIdx.x) < P.grid) {
+        d0 = __ldcg(reinterpret_cast<const uint4 *>(P.tree_parts + threadIdx.x));
+        d1 = __ldcg(reinterpret_cast<const uint4 *>(P.tree_parts + threadIdx.x) + 1);
+    }
+    const unsigned split = __ballot_sync(pkv::kFullMask, static_cast<int>(d0.x) >= 0);
+    if (lane == 0) s_warp[warp] = __popc(split);
+    __syncthreads();
+    int before = 0, items = 0;
 #pragma unroll
-        for (int sh = 16; sh >= 1; sh >>= 1) top = fmaxf(top, __shfl_xor_sync(pkv::kFullMask, top, sh));
-        float total = 0.f;
+    for (int w = 0; w < kJoinRows; ++w) {
+        before += w < warp ? s_warp[w] : 0;
+        items += s_warp[w];
+    }
+    if (static_cast<int>(d0.x) >= 0) {
+        const int i = before + __popc(split & ((1u << lane) - 1u));
+        reinterpret_cast<uint4 *>(s_part + i)[0] = d0;
+        reinterpret_cast<uint4 *>(s_part + i)[1] = d1;
+        s_first[i] = threadIdx.x;
+    }
+    __syncthreads();
+    const int per_item = (min(P.max_query_len << P.group_log2, P.slot_rows) + kJoinRows - 1) / kJoinRows;  // eights of rows
+    const int chunks = items * per_item;
+    for (int chunk = blockIdx.x; chunk < chunks; chunk += gridDim.x) {
+        const int item = chunk / per_item, row = (chunk - item * per_item) * kJoinRows + warp, c0 = s_first[item];
+        const TreePart &part = s_part[item];
+        if (row >= part.tokens << P.group_log2) continue;
+        const int parts = part.last - c0 + 1;
+        const int64_t slot_rows = P.slot_rows, first_at = (2 * c0 + 1) * slot_rows + row;
+        auto part_of = [&](int i) { return i == 0 ? first_at : 2 * (c0 + i) * slot_rows + row; };
+        const float *const outputs = P.o_part + 4 * lane;
+        float top = -INFINITY, total = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i0 = 0; i0 < parts; i0 += 32) {
-            if (parts > 32) {
-                const bool here = i0 + lane < parts;
-                m = here ? __ldcg(P.m_part + part_of(i0 + lane)) : -INFINITY;
-                l = here ? __ldcg(P.l_part + part_of(i0 + lane)) : 0.f;
-            }
-            const float weight = l == 0.f ? 0.f : l * exp2f(m - top);  // (0 past the last part, and where a part holds none of the row's keys)
+        for (int i0 = 0; i0 < parts; i0 += 32) {  // (one round but for items of over 32 CTAs)
             const int here = min(32, parts - i0);
-            for (int j0 = 0; j0 < here; j0 += 8) {
-                float4 o[8];
+            float m = -INFINITY, l = 0.f;
+            float4 o[kJoinBatch];
+            if (lane < here) {
+                m = __ldcg(P.m_part + part_of(i0 + lane));
+                l = __ldcg(P.l_part + part_of(i0 + lane));
+            }
+            auto ask = [&](int j0) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) o[j] = __ldcg(reinterpret_cast<const float4 *>(P.o_part + part_of(i0 + min(j0 + j, here - 1)) * kDim) + lane);
+                for (int j = 0; j < kJoinBatch; ++j) o[j] = __ldcg(reinterpret_cast<const float4 *>(outputs + part_of(i0 + min(j0 + j, here - 1)) * kDim));
+            };
+            ask(0);
+            float most = m;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float w = __shfl_sync(pkv::kFullMask, weight, j0 + j);
+            for (int sh = 16; sh >= 1; sh >>= 1) most = fmaxf(most, __shfl_xor_sync(pkv::kFullMask, most, sh));
+            const float now = fmaxf(top, most), f = top == -INFINITY ? 0.f : exp2f(top - now);
+            top = now;
+            total *= f;
+            acc.x *= f;
+            acc.y *= f;
+            acc.z *= f;
+            acc.w *= f;
+            const float weight = l == 0.f ? 0.f : l * exp2f(m - top);  // (0 past the last part, and where a part holds none of the row's keys)
+            for (int j0 = 0; j0 < here; j0 += kJoinBatch) {
+                if (j0 > 0) ask(j0);
+#pragma unroll
+                for (int j = 0; j < kJoinBatch; ++j) {
+                    const float w = __shfl_sync(pkv::kFullMask, weight, (j0 + j) & 31);
                     if (j0 + j >= here || w == 0.f) continue;
                     total += w;
                     acc.x = fmaf(w, o[j].x, acc.x);
@@ -1505,11 +1654,11 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
                 }
             }
         }
-        const int64_t token = static_cast<int64_t>(row0) + (row >> P.group_log2);
-        const bool blind = total == 0.f && pkv::tree_blind(P.tree_mask + token * P.mask_words, static_cast<int>(d1.x), static_cast<int>(d1.y));
+        const int64_t token = static_cast<int64_t>(part.row0) + (row >> P.group_log2);
+        const bool blind = total == 0.f && pkv::tree_blind(P.tree_mask + token * P.mask_words, part.base, part.nodes);
         const float inv = blind ? 0.f : 1.f / total;
         const __half2 lo = __floats2half2_rn(acc.x * inv, acc.y * inv), hi = __floats2half2_rn(acc.z * inv, acc.w * inv);
-        const int64_t out_row = token * P.num_q_heads + (kvh << P.group_log2) + (row & ((1 << P.group_log2) - 1));
+        const int64_t out_row = token * P.num_q_heads + (part.kvh << P.group_log2) + (row & ((1 << P.group_log2) - 1));
         *reinterpret_cast<uint2 *>(P.out + out_row * kDim + 4 * lane) =
             make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
         if (lane == 0 && P.lse != nullptr) P.lse[out_row] = (top + log2f(total)) * kLn2;
@@ -2277,6 +2426,7 @@ extern "C" PKV_API int pkv_decode_attention_tree(void *out, float *lse, const vo
     p.tree_mask = reinterpret_cast<const uint32_t *>(tree_mask);
     p.mask_words = mask_words;
     p.slot_rows = sizes.slot_rows;
+    p.read_once = (max_query_len << p.group_log2) <= 2 * kTileRows;  // one item per request and kv head
     p.splits = sizes.split ? 2 * sizes.ctas : 0;
     st = encode_paged(&p, q, q_stride, k_cache, v_cache);
     if (st != PKV_OK) return st;
@@ -2286,7 +2436,7 @@ extern "C" PKV_API int pkv_decode_attention_tree(void *out, float *lse, const vo
     st = sizes.slot_rows == kTileRows ? launch_prompt_kernel<true, SmallTreeLayout>(p, static_cast<unsigned>(p.grid), stream)
                                       : launch_prompt_kernel<true, TreeLayout>(p, static_cast<unsigned>(p.grid), stream);
     if (st != PKV_OK || !sizes.split) return st;
-    return launch_after(tree_join_kernel, p, dim3(static_cast<unsigned>(p.slot_rows / kJoinRows), static_cast<unsigned>(p.grid)), stream);
+    return launch_after(tree_join_kernel, p, dim3(static_cast<unsigned>(4 * sms)), stream);
 }
 
 extern "C" PKV_API int pkv_prefill_attention_weights(float *scores, int64_t score_capacity, const void *q, int64_t q_stride,
