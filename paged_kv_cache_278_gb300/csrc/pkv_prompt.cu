@@ -1611,9 +1611,8 @@ __global__ void __launch_bounds__(kJoinThreads, 4) tree_join_kernel(const __grid
         const TreePart &part = s_part[item];
         if (row >= part.tokens << P.group_log2) continue;
         const int parts = part.last - c0 + 1;
-        const int64_t slot_rows = P.slot_rows, first_at = (2 * c0 + 1) * slot_rows + row;
-        auto part_of = [&](int i) { return i == 0 ? first_at : 2 * (c0 + i) * slot_rows + row; };
-        const float *const outputs = P.o_part + 4 * lane;
+        auto part_of = [&](int i) { return (2 * (c0 + i) + (i == 0 ? 1 : 0)) * P.slot_rows + row; };  // (the workspace's bytes fit 32 bits)
+        const float4 *const outputs = reinterpret_cast<const float4 *>(P.o_part) + lane;
         float top = -INFINITY, total = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int i0 = 0; i0 < parts; i0 += 32) {  // (one round but for items of over 32 CTAs)
@@ -1626,7 +1625,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) tree_join_kernel(const __grid
             }
             auto ask = [&](int j0) {
 #pragma unroll
-                for (int j = 0; j < kJoinBatch; ++j) o[j] = __ldcg(reinterpret_cast<const float4 *>(outputs + part_of(i0 + min(j0 + j, here - 1)) * kDim));
+                for (int j = 0; j < kJoinBatch; ++j) o[j] = __ldcg(outputs + part_of(i0 + min(j0 + j, here - 1)) * (kDim / 4));
             };
             ask(0);
             float most = m;
