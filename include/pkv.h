@@ -761,7 +761,7 @@ PKV_API int pkv_rope_append(void *q_out, int64_t q_out_stride, const void *q, in
  *   positions : DEVICE int32 [num_tokens][num_axes]
  *   axes      : DEVICE int32 [rotary_dim / 2], the axis that turns each pair (may be NULL with one axis); an entry
  *               outside [0, num_axes) counts as 0 and is recorded as PKV_DEV_BAD_AXIS
- * float32 arithmetic from the row to the rotated row, one rounding.  eps >= 0.  Other arguments, in-place use and
+ * float32 arithmetic from the row to the rotated row, one rounding.  eps >= 0 (0 makes NaN of a row of zeros).  Other arguments, in-place use and
  * errors as pkv_rope's and pkv_rope_append's. */
 #define PKV_MAX_ROPE_AXES 4
 
@@ -857,13 +857,14 @@ PKV_API int pkv_prefill_attention_paged(void *out, float *lse, const void *q, in
  * zero row with an lse of minus infinity.  max_query_len <= PKV_MAX_QUERY_LEN.  Rows, ranges, bad requests, lse,
  * rounding and what reaches a result as in "prompts and chunks". */
 
-/* Bytes of workspace (0: none) for tables of max_context = max_blocks_per_seq * block_size positions; 41 MB at most.  No
+/* Bytes of workspace that are enough (0: none) for tables of max_context = max_blocks_per_seq * block_size positions; 41 MB at most.  No
  * initial contents, and nothing kept in it from one call to the next.  Calls that may run at the same time need one
  * each. */
 PKV_API size_t pkv_tree_workspace_size(int num_seqs, int total_q, int max_query_len, int num_q_heads, int num_kv_heads,
                                        int head_dim, int max_context);
 
-/* Attention of every request's tree over its paged cache, on the 5th-generation tensor cores.
+/* Attention of every request's tree over its paged cache, on the 5th-generation tensor cores (few rows over tables of up
+ * to 1024 positions: on warp-wide MMAs, without a workspace).  UNSUPPORTED also where the call's key tiles could be 2^31.
  * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */
 PKV_API int pkv_decode_attention_tree(void *out, float *lse, const void *q, int64_t q_stride, const void *k_cache,
                                       const void *v_cache, const int32_t *block_tables, const int32_t *context_lens,

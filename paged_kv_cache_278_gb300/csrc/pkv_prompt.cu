@@ -41,6 +41,24 @@
 // Keys past the context are never multiplied: the last key tile's MMAs stop at its 16-key group and
 // that group's unused V rows are zeroed in shared memory, whatever the cache holds there.  Infinities and NaN in V
 // reach the rows that see their position and no others (clean_values).
+//
+// Trees of drafted tokens (the instances with TREE) are the same tiles with a mask of the last n_b positions in the border's
+// place, and few rows over many keys.  Clock stamps from the first scores to the last weights: one tile of rows 1.46 us a 128-key
+// tile and SM, which is HBM (1.47 at the rate of a plain copy); two tiles 1.58 us, and 1.8 where K and V stay in L2 (one tree of 61
+// nodes, 16k for 8k keys), so there it is the turns of the two tiles.  Every further tile of longer contexts costs 1.38 and 1.96 us (8
+// requests for 4 of 32k); why the second lies above what the stamps show is not known.  What the rest is about is the time
+// around that stream, some 20 us of a call.  All key tiles of the call are one stretch cut evenly over the SMs (struct
+// TreeWalk), so that they end together whatever the contexts are, and at most two parts of an SM's stretch have to be joined;
+// the first item is looked for during set-up; trees of one tile give Q's second tile to a third V stage; one thread issues all
+// MMAs; K and V, read once, leave L2 first, so that tables, parts and the code itself stay there.  64 trees of 13 to 16 nodes
+// behind 1025 to 2049 keys in 16-token blocks 83 us, 5.1 TB/s; 4 of 52 to 61 nodes behind 16385 to 32768 keys in 64-token blocks
+// 89 us, 4.6 TB/s.  Around the stream, from clock stamps: 7.5 us to the first scores (three reads that depend on each other:
+// lengths, block ids, K; and code that is read for the first time), 2-3 us of output or parts, 3-4 us that SMs end
+// apart, 6-8 us for the joining launch (its list after 1-1.5 us, the weights 2 later).  Slower: scores by 64 keys, so that a
+// tile's first half is there before the last one's second half is used (107 us where this takes 95; an MMA of 64 columns
+// reads as much of Q as one of 128), K and V brought near L2 four tiles ahead (110 and 114 us for 93 and 96), rows stored
+// without being put together in lines and a further stage in that room (two tiles 98 for 95; one 86 for 87, not worth a second form)
+// (each beside the time that this kernel had then).
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

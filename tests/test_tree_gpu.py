@@ -148,6 +148,29 @@ def test_long_contexts(lens, counts, hq, hkv, bs):
     assert_no_device_error()
 
 
+@pytest.mark.parametrize("seqs", [127, 128, 300])
+def test_hundreds_of_requests(seqs):
+    """More requests than are read at once, most of them without a tree, some with long contexts cut over CTAs."""
+    counts = [(7 * i) % 5 if i % 3 else 0 for i in range(seqs)]
+    lens = [c + (13 * i) % 90 + (2000 if i % 50 == 1 else 0) for i, c in enumerate(counts)]
+    c = Call(lens, counts, 4, 2, 16, seqs, before=1, behind=2)
+    out, z = c.run()
+    c.check(out, z)
+    assert torch.equal(c.run()[0], out)
+    assert_no_device_error()
+
+
+def test_out_may_be_q():
+    for lens, counts in (([300, 40], [8, 5]), ([3000, 700], [50, 70])):
+        c = Call(lens, counts, 8, 2, 16, 3)
+        want = c.run()[0]
+        q = c.q.clone()
+        c.run(out=c.q)
+        assert torch.equal(c.q, want)
+        c.q.copy_(q)
+    assert_no_device_error()
+
+
 def test_a_line_is_the_causal_step():
     """A tree without branches is a chunk: the same values as the causal call to its own tolerance."""
     lens, counts = [500, 90, 1500], [16, 5, 33]
