@@ -865,6 +865,7 @@ PKV_API size_t pkv_tree_workspace_size(int num_seqs, int total_q, int max_query_
 
 /* Attention of every request's tree over its paged cache, on the 5th-generation tensor cores (few rows over tables of up
  * to 1024 positions: on warp-wide MMAs, without a workspace).  UNSUPPORTED also where the call's key tiles could be 2^31.
+ * out may be q itself where q's rows are contiguous.
  * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */
 PKV_API int pkv_decode_attention_tree(void *out, float *lse, const void *q, int64_t q_stride, const void *k_cache,
                                       const void *v_cache, const int32_t *block_tables, const int32_t *context_lens,

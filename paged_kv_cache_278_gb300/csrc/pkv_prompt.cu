@@ -734,6 +734,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
     pkv::pdl_launch_dependents();
     if (!aligned) {
         if (threadIdx.x == 0) pkv::record_error(&g_prompt_error, PKV_DEV_SMEM_MISALIGNED);
+        if (TREE && threadIdx.x == 0 && P.splits > 0) P.tree_parts[blockIdx.x].last = -1;  // nothing for the joining launch
         return;
     }
     const uint32_t tmem = uniform(*tmem_slot);
