@@ -855,7 +855,8 @@ PKV_API int pkv_prefill_attention_paged(void *out, float *lse, const void *q, in
  *               from n_b on are not read.
  * Any mask is allowed, not only a tree's.  A row that sees nothing (no context before the tree and no bit) is a
  * zero row with an lse of minus infinity.  max_query_len <= PKV_MAX_QUERY_LEN.  Rows, ranges, bad requests, lse,
- * rounding and what reaches a result as in "prompts and chunks". */
+ * rounding and what reaches a result as in "prompts and chunks" (few rows over short tables: weights in two fp16 parts,
+ * off by at most 2^-21 of the weight or 2^-32 of the row's largest). */
 
 /* Bytes of workspace that are enough (0: none) for tables of max_context = max_blocks_per_seq * block_size positions; 41 MB at most.  No
  * initial contents, and nothing kept in it from one call to the next.  Calls that may run at the same time need one

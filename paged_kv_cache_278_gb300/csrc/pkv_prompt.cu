@@ -52,7 +52,9 @@
 // the first item is looked for during set-up; trees of one tile give Q's second tile to a third V stage; one thread issues all
 // MMAs; K and V, read once, leave L2 first, so that tables, parts and the code itself stay there.  64 trees of 13 to 16 nodes
 // behind 1025 to 2049 keys in 16-token blocks 83 us, 5.1 TB/s; 4 of 52 to 61 nodes behind 16385 to 32768 keys in 64-token blocks
-// 89 us, 4.6 TB/s.  Around the stream, from clock stamps: 7.5 us to the first scores (three reads that depend on each other:
+// 89 us, 4.6 TB/s.  Weights are one fp16 part here too (an output's error 2.9e-4 of its norm instead of 2.1e-4): a second one behind
+// it in S's columns, with P V done twice, costs the softmax's chain more than HBM leaves it (64 trees of 13 to 16 nodes 82.6 -> 120.8 us, 4
+// of 52 to 61 90 -> 146, 16 nodes behind 8192 keys 19.7 -> 23.2).  Around the stream, from clock stamps: 7.5 us to the first scores (three reads that depend on each other:
 // lengths, block ids, K; and code that is read for the first time), 2-3 us of output or parts, 3-4 us that SMs end
 // apart, 6-8 us for the joining launch (its list after 1-1.5 us, the weights 2 later).  Slower: scores by 64 keys, so that a
 // tile's first half is there before the last one's second half is used (107 us where this takes 95; an MMA of 64 columns

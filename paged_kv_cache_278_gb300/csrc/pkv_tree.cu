@@ -168,7 +168,9 @@ __global__ void __launch_bounds__(kKeepThreads) keep_path_kernel(const __grid_co
 // saying which 32, and gives the product's k index a meaning of its own: in step s its four k are dims 4 s .. 4 s + 3 of
 // its 32, for Q and K alike.  V's 8 x 8 blocks of (key, two of a lane's dims) are transposed by movmatrix, so that an
 // output tile's columns are two dims of each of the four lanes', and a lane ends up with the same 32 dims of its output rows.
-// Weights, lifted by 2^7 as in the other kernel, are rounded to fp16 for the product with V; sums are float32.
+// Weights, lifted by 2^7 as in the other kernel, go into the product with V as two fp16 parts, like the decode kernels': with one
+// the output's error is 2.5e-4 of its norm, with two the 2.1e-4 of its own rounding, for 0.3 us (8 nodes over 300 keys 8.6 and
+// 8.9; over 1000 keys 15.0 and 16.3).  Sums are float32.
 constexpr int kShortWarps = 8;
 constexpr int kShortThreads = 32 * kShortWarps;
 constexpr int kShortSmem = kShortWarps * 16 * PKV_HEAD_DIM * 4;  // the warps' outputs
@@ -196,6 +198,19 @@ __device__ __forceinline__ void load_dims(uint32_t (&r)[16], const __half *row) 
         r[4 * i + 2] = v.z;
         r[4 * i + 3] = v.w;
     }
+}
+
+// Two softmax weights (lifted by 2^7: from 0 to 2^7) as the sum of two fp16 each, packed: off by at most 2^-21 of
+// the weight, or 2^-25 where that is more.  The upper part is taken at least 2^-11 of the weight and one fp16 step (2^-24)
+// below it, so that from 2^-23 on (2^-30 of the row's largest) both parts are above 0: an infinity in V times each of
+// them is the same infinity, where a part of 0 or below would make NaN of it.
+__device__ __forceinline__ void split_weights(float w0, float w1, uint32_t &upper, uint32_t &lower) {
+    constexpr float kBelow = 1.f - 0x1p-11f, kStep = 0x1p-24f;
+    const float u0 = fminf(w0 * kBelow, w0 - kStep), u1 = fminf(w1 * kBelow, w1 - kStep);
+    asm("cvt.rz.relu.f16x2.f32 %0, %1, %2;" : "=r"(upper) : "f"(u1), "f"(u0));
+    const float2 taken = pkv::half2_bits_to_float2(upper);
+    const __half2 rest = __floats2half2_rn(w0 - taken.x, w1 - taken.y);
+    lower = *reinterpret_cast<const uint32_t *>(&rest);
 }
 
 __global__ void __launch_bounds__(kShortThreads, 1) tree_short_kernel(const __grid_constant__ pkv_internal::TreeCall P) {
@@ -295,7 +310,7 @@ __global__ void __launch_bounds__(kShortThreads, 1) tree_short_kernel(const __gr
                 }
             }
         }
-        uint32_t p[4];
+        uint32_t p[4], low[4];  // the weights' upper and lower parts
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             float top = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1])) * P.q_scale;
@@ -309,8 +324,7 @@ __global__ void __launch_bounds__(kShortThreads, 1) tree_short_kernel(const __gr
             for (int t = 0; t < 2; ++t) {
                 const float w0 = pkv::exp2_approx(fmaf(s[t][2 * r], P.q_scale, -ms)), w1 = pkv::exp2_approx(fmaf(s[t][2 * r + 1], P.q_scale, -ms));
                 l[r] += w0 + w1;
-                const __half2 pk = __floats2half2_rn(w0, w1);
-                p[2 * t + r] = *reinterpret_cast<const uint32_t *>(&pk);
+                split_weights(w0, w1, p[2 * t + r], low[2 * t + r]);
             }
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
@@ -319,7 +333,11 @@ __global__ void __launch_bounds__(kShortThreads, 1) tree_short_kernel(const __gr
             }
         }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) pkv::mma16816(o[i], p, transpose8x8(v[0][i]), transpose8x8(v[1][i]));
+        for (int i = 0; i < 16; ++i) {
+            const uint32_t v0 = transpose8x8(v[0][i]), v1 = transpose8x8(v[1][i]);
+            pkv::mma16816(o[i], p, v0, v1);
+            pkv::mma16816(o[i], low, v0, v1);
+        }
         if (more) load(v, v_cache, next_at);
     }
     // Outputs to shared memory: piece x (four dims) of quarter y's 32 dims of row z.

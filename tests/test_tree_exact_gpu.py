@@ -1,0 +1,81 @@
+"""How exact tree attention is where one key or one infinity decides, whichever kernel and cut of the keys a call gets: a short
+table, whole items, split items."""
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_278_gb300 as pkv
+import tree_ref
+from gpu_util import assert_no_device_error
+
+pytestmark = pytest.mark.gpu
+SCALE = tree_ref.SCALE
+GROUP, BS = 4, 16
+
+
+def i32(x):
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+
+
+def attend(q, k, v, seen, copies=1, width=None):
+    """Tree attention of the same request (q [c, Hq, 128] behind the first n - c of k, v [n, Hkv, 128]) `copies` times over, in
+    blocks of its own each, tables `width` positions wide: out, lse of every copy."""
+    n, c, hkv = k.shape[0], q.shape[0], k.shape[1]
+    blocks = -(-n // BS)
+    wide = max(blocks, -(-(width or 0) // BS))
+    g = torch.Generator().manual_seed(3)
+    table = torch.full((copies, wide), -7, dtype=torch.int32)
+    table[:, :blocks] = torch.randperm(copies * blocks, generator=g).to(torch.int32).view(copies, blocks)
+    kc, vc = (torch.full((copies * blocks, hkv, BS, 128), float("nan"), dtype=torch.float16, device="cuda") for _ in range(2))
+    for b in range(copies):
+        slots = pkv.slot_mapping(table[b:b + 1, :blocks].expand(n, -1).contiguous(), torch.arange(n, dtype=torch.int32), BS).cuda()
+        pkv.append(kc, vc, slots, torch.from_numpy(k).cuda(), torch.from_numpy(v).cuda())
+    mask = torch.from_numpy(tree_ref.pack_masks(seen, -(-c // 32))).cuda().repeat(copies, 1)
+    qs = torch.from_numpy(q).cuda().repeat(copies, 1, 1)
+    out = torch.full(qs.shape, 7.0, dtype=torch.float16, device="cuda")
+    z = torch.full(qs.shape[:2], 7.0, device="cuda")
+    ws = pkv.make_tree_workspace(copies, copies * c, c, q.shape[1], hkv, wide * BS, "cuda")
+    pkv.decode_attention_tree(out, qs, kc, vc, table.cuda(), i32([n] * copies), i32(np.arange(copies + 1) * c), mask, c, SCALE, lse=z, workspace=ws)
+    assert_no_device_error()
+    return out.view(copies, c, -1, 128).double().cpu().numpy(), z.view(copies, c, -1).double().cpu().numpy()
+
+
+def tree(c, seed=1):
+    rng = np.random.default_rng(seed)
+    return tree_ref.ancestors([int(rng.integers(-1, i)) if i else -1 for i in range(c)])
+
+
+# (positions, nodes, kv heads, copies, table, how exact a weight is): few rows over short tables, the longest among them, take two fp16
+# parts; whole items of a call of many, short contexts behind a wide table and split items one
+SHORT = [(300, 8, 1, 1, None, 2.0 ** -21), (1000, 5, 1, 1, 1024, 2.0 ** -21), (41, 33, 2, 1, None, 2.0 ** -21)]
+LONG = [(700, 16, 8, 40, 1100, 2.0 ** -11), (300, 8, 1, 1, 20000, 2.0 ** -11), (5000, 16, 1, 1, None, 2.0 ** -11),
+        (20000, 33, 2, 1, None, 2.0 ** -11)]
+
+
+@pytest.mark.parametrize("n,c,hkv,copies,width,part", SHORT + LONG)
+def test_weights_in_the_product(n, c, hkv, copies, width, part):
+    """How far a weight is off in the product with V, where little else is.
+
+    24 keys have scores between -2 and 2, the others some 40 less (their weights, e^-36 at most, are 0 in the product: n e^-36 max|v|
+    of the output).  A score is one exact product, so that it is off by a few steps of 2^-23 of its size, 4 at most with the scale; a
+    weight besides by 8 steps for exponential, scaling and rescaling, the float32 sums by one per addition that changes them: 24
+    keys in two parts, 24 in the row's sum.  The output's rounding is half a step of fp16."""
+    rng = np.random.default_rng(n)
+    q, k = np.zeros((c, GROUP * hkv, 128), np.float16), np.zeros((n, hkv, 128), np.float16)
+    q[..., 0] = 16.0
+    live = np.concatenate([rng.choice(n - c, 20, replace=False) if n - c >= 20 else np.arange(n - c), n - c + rng.permutation(c)[:4]])
+    k[..., 0] = -40.0 / (16.0 * SCALE)
+    k[live, :, 0] = rng.uniform(-2.0, 2.0, (len(live), hkv)) / (16.0 * SCALE)
+    v = rng.standard_normal((n, hkv, 128)).astype(np.float16)
+    seen = tree(c)
+    out, z = attend(q, k, v, seen, copies, width)
+    want, lse, p = tree_ref.attend(q.astype(np.float64), k.astype(np.float64), v.astype(np.float64), seen)
+    whole = np.concatenate([np.ones((c, n - c), bool), seen], 1)
+    near = whole[:, live].any(1)  # rows that see one of the live keys: the others see keys of one score
+    size = np.einsum("chn,nhd->chd", p, np.abs(np.repeat(v.astype(np.float64), GROUP, 1)))
+    tol = size * (part + (4 * 4 + 8 + 3 * 24) * 2.0 ** -23) + n * np.exp(-36.0) * 8 + 2.0 ** -11 * np.abs(want) + 2.0 ** -25
+    assert near.sum() >= min(c, 4)
+    for b in range(copies):
+        err = np.abs(out[b] - want)[near]
+        assert (err <= tol[near]).all(), (b, err.max(), (err / tol[near]).max())
+        assert (np.abs(z[b] - lse)[near] <= 64 * 2.0 ** -23 * (1 + np.abs(lse[near]))).all()
