@@ -1520,6 +1520,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
     }
 }
 
+// What a part whose weight has underflowed to 0 brings into a join: its infinities and NaN, whole, as in an item that is
+// not split.
+__device__ __forceinline__ float unless_finite(float x) { return isfinite(x) ? 0.f : x; }
+
 // Joins the splits of each (token, head) row: one warp per row, four dims a lane, BATCH splits' loads in flight.
 // Sixteen take 120 registers, two CTAs per SM; where those hold fewer rows than there are, eight loads a lane and
 // four CTAs do better (one call alone between flushes: 512 tokens ending at 8192, three splits, 90 -> 87 us in all;
@@ -1665,7 +1669,14 @@ __global__ void __launch_bounds__(kJoinThreads, 4) tree_join_kernel(const __grid
 #pragma unroll
                 for (int j = 0; j < kJoinBatch; ++j) {
                     const float w = __shfl_sync(pkv::kFullMask, weight, (j0 + j) & 31);
-                    if (j0 + j >= here || w == 0.f) continue;
+                    if (j0 + j >= here) continue;
+                    if (w == 0.f) {
+                        acc.x += unless_finite(o[j].x);
+                        acc.y += unless_finite(o[j].y);
+                        acc.z += unless_finite(o[j].z);
+                        acc.w += unless_finite(o[j].w);
+                        continue;
+                    }
                     total += w;
                     acc.x = fmaf(w, o[j].x, acc.x);
                     acc.y = fmaf(w, o[j].y, acc.y);

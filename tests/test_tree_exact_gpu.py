@@ -79,3 +79,42 @@ def test_weights_in_the_product(n, c, hkv, copies, width, part):
         err = np.abs(out[b] - want)[near]
         assert (err <= tol[near]).all(), (b, err.max(), (err / tol[near]).max())
         assert (np.abs(z[b] - lse)[near] <= 64 * 2.0 ** -23 * (1 + np.abs(lse[near]))).all()
+
+
+def case_of_infinity(kind, n, c, hkv, far):
+    """One key 140 nats above all others, or half of the keys at minus infinity, and an infinity or a NaN in V of a key `far` away
+    from what decides the row: (q, k, v, the key, and the key that decides or None)."""
+    rng = np.random.default_rng(n + c)
+    q, k = np.zeros((c, GROUP * hkv, 128), np.float16), np.zeros((n, hkv, 128), np.float16)
+    v = rng.standard_normal((n, hkv, 128)).astype(np.float16)
+    q[..., 0] = 16.0
+    at, decides = (n - c // 2 - 1, (n - c) // 8) if far == "node" else ((n - c) // 8, (n - c) // 8 * 7)
+    if kind == "minus infinity":
+        k[:(n - c) // 2, :, 0] = -np.inf
+        v[at, 0, 5] = np.inf
+        return q, k, v, at, None
+    k[decides, :, 0] = 140.0 / (16.0 * SCALE)
+    v[at, 0, 5] = np.nan if kind == "nan" else -np.inf
+    return q, k, v, at, decides
+
+
+@pytest.mark.parametrize("n,c,hkv,copies,width,part", SHORT + LONG)
+@pytest.mark.parametrize("kind,far", [("infinity", "node"), ("infinity", "context"), ("nan", "node"), ("nan", "context"), ("minus infinity", "context")])
+def test_an_infinity_far_below_the_largest_score(n, c, hkv, copies, width, part, kind, far):
+    """An infinity or a NaN in V of a key that a row sees is in that row's output, however small its weight is and wherever the
+    keys are cut; the rest of the output is what the largest score says.  (A weight is off by 2^-11 of itself, an output by as
+    much; all other weights together are below n e^-140.)"""
+    q, k, v, at, decides = case_of_infinity(kind, n, c, hkv, far)
+    seen = tree(c)
+    out, _ = attend(q, k, v, seen, copies, width)
+    sees = seen[:, at - (n - c)] if far == "node" else np.ones(c, bool)
+    assert sees.any()
+    for b in range(copies):
+        got = out[b].reshape(c, hkv, GROUP, 128)
+        assert not np.isfinite(got[sees, 0, :, 5]).any(), (b, got[sees, 0, :, 5])
+        rest = np.ones(got.shape, bool)
+        rest[sees, 0, :, 5] = False
+        assert np.isfinite(got[rest]).all()
+        if decides is not None:
+            want = np.broadcast_to(v[decides].astype(np.float64)[None, :, None], got.shape)
+            assert (np.abs(got - want)[rest] <= (2.0 ** -9 * np.abs(want) + 2.0 ** -24)[rest]).all()
