@@ -109,7 +109,7 @@ struct PromptParams {
     const int32_t *query_start;   // [num_seqs + 1]
     const int32_t *block_tables;  // null: K and V are packed like q
     const int32_t *context_lens;
-    float *o_part, *m_part, *l_part;  // splits > 1: [total_q][Hq][splits](x 128), m in log2 units
+    float *o_part, *m_part, *l_part;  // splits > 1: [total_q][Hq][splits](x 128), m in log2 units; l -1: the split has no output
     int num_seqs, total_q, max_query_len, max_blocks, num_q_heads, num_kv_heads, block_size;
     int64_t num_blocks;
     int group_log2, box_rows, box_log2;
@@ -1499,7 +1499,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                 if (split >= 0) {
                     const int64_t part = TREE ? static_cast<int64_t>(split) * P.slot_rows + tile * kTileRows + r : row * P.splits + split;
                     P.m_part[part] = total == 0.f ? -INFINITY : m;
-                    P.l_part[part] = total;
+                    P.l_part[part] = TREE || n > 0 || n_other > 0 ? total : -1.f;
                 } else if (P.lse != nullptr) {
                     P.lse[row] = (m + log2f(total)) * kLn2;
                 }
@@ -1556,16 +1556,16 @@ __global__ void __launch_bounds__(kJoinThreads, BATCH == 8 ? 4 : 2) prompt_join_
         for (int u = 0; u < 2; ++u) {
             const int s = lane + 32 * u;
             ms[u] = s < splits ? __ldcg(m + s) : -INFINITY;
-            ls[u] = s < splits ? __ldcg(l + s) : 0.f;
+            ls[u] = s < splits ? __ldcg(l + s) : -1.f;
         }
         float top = fmaxf(ms[0], ms[1]);
 #pragma unroll
         for (int sh = 16; sh >= 1; sh >>= 1) top = fmaxf(top, __shfl_xor_sync(pkv::kFullMask, top, sh));
         float total = 0.f;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            ls[u] = ls[u] == 0.f ? 0.f : ls[u] * exp2f(ms[u] - top);  // a split without visible keys wrote no output
-            total += ls[u];
+        for (int u = 0; u < 2; ++u) {  // (below 0: there is no such split, or its slot holds anything)
+            ls[u] = ls[u] <= 0.f ? ls[u] : ls[u] * exp2f(ms[u] - top);
+            total += ls[u] < 0.f ? 0.f : ls[u];
         }
 #pragma unroll
         for (int sh = 16; sh >= 1; sh >>= 1) total += __shfl_xor_sync(pkv::kFullMask, total, sh);
@@ -1576,16 +1576,23 @@ __global__ void __launch_bounds__(kJoinThreads, BATCH == 8 ? 4 : 2) prompt_join_
 #pragma unroll
             for (int u = 0; u < BATCH; ++u) {
                 const int s = s0 + u;
-                w[u] = __shfl_sync(pkv::kFullMask, s < 32 ? ls[0] : ls[1], s & 31);  // (0 past the last split)
+                w[u] = __shfl_sync(pkv::kFullMask, s < 32 ? ls[0] : ls[1], s & 31);  // (-1 past the last split)
                 o[u] = __ldcg(reinterpret_cast<const float4 *>(P.o_part + (row * P.splits + min(s, splits - 1)) * kDim) + lane);
             }
 #pragma unroll
             for (int u = 0; u < BATCH; ++u) {
-                const bool written = w[u] != 0.f;  // else the slot holds anything (selected away, so that all loads are in flight)
-                acc.x = fmaf(w[u], written ? o[u].x : 0.f, acc.x);
-                acc.y = fmaf(w[u], written ? o[u].y : 0.f, acc.y);
-                acc.z = fmaf(w[u], written ? o[u].z : 0.f, acc.z);
-                acc.w = fmaf(w[u], written ? o[u].w : 0.f, acc.w);
+                if (w[u] < 0.f) continue;
+                if (w[u] == 0.f) {
+                    acc.x += unless_finite(o[u].x);
+                    acc.y += unless_finite(o[u].y);
+                    acc.z += unless_finite(o[u].z);
+                    acc.w += unless_finite(o[u].w);
+                    continue;
+                }
+                acc.x = fmaf(w[u], o[u].x, acc.x);
+                acc.y = fmaf(w[u], o[u].y, acc.y);
+                acc.z = fmaf(w[u], o[u].z, acc.z);
+                acc.w = fmaf(w[u], o[u].w, acc.w);
             }
         }
         const float inv = 1.f / total;
