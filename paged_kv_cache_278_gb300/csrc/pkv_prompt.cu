@@ -28,7 +28,7 @@
 //       The weights are taken 2^7 too large, and so are the sums: fp16's range up to 2^15 is used, and a weight keeps its
 //       11 bits down to 2^-21 of the row's largest, some of them down to 2^-32, instead of 2^-14 and 2^-25: the
 //       tail behind one dominant key counts in P V as it does in the sum.
-//   warp 8  issues every tcgen05.mma (one lane).
+//   warp 8  issues every tcgen05.mma, one thread of it throughout.
 //   warps 9, 10  issue the tensor copies: Q (64 KB) once per item and the K tiles of 128 keys, and the V tiles,
 //       each through a ring of two 32 KB stages.  Two warps: with 16-token blocks a tile is 16 copies of 2 KB, and
 //       one warp issuing both K's and V's held the MMAs up (the four chunks 632 us against 551 then).
@@ -928,8 +928,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
             if (!ok)
                 for (uint32_t s = stage > kVRing ? stage - kVRing : 0; s < stage; ++s)
                     wait_phase(bar(kBarVFull + s % kVRing), (s / kVRing) & 1);
-        } else if (TREE && warp == kMmaWarp) {
+        } else if (warp == kMmaWarp) {
             // ---------------------------------------------------------------- tensor-core issue, by one thread throughout
+            // (with one elected anew for each step, and the warp meeting behind it: 16k prompt 1486 us for 1384, chunk of 2k 497 for
+            // 444, 512 tokens behind 8k 87 for 80, 37 and 34 behind 32k and 16k 73 for 71)
             if (elected()) {
                 auto wait1 = [&](int b, uint32_t phase) {
                     if (wait_phase(bar(b), phase & 1)) return true;
@@ -949,6 +951,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                     mbar_arrive(bar(kBarItemEmpty + slot));
                     if (seq < 0) break;
                     const int n_kv = key_tiles(shared, n[0], n[1]);
+                    if (n_kv == 0) continue;  // an empty split
                     // 16-key groups of key tile j that hold cached keys
                     auto groups_of = [&](int j) { return (min(kTileRows, keys - (first + j) * kTileRows) + 15) / 16; };
                     auto qk = [&](int t, int groups) {
@@ -1021,106 +1024,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1) prompt_kernel(const __grid_
                 }
             }
             __syncwarp();
-        } else if (warp == kMmaWarp) {
-            // ---------------------------------------------------------------- tensor-core issue
-            constexpr uint32_t kIdescPV = pkv::umma_idesc_f16_f32(kTileRows, kDim) | (1u << 16);  // V: MN-major
-            uint32_t k_stage = 0, v_stage = 0, loaded = 0, p_count[2] = {0, 0};
-            bool ok = true;
-            for (uint32_t k = 0; ok; ++k) {
-                const int slot = k % kItems;
-                if (!(ok = wait(kBarItemFull + slot, k / kItems))) break;
-                const int seq = uniform(slots[slot].seq), keys = uniform(slots[slot].keys), first = uniform(slots[slot].kv_first);
-                const int n[2] = {uniform(slots[slot].kv_count[0]), uniform(slots[slot].kv_count[1])};
-                const bool shared = uniform(slots[slot].shared) != 0;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(kBarItemEmpty + slot));
-                if (seq < 0) break;
-                const int n_kv = key_tiles(shared, n[0], n[1]);
-                if (n_kv == 0) continue;  // an empty split
-                // 16-key groups of key tile j that hold cached keys
-                auto groups_of = [&](int j) { return (min(kTileRows, keys - (first + j) * kTileRows) + 15) / 16; };
-                auto qk = [&](int t, uint32_t st, int groups) {
-                    if (elected()) {
-                        const uint32_t q = base + L::q + (shared ? 0 : t) * kOperand, kk = base + L::ring + (st % kKRing) * kOperand;
-                        const uint32_t idesc = pkv::umma_idesc_f16_f32(kTileRows, groups * 16);
-    #pragma unroll
-                        for (int ks = 0; ks < kDim / 16; ++ks) {
-                            const uint32_t off = (ks >> 2) * kSlab + (ks & 3) * 32;
-                            pkv::umma_f16(tmem + t * kTileRows, pkv::umma_desc_k_sw128(q + off), pkv::umma_desc_k_sw128(kk + off), idesc,
-                                          ks > 0);
-                        }
-                        pkv::umma_commit(bar(kBarS + t));
-                    }
-                    __syncwarp();
-                };
-                auto commit = [&](int b) {
-                    if (elected()) pkv::umma_commit(bar(b));
-                    __syncwarp();
-                };
-                if (!(ok = wait(kBarQFull, loaded))) break;
-                ++loaded;
-                // O of group t += P V of key tile j (the group's `local`-th)
-                auto pv = [&](int t, uint32_t v, int groups, int local) {
-                    for (int half = 0; half < 2; ++half) {  // keys 0-63 while the softmax finishes 64-127
-                        if (!wait(kBarP + 2 * t + half, p_count[t])) return false;
-                        pkv::tmem_fence_after_sync();
-                        if (elected()) {
-#pragma unroll
-                            for (int g = 4 * half; g < 4 * half + 4; ++g)
-                                if (g < groups)
-                                    umma_f16_ta(tmem + 2 * kTileRows + t * kDim, tmem + t * kTileRows + g * 8,
-                                                pkv::umma_desc_mn_sw128(v + g * 2048, kSlab, 1024), kIdescPV, local > 0 || g > 0);
-                            if (half == 1 && local + 1 == n[t]) pkv::umma_commit(bar(kBarO + t));
-                        }
-                        __syncwarp();
-                    }
-                    ++p_count[t];
-                    return true;
-                };
-                auto k_landed = [&]() { return wait(kBarKFull + k_stage % kKRing, k_stage / kKRing); };
-                // Q K^T of the first key tile for both groups, or of the first two for one each
-                const int firsts = shared ? min(2, n_kv) : 1;
-                for (int x = 0; x < firsts && ok; ++x) {
-                    if (!(ok = k_landed())) break;
-                    pkv::tmem_fence_after_sync();
-                    for (int t = 0; t < 2; ++t)
-                        if (shared ? t == x : n[t] > 0) qk(t, k_stage, groups_of(x));
-                    commit(kBarKEmpty + k_stage % kKRing);
-                    ++k_stage;
-                }
-                if (!ok) break;
-                if (n_kv == firsts) commit(kBarQEmpty);
-                for (int j = 0; j < n_kv && ok; ++j) {
-                    const int k_tile = j + (shared ? 2 : 1);
-                    const bool more = k_tile < n_kv;
-                    if (!(ok = wait(kBarVFull + v_stage % kVRing, v_stage / kVRing))) break;
-                    const uint32_t v = base + L::values + (v_stage % kVRing) * kOperand;
-                    const int groups = groups_of(j), local = shared ? j >> 1 : j;
-                    bool k_here = false;
-                    for (int t = 0; t < 2; ++t) {
-                        if (shared ? t != (j & 1) : j >= n[t]) continue;
-                        if (!(ok = pv(t, v, groups, local))) break;
-                        if (local + 1 < n[t]) {
-                            if (!k_here && !(ok = k_landed())) break;
-                            k_here = true;
-                            qk(t, k_stage, groups_of(k_tile));
-                        }
-                    }
-                    if (!ok) break;
-                    commit(kBarVEmpty + v_stage % kVRing);
-                    ++v_stage;
-                    if (more) {  // (some group always takes the next K tile)
-                        commit(kBarKEmpty + k_stage % kKRing);
-                        ++k_stage;
-                        if (k_tile + 1 == n_kv) commit(kBarQEmpty);  // the item's last Q K^T has been issued
-                    }
-                }
-            }
-            if (!ok) {  // MMAs in flight end before tensor memory is freed (bounded)
-                if (elected()) pkv::umma_commit(bar(kBarDrain));
-                __syncwarp();
-                wait_phase(bar(kBarDrain), 0);
-            }
         }
     } else {
         // ---------------------------------------------------------------- softmax and output of one tile
