@@ -762,7 +762,8 @@ PKV_API int pkv_rope_append(void *q_out, int64_t q_out_stride, const void *q, in
  *   axes      : DEVICE int32 [rotary_dim / 2], the axis that turns each pair (may be NULL with one axis); an entry
  *               outside [0, num_axes) counts as 0 and is recorded as PKV_DEV_BAD_AXIS
  * float32 arithmetic from the row to the rotated row, one rounding.  eps >= 0 (0 makes NaN of a row of zeros).  Other arguments, in-place use and
- * errors as pkv_rope's and pkv_rope_append's. */
+ * errors as pkv_rope's and pkv_rope_append's.  The two calls with an append write the cache, so a step call issued right
+ * behind them on the same cache must not set PKV_STEP_OVERLAP. */
 #define PKV_MAX_ROPE_AXES 4
 
 PKV_API int pkv_norm_rope(void *q_out, int64_t q_out_stride, void *k_out, int64_t k_out_stride, const void *q,
