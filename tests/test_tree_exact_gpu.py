@@ -118,3 +118,28 @@ def test_an_infinity_far_below_the_largest_score(n, c, hkv, copies, width, part,
         if decides is not None:
             want = np.broadcast_to(v[decides].astype(np.float64)[None, :, None], got.shape)
             assert (np.abs(got - want)[rest] <= (2.0 ** -9 * np.abs(want) + 2.0 ** -24)[rest]).all()
+
+
+@pytest.mark.parametrize("nats", [12.0, 18.0, 19.5])
+@pytest.mark.parametrize("n,c,hkv,copies,width,part", SHORT + LONG + [(700, 90, 1, 1, None, 2.0 ** -11), (9000, 61, 1, 1, None, 2.0 ** -11)])
+def test_a_long_tail_below_one_key(n, c, hkv, copies, width, part, nats):
+    """One key far above all others, whose values are all positive: what the tail gives is there.
+
+    A weight of w relative to the row's largest is held at 2^7 w: what it is off by is `part` of it, or 2^-25 where fp16 is subnormal, so at
+    most 2^-32 / w of itself.  The output is off by no more than the weights are, whatever the number of keys, but for the float32
+    sums: a step of 2^-23 per matrix instruction of 16 keys, of two parts, and tile of 128, and a few for the scores, one product each."""
+    at = (n - c) // 3
+    rng = np.random.default_rng(5)
+    q, k = np.zeros((c, GROUP * hkv, 128), np.float16), np.zeros((n, hkv, 128), np.float16)
+    q[..., 0], k[at, :, 0] = 16.0, nats / (16.0 * SCALE)
+    v = rng.uniform(16.0, 64.0, (n, hkv, 128)).astype(np.float16)
+    v[at] = 0
+    seen = tree(c)
+    out, z = attend(q, k, v, seen, copies, width)
+    want, lse, _ = tree_ref.attend(q.astype(np.float64), k.astype(np.float64), v.astype(np.float64), seen)
+    w = np.exp(-SCALE * 16.0 * float(k[at, 0, 0]))
+    tol = want * (max(part, 2.0 ** -32 / w) + 2.0 ** -11 + (64 + n / 8 + n / 128) * 2.0 ** -23) + 2.0 ** -25
+    for b in range(copies):
+        err = np.abs(out[b] - want)
+        assert (err <= tol).all(), (b, err.max(), want.max(), (err / tol).max())
+        assert (np.abs(z[b] - lse) <= 64 * 2.0 ** -23 * (1 + np.abs(lse))).all()
