@@ -10,10 +10,10 @@
 // What bounds it: the tensor cores, 4 x 128 flops a (row, key) pair, with one exponential per pair close
 // behind (128 x 128 pairs: 1024 tensor cycles, 512 or more of the special-function units).  The two tiles
 // take turns: while the tensor cores run tile A's P V and next Q K^T, tile B's warps do their softmax.
-// Measured: one prompt of 16384 tokens (32 heads, G = 4) 1.52 ms, 1.45 PFLOP/s, 76 % of the measured bf16 rate (the
-// same MMAs without the softmax arithmetic: 1.34 ms); four chunks of 2039 to 2048 tokens that end at 8192, 6827, 5462 and 4097
-// cached ones in 16-token blocks 0.53 ms, 1.3 PFLOP/s; 37 and 34 tokens that end at 32768 and 16385 in 64-token blocks
-// 60 us, 3.4 TB/s of K and V; sixteen prompts of 17 to 1000 tokens 71 us: a pair there is three key tiles long, and its start, its border tile, the last P V and the epilogue
+// Measured: one prompt of 16384 tokens (32 heads, G = 4) 1.41 ms, 1.56 PFLOP/s, 82 % of the measured bf16 rate;
+// four chunks of 2039 to 2048 tokens that end at 8192, 6827, 5462 and 4097
+// cached ones in 16-token blocks 0.45 to 0.48 ms, 1.4 to 1.5 PFLOP/s; 37 and 34 tokens that end at 32768 and 16385 in 64-token blocks
+// 58 us, 3.5 TB/s of K and V; sixteen prompts of 17 to 1000 tokens 71 us: a pair there is three key tiles long, and its start, its border tile, the last P V and the epilogue
 // (some 7000 cycles together) outweigh them.
 //
 //   TMEM (512 columns): S_A | S_B | O_A | O_B, 128 fp32 columns each.  P (fp16, two per column) replaces
@@ -52,7 +52,7 @@
 // the first item is looked for during set-up; trees of one tile give Q's second tile to a third V stage; one thread issues all
 // MMAs; K and V, read once, leave L2 first, so that tables, parts and the code itself stay there.  64 trees of 13 to 16 nodes
 // behind 1025 to 2049 keys in 16-token blocks 83 us, 5.1 TB/s; 4 of 52 to 61 nodes behind 16385 to 32768 keys in 64-token blocks
-// 89 us, 4.6 TB/s.  Weights are one fp16 part here too (an output's error 2.9e-4 of its norm instead of 2.1e-4): a second one behind
+// 90 us, 4.5 TB/s.  Weights are one fp16 part here too (an output's error 2.9e-4 of its norm instead of 2.1e-4): a second one behind
 // it in S's columns, with P V done twice, costs the softmax's chain more than HBM leaves it (64 trees of 13 to 16 nodes 82.6 -> 120.8 us, 4
 // of 52 to 61 90 -> 146, 16 nodes behind 8192 keys 19.7 -> 23.2).  Around the stream, from clock stamps: 7.5 us to the first scores (three reads that depend on each other:
 // lengths, block ids, K; and code that is read for the first time), 2-3 us of output or parts, 3-4 us that SMs end
@@ -1506,9 +1506,11 @@ __global__ void __launch_bounds__(kJoinThreads, BATCH == 8 ? 4 : 2) prompt_join_
     }
 }
 
-// Joins the parts of a tree's split items: one warp per row, four dims a lane.  What it takes is latency (20 MB of parts at
-// most), so there are two rounds of loads only: every CTA of one full round lists the split items with one load a record, and
-// a row's outputs are asked for together with what they weigh.  (Some CTAs for each stretch, four times too many for one round
+// Joins the parts of a tree's split items: one warp per row, four dims a lane.  The parts are 40 MB at most (two slots of 256
+// rows for each CTA), mostly still in L2, and what it takes is latency first: every CTA of one full round lists the split items
+// with one load a record, and a row's outputs, kJoinBatch parts at a time, are asked for together with what they weigh.  (By ncu, from
+// HBM: 3 MB of parts 8 us, 22 MB 11, and 30 MB 19, of which HBM's rate is 4.5: 18 trees of 61 nodes, where nearly every CTA leaves
+// two parts and a CTA here has two chunks of rows in turn.)  (Some CTAs for each stretch, four times too many for one round
 // and most without a part to join: 5 to 8 us more.)
 constexpr int kJoinRows = kJoinThreads / 32, kJoinBatch = 6;
 __global__ void __launch_bounds__(kJoinThreads, 4) tree_join_kernel(const __grid_constant__ PromptParams P) {

@@ -34,7 +34,9 @@ constexpr int kKeepCluster = 8;  // CTAs of one request at most (portable cluste
 constexpr int kPieces = PKV_HEAD_DIM / 8;
 
 // One CTA per request, one thread per node: up the parents to a root.  Parents come before their children, so
-// the walk ends after at most `node` steps.
+// the walk ends after at most `node` steps.  Bound by the deepest climb, a parent's load and a mask word read and written back
+// in global memory a step, and past 128 nodes by several of them in turn (in a graph: 64 trees of 16 nodes 1.9 us, 256 of 61 3.2, a
+// tree of 1024 with random parents 32, a line of 1024 661; the masks and parents are 0.02 us of HBM).
 __global__ void __launch_bounds__(kMaskThreads)
     tree_masks_kernel(uint32_t *mask, int32_t *depths, const int32_t *__restrict__ parents, const int32_t *__restrict__ query_start,
                       int total_q, int max_query_len, int words) {
@@ -161,8 +163,8 @@ __global__ void __launch_bounds__(kKeepThreads) keep_path_kernel(const __grid_co
 // Where a call has few rows and few keys, the time of the tensor-memory kernel is its start: barriers, tensor memory,
 // copies' descriptors.  Here one CTA takes 16 (token, head) rows of one kv head, its eight warps a 16-key chunk each in
 // turn, everything from global memory straight into registers, and one meeting at the end.  Bound by latency: 8 nodes over
-// 300 keys (32 heads, 8 kv heads) 8.4 us where the other
-// kernel takes 14.4.
+// 300 keys (32 heads, 8 kv heads) 8.9 us where the other
+// kernel takes 14.6.
 //
 // m16n8k16 products without shared memory.  A thread holds 32 neighbouring dims of a row (64 bytes, four loads), lane % 4
 // saying which 32, and gives the product's k index a meaning of its own: in step s its four k are dims 4 s .. 4 s + 3 of
@@ -170,16 +172,17 @@ __global__ void __launch_bounds__(kKeepThreads) keep_path_kernel(const __grid_co
 // output tile's columns are two dims of each of the four lanes', and a lane ends up with the same 32 dims of its output rows.
 // Weights, lifted by 2^7 as in the other kernel, go into the product with V as two fp16 parts, like the decode kernels': with one
 // the output's error is 2.5e-4 of its norm, with two the 2.1e-4 of its own rounding, for 0.3 us (8 nodes over 300 keys 8.6 and
-// 8.9; over 1000 keys 15.0 and 16.3).  Sums are float32.
+// 8.9; over 1000 keys 15.0 and 15.9).  Sums are float32.
 constexpr int kShortWarps = 8;
 constexpr int kShortThreads = 32 * kShortWarps;
 constexpr int kShortSmem = kShortWarps * 16 * PKV_HEAD_DIM * 4;  // the warps' outputs
 constexpr float kShortLift = 7.0f;
 constexpr float kShortLn2 = 0.6931471805599453f;
 // It is taken where its CTAs are no more than the SMs and the tables no longer than 1024 positions (32 heads, 8 kv heads,
-// 16-token blocks, in a graph, this kernel and the other: 8 nodes over 300 keys 8.4 and 14.4 us, 61 over 300 8.6 and 19.7,
-// 4 x 16 over 300 8.4 and 14.6, 8 x 16 over 300 (256 CTAs) 14.1 and 14.9, 16 x 16 over 300 25.9 and 16.3; 8 over 1000 14.7 and
-// 17.2, 61 over 1000 16.2 and 25.0; 8 over 2000 24.1 and 16.5, 61 over 2000 26.3 and 25.0).
+// 16-token blocks, in a graph, this kernel and the other: 8 nodes over 300 keys 8.9 and 14.6 us, 61 over 300 9.0 and 20.2,
+// 4 x 16 over 300 8.9 and 15.2, 8 x 16 over 300 (256 CTAs) 14.7 and 15.7, 16 x 16 over 300 27.0 and 17.1; 8 over 1000 15.9 and
+// 17.5, 61 over 1000 18.3 and 23.0; 8 over 2000 26.8 and 16.5, 61 over 2000 32.1 and 22.0).  The host does not know the
+// contexts: a short one behind a longer table takes the other kernel.
 constexpr int kShortCtas = 152, kShortContext = 1024;
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
